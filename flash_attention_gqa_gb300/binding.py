@@ -21,10 +21,15 @@ FA_ERR_INVALID_ARG = 1
 FA_ERR_UNSUPPORTED = 2
 FA_ERR_CUDA = 3
 FA_ERR_DEVICE_TIMEOUT = 4
+FA_ERR_DEVICE_VALUE = 5
+
+FA_CACHE_BF16 = 0
+FA_CACHE_E4M3 = 1
 
 # Every symbol include/fa.h declares, with (restype, argtypes).
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
 SIGNATURES = {
     "fa_fwd": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "fa_bwd_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I]),
@@ -44,6 +49,12 @@ SIGNATURES = {
                            ctypes.c_size_t, _I, _I, _I, _I, _I, _I, _P]),
     "fa_block_mask_build": (_I, [_P, _I, _I, _I, _P, _P, _P, ctypes.c_int64,
                                  ctypes.POINTER(ctypes.c_int64)]),
+    "fa_paged_tables": (_I, [_P, _P, _P, _I, _P, _P, _I, _P, _P, _P, _P, _I, _P, _I, _I, _I, _P]),
+    "fa_paged_append": (_I, [_P, _P, _L, _L, _L, _L, _P, _P, _P, _I, _P, _P, _L, _L, _L,
+                             _I, _I, _I, _I, _I, _P]),
+    "fa_paged_decode": (_I, [_P, _P, _P, _I, _P, _P, _L, _L, _L, _P, _P, _I, _P, _P, _P,
+                             ctypes.c_size_t, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "fa_paged_decode_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
     "fa_check_status": (_I, [_P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_set_wait_limit_ns": (_I, [ctypes.c_uint64]),
@@ -260,6 +271,140 @@ def fa_bwd_masked(q, k, v, o, lse, dO, seg_q, seg_kv, causal, mask, dq, dk, dv, 
     return rc
 
 
+# ----------------------------------------------------- paged cache, C names
+#
+# The caches are tensors [n_pages, K, page_size, H] (bf16 or float8_e4m3fn) with any
+# strides whose innermost is 1; [n_pages, page_size, K, H] memory is passed as its
+# transpose(1, 2).  Work goes to the tensors' own device.
+
+def _dense(t: torch.Tensor, dtype, shape, device, name: str) -> int:
+    """Address of a dense tensor of the given type, shape and device."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
+                         f"on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _paged_cache(k_cache, v_cache, k_scale, v_scale, K: int, H: int, device):
+    """(cache type, strides, k_scale address, v_scale address) of a checked cache pair."""
+    P, Kc, page, Hc = k_cache.shape
+    if (Kc, Hc) != (K, H) or v_cache.shape != k_cache.shape:
+        raise ValueError(f"k_cache and v_cache must be [n_pages, {K}, page_size, {H}], "
+                         f"got {tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
+    stride = k_cache.stride()
+    if (stride[3] != 1 or v_cache.stride() != stride) and k_cache.numel():
+        raise ValueError("k_cache and v_cache must have the same strides, innermost 1")
+    if k_cache.device != device or v_cache.device != device or device.type != "cuda":
+        raise ValueError("k_cache and v_cache must be on the CUDA device of the other tensors")
+    if v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must have one type")
+    if k_cache.dtype == torch.bfloat16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("a bfloat16 cache takes no scales")
+        return FA_CACHE_BF16, stride, None, None
+    if k_cache.dtype != torch.float8_e4m3fn:
+        raise ValueError(f"the cache must be bfloat16 or float8_e4m3fn, got {k_cache.dtype}")
+    return (FA_CACHE_E4M3, stride,
+            None if k_scale is None else _dense(k_scale, torch.float32, (K,), device, "k_scale"),
+            None if v_scale is None else _dense(v_scale, torch.float32, (K,), device, "v_scale"))
+
+
+def _raw_stream(stream, device) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def fa_paged_tables(cached_lens, new_lens, free_pages, free_used, block_table, total_lens,
+                    token_starts, slots, positions, free_used_out, n_pages, page_size,
+                    stream=None, check=True) -> int:
+    """Pages and slots of a step's new tokens (see fa.h).  total_lens may be cached_lens and
+    free_used_out may be free_used; positions may be None."""
+    dev = cached_lens.device
+    if dev.type != "cuda":
+        raise ValueError("cached_lens must be a CUDA tensor")
+    if dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return fa_paged_tables(cached_lens, new_lens, free_pages, free_used, block_table,
+                                   total_lens, token_starts, slots, positions, free_used_out,
+                                   n_pages, page_size, stream, check)
+    i32 = torch.int32
+    B, tokens, n_free = cached_lens.shape[0], slots.shape[0], free_pages.shape[0]
+    max_pages = block_table.shape[1]
+    rc = load().fa_paged_tables(
+        _dense(cached_lens, i32, (B,), dev, "cached_lens"),
+        _dense(new_lens, i32, (B,), dev, "new_lens"),
+        _dense(free_pages, i32, (n_free,), dev, "free_pages"), n_free,
+        _dense(free_used, i32, (1,), dev, "free_used"),
+        _dense(block_table, i32, (B, max_pages), dev, "block_table"), max_pages,
+        _dense(total_lens, i32, (B,), dev, "total_lens"),
+        _dense(token_starts, i32, (B + 1,), dev, "token_starts"),
+        _dense(slots, torch.int64, (tokens,), dev, "slots"),
+        None if positions is None else _dense(positions, i32, (tokens,), dev, "positions"), tokens,
+        _dense(free_used_out, i32, (1,), dev, "free_used_out"),
+        B, int(n_pages), int(page_size), _raw_stream(stream, dev))
+    if check:
+        _check("fa_paged_tables", rc)
+    return rc
+
+
+def fa_paged_append(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, stream=None,
+                    check=True) -> int:
+    """Write k, v [N, K, H] (bf16, any token and head strides) into the pages of `slots`."""
+    dev = k.device
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return fa_paged_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream, check)
+    N, K, H = k.shape
+    sk, sv = k.stride(), v.stride()
+    if (k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or v.shape != k.shape
+            or v.device != dev or (k.numel() and (sk[2] != 1 or sv[2] != 1))):
+        raise ValueError("k and v must be bfloat16 tensors of one shape [N, K, H] on one device, "
+                         "innermost stride 1")
+    kind, st, ks, vs = _paged_cache(k_cache, v_cache, k_scale, v_scale, K, H, dev)
+    rc = load().fa_paged_append(
+        k.data_ptr(), v.data_ptr(), sk[0], sk[1], sv[0], sv[1],
+        _dense(slots, torch.int64, (N,), dev, "slots"), k_cache.data_ptr(), v_cache.data_ptr(),
+        kind, ks, vs, st[0], st[1], st[2], N, K, H, k_cache.shape[0], k_cache.shape[2],
+        _raw_stream(stream, dev))
+    if check:
+        _check("fa_paged_append", rc)
+    return rc
+
+
+def fa_paged_decode(q, k_cache, v_cache, block_table, lens, o, lse, workspace, k_scale=None,
+                    v_scale=None, window=0, stream=None, check=True) -> int:
+    """Attention of q [B, K, G, T, H], each request's T newest tokens, over its pages."""
+    dev = q.device
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return fa_paged_decode(q, k_cache, v_cache, block_table, lens, o, lse, workspace,
+                                   k_scale, v_scale, window, stream, check)
+    B, K, G, T, H = shape = q.shape
+    kind, st, ks, vs = _paged_cache(k_cache, v_cache, k_scale, v_scale, K, H, dev)
+    max_pages = block_table.shape[1]
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    rc = load().fa_paged_decode(
+        _dense(q, torch.bfloat16, shape, dev, "q"), k_cache.data_ptr(), v_cache.data_ptr(), kind,
+        ks, vs, st[0], st[1], st[2],
+        _dense(block_table, torch.int32, (B, max_pages), dev, "block_table"),
+        _dense(lens, torch.int32, (B,), dev, "lens"), int(window),
+        _dense(o, torch.bfloat16, shape, dev, "o"),
+        _dense(lse, torch.float32, shape[:4], dev, "lse"), ws, ws_bytes,
+        B, K, G, T, H, k_cache.shape[0], k_cache.shape[2], max_pages, _raw_stream(stream, dev))
+    if check:
+        _check("fa_paged_decode", rc)
+    return rc
+
+
+def fa_paged_decode_workspace_size(B, K, G, T, H) -> int:
+    return int(load().fa_paged_decode_workspace_size(B, K, G, T, H))
+
+
 # ------------------------------------------------------- tensor helpers
 
 def block_mask_from_dense(mask, device=None):
@@ -319,3 +464,32 @@ def attention_backward(q, k, v, o, lse, dO, *, causal=False, seg_q=None, seg_kv=
         workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
     fa_bwd(q, k, v, o, lse, dO, seg_q, seg_kv, causal, dq, dk, dv, workspace, stream)
     return dq, dk, dv
+
+
+def paged_tables(cached_lens, new_lens, free_pages, free_used, block_table, *, n_pages, page_size,
+                 max_tokens, stream=None):
+    """Allocate a step's outputs with torch and run fa_paged_tables, which also writes the
+    newly opened pages into block_table.  Returns (total_lens, token_starts, slots, positions,
+    free_used) tensors, the last for the next step."""
+    new = lambda n, dtype=torch.int32: torch.empty(n, dtype=dtype, device=cached_lens.device)
+    B = cached_lens.shape[0]
+    total, starts, used = new(B), new(B + 1), new(1)
+    slots, positions = new(max_tokens, torch.int64), new(max_tokens)
+    fa_paged_tables(cached_lens, new_lens, free_pages, free_used, block_table, total, starts, slots,
+                    positions, used, n_pages, page_size, stream)
+    return total, starts, slots, positions, used
+
+
+def paged_attention_decode(q, k_cache, v_cache, block_table, lens, *, k_scale=None, v_scale=None,
+                           window=0, stream=None, workspace=None):
+    """Allocate o / lse (and the workspace unless given) and run fa_paged_decode."""
+    B, K, G, T, H = q.shape
+    o = torch.empty_like(q)
+    lse = torch.empty((B, K, G, T), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        with torch.cuda.device(q.device):
+            n = fa_paged_decode_workspace_size(B, K, G, T, H)
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+    fa_paged_decode(q, k_cache, v_cache, block_table, lens, o, lse, workspace, k_scale, v_scale,
+                    window, stream)
+    return o, lse

@@ -13,10 +13,27 @@
 
 #include "../../include/fa.h"
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace fa {
-// Device error word: bounded waits that give up OR their code in here.
+// Device error word: bounded waits that give up and device values out of range
+// OR their code in here.
 __device__ uint32_t g_fa_error = 0;
+
+// Device address of the error word on the current device (cached per device).
+uint32_t* device_error_word() {
+  static uint32_t* addr[64] = {};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!addr[dev]) {
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_fa_error) != cudaSuccess) return nullptr;
+    addr[dev] = static_cast<uint32_t*>(p);
+  }
+  return addr[dev];
+}
 }  // namespace fa
 
 namespace {
@@ -53,21 +70,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
   });
   return fn;
-}
-
-// Device address of the error word on the current device (cached per device).
-uint32_t* error_word() {
-  static uint32_t* addr[64] = {};
-  static std::mutex mu;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
-  std::lock_guard<std::mutex> lk(mu);
-  if (!addr[dev]) {
-    void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, fa::g_fa_error) != cudaSuccess) return nullptr;
-    addr[dev] = static_cast<uint32_t*>(p);
-  }
-  return addr[dev];
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -203,7 +205,7 @@ int fwd_common(const void* q, const void* k, const void* v, const int32_t* seg_q
     a.part_o = static_cast<float*>(workspace);
     a.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + o_bytes);
   }
-  a.err = error_word();
+  a.err = fa::device_error_word();
   a.wait_limit_ns = wait_limit();
   if (!a.err) return FA_ERR_CUDA;
   cudaError_t e = fa::launch_fwd(a, st, g_fwd_schedule.load());
@@ -353,7 +355,7 @@ int bwd_impl(int stage, const void* q, const void* k, const void* v, const void*
     a.dkv_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + wl.partials);
   }
   a.bm = bm;
-  a.err = error_word();
+  a.err = fa::device_error_word();
   a.wait_limit_ns = wait_limit();
   if (!a.err) return FA_ERR_CUDA;
   cudaError_t e = cudaSuccess;
@@ -495,7 +497,7 @@ int fa_check_status(void* stream) {
   if (err != 0) {
     const uint32_t zero = 0;
     if (cudaMemcpyToSymbol(fa::g_fa_error, &zero, sizeof(zero)) != cudaSuccess) return FA_ERR_CUDA;
-    return FA_ERR_DEVICE_TIMEOUT;
+    return (err & fa::DEV_TIMEOUT) ? FA_ERR_DEVICE_TIMEOUT : FA_ERR_DEVICE_VALUE;
   }
   return FA_OK;
 }
@@ -507,6 +509,7 @@ const char* fa_status_string(int status) {
     case FA_ERR_UNSUPPORTED: return "unsupported shape or option";
     case FA_ERR_CUDA: return "CUDA error";
     case FA_ERR_DEVICE_TIMEOUT: return "a bounded device wait timed out";
+    case FA_ERR_DEVICE_VALUE: return "a length, page id or slot in device memory was out of range";
     default: return "unknown status";
   }
 }
@@ -548,7 +551,7 @@ int fa_set_fwd_schedule(int mode) {
 }
 
 int fa_selftest_wait_timeout(void* stream) {
-  uint32_t* err = error_word();
+  uint32_t* err = fa::device_error_word();
   if (!err) return FA_ERR_CUDA;
   if (fa::launch_wait_selftest(err, wait_limit(), static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return FA_ERR_CUDA;

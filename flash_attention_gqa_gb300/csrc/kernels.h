@@ -96,6 +96,9 @@ cudaError_t launch_split_combine(const float* part_o, const float* part_lse, int
                                  float* lse, long rows, int H, cudaStream_t st);
 cudaError_t launch_wait_selftest(uint32_t* err, uint64_t limit_ns, cudaStream_t st);
 
+// Device address of the error word on the current device (null on failure).
+uint32_t* device_error_word();
+
 // KV rows per tile of the backward kernels.  H = 256 always takes 64 (a
 // 128-key K/V pair does not fit in shared memory next to the Q/dO tiles); H <=
 // 128 takes 128 unless that leaves the dK/dV grid (one CTA per KV tile and

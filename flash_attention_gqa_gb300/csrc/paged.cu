@@ -1,0 +1,279 @@
+// Paged key-value cache: block tables and slot maps from request lengths, new
+// keys and values written into pages, and attention over the pages.
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "paged.h"
+#include "ptx.cuh"
+
+namespace fa {
+namespace {
+
+// ----------------------------------------------------------------- tables
+
+constexpr int kTablesThreads = 1024;
+
+// Request b holds ceil(c_b / P) pages and needs ceil((c_b + n_b) / P): two
+// exclusive sums over the requests (tokens, opened pages) place every token
+// and every page.  All lengths are read before anything is written, so the
+// outputs may replace the inputs; a call that cannot be met changes nothing.
+__global__ void __launch_bounds__(kTablesThreads) paged_tables_kernel(const PagedTablesArgs a) {
+  extern __shared__ int sm[];
+  int* starts = sm;               // [B + 1] first token of each request
+  int* cached = sm + a.B + 1;     // [B]
+  int* taken = cached + a.B;      // [B] free pages taken before the request
+  __shared__ long long warp_tok[32], warp_pg[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int P = 1 << a.page_shift;
+  const int per = (a.B + kTablesThreads - 1) / kTablesThreads;
+  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  const long long most = (long long)a.max_pages << a.page_shift;
+
+  auto pages = [&](long long n) { return (n + P - 1) >> a.page_shift; };
+  bool bad = false;
+  long long tok = 0, pg = 0;
+  for (int b = b0; b < b1; ++b) {
+    const long long c = a.cached_lens[b], n = a.new_lens[b];
+    bad |= c < 0 || n < 0 || c + n > most;
+    tok += n;
+    pg += pages(c + n) - pages(c);
+  }
+  long long it = tok, ip = pg;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long t = __shfl_up_sync(~0u, it, d), p = __shfl_up_sync(~0u, ip, d);
+    if (lane >= d) { it += t; ip += p; }
+  }
+  if (lane == 31) { warp_tok[warp] = it; warp_pg[warp] = ip; }
+  __syncthreads();
+  if (warp == 0) {
+    long long t = warp_tok[lane], p = warp_pg[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long x = __shfl_up_sync(~0u, t, d), y = __shfl_up_sync(~0u, p, d);
+      if (lane >= d) { t += x; p += y; }
+    }
+    warp_tok[lane] = t;
+    warp_pg[lane] = p;
+  }
+  __syncthreads();
+  const long long all_tok = warp_tok[31], all_pg = warp_pg[31];
+  const int used = *a.free_used;
+  bad |= all_tok > a.max_tokens || used < 0 || used + all_pg > a.n_free;
+  const bool fail = __syncthreads_or(bad);
+  if (!fail) {
+    long long t = it - tok + (warp ? warp_tok[warp - 1] : 0);
+    long long p = ip - pg + (warp ? warp_pg[warp - 1] : 0);
+    for (int b = b0; b < b1; ++b) {
+      const long long c = a.cached_lens[b], n = a.new_lens[b];
+      starts[b] = (int)t;
+      cached[b] = (int)c;
+      taken[b] = (int)p;
+      t += n;
+      p += pages(c + n) - pages(c);
+    }
+    if (tid == 0) starts[a.B] = (int)all_tok;
+  }
+  __syncthreads();
+  if (fail) {
+    for (int b = tid; b < a.B; b += kTablesThreads) a.total_lens[b] = a.cached_lens[b];
+    for (int b = tid; b <= a.B; b += kTablesThreads) a.token_starts[b] = 0;
+    if (tid == 0) {
+      *a.free_used_out = used;
+      atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+    }
+  } else {
+    for (int b = tid; b < a.B; b += kTablesThreads) a.total_lens[b] = cached[b] + starts[b + 1] - starts[b];
+    for (int b = tid; b <= a.B; b += kTablesThreads) a.token_starts[b] = starts[b];
+    if (tid == 0) *a.free_used_out = used + (int)all_pg;
+  }
+  const int tokens = fail ? 0 : (int)all_tok;
+  for (int i = tid; i < a.max_tokens; i += kTablesThreads) {
+    if (i >= tokens) {
+      a.slots[i] = -1;
+      if (a.positions) a.positions[i] = -1;
+      continue;
+    }
+    int lo = 0, hi = a.B;   // the request with starts[b] <= i < starts[b + 1]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (starts[mid] <= i) lo = mid; else hi = mid;
+    }
+    const int b = lo;
+    const int pos = cached[b] + i - starts[b];
+    const int col = pos >> a.page_shift, held = (int)pages(cached[b]);
+    int32_t* entry = a.block_table + (int64_t)b * a.max_pages + col;
+    int page;
+    if (col >= held) {
+      page = a.free_pages[used + taken[b] + col - held];
+      if ((pos & (P - 1)) == 0) *entry = page;
+    } else {
+      page = *entry;
+    }
+    int64_t slot = ((int64_t)page << a.page_shift) + (pos & (P - 1));
+    if (page < 0 || page >= a.n_pages) {
+      atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+      slot = -1;
+    }
+    a.slots[i] = slot;
+    if (a.positions) a.positions[i] = pos;
+  }
+}
+
+// ----------------------------------------------------------------- append
+
+constexpr int kAppendThreads = 256;
+
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;   // round to nearest even, saturating at +-448; NaN stays NaN
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+// One thread per 8 head dims of a key and of the value beside it.
+template <bool E4M3>
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const PagedAppendArgs a) {
+  const int vecs = a.H / 8;
+  const int64_t i = (int64_t)blockIdx.x * kAppendThreads + threadIdx.x;
+  if (i >= (int64_t)a.N * a.K * vecs) return;
+  const int u = (int)(i % vecs);
+  const int k = (int)(i / vecs % a.K);
+  const int64_t n = i / vecs / a.K;
+  const int64_t slot = a.slots[n];
+  if (slot < 0) return;   // padding
+  if (slot >> a.lay.page_shift >= a.lay.n_pages) {
+    atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+    return;
+  }
+  const int64_t page = slot >> a.lay.page_shift, in = slot & ((1 << a.lay.page_shift) - 1);
+  const int64_t dst = page * a.lay.page + k * a.lay.head + in * a.lay.token;
+  const uint4 xk = *reinterpret_cast<const uint4*>((const char*)a.k + n * a.k_token + k * a.k_head + u * 16);
+  const uint4 xv = *reinterpret_cast<const uint4*>((const char*)a.v + n * a.v_token + k * a.v_head + u * 16);
+  if (!E4M3) {
+    *reinterpret_cast<uint4*>((char*)a.k_cache + dst + u * 16) = xk;
+    *reinterpret_cast<uint4*>((char*)a.v_cache + dst + u * 16) = xv;
+  } else {
+    auto squeeze = [](uint4 x, float s) {
+      const float2 p = unpack_bf16x2(x.x), q = unpack_bf16x2(x.y), r = unpack_bf16x2(x.z), t = unpack_bf16x2(x.w);
+      return make_uint2(pack_e4m3x4(p.x / s, p.y / s, q.x / s, q.y / s),
+                        pack_e4m3x4(r.x / s, r.y / s, t.x / s, t.y / s));
+    };
+    const float sk = a.k_scale ? a.k_scale[k] : 1.0f, sv = a.v_scale ? a.v_scale[k] : 1.0f;
+    *reinterpret_cast<uint2*>((char*)a.k_cache + dst + u * 8) = squeeze(xk, sk);
+    *reinterpret_cast<uint2*>((char*)a.v_cache + dst + u * 8) = squeeze(xv, sv);
+  }
+}
+
+// ----------------------------------------------------------------- decode
+
+constexpr int kDecodeWarps = 4;
+
+template <bool E4M3>
+__device__ __forceinline__ float cache_value(const char* row, int d) {
+  if (E4M3) {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw(*(const uint8_t*)(row + d), __NV_E4M3);
+    return __half2float(__half(h));
+  }
+  return __bfloat162float(*(const __nv_bfloat16*)(row + 2 * d));
+}
+
+// One CTA per query row; its warps take the keys in turn, each with its own
+// running maximum and sum, and are joined at the end.
+template <int H, bool E4M3>
+__global__ void __launch_bounds__(kDecodeWarps * 32) paged_decode_kernel(const PagedDecodeArgs a) {
+  constexpr int D = H / 32;
+  const int rows = a.G * a.T, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int bk = blockIdx.x / rows, r = blockIdx.x % rows, b = bk / a.K, k = bk % a.K;
+  int len = a.lens[b];
+  if (len < 0 || len > (a.max_pages << a.lay.page_shift)) {
+    if (threadIdx.x == 0) atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+    len = len < 0 ? 0 : a.max_pages << a.lay.page_shift;
+  }
+  const int hi = len - a.T + r % a.T + 1;
+  const int lo = a.window > 0 ? max(0, hi - a.window) : 0;
+  const float ks = a.k_scale ? a.k_scale[k] : 1.0f, vs = a.v_scale ? a.v_scale[k] : 1.0f;
+  float q[D], acc[D], m = -INFINITY, l = 0.0f;
+  const __nv_bfloat16* qr = (const __nv_bfloat16*)a.q + (int64_t)blockIdx.x * H;
+#pragma unroll
+  for (int i = 0; i < D; ++i) { q[i] = __bfloat162float(qr[i * 32 + lane]) * ks; acc[i] = 0.0f; }
+  for (int s = lo + warp; s < hi; s += kDecodeWarps) {
+    const int page = a.block_table[(int64_t)b * a.max_pages + (s >> a.lay.page_shift)];
+    const bool ok = page >= 0 && page < a.lay.n_pages;   // else the key and value count as zeros
+    if (!ok && lane == 0) atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+    const int64_t off = ok ? page * a.lay.page + k * a.lay.head +
+                                 (s & ((1 << a.lay.page_shift) - 1)) * a.lay.token : 0;
+    float x = 0.0f, v[D];
+#pragma unroll
+    for (int i = 0; i < D; ++i) {
+      x += ok ? q[i] * cache_value<E4M3>((const char*)a.k_cache + off, i * 32 + lane) : 0.0f;
+      v[i] = ok ? cache_value<E4M3>((const char*)a.v_cache + off, i * 32 + lane) : 0.0f;
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
+    const float mn = fmaxf(m, x), base = mn == -INFINITY ? 0.0f : mn;
+    const float c = expf(m - base), p = expf(x - base);
+    m = mn;
+    l = l * c + p;
+#pragma unroll
+    for (int i = 0; i < D; ++i) acc[i] = acc[i] * c + p * v[i];
+  }
+  __shared__ float sm[kDecodeWarps], sl[kDecodeWarps], so[kDecodeWarps][H];
+  if (lane == 0) { sm[warp] = m; sl[warp] = l; }
+#pragma unroll
+  for (int i = 0; i < D; ++i) so[warp][i * 32 + lane] = acc[i];
+  __syncthreads();
+  float M = -INFINITY, L = 0.0f;
+  for (int w = 0; w < kDecodeWarps; ++w) M = fmaxf(M, sm[w]);
+  const float base = M == -INFINITY ? 0.0f : M;
+  for (int w = 0; w < kDecodeWarps; ++w) L += sl[w] * expf(sm[w] - base);
+  for (int d = threadIdx.x; d < H; d += kDecodeWarps * 32) {
+    float o = 0.0f;
+    for (int w = 0; w < kDecodeWarps; ++w) o += so[w][d] * expf(sm[w] - base);
+    ((__nv_bfloat16*)a.o)[(int64_t)blockIdx.x * H + d] = __float2bfloat16(L == 0.0f ? 0.0f : o * vs / L);
+  }
+  if (threadIdx.x == 0) a.lse[blockIdx.x] = M + logf(L);   // -inf where nothing is visible
+}
+
+template <int H>
+void decode_h(const PagedDecodeArgs& a, cudaStream_t st) {
+  const unsigned grid = (unsigned)(a.B * a.K * a.G * a.T);
+  if (a.e4m3) paged_decode_kernel<H, true><<<grid, kDecodeWarps * 32, 0, st>>>(a);
+  else paged_decode_kernel<H, false><<<grid, kDecodeWarps * 32, 0, st>>>(a);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_tables(const PagedTablesArgs& a, cudaStream_t st) {
+  const size_t smem = (3 * (size_t)a.B + 1) * sizeof(int);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  paged_tables_kernel<<<1, kTablesThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t st) {
+  const int64_t n = (int64_t)a.N * a.K * (a.H / 8);
+  const int64_t blocks = (n + kAppendThreads - 1) / kAppendThreads;
+  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  if (a.e4m3) paged_append_kernel<true><<<(unsigned)blocks, kAppendThreads, 0, st>>>(a);
+  else paged_append_kernel<false><<<(unsigned)blocks, kAppendThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_decode(const PagedDecodeArgs& a, cudaStream_t st) {
+  switch (a.H) {
+    case 64: decode_h<64>(a, st); break;
+    case 128: decode_h<128>(a, st); break;
+    case 256: decode_h<256>(a, st); break;
+    default: return cudaErrorInvalidValue;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace fa

@@ -1,0 +1,68 @@
+// Internal interface of the paged key-value cache operators (paged.cu).
+#pragma once
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace fa {
+
+constexpr int kMaxPagedBatch = 8192;       // requests of one call: their offsets stay in shared memory
+constexpr int kMaxPageSize = 65536;        // tokens per page, a power of two
+constexpr int kMaxPagedLen = 1 << 30;      // keys of one request (max_pages * page_size)
+constexpr int kMaxPagedRows = 128;         // query rows per kv head, G * T
+constexpr float kE4m3Max = 448.0f;
+
+// Where key (page, kv head, offset in the page) of a cache starts, in bytes
+// from the cache's base: the strides are those of [pages, K, page_size, H].
+struct PagedLayout {
+  int64_t page, head, token;   // byte strides
+  int n_pages;
+  int page_shift;              // log2(page_size)
+};
+
+struct PagedTablesArgs {
+  const int32_t* cached_lens;  // [B]
+  const int32_t* new_lens;     // [B]
+  const int32_t* free_pages;   // [n_free]
+  const int32_t* free_used;    // [1]
+  int32_t* block_table;        // [B, max_pages]
+  int32_t* total_lens;         // [B], may be cached_lens
+  int32_t* token_starts;       // [B + 1]
+  int64_t* slots;              // [max_tokens]
+  int32_t* positions;          // [max_tokens] or null
+  int32_t* free_used_out;      // [1], may be free_used
+  int B, n_free, n_pages, page_shift, max_pages, max_tokens;
+  uint32_t* err;
+};
+
+struct PagedAppendArgs {
+  const void *k, *v;                       // bf16 [N, K, H], through the strides below
+  int64_t k_token, k_head, v_token, v_head;  // byte strides
+  const int64_t* slots;                    // [N]
+  void *k_cache, *v_cache;
+  const float *k_scale, *v_scale;          // [K] or null
+  PagedLayout lay;
+  int N, K, H;
+  bool e4m3;
+  uint32_t* err;
+};
+
+struct PagedDecodeArgs {
+  const void* q;               // bf16 [B, K, G, T, H]
+  const void *k_cache, *v_cache;
+  const float *k_scale, *v_scale;  // [K] or null
+  PagedLayout lay;
+  const int32_t* block_table;  // [B, max_pages]
+  const int32_t* lens;         // [B]
+  void* o;                     // bf16 [B, K, G, T, H]
+  float* lse;                  // [B, K, G, T]
+  int B, K, G, T, H, max_pages;
+  int window;                  // 0: none
+  bool e4m3;
+  uint32_t* err;
+};
+
+cudaError_t launch_paged_tables(const PagedTablesArgs& a, cudaStream_t st);
+cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t st);
+cudaError_t launch_paged_decode(const PagedDecodeArgs& a, cudaStream_t st);
+
+}  // namespace fa

@@ -1,0 +1,167 @@
+// C ABI of the paged key-value cache operators: argument checks and launches.
+// Every check happens on the host before anything is enqueued; nothing here
+// allocates device memory or synchronises.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/fa.h"
+#include "kernels.h"
+#include "paged.h"
+
+namespace {
+
+bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// A required pointer of `n`-byte aligned elements.
+bool usable(const void* p, unsigned n) { return p != nullptr && aligned(p, n); }
+
+int log2_exact(int n) {
+  if (n < 1 || (n & (n - 1)) != 0) return -1;
+  int s = 0;
+  while ((1 << s) < n) ++s;
+  return s;
+}
+
+bool head_dim_ok(int H) { return H == 64 || H == 128 || H == 256; }
+
+// Checks a cache's type, strides (in elements) and page geometry, and fills
+// `lay` with them in bytes.  Rows start on 16-byte boundaries.  The stride of a
+// dimension of one is never used, whatever it is.
+int make_layout(fa::PagedLayout* lay, int cache_type, int64_t page_stride, int64_t head_stride,
+                int64_t token_stride, int K, int n_pages, int page_size) {
+  if (cache_type != FA_CACHE_BF16 && cache_type != FA_CACHE_E4M3) return FA_ERR_INVALID_ARG;
+  if (n_pages <= 1) page_stride = 0;
+  if (K <= 1) head_stride = 0;
+  if (page_size == 1) token_stride = 0;
+  if (n_pages < 0 || page_size < 1 || page_stride < 0 || head_stride < 0 || token_stride < 0)
+    return FA_ERR_INVALID_ARG;
+  const int shift = log2_exact(page_size);
+  if (shift < 0 || page_size > fa::kMaxPageSize) return FA_ERR_UNSUPPORTED;
+  const int64_t es = cache_type == FA_CACHE_BF16 ? 2 : 1;
+  const int64_t most = int64_t{1} << 40;
+  if (page_stride > most || head_stride > most || token_stride > most) return FA_ERR_INVALID_ARG;
+  if (((page_stride | head_stride | token_stride) * es) & 15) return FA_ERR_INVALID_ARG;
+  *lay = fa::PagedLayout{page_stride * es, head_stride * es, token_stride * es, n_pages, shift};
+  return FA_OK;
+}
+
+int status(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" {
+
+int fa_paged_tables(const int32_t* cached_lens, const int32_t* new_lens, const int32_t* free_pages,
+                    int n_free, const int32_t* free_used, int32_t* block_table, int max_pages,
+                    int32_t* total_lens, int32_t* token_starts, int64_t* slots, int32_t* positions,
+                    int max_tokens, int32_t* free_used_out, int B, int n_pages, int page_size,
+                    void* stream) {
+  if (B < 0 || n_free < 0 || max_pages < 0 || max_tokens < 0 || n_pages < 0 || page_size < 1)
+    return FA_ERR_INVALID_ARG;
+  const int shift = log2_exact(page_size);
+  if (shift < 0 || page_size > fa::kMaxPageSize || B > fa::kMaxPagedBatch) return FA_ERR_UNSUPPORTED;
+  if ((int64_t)max_pages * page_size > fa::kMaxPagedLen || max_tokens > fa::kMaxPagedLen)
+    return FA_ERR_UNSUPPORTED;
+  if (!usable(token_starts, 4) || !usable(free_used, 4) || !usable(free_used_out, 4))
+    return FA_ERR_INVALID_ARG;
+  if (B > 0 && (!usable(cached_lens, 4) || !usable(new_lens, 4) || !usable(total_lens, 4)))
+    return FA_ERR_INVALID_ARG;
+  if (n_free > 0 && !usable(free_pages, 4)) return FA_ERR_INVALID_ARG;
+  if (B > 0 && max_pages > 0 && !usable(block_table, 4)) return FA_ERR_INVALID_ARG;
+  if (max_tokens > 0 && !usable(slots, 8)) return FA_ERR_INVALID_ARG;
+  if (!aligned(positions, 4)) return FA_ERR_INVALID_ARG;
+  fa::PagedTablesArgs a{};
+  a.cached_lens = cached_lens;
+  a.new_lens = new_lens;
+  a.free_pages = free_pages;
+  a.free_used = free_used;
+  a.block_table = block_table;
+  a.total_lens = total_lens;
+  a.token_starts = token_starts;
+  a.slots = slots;
+  a.positions = positions;
+  a.free_used_out = free_used_out;
+  a.B = B; a.n_free = n_free; a.n_pages = n_pages;
+  a.page_shift = shift; a.max_pages = max_pages; a.max_tokens = max_tokens;
+  a.err = fa::device_error_word();
+  if (!a.err) return FA_ERR_CUDA;
+  return status(fa::launch_paged_tables(a, static_cast<cudaStream_t>(stream)));
+}
+
+int fa_paged_append(const void* k, const void* v, int64_t k_token_stride, int64_t k_head_stride,
+                    int64_t v_token_stride, int64_t v_head_stride, const int64_t* slots,
+                    void* k_cache, void* v_cache, int cache_type, const float* k_scale,
+                    const float* v_scale, int64_t page_stride, int64_t head_stride,
+                    int64_t token_stride, int N, int K, int H, int n_pages, int page_size,
+                    void* stream) {
+  if (N < 0 || K < 0 || H < 0) return FA_ERR_INVALID_ARG;
+  fa::PagedAppendArgs a{};
+  const int rc = make_layout(&a.lay, cache_type, page_stride, head_stride, token_stride, K, n_pages, page_size);
+  if (rc != FA_OK) return rc;
+  if (!head_dim_ok(H) || K > 65535) return FA_ERR_UNSUPPORTED;
+  if (N <= 1) k_token_stride = v_token_stride = 0;
+  if (K <= 1) k_head_stride = v_head_stride = 0;
+  const int64_t most = int64_t{1} << 40;
+  if (k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 || v_head_stride < 0 ||
+      k_token_stride > most || k_head_stride > most || v_token_stride > most || v_head_stride > most ||
+      ((k_token_stride | k_head_stride | v_token_stride | v_head_stride) & 7))
+    return FA_ERR_INVALID_ARG;
+  if (!aligned(k_scale, 4) || !aligned(v_scale, 4)) return FA_ERR_INVALID_ARG;
+  if (cache_type == FA_CACHE_BF16 && (k_scale || v_scale)) return FA_ERR_INVALID_ARG;
+  if (N == 0 || K == 0) return FA_OK;
+  if (!usable(k, 16) || !usable(v, 16) || !usable(slots, 8)) return FA_ERR_INVALID_ARG;
+  if (n_pages > 0 && (!usable(k_cache, 16) || !usable(v_cache, 16))) return FA_ERR_INVALID_ARG;
+  a.k = k; a.v = v;
+  a.k_token = k_token_stride * 2; a.k_head = k_head_stride * 2;
+  a.v_token = v_token_stride * 2; a.v_head = v_head_stride * 2;
+  a.slots = slots;
+  a.k_cache = k_cache; a.v_cache = v_cache;
+  a.k_scale = k_scale; a.v_scale = v_scale;
+  a.N = N; a.K = K; a.H = H;
+  a.e4m3 = cache_type == FA_CACHE_E4M3;
+  a.err = fa::device_error_word();
+  if (!a.err) return FA_ERR_CUDA;
+  return status(fa::launch_paged_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_paged_decode_workspace_size(int B, int K, int G, int T, int H) {
+  (void)B; (void)K; (void)G; (void)T; (void)H;
+  return 0;
+}
+
+int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int cache_type,
+                    const float* k_scale, const float* v_scale, int64_t page_stride,
+                    int64_t head_stride, int64_t token_stride, const int32_t* block_table,
+                    const int32_t* lens, int window, void* o, float* lse, void* workspace,
+                    size_t workspace_bytes, int B, int K, int G, int T, int H, int n_pages,
+                    int page_size, int max_pages, void* stream) {
+  if (B < 0 || K < 0 || G < 0 || T < 0 || H < 0 || max_pages < 0 || window < 0)
+    return FA_ERR_INVALID_ARG;
+  fa::PagedDecodeArgs a{};
+  const int rc = make_layout(&a.lay, cache_type, page_stride, head_stride, token_stride, K, n_pages, page_size);
+  if (rc != FA_OK) return rc;
+  if (!head_dim_ok(H) || (int64_t)G * T > fa::kMaxPagedRows || B > fa::kMaxPagedBatch ||
+      (int64_t)B * K > 65535 || (int64_t)max_pages * page_size > fa::kMaxPagedLen)
+    return FA_ERR_UNSUPPORTED;
+  if (!aligned(k_scale, 4) || !aligned(v_scale, 4)) return FA_ERR_INVALID_ARG;
+  if (cache_type == FA_CACHE_BF16 && (k_scale || v_scale)) return FA_ERR_INVALID_ARG;
+  if ((int64_t)B * K * G * T == 0) return FA_OK;
+  if (!usable(q, 16) || !usable(o, 16) || !usable(lse, 4) || !usable(lens, 4)) return FA_ERR_INVALID_ARG;
+  if (max_pages > 0 && !usable(block_table, 4)) return FA_ERR_INVALID_ARG;
+  if (n_pages > 0 && (!usable(k_cache, 16) || !usable(v_cache, 16))) return FA_ERR_INVALID_ARG;
+  (void)workspace; (void)workspace_bytes;
+  a.q = q; a.k_cache = k_cache; a.v_cache = v_cache;
+  a.k_scale = k_scale; a.v_scale = v_scale;
+  a.block_table = block_table; a.lens = lens;
+  a.o = o; a.lse = lse;
+  a.B = B; a.K = K; a.G = G; a.T = T; a.H = H; a.max_pages = max_pages;
+  // A window that reaches past the longest request is none.
+  a.window = window >= max_pages * page_size ? 0 : window;
+  a.e4m3 = cache_type == FA_CACHE_E4M3;
+  a.err = fa::device_error_word();
+  if (!a.err) return FA_ERR_CUDA;
+  return status(fa::launch_paged_decode(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -16,7 +16,8 @@ namespace fa {
 // ----------------------------------------------------------------- errors
 enum DeviceError : uint32_t {
   DEV_OK = 0,
-  DEV_TIMEOUT = 1,  // a bounded mbarrier wait ran out
+  DEV_TIMEOUT = 1,    // a bounded mbarrier wait ran out
+  DEV_BAD_VALUE = 2,  // a length, page id or slot read from device memory was out of range
 };
 
 struct Abort {

@@ -21,7 +21,10 @@
  * Errors: every call validates all arguments on the host before launching
  * anything and returns one of the FA_* codes below.  A bounded device-side
  * wait that runs out of time sets a device error word; fa_check_status()
- * reports it as FA_ERR_DEVICE_TIMEOUT (and clears it).
+ * reports it as FA_ERR_DEVICE_TIMEOUT (and clears it).  Lengths, page ids and
+ * slots that the paged operators find out of range in device memory set the
+ * same word (FA_ERR_DEVICE_VALUE); nothing outside the caller's buffers is
+ * touched for them.
  */
 #ifndef FA_GB300_H
 #define FA_GB300_H
@@ -40,7 +43,9 @@ enum {
   FA_ERR_UNSUPPORTED = 2,     /* H not in {64,128,256}, G not a power of two <= 128,
                                  S > 131072, B*K > 65535 */
   FA_ERR_CUDA = 3,            /* a CUDA runtime/driver call or launch failed */
-  FA_ERR_DEVICE_TIMEOUT = 4   /* a bounded device wait ran out (kernel gave up) */
+  FA_ERR_DEVICE_TIMEOUT = 4,  /* a bounded device wait ran out (kernel gave up) */
+  FA_ERR_DEVICE_VALUE = 5     /* a length, page id or slot read from device memory was out of
+                                 range (the paged cache operators; reported like a timeout) */
 };
 
 /*
@@ -222,9 +227,111 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v,
                    void* dq, void* dk, void* dv,
                    int B, int K, int G, int T, int S, int H, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Paged key-value cache.  K and V live in pages of `page_size` tokens (a power
+ * of two, 1..65536) that belong to no request until a block table says so:
+ *   k_cache, v_cache : [n_pages, K, page_size, H], bf16 or e4m3, one set of
+ *                      strides for both (page, head, token; in elements, each a
+ *                      multiple of 16 bytes, innermost dim contiguous), so
+ *                      [n_pages, page_size, K, H] memory works as well
+ *   block_table      : [B, max_pages] int32, entry j = page of the request's
+ *                      tokens [j * page_size, (j + 1) * page_size)
+ *   slot             : page * page_size + offset in the page (int64)
+ * A step of a serving program: fa_paged_tables (pages and slots of the step's
+ * new tokens), fa_paged_append (their keys and values), fa_paged_decode.
+ * Lengths, tables and slots stay on the device, so a step can be captured into
+ * a CUDA graph and replayed while the lengths grow.
+ */
+enum {
+  FA_CACHE_BF16 = 0,
+  FA_CACHE_E4M3 = 1   /* 8-bit floating point: value = e4m3 * scale of its kv head */
+};
+
+/*
+ * Pages and slots of a step's new tokens.  Request b (of B <= 8192) has
+ * cached_lens[b] tokens in its pages and gets new_lens[b] more; with
+ * pages(n) = ceil(n / page_size), in request order:
+ *   block_table[b][j], pages(cached) <= j < pages(cached + new): the next
+ *                      entries of free_pages, from free_pages[*free_used] on
+ *   total_lens[b]    = cached_lens[b] + new_lens[b]
+ *   token_starts[b]  = new tokens of the requests before b; [B + 1] entries
+ *   slots[i], positions[i] (may be NULL): slot and position of new token i, the
+ *                      requests' tokens one request after the other; -1 from
+ *                      token_starts[B] to max_tokens
+ *   *free_used_out   = *free_used + pages taken
+ * All pointers are device memory.  Other table entries stay as they were.
+ * total_lens may be cached_lens and free_used_out may be free_used (updated in
+ * place); no other output may overlap another argument.
+ * A step that cannot be met changes nothing: where a length is negative, a
+ * request needs over max_pages pages, the tokens exceed max_tokens or the free
+ * pages run out, total_lens = cached_lens, token_starts = 0, slots = positions
+ * = -1, *free_used_out = *free_used, the table is untouched, and
+ * fa_check_status() reports FA_ERR_DEVICE_VALUE.  A page id outside
+ * [0, n_pages) gives its tokens slot -1, and the same status.
+ */
+int fa_paged_tables(const int32_t* cached_lens, const int32_t* new_lens,
+                    const int32_t* free_pages, int n_free, const int32_t* free_used,
+                    int32_t* block_table, int max_pages,
+                    int32_t* total_lens, int32_t* token_starts,
+                    int64_t* slots, int32_t* positions, int max_tokens,
+                    int32_t* free_used_out,
+                    int B, int n_pages, int page_size, void* stream);
+
+/*
+ * Writes the keys and values of N tokens into the cache:
+ *   cache[slot / page_size, k, slot % page_size, :] = x[n, k, :],  slot = slots[n]
+ * k, v: bf16 [N, K, H] with token and head strides in elements (multiples of 8,
+ * so views of a fused projection's output work), 16-byte aligned.  An e4m3
+ * cache gets x / scale[k] rounded to nearest even and saturated at +-448 (NaN
+ * stays NaN); k_scale, v_scale: float32 [K] in device memory, positive, or
+ * NULL for 1 (NULL with a bf16 cache).  Tokens with slot < 0 are skipped
+ * (padding); so is a slot past the cache, which sets FA_ERR_DEVICE_VALUE.
+ * The slots of one call are distinct: of two tokens with one slot, either may
+ * be kept, or parts of both.
+ */
+int fa_paged_append(const void* k, const void* v,
+                    int64_t k_token_stride, int64_t k_head_stride,
+                    int64_t v_token_stride, int64_t v_head_stride,
+                    const int64_t* slots, void* k_cache, void* v_cache, int cache_type,
+                    const float* k_scale, const float* v_scale,
+                    int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                    int N, int K, int H, int n_pages, int page_size, void* stream);
+
+/*
+ * Attention of each request's T newest tokens over its pages: for query t of
+ * request b, whose lens[b] tokens (the T newest included) are in the cache,
+ *   keys s with  s <= lens[b] - T + t  and, when window > 0,
+ *                s >  lens[b] - T + t - window
+ * and otherwise as fa_fwd: q [B, K, G, T, H] pre-scaled by H**-0.5, softmax over
+ * the kept keys, o bf16, lse float32, o = 0 and lse = -inf for a query with no
+ * key.  T = 1 is a decode step; larger T verifies drafted tokens or continues
+ * a short prompt.  G and T are arbitrary with G * T <= 128; H in {64, 128, 256};
+ * B <= 8192, B * K <= 65535.
+ * k_scale, v_scale: as in fa_paged_append.  Keys past lens[b] are never read, so
+ * what a page holds behind its last token does not matter, nor do table
+ * entries behind the last page.  A length that is negative or past
+ * max_pages * page_size is clamped, and keys of a page id outside
+ * [0, n_pages) count as zero keys with zero values; both set
+ * FA_ERR_DEVICE_VALUE.
+ * `workspace` (256-byte aligned, fa_paged_decode_workspace_size bytes; its
+ * contents on entry do not matter) may be used by one call at a time.
+ */
+int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int cache_type,
+                    const float* k_scale, const float* v_scale,
+                    int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                    const int32_t* block_table, const int32_t* lens, int window,
+                    void* o, float* lse, void* workspace, size_t workspace_bytes,
+                    int B, int K, int G, int T, int H,
+                    int n_pages, int page_size, int max_pages, void* stream);
+
+/* Workspace bytes of fa_paged_decode on the current device (0 for empty or
+   unsupported sizes). */
+size_t fa_paged_decode_workspace_size(int B, int K, int G, int T, int H);
+
 /*
  * Synchronises `stream`, then reads and clears the device error word of the
- * current device.  Returns FA_OK, FA_ERR_DEVICE_TIMEOUT or FA_ERR_CUDA.
+ * current device.  Returns FA_OK, FA_ERR_DEVICE_TIMEOUT, FA_ERR_DEVICE_VALUE (a
+ * timeout comes before it) or FA_ERR_CUDA.
  */
 int fa_check_status(void* stream);
 
