@@ -11,7 +11,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfa_gb300.so")
-SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "paged_api.cu", "paged.cu"]
+SOURCES = ["api.cu", "fwd.cu", "bwd.cu", "paged_api.cu", "paged.cu",
+           *(f"paged_decode_h{h}_{t}.cu" for h in (64, 128, 256) for t in ("bf16", "e4m3"))]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr",
          "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]

@@ -1,8 +1,6 @@
-// Paged key-value cache: block tables and slot maps from request lengths, new
-// keys and values written into pages, and attention over the pages.
+// Paged key-value cache: block tables and slot maps from request lengths, and new
+// keys and values written into pages.
 #include <cstdint>
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include "paged.h"
@@ -167,83 +165,6 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
   }
 }
 
-// ----------------------------------------------------------------- decode
-
-constexpr int kDecodeWarps = 4;
-
-template <bool E4M3>
-__device__ __forceinline__ float cache_value(const char* row, int d) {
-  if (E4M3) {
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(*(const uint8_t*)(row + d), __NV_E4M3);
-    return __half2float(__half(h));
-  }
-  return __bfloat162float(*(const __nv_bfloat16*)(row + 2 * d));
-}
-
-// One CTA per query row; its warps take the keys in turn, each with its own
-// running maximum and sum, and are joined at the end.
-template <int H, bool E4M3>
-__global__ void __launch_bounds__(kDecodeWarps * 32) paged_decode_kernel(const PagedDecodeArgs a) {
-  constexpr int D = H / 32;
-  const int rows = a.G * a.T, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int bk = blockIdx.x / rows, r = blockIdx.x % rows, b = bk / a.K, k = bk % a.K;
-  int len = a.lens[b];
-  if (len < 0 || len > (a.max_pages << a.lay.page_shift)) {
-    if (threadIdx.x == 0) atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
-    len = len < 0 ? 0 : a.max_pages << a.lay.page_shift;
-  }
-  const int hi = len - a.T + r % a.T + 1;
-  const int lo = a.window > 0 ? max(0, hi - a.window) : 0;
-  const float ks = a.k_scale ? a.k_scale[k] : 1.0f, vs = a.v_scale ? a.v_scale[k] : 1.0f;
-  float q[D], acc[D], m = -INFINITY, l = 0.0f;
-  const __nv_bfloat16* qr = (const __nv_bfloat16*)a.q + (int64_t)blockIdx.x * H;
-#pragma unroll
-  for (int i = 0; i < D; ++i) { q[i] = __bfloat162float(qr[i * 32 + lane]) * ks; acc[i] = 0.0f; }
-  for (int s = lo + warp; s < hi; s += kDecodeWarps) {
-    const int page = a.block_table[(int64_t)b * a.max_pages + (s >> a.lay.page_shift)];
-    const bool ok = page >= 0 && page < a.lay.n_pages;   // else the key and value count as zeros
-    if (!ok && lane == 0) atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
-    const int64_t off = ok ? page * a.lay.page + k * a.lay.head +
-                                 (s & ((1 << a.lay.page_shift) - 1)) * a.lay.token : 0;
-    float x = 0.0f, v[D];
-#pragma unroll
-    for (int i = 0; i < D; ++i) {
-      x += ok ? q[i] * cache_value<E4M3>((const char*)a.k_cache + off, i * 32 + lane) : 0.0f;
-      v[i] = ok ? cache_value<E4M3>((const char*)a.v_cache + off, i * 32 + lane) : 0.0f;
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(~0u, x, d);
-    const float mn = fmaxf(m, x), base = mn == -INFINITY ? 0.0f : mn;
-    const float c = expf(m - base), p = expf(x - base);
-    m = mn;
-    l = l * c + p;
-#pragma unroll
-    for (int i = 0; i < D; ++i) acc[i] = acc[i] * c + p * v[i];
-  }
-  __shared__ float sm[kDecodeWarps], sl[kDecodeWarps], so[kDecodeWarps][H];
-  if (lane == 0) { sm[warp] = m; sl[warp] = l; }
-#pragma unroll
-  for (int i = 0; i < D; ++i) so[warp][i * 32 + lane] = acc[i];
-  __syncthreads();
-  float M = -INFINITY, L = 0.0f;
-  for (int w = 0; w < kDecodeWarps; ++w) M = fmaxf(M, sm[w]);
-  const float base = M == -INFINITY ? 0.0f : M;
-  for (int w = 0; w < kDecodeWarps; ++w) L += sl[w] * expf(sm[w] - base);
-  for (int d = threadIdx.x; d < H; d += kDecodeWarps * 32) {
-    float o = 0.0f;
-    for (int w = 0; w < kDecodeWarps; ++w) o += so[w][d] * expf(sm[w] - base);
-    ((__nv_bfloat16*)a.o)[(int64_t)blockIdx.x * H + d] = __float2bfloat16(L == 0.0f ? 0.0f : o * vs / L);
-  }
-  if (threadIdx.x == 0) a.lse[blockIdx.x] = M + logf(L);   // -inf where nothing is visible
-}
-
-template <int H>
-void decode_h(const PagedDecodeArgs& a, cudaStream_t st) {
-  const unsigned grid = (unsigned)(a.B * a.K * a.G * a.T);
-  if (a.e4m3) paged_decode_kernel<H, true><<<grid, kDecodeWarps * 32, 0, st>>>(a);
-  else paged_decode_kernel<H, false><<<grid, kDecodeWarps * 32, 0, st>>>(a);
-}
-
 }  // namespace
 
 cudaError_t launch_paged_tables(const PagedTablesArgs& a, cudaStream_t st) {
@@ -263,16 +184,6 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t st) {
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   if (a.e4m3) paged_append_kernel<true><<<(unsigned)blocks, kAppendThreads, 0, st>>>(a);
   else paged_append_kernel<false><<<(unsigned)blocks, kAppendThreads, 0, st>>>(a);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_paged_decode(const PagedDecodeArgs& a, cudaStream_t st) {
-  switch (a.H) {
-    case 64: decode_h<64>(a, st); break;
-    case 128: decode_h<128>(a, st); break;
-    case 256: decode_h<256>(a, st); break;
-    default: return cudaErrorInvalidValue;
-  }
   return cudaGetLastError();
 }
 

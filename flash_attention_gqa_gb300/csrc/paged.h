@@ -57,12 +57,40 @@ struct PagedDecodeArgs {
   float* lse;                  // [B, K, G, T]
   int B, K, G, T, H, max_pages;
   int window;                  // 0: none
-  bool e4m3;
+  float* partials;             // workspace: [CTAs][2][paged_partial_floats] of split items
+  uint64_t* counters;          // workspace: [CTAs] arrivals, the call's tag above 16 bits of count
+  unsigned long long tag;      // names the call, 48 bits
   uint32_t* err;
 };
 
+// Workspace of a decode: counters, then partials, on a GPU with sm_count SMs.
+// CTAs an SM: as many as the rings leave room for.  Up to 16 query rows: two
+// up to H = 128, one at 256; more rows: two up to 64 rows (4 warps each) and H
+// = 128, else one.
+struct PagedDecodePlan {
+  int ctas;
+  size_t partials;   // offset
+  size_t total;
+};
+// Floats of one partial: o [R, H], m [R], l [R], rounded up to 16 bytes.
+__host__ __device__ inline int64_t paged_partial_floats(int R, int H) {
+  return ((int64_t)R * (H + 2) + 3) & ~(int64_t)3;
+}
+inline PagedDecodePlan paged_decode_plan(int R, int H, int sm_count) {
+  PagedDecodePlan p;
+  p.ctas = sm_count * (H <= 128 && R <= 64 ? 2 : 1);
+  p.partials = ((size_t)p.ctas * 8 + 255) & ~(size_t)255;
+  p.total = p.partials + (((size_t)p.ctas * 2 * paged_partial_floats(R, H) * 4 + 255) & ~(size_t)255);
+  return p;
+}
+
 cudaError_t launch_paged_tables(const PagedTablesArgs& a, cudaStream_t st);
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t st);
-cudaError_t launch_paged_decode(const PagedDecodeArgs& a, cudaStream_t st);
+cudaError_t launch_paged_decode_h64_bf16(const PagedDecodeArgs& a, int grid, cudaStream_t st);
+cudaError_t launch_paged_decode_h64_e4m3(const PagedDecodeArgs& a, int grid, cudaStream_t st);
+cudaError_t launch_paged_decode_h128_bf16(const PagedDecodeArgs& a, int grid, cudaStream_t st);
+cudaError_t launch_paged_decode_h128_e4m3(const PagedDecodeArgs& a, int grid, cudaStream_t st);
+cudaError_t launch_paged_decode_h256_bf16(const PagedDecodeArgs& a, int grid, cudaStream_t st);
+cudaError_t launch_paged_decode_h256_e4m3(const PagedDecodeArgs& a, int grid, cudaStream_t st);
 
 }  // namespace fa

@@ -3,6 +3,7 @@
 // allocates device memory or synchronises.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/fa.h"
@@ -44,6 +45,21 @@ int make_layout(fa::PagedLayout* lay, int cache_type, int64_t page_stride, int64
   if (((page_stride | head_stride | token_stride) * es) & 15) return FA_ERR_INVALID_ARG;
   *lay = fa::PagedLayout{page_stride * es, head_stride * es, token_stride * es, n_pages, shift};
   return FA_OK;
+}
+
+bool decode_shape_ok(int B, int K, int G, int T, int H) {
+  return head_dim_ok(H) && (int64_t)G * T <= fa::kMaxPagedRows && B <= fa::kMaxPagedBatch &&
+         (int64_t)B * K <= 65535;
+}
+
+// A number of its own for each decode call (48 bits, never 0): a word that some
+// other call or program left in a workspace does not look like it.
+unsigned long long call_tag() {
+  static std::atomic<unsigned long long> calls{0};
+  unsigned long long x = calls.fetch_add(1) * 0x9e3779b97f4a7c15ull + 0x632be59bd9b4e019ull;
+  x = (x ^ (x >> 31)) * 0xd6e8feb86659fd93ull;
+  x = (x ^ (x >> 29)) >> 16;
+  return x ? x : 1;
 }
 
 int status(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
@@ -126,8 +142,8 @@ int fa_paged_append(const void* k, const void* v, int64_t k_token_stride, int64_
 }
 
 size_t fa_paged_decode_workspace_size(int B, int K, int G, int T, int H) {
-  (void)B; (void)K; (void)G; (void)T; (void)H;
-  return 0;
+  if (B <= 0 || K <= 0 || G <= 0 || T <= 0 || !decode_shape_ok(B, K, G, T, H)) return 0;
+  return fa::paged_decode_plan(G * T, H, fa_device_sm_count()).total;
 }
 
 int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int cache_type,
@@ -141,8 +157,7 @@ int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int
   fa::PagedDecodeArgs a{};
   const int rc = make_layout(&a.lay, cache_type, page_stride, head_stride, token_stride, K, n_pages, page_size);
   if (rc != FA_OK) return rc;
-  if (!head_dim_ok(H) || (int64_t)G * T > fa::kMaxPagedRows || B > fa::kMaxPagedBatch ||
-      (int64_t)B * K > 65535 || (int64_t)max_pages * page_size > fa::kMaxPagedLen)
+  if (!decode_shape_ok(B, K, G, T, H) || (int64_t)max_pages * page_size > fa::kMaxPagedLen)
     return FA_ERR_UNSUPPORTED;
   if (!aligned(k_scale, 4) || !aligned(v_scale, 4)) return FA_ERR_INVALID_ARG;
   if (cache_type == FA_CACHE_BF16 && (k_scale || v_scale)) return FA_ERR_INVALID_ARG;
@@ -150,7 +165,8 @@ int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int
   if (!usable(q, 16) || !usable(o, 16) || !usable(lse, 4) || !usable(lens, 4)) return FA_ERR_INVALID_ARG;
   if (max_pages > 0 && !usable(block_table, 4)) return FA_ERR_INVALID_ARG;
   if (n_pages > 0 && (!usable(k_cache, 16) || !usable(v_cache, 16))) return FA_ERR_INVALID_ARG;
-  (void)workspace; (void)workspace_bytes;
+  const fa::PagedDecodePlan plan = fa::paged_decode_plan(G * T, H, fa_device_sm_count());
+  if (!usable(workspace, 256) || workspace_bytes < plan.total) return FA_ERR_INVALID_ARG;
   a.q = q; a.k_cache = k_cache; a.v_cache = v_cache;
   a.k_scale = k_scale; a.v_scale = v_scale;
   a.block_table = block_table; a.lens = lens;
@@ -158,10 +174,24 @@ int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int
   a.B = B; a.K = K; a.G = G; a.T = T; a.H = H; a.max_pages = max_pages;
   // A window that reaches past the longest request is none.
   a.window = window >= max_pages * page_size ? 0 : window;
-  a.e4m3 = cache_type == FA_CACHE_E4M3;
+  a.counters = static_cast<uint64_t*>(workspace);
+  a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.partials);
+  a.tag = call_tag();
   a.err = fa::device_error_word();
-  if (!a.err) return FA_ERR_CUDA;
-  return status(fa::launch_paged_decode(a, static_cast<cudaStream_t>(stream)));
+  if (!a.err || plan.ctas == 0) return FA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool e4m3 = cache_type == FA_CACHE_E4M3;
+  switch (H) {
+    case 64:
+      return status(e4m3 ? fa::launch_paged_decode_h64_e4m3(a, plan.ctas, st)
+                         : fa::launch_paged_decode_h64_bf16(a, plan.ctas, st));
+    case 128:
+      return status(e4m3 ? fa::launch_paged_decode_h128_e4m3(a, plan.ctas, st)
+                         : fa::launch_paged_decode_h128_bf16(a, plan.ctas, st));
+    default:
+      return status(e4m3 ? fa::launch_paged_decode_h256_e4m3(a, plan.ctas, st)
+                         : fa::launch_paged_decode_h256_bf16(a, plan.ctas, st));
+  }
 }
 
 }  // extern "C"

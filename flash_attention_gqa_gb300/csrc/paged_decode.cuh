@@ -1,0 +1,811 @@
+// Attention of each request's T newest tokens over its pages.
+//
+//   x[r, s] = q[r] . k[s],  w = softmax over the keys that row r keeps,  o[r] = sum_s w[r, s] v[s]
+//
+// for the R = G * T query rows of a kv head, which share its keys.  Every key
+// and value byte is needed once and meets R rows: R FLOP per byte in bf16, so
+// memory bandwidth is the bound up to R ~ 100, and the kernel is built around
+// keeping copies in flight.
+//
+// Split.  The (request, kv head) items are cut into tiles of keys; all tiles of
+// all items, in order, are dealt evenly to the CTAs (about one wave of them), so
+// ragged lengths and single long requests load the GPU alike.  The lengths
+// stay on the device: every CTA sums the tile counts for itself.  An item that
+// ends up in several CTAs leaves one partial (o, m, l) in each; the CTA that
+// arrives last (a counter per split item) joins them in key order, so the
+// result does not depend on timing.
+//
+// Products.  mma.sync with the keys as the 16-row operand: S^T = K Q^T and
+// O^T += V^T P^T waste nothing at R = 8 (tcgen05's 128-row tile would be
+// mostly padding there, and its operands would have to pass through tensor
+// memory and barriers for work that takes a quarter of the issue slots here).
+// The S^T accumulator becomes the P^T operand by one 8x8 transpose
+// (movmatrix), and running maxima live in the lanes that own the columns.
+//
+// Streams.  With R <= 16 each warp is on its own: it copies its keys (16-byte
+// cp.async, swizzled so that ldmatrix is conflict-free) into its own ring, and
+// waits for nobody until its CTA's part of the item ends; the ring runs ahead
+// across items.  With more rows the CTA's warps share one ring, 16 rows each.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "paged.h"
+#include "ptx.cuh"
+
+namespace fa {
+
+constexpr int kDecodeWarps = 4;   // warps of a CTA whose warps stream alone
+
+// ------------------------------------------------------------- primitives
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// d += a b, a 16 x 16 (row), b 16 x 8 (column): bf16 or f16 in, f32 out.
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+                 " {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+                 " {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Four e4m3 bytes to two f16 pairs (exact): bytes 0, 1 and bytes 2, 3.
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi) : "r"(x));
+}
+
+// ------------------------------------------------------------ configuration
+// NT: n-tiles of 8 query rows per warp.  TEAM: the CTA's warps share a ring.
+template <int H_, bool E4M3_, int NT_, bool TEAM_>
+struct DecodeCfg {
+  static constexpr int H = H_, NT = NT_;
+  static constexpr bool E4M3 = E4M3_, TEAM = TEAM_;
+  static constexpr int ROWB = E4M3 ? H : 2 * H;        // bytes of a key
+  static constexpr int UPR = ROWB / 16;                // 16-byte units of a key
+  static constexpr int CK = TEAM || E4M3 ? 32 : 16;    // keys of a ring slot
+  static constexpr int HALF = CK * ROWB;               // a slot holds K, then V
+  static constexpr int SLOT = 2 * HALF;
+  static constexpr int TEAMS = TEAM ? 1 : kDecodeWarps;
+  static constexpr int TK = TEAMS * CK;                // keys of a tile
+  // Streams of one warp: 24 KB of ring a warp up to H = 128 (two CTAs an SM,
+  // up to 128 KB of copies in flight on it), 48 KB at H = 256 (one CTA).
+  static constexpr int STAGES = TEAM ? 4 : (H == 256 ? 48 : 24) * 1024 / SLOT;
+  static constexpr int RING = TEAMS * STAGES * SLOT;
+  static constexpr bool QSMEM = H * NT > 256;          // query fragments in shared memory
+  static constexpr int QBYTES = QSMEM ? H / 16 * NT * 32 * 8 : 0;   // per warp
+  static constexpr int MIN_CTAS = !TEAM && H <= 128 ? 2 : 1;
+  static_assert(TEAM || NT * 8 * H * 4 <= SLOT, "a warp's O^T fits in a ring slot");
+  static_assert(STAGES >= 3, "");
+};
+
+// Byte offset of 16-byte unit `u` of row `r`: any 8 consecutive rows have one
+// unit in 8 different bank groups.
+template <int UPR>
+__device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t u) {
+  return UPR >= 8 ? r * (UPR * 16) + ((u ^ (r & 7)) << 4) : r * 64 + ((u ^ ((r >> 1) & 3)) << 4);
+}
+
+// ------------------------------------------------------------------ the walk
+// A position in the flattened list of tiles: tile `tile` of item (b, k), which
+// has `tiles` of them, this CTA's being [.., end).
+struct DecodeWalk {
+  int b, k, len, first, tiles;   // first: key of tile 0, a multiple of CK
+  int tile, end;
+  int64_t left;                  // tiles of this CTA from the item's `tile` at entry on
+};
+
+template <class C>
+struct DecodeShape {
+  const PagedDecodeArgs& a;
+  __device__ __forceinline__ int length(int b) const {
+    const int n = a.lens[b];
+    return min(max(n, 0), a.max_pages << a.lay.page_shift);
+  }
+  // First key any of the T queries keeps.
+  __device__ __forceinline__ int low(int len) const {
+    return a.window > 0 ? max(0, len - a.T + 1 - a.window) : 0;
+  }
+  __device__ __forceinline__ int first(int len) const { return low(len) & ~(C::CK - 1); }
+  __device__ __forceinline__ int tiles(int len) const {
+    return max(1, (len - first(len) + C::TK - 1) / C::TK);   // an empty item writes its zeros
+  }
+  __device__ __forceinline__ void enter(DecodeWalk& w) const {
+    w.len = length(w.b);
+    w.first = first(w.len);
+    w.tiles = tiles(w.len);
+  }
+  // To the item after the walk's current one; false at the end of the CTA's part.
+  __device__ __forceinline__ bool next_item(DecodeWalk& w, int begun) const {
+    w.left -= w.end - begun;
+    if (w.left <= 0) return false;
+    if (++w.k == a.K) {
+      w.k = 0;
+      ++w.b;
+      enter(w);
+    }
+    w.tile = 0;
+    w.end = (int)min((int64_t)w.tiles, w.left);
+    return true;
+  }
+};
+
+// Whether any 16-bit (bf16) or 8-bit (e4m3) value of the `bytes` at `p` is not
+// finite; warp-wide.
+template <bool E4M3>
+__device__ __forceinline__ bool any_not_finite(const char* p, int bytes, int lane) {
+  bool bad = false;
+  for (int i = lane * 16; i < bytes; i += 512) {
+    const uint4 x = *reinterpret_cast<const uint4*>(p + i);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (E4M3) {   // all seven low bits of a byte set: NaN (e4m3 has no infinity)
+        const uint32_t y = ~w[j] & 0x7f7f7f7fu;
+        bad |= ((y - 0x01010101u) & ~y & 0x80808080u) != 0;
+      } else {
+        bad |= (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
+      }
+    }
+  }
+  return __any_sync(~0u, bad);
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::TEAM ? 256 : kDecodeWarps * 32, C::MIN_CTAS)
+paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
+  constexpr int H = C::H, NT = C::NT, CK = C::CK, KT = CK / 16, KS = H / 16, S = C::STAGES;
+  constexpr bool E4M3 = C::E4M3, TEAM = C::TEAM;
+  constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+  extern __shared__ __align__(1024) char smem[];
+  __shared__ float sh_m[kDecodeWarps][16], sh_l[kDecodeWarps][16];
+  __shared__ long long sh_scan[9];
+  __shared__ int sh_b;
+  __shared__ long long sh_rem;
+  __shared__ int sh_last;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+  const int g = lane >> 2, c = lane & 3;
+  const int R = a.G * a.T;
+  const DecodeShape<C> shape{a};
+
+  // ---- this CTA's part of the tiles
+  long long total;
+  {
+    const int per = (a.B + threads - 1) / threads;
+    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) {
+      if (blockIdx.x == 0) {
+        const int n = a.lens[b];
+        if (n != shape.length(b)) atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+      }
+      mine += (long long)shape.tiles(shape.length(b)) * a.K;
+    }
+    long long inc = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long x = __shfl_up_sync(~0u, inc, d);
+      if (lane >= d) inc += x;
+    }
+    if (lane == 31) sh_scan[warp] = inc;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+    for (int w = 0; w < threads / 32; ++w) {
+      if (w < warp) before += sh_scan[w];
+      total += sh_scan[w];
+    }
+    const long long n = min((long long)gridDim.x, total);
+    if (blockIdx.x >= n) return;
+    const long long t0 = blockIdx.x * total / n;
+    long long at = before + inc - mine;
+    if (t0 >= at && t0 < at + mine) {
+      for (int b = b0; b < b1; ++b) {
+        const long long x = (long long)shape.tiles(shape.length(b)) * a.K;
+        if (t0 < at + x) {
+          sh_b = b;
+          sh_rem = t0 - at;
+          break;
+        }
+        at += x;
+      }
+    }
+    __syncthreads();
+  }
+  const long long ctas = min((long long)gridDim.x, total);
+  const long long t0 = blockIdx.x * total / ctas, t1 = (blockIdx.x + 1) * total / ctas;
+  DecodeWalk walk;
+  walk.b = sh_b;
+  shape.enter(walk);
+  walk.k = (int)(sh_rem / walk.tiles);
+  walk.tile = (int)(sh_rem % walk.tiles);
+  walk.left = t1 - t0;
+  walk.end = (int)min((int64_t)walk.tiles, walk.tile + walk.left);
+  DecodeWalk ahead = walk;   // where the copies are
+  int ahead_from = ahead.tile;
+  bool more = true;
+
+  // ---- copies: lane r looks up key r of the next slot one slot early, then all
+  // lanes copy 16-byte units of it
+  const int team = TEAM ? 0 : warp;
+  char* ring = smem + team * S * C::SLOT;
+  const uint32_t ring_u = smem_u32(ring);
+  int64_t key_off = -1;   // lane r: byte offset of key r of the slot to come, -1: zeros
+  int key_page = -1, key_in = 0, key_head = 0;
+  bool key_live = false;
+  auto look_up = [&]() {
+    key_live = false;
+    if (!more) return;
+    const int s = ahead.first + (ahead.tile * C::TEAMS + team) * CK + (lane & (CK - 1));
+    key_live = s >= shape.low(ahead.len) && s < ahead.len;
+    key_in = s & ((1 << a.lay.page_shift) - 1);
+    key_head = ahead.k;
+    if (key_live) key_page = __ldg(a.block_table + (int64_t)ahead.b * a.max_pages + (s >> a.lay.page_shift));
+  };
+  auto issue = [&](int slot) {
+    key_off = -1;
+    if (key_live) {
+      if (key_page >= 0 && key_page < a.lay.n_pages)
+        key_off = key_page * a.lay.page + key_head * a.lay.head + key_in * a.lay.token;
+      else
+        atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+    }
+    if (__any_sync(~0u, key_live)) {
+      const uint32_t dst = ring_u + slot * C::SLOT;
+      constexpr int NJ = CK * C::UPR / 32;
+#pragma unroll
+      for (int j0 = 0; j0 < NJ; ++j0) {
+        if (TEAM && j0 % (threads / 32) != warp) continue;
+        const int row = (j0 * 32 + lane) / C::UPR, u = (j0 * 32 + lane) % C::UPR;
+        const int64_t off = __shfl_sync(~0u, key_off, row);
+        const uint32_t n = off >= 0 ? 16 : 0, d = dst + swz<C::UPR>(row, u);
+        // nothing is read where n = 0 (q: an address that exists)
+        cp_async16(d, off >= 0 ? (const char*)a.k_cache + off + u * 16 : (const char*)a.q, n);
+        cp_async16(d + C::HALF, off >= 0 ? (const char*)a.v_cache + off + u * 16 : (const char*)a.q, n);
+      }
+    }
+    cp_async_commit();
+    if (more && ++ahead.tile == ahead.end) {
+      more = shape.next_item(ahead, ahead_from);
+      ahead_from = 0;
+    }
+    look_up();
+  };
+  look_up();
+#pragma unroll 1
+  for (int i = 0; i < S - 1; ++i) issue(i);
+
+  // ---- items
+  int cur = 0;
+  const int row0 = TEAM ? warp * 16 : 0;   // first query row of this warp
+  uint2* const q_sm = reinterpret_cast<uint2*>(smem + C::RING + warp * C::QBYTES);
+  while (true) {
+    const int begun = walk.tile;
+    const int64_t item = (int64_t)walk.b * a.K + walk.k;
+    uint2 qf[C::QSMEM ? 1 : KS][NT];
+    float sl2[NT][2];      // score to log2 units, per column
+    // Query fragments: column n = lane / 4, dims as the key operand has them.
+    // For 8-bit caches rows are scaled to [2^10, 2^11) and rounded to f16: exact
+    // for bf16 values down to 2^-27 of the row's largest.
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = row0 + nt * 8 + g;
+      const char* src = (const char*)a.q + (item * R + r) * (H * 2);
+      uint2 x[KS];
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        x[ks] = make_uint2(0, 0);
+        if (r < R) {
+          if (E4M3) {
+            x[ks] = __ldg(reinterpret_cast<const uint2*>(src + ks * 32 + c * 8));
+          } else {
+            x[ks].x = __ldg(reinterpret_cast<const uint32_t*>(src + ks * 32 + c * 4));
+            x[ks].y = __ldg(reinterpret_cast<const uint32_t*>(src + ks * 32 + 16 + c * 4));
+          }
+        }
+      }
+      if (E4M3) {
+        float big = 0.0f;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const float2 p = unpack_bf16x2(x[ks].x), q = unpack_bf16x2(x[ks].y);
+          big = fmaxf(fmaxf(big, fmaxf(fabsf(p.x), fabsf(p.y))), fmaxf(fabsf(q.x), fabsf(q.y)));
+        }
+        big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
+        // 2^e with big * 2^e in [2^10, 2^11); 1 for rows of zeros or infinities
+        const int e = big > 0.0f && big < INFINITY
+                          ? min(10 - ((int)(__float_as_uint(big) >> 23) - 127), 126) : 0;
+        const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const float2 p = unpack_bf16x2(x[ks].x), q = unpack_bf16x2(x[ks].y);
+          x[ks] = make_uint2(pack_f16x2(p.x * up, p.y * up), pack_f16x2(q.x * up, q.y * up));
+        }
+        const float kscale = a.k_scale ? __ldg(a.k_scale + walk.k) : 1.0f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          sl2[nt][j] = __shfl_sync(~0u, down, (2 * c + j) * 4) * kscale * LOG2E;
+      } else {
+        sl2[nt][0] = sl2[nt][1] = LOG2E;
+      }
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        if (C::QSMEM) q_sm[(ks * NT + nt) * 32 + lane] = x[ks];
+        else qf[C::QSMEM ? 0 : ks][nt] = x[ks];
+      }
+    }
+    // Keys that column (nt, j) keeps: [hi - window, hi)
+    int col_hi[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        col_hi[nt][j] = walk.len - a.T + 1 + (a.T == 1 ? 0 : (row0 + nt * 8 + 2 * c + j) % a.T);
+    const int full_hi = walk.len - a.T + 1;                              // all columns keep keys
+    const int full_lo = a.window > 0 ? max(0, walk.len - a.window) : 0;   // in [full_lo, full_hi)
+
+    float o[KS][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.0f;
+#pragma unroll
+      for (int ds = 0; ds < KS; ++ds) o[ds][nt][0] = o[ds][nt][1] = o[ds][nt][2] = o[ds][nt][3] = 0.0f;
+    }
+
+    for (; walk.tile < walk.end; ++walk.tile) {
+      cp_async_wait<S - 2>();
+      if (TEAM) __syncthreads(); else __syncwarp();
+      {
+        const int next = cur == 0 ? S - 1 : cur - 1;   // the slot of the chunk before: free
+        issue(next);
+      }
+      const uint32_t ks_u = ring_u + cur * C::SLOT, vs_u = ks_u + C::HALF;
+      const char* const vs_p = ring + cur * C::SLOT + C::HALF;
+      cur = cur + 1 == S ? 0 : cur + 1;
+      const int key0 = walk.first + (walk.tile * C::TEAMS + team) * CK;
+      if (key0 >= walk.len) continue;   // this team has no keys in the tile
+
+      // S^T = K Q^T
+      float s[KT][NT][4];
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt) {
+        float s2[NT][4];   // a second chain of products where there is only one
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[kt][nt][i] = s2[nt][i] = 0.0f;
+        const uint32_t row = kt * 16 + (lane & 15);
+#pragma unroll
+        for (int ks = 0; ks < KS; ks += E4M3 ? 2 : 1) {
+          uint32_t x[4];
+          ldsm4(ks_u + swz<C::UPR>(row, (E4M3 ? ks : 2 * ks) + (lane >> 4)), x);
+          if (E4M3) {
+            uint32_t a0[4], a1[4];
+            e4m3x4_to_f16(x[0], a0[0], a0[2]);
+            e4m3x4_to_f16(x[1], a0[1], a0[3]);
+            e4m3x4_to_f16(x[2], a1[0], a1[2]);
+            e4m3x4_to_f16(x[3], a1[1], a1[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint2 q0 = C::QSMEM ? q_sm[(ks * NT + nt) * 32 + lane] : qf[C::QSMEM ? 0 : ks][nt];
+              const uint2 q1 = C::QSMEM ? q_sm[((ks + 1) * NT + nt) * 32 + lane] : qf[C::QSMEM ? 0 : ks + 1][nt];
+              mma16816<true>(s[kt][nt], a0, q0.x, q0.y);
+              mma16816<true>(s2[nt], a1, q1.x, q1.y);
+            }
+          } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint2 q0 = C::QSMEM ? q_sm[(ks * NT + nt) * 32 + lane] : qf[C::QSMEM ? 0 : ks][nt];
+              mma16816<false>(ks & 1 ? s2[nt] : s[kt][nt], x, q0.x, q0.y);
+            }
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[kt][nt][i] += s2[nt][i];
+      }
+      const bool masked = key0 < full_lo || key0 + CK > full_hi;
+      if (masked) {
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int key = key0 + kt * 16 + g + (i >> 1) * 8, hi = col_hi[nt][i & 1];
+              if (key >= hi || (a.window > 0 && key < hi - a.window)) s[kt][nt][i] = -INFINITY;
+            }
+      }
+
+      // online softmax, per column
+      float alpha[NT][2];
+      bool moved = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float mx = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
+#pragma unroll
+          for (int kt = 1; kt < KT; ++kt) mx = fmaxf(mx, fmaxf(s[kt][nt][j], s[kt][nt][j + 2]));
+          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
+          const float mn = fmaxf(m[nt][j], mx * sl2[nt][j]);
+          const float base = mn == -INFINITY ? 0.0f : mn;
+          alpha[nt][j] = fast_exp2(m[nt][j] - base);
+          moved |= mn != m[nt][j];
+          m[nt][j] = mn;
+          float sum = 0.0f;
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt) {
+            s[kt][nt][j] = fast_exp2(fmaf(s[kt][nt][j], sl2[nt][j], -base));
+            s[kt][nt][j + 2] = fast_exp2(fmaf(s[kt][nt][j + 2], sl2[nt][j], -base));
+            sum += s[kt][nt][j] + s[kt][nt][j + 2];
+          }
+          l[nt][j] = l[nt][j] * alpha[nt][j] + sum;
+        }
+      if (__any_sync(~0u, moved)) {
+#pragma unroll
+        for (int ds = 0; ds < KS; ++ds)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            o[ds][nt][0] *= alpha[nt][0];
+            o[ds][nt][1] *= alpha[nt][1];
+            o[ds][nt][2] *= alpha[nt][0];
+            o[ds][nt][3] *= alpha[nt][1];
+          }
+      }
+
+      // O^T += V^T P^T.  bf16 caches: the weights go in as two bf16 terms (their
+      // sum is off by 2^-17), so that o is rounded to bf16 once, at the end; the
+      // products are a quarter of the issue slots either way.  8-bit caches:
+      // one f16 term, off by 2^-12, against values of 2^-4.
+      uint32_t p[KT][NT][2], pl[KT][NT][2];
+#pragma unroll
+      for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float x = s[kt][nt][2 * h], y = s[kt][nt][2 * h + 1];
+            if (E4M3) {
+              p[kt][nt][h] = transpose8x8(pack_f16x2(x, y));
+            } else {
+              const uint32_t hi = pack_bf16x2(x, y);
+              const float2 r = unpack_bf16x2(hi);
+              p[kt][nt][h] = transpose8x8(hi);
+              pl[kt][nt][h] = transpose8x8(pack_bf16x2(x - r.x, y - r.y));
+            }
+          }
+      // Operand V^T of 16 keys and 16 dims (8-bit: 32 dims, two operands).
+      auto load_v = [&](int kt, int ds, uint32_t (&v0)[4], uint32_t (&v1)[4]) {
+        if (E4M3) {
+          uint32_t x[4];
+          ldsm4_trans(vs_u + swz<C::UPR>(kt * 16 + (lane & 15), ds + (lane >> 4)), x);
+          // bytes (key 2c: dims 2g, 2g+1), (key 2c+1: the same) -> pairs of keys per dim
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = __byte_perm(x[i], 0, 0x3120);
+          e4m3x4_to_f16(x[0], v0[0], v0[1]);
+          e4m3x4_to_f16(x[1], v0[2], v0[3]);
+          e4m3x4_to_f16(x[2], v1[0], v1[1]);
+          e4m3x4_to_f16(x[3], v1[2], v1[3]);
+        } else {
+          ldsm4_trans(vs_u + swz<C::UPR>(kt * 16 + (lane & 7) + ((lane >> 4) << 3),
+                                         2 * ds + ((lane >> 3) & 1)), v0);
+        }
+      };
+      auto add_v = [&](float (&d)[4], const uint32_t (&v)[4], int kt, int nt) {
+        mma16816<E4M3>(d, v, p[kt][nt][0], p[kt][nt][1]);
+        if (!E4M3) mma16816<E4M3>(d, v, pl[kt][nt][0], pl[kt][nt][1]);
+      };
+      if (masked && a.T > 1 && any_not_finite<E4M3>(vs_p, C::HALF, lane)) {
+        // Some column does not keep a key whose value is an infinity or NaN, and
+        // 0 x inf would reach it: each query position gets its own products, the
+        // keys that it does not keep zeroed, and takes its columns of them.
+#pragma unroll 1
+        for (int t = 0; t < a.T; ++t) {
+          const int hi = full_hi + t, lo = a.window > 0 ? hi - a.window : 0;
+#pragma unroll
+          for (int kt = 0; kt < KT; ++kt) {
+            uint32_t keep[2];   // of keys 2c, 2c + 1 and those + 8, as halves
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int key = key0 + kt * 16 + 2 * c + 8 * h;
+              keep[h] = (key >= lo && key < hi ? 0xffffu : 0u) |
+                        (key + 1 >= lo && key + 1 < hi ? 0xffff0000u : 0u);
+            }
+#pragma unroll
+            for (int ds = 0; ds < KS; ds += E4M3 ? 2 : 1) {
+              uint32_t v[2][4];
+              load_v(kt, ds, v[0], v[1]);
+#pragma unroll
+              for (int i = 0; i < (E4M3 ? 2 : 1); ++i) {
+                v[i][0] &= keep[0];
+                v[i][1] &= keep[0];
+                v[i][2] &= keep[1];
+                v[i][3] &= keep[1];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                  add_v(d, v[i], kt, nt);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    if (col_hi[nt][e & 1] == hi) o[ds + i][nt][e] += d[e];
+                }
+              }
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+          for (int ds = 0; ds < KS; ds += E4M3 ? 2 : 1) {
+            uint32_t v[2][4];
+            load_v(kt, ds, v[0], v[1]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              add_v(o[ds][nt], v[0], kt, nt);
+              if (E4M3) add_v(o[ds + (E4M3 ? 1 : 0)][nt], v[1], kt, nt);
+            }
+          }
+      }
+    }
+
+    // ---- end of the CTA's part of the item
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        l[nt][j] += __shfl_xor_sync(~0u, l[nt][j], 4);
+        l[nt][j] += __shfl_xor_sync(~0u, l[nt][j], 8);
+        l[nt][j] += __shfl_xor_sync(~0u, l[nt][j], 16);
+      }
+    const bool whole = begun == 0 && walk.end == walk.tiles;
+    const float vscale = a.v_scale ? __ldg(a.v_scale + walk.k) : 1.0f;
+    const int64_t out_row = item * R;
+    // Partials: slot 1 of a CTA holds the item that starts in it, slot 0 one
+    // that started before.
+    const int64_t part = paged_partial_floats(R, H);
+    float* const mine = a.partials + ((int64_t)blockIdx.x * 2 + (begun == 0 ? 1 : 0)) * part;
+    auto put = [&](int r, int d, float4 x, float M, float L) {   // four dims of row r
+      if (whole) {
+        const float f = L == 0.0f ? 0.0f : vscale / L;
+        const uint2 y = make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
+        *reinterpret_cast<uint2*>((char*)a.o + ((out_row + r) * H + d) * 2) = y;
+        if (d == 0) a.lse[out_row + r] = (M + log2f(L)) * LN2;   // -inf with no key
+      } else {
+        *reinterpret_cast<float4*>(mine + (int64_t)r * H + d) = x;
+        if (d == 0) {
+          mine[(int64_t)R * H + r] = M;
+          mine[(int64_t)R * (H + 1) + r] = L;
+        }
+      }
+    };
+    // O^T goes through shared memory: the slot just used, free until the next
+    // copies are issued.  Four dims stay together; dims move by 8 with the column
+    // pair, against bank conflicts.
+    float* const so = reinterpret_cast<float*>(ring + (cur == 0 ? S - 1 : cur - 1) * C::SLOT);
+    if (!TEAM) {
+      __syncwarp();
+#pragma unroll
+      for (int ds = 0; ds < KS; ++ds)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float* const row = so + (nt * 8 + 2 * c + j) * H;
+            if (E4M3) {
+              *reinterpret_cast<float2*>(row + ((ds * 16 + 2 * g) ^ (c << 3))) =
+                  make_float2(o[ds][nt][j], o[ds][nt][j + 2]);
+            } else {
+              row[(ds * 16 + g) ^ (c << 3)] = o[ds][nt][j];
+              row[(ds * 16 + g + 8) ^ (c << 3)] = o[ds][nt][j + 2];
+            }
+          }
+      if (g == 0) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            sh_m[warp][nt * 8 + 2 * c + j] = m[nt][j];
+            sh_l[warp][nt * 8 + 2 * c + j] = l[nt][j];
+          }
+      }
+      __syncthreads();
+      for (int i = tid; i < R * (H / 4); i += kDecodeWarps * 32) {
+        const int r = i / (H / 4), d = i % (H / 4) * 4;
+        float M = sh_m[0][r], L = 0.0f;
+#pragma unroll
+        for (int w = 1; w < kDecodeWarps; ++w) M = fmaxf(M, sh_m[w][r]);
+        const float base = M == -INFINITY ? 0.0f : M;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        // every warp's ring has the same slot at the same place
+        const float* at = reinterpret_cast<const float*>(smem + ((const char*)so - ring)) + r * H +
+                          (d ^ (((r >> 1) & 3) << 3));
+#pragma unroll
+        for (int w = 0; w < kDecodeWarps; ++w) {
+          const float f = fast_exp2(sh_m[w][r] - base);
+          const float4 y = *reinterpret_cast<const float4*>(at + w * (S * C::SLOT / 4));
+          L += sh_l[w][r] * f;
+          x.x += y.x * f;
+          x.y += y.y * f;
+          x.z += y.z * f;
+          x.w += y.w * f;
+        }
+        put(r, d, x, M, L);
+      }
+      __syncthreads();
+    } else {
+      // 16 rows of this warp, H dims, through 16 dims x 16 rows of shuffles: a
+      // transpose of four lanes' columns would cost more than these stores
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int r = row0 + nt * 8 + 2 * c + j;
+          if (r >= R) continue;
+          const float L = l[nt][j], M = m[nt][j], f = L == 0.0f ? 0.0f : vscale / L;
+#pragma unroll
+          for (int ds = 0; ds < KS; ++ds) {
+            const int d0 = ds * 16 + (E4M3 ? 2 * g : g), d1 = d0 + (E4M3 ? 1 : 8);
+            if (whole) {
+              __nv_bfloat16* const dst = (__nv_bfloat16*)a.o + (out_row + r) * H;
+              dst[d0] = __float2bfloat16(o[ds][nt][j] * f);
+              dst[d1] = __float2bfloat16(o[ds][nt][j + 2] * f);
+            } else {
+              mine[(int64_t)r * H + d0] = o[ds][nt][j];
+              mine[(int64_t)r * H + d1] = o[ds][nt][j + 2];
+            }
+          }
+          if (g == 0) {
+            if (whole) {
+              a.lse[out_row + r] = (M + log2f(L)) * LN2;
+            } else {
+              mine[(int64_t)R * H + r] = M;
+              mine[(int64_t)R * (H + 1) + r] = L;
+            }
+          }
+        }
+    }
+
+    // ---- join of an item that several CTAs share, by the last of them
+    if (!whole) {
+      const int64_t at0 = t1 - walk.left - begun;   // the item's first tile in the list
+      const int c0 = (int)(((at0 + 1) * ctas - 1) / total);
+      const int c1 = (int)(((at0 + walk.tiles) * ctas - 1) / total);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) {
+        // The counter's upper bits name the call, so what the word held before
+        // does not matter; the last arrival clears it for a replay of the call.
+        unsigned long long* const word = reinterpret_cast<unsigned long long*>(a.counters) + c0;
+        unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word), now;
+        while (true) {
+          const unsigned long long n = (old >> 16) == a.tag ? (old & 0xffff) + 1 : 1;
+          now = n;
+          const unsigned long long to = n == (unsigned long long)(c1 - c0 + 1) ? 0 : (a.tag << 16) | n;
+          const unsigned long long seen = atomicCAS(word, old, to);
+          if (seen == old) break;
+          old = seen;
+        }
+        sh_last = now == (unsigned long long)(c1 - c0 + 1);
+        __threadfence();
+      }
+      __syncthreads();
+      if (sh_last) {
+        for (int i = tid; i < R * (H / 4); i += threads) {
+          const int r = i / (H / 4), d = i % (H / 4) * 4;
+          float M = -INFINITY, L = 0.0f;
+          float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          constexpr int U = 8;   // partials read at once
+          for (int p0 = c0; p0 <= c1; p0 += U) {
+            float4 y[U];
+            float pm[U], pn[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              pm[u] = -INFINITY;
+              pn[u] = 0.0f;
+              y[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (p0 + u <= c1) {
+                const float* src = a.partials + ((int64_t)(p0 + u) * 2 + (p0 + u == c0 ? 1 : 0)) * part;
+                y[u] = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)r * H + d));
+                pm[u] = __ldcg(src + (int64_t)R * H + r);
+                pn[u] = __ldcg(src + (int64_t)R * (H + 1) + r);
+              }
+            }
+            float mn = M;
+#pragma unroll
+            for (int u = 0; u < U; ++u) mn = fmaxf(mn, pm[u]);
+            const float base = mn == -INFINITY ? 0.0f : mn;
+            const float f0 = fast_exp2(M - base);
+            M = mn;
+            L *= f0;
+            x.x *= f0; x.y *= f0; x.z *= f0; x.w *= f0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const float f = fast_exp2(pm[u] - base);
+              L += pn[u] * f;
+              x.x += y[u].x * f;
+              x.y += y[u].y * f;
+              x.z += y[u].z * f;
+              x.w += y[u].w * f;
+            }
+          }
+          const float f = L == 0.0f ? 0.0f : vscale / L;
+          const uint2 y = make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
+          *reinterpret_cast<uint2*>((char*)a.o + ((out_row + r) * H + d) * 2) = y;
+          if (d == 0) a.lse[out_row + r] = (M + log2f(L)) * LN2;
+        }
+      }
+    }
+    if (!shape.next_item(walk, begun)) break;
+  }
+  cp_async_wait<0>();
+}
+
+template <class C>
+cudaError_t launch_decode(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
+  const int warps = C::TEAM ? (a.G * a.T + 15) / 16 : kDecodeWarps;
+  const size_t smem = C::RING + (size_t)warps * C::QBYTES;
+  static bool ready[64] = {};   // per device; setting it twice is harmless
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !ready[dev]) {
+    const size_t most = C::RING + (size_t)(C::TEAM ? kMaxPagedRows / 16 : kDecodeWarps) * C::QBYTES;
+    e = cudaFuncSetAttribute(paged_decode_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev] = true;
+  }
+  paged_decode_kernel<C><<<grid, warps * 32, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+// Rows 1..8 and 9..16: warps on their own; more: a CTA's warps share the keys.
+template <int H, bool E4M3>
+cudaError_t launch_decode_rows(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
+  const int R = a.G * a.T;
+  if (R <= 8) return launch_decode<DecodeCfg<H, E4M3, 1, false>>(a, grid, st);
+  if (R <= 16) return launch_decode<DecodeCfg<H, E4M3, 2, false>>(a, grid, st);
+  return launch_decode<DecodeCfg<H, E4M3, 2, true>>(a, grid, st);
+}
+
+}  // namespace fa

@@ -64,7 +64,8 @@ def _decode(lib, q=16, kc=16, vc=16, kind=0, ks=None, vs=None, sp=16384, sh=2048
     (dict(T=-1), BAD), (dict(max_pages=-1), BAD), (dict(st=132), BAD), (dict(ks=16), BAD),
     (dict(kind=1, ks=2), BAD), (dict(page=48), UNSUP), (dict(H=192), UNSUP), (dict(G=129), UNSUP),
     (dict(G=16, T=9), UNSUP), (dict(B=8193), UNSUP), (dict(B=8192, K=8), UNSUP),
-    (dict(max_pages=1 << 27), UNSUP), (dict(B=0), OK), (dict(T=0, q=None), OK),
+    (dict(max_pages=1 << 27), UNSUP), (dict(ws=None), BAD), (dict(ws=128), BAD),
+    (dict(B=0), OK), (dict(T=0, q=None), OK),
     (dict(G=0), OK), (dict(K=0), OK),
 ])
 def test_decode_refusals(clib, kw, rc):  # noqa: F811
