@@ -38,6 +38,7 @@
 namespace fa {
 
 constexpr int kDecodeWarps = 4;   // warps of a CTA whose warps stream alone
+constexpr int kJoinMost = 64;     // partials joined at once; more go in groups
 
 // ------------------------------------------------------------- primitives
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -55,6 +56,12 @@ __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
 __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// Not to be hoisted out of the loop that it stands in: that would take registers.
+__device__ __forceinline__ uint2 lds8(uint32_t addr) {
+  uint2 x;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(addr));
+  return x;
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
@@ -95,7 +102,7 @@ struct DecodeCfg {
   static constexpr bool E4M3 = E4M3_, TEAM = TEAM_;
   static constexpr int ROWB = E4M3 ? H : 2 * H;        // bytes of a key
   static constexpr int UPR = ROWB / 16;                // 16-byte units of a key
-  static constexpr int CK = TEAM || E4M3 ? 32 : 16;    // keys of a ring slot
+  static constexpr int CK = TEAM || E4M3 || H == 64 ? 32 : 16;   // keys of a ring slot
   static constexpr int HALF = CK * ROWB;               // a slot holds K, then V
   static constexpr int SLOT = 2 * HALF;
   static constexpr int TEAMS = TEAM ? 1 : kDecodeWarps;
@@ -105,26 +112,42 @@ struct DecodeCfg {
   static constexpr int STAGES = TEAM ? 4 : (H == 256 ? 48 : 24) * 1024 / SLOT;
   static constexpr int RING = TEAMS * STAGES * SLOT;
   static constexpr bool QSMEM = H * NT > 256;          // query fragments in shared memory
-  static constexpr int QBYTES = QSMEM ? H / 16 * NT * 32 * 8 : 0;   // per warp
+  static constexpr int QBYTES = QSMEM ? H / 16 * NT * 32 * 8 : 0;   // TEAM: per warp
   static constexpr int MIN_CTAS = !TEAM && H <= 128 ? 2 : 1;
-  static_assert(TEAM || NT * 8 * H * 4 <= SLOT, "a warp's O^T fits in a ring slot");
+  static_assert(TEAM || (NT < 2 ? NT : 2) * 8 * H * 4 <= SLOT, "16 rows of a warp's O^T fit in a ring slot");
   static_assert(STAGES >= 3, "");
 };
 
 // Byte offset of 16-byte unit `u` of row `r`: any 8 consecutive rows have one
 // unit in 8 different bank groups.
+// A lane's address of unit u0 in its row, xor (u << 4), is that of unit u0 ^ u: slots
+// are aligned to whole rows.
 template <int UPR>
 __device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t u) {
   return UPR >= 8 ? r * (UPR * 16) + ((u ^ (r & 7)) << 4) : r * 64 + ((u ^ ((r >> 1) & 3)) << 4);
 }
 
 // ------------------------------------------------------------------ the walk
-// A position in the flattened list of tiles: tile `tile` of item (b, k), which
-// has `tiles` of them, this CTA's being [.., end).
+// The list that is dealt to the CTAs: per item (b, k) kItemUnits units that
+// stand for its start and end, then one unit per tile.
+constexpr int kItemUnits = 2;
+
+// a / b for a, b >= 0: mostly in 32 bits, which takes a fraction of the time.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// A place in the list: unit `rem` of item (b, k).
+struct DecodePlace {
+  int b, k, rem;
+};
+
+// The part of an item that a CTA does: tiles [begun, end) of its `tiles`.
 struct DecodeWalk {
   int b, k, len, first, tiles;   // first: key of tile 0, a multiple of CK
-  int tile, end;
-  int64_t left;                  // tiles of this CTA from the item's `tile` at entry on
+  int tile, begun, end;
+  int todo;                      // whole items that follow
+  bool tail;                     // this is the CTA's last item, done first
 };
 
 template <class C>
@@ -142,22 +165,54 @@ struct DecodeShape {
   __device__ __forceinline__ int tiles(int len) const {
     return max(1, (len - first(len) + C::TK - 1) / C::TK);   // an empty item writes its zeros
   }
-  __device__ __forceinline__ void enter(DecodeWalk& w) const {
-    w.len = length(w.b);
+  __device__ __forceinline__ void enter(DecodeWalk& w, int b, int k) const {
+    w.b = b;
+    w.k = k;
+    w.len = length(b);
     w.first = first(w.len);
     w.tiles = tiles(w.len);
+    w.tile = w.begun = 0;
+    w.end = w.tiles;
   }
-  // To the item after the walk's current one; false at the end of the CTA's part.
-  __device__ __forceinline__ bool next_item(DecodeWalk& w, int begun) const {
-    w.left -= w.end - begun;
-    if (w.left <= 0) return false;
-    if (++w.k == a.K) {
-      w.k = 0;
-      ++w.b;
-      enter(w);
+  // The CTA's items: the one its units end in first, where that goes on in
+  // the next CTA, so that by the end of the kernel most joins are over; then
+  // from the one that its units begin in.  False where it has no tile at all.
+  __device__ __forceinline__ bool begin(DecodeWalk& w, const DecodePlace& h, const DecodePlace& e) const {
+    const int between = (e.b - h.b) * a.K + e.k - h.k;   // items
+    enter(w, e.b, e.k);
+    const int end = min(w.tiles, e.rem + 1 - kItemUnits);
+    if (between == 0) {
+      w.tile = w.begun = max(0, h.rem - kItemUnits);
+      w.end = end;
+      w.todo = 0;
+      w.tail = false;
+      return w.end > w.begun;
     }
-    w.tile = 0;
-    w.end = (int)min((int64_t)w.tiles, w.left);
+    w.tail = end > 0 && end < w.tiles;
+    w.todo = between - (w.tail || end <= 0 ? 1 : 0);
+    if (w.tail) w.end = end;
+    else head(w, h);
+    return true;
+  }
+  __device__ __forceinline__ void head(DecodeWalk& w, const DecodePlace& h) const {
+    enter(w, h.b, h.k);
+    w.tile = w.begun = max(0, h.rem - kItemUnits);
+  }
+  __device__ __forceinline__ bool next_item(DecodeWalk& w, const DecodePlace& h) const {
+    if (w.tail) {
+      head(w, h);
+      w.tail = false;
+      return true;
+    }
+    if (w.todo == 0) return false;
+    --w.todo;
+    if (w.k + 1 == a.K) {
+      enter(w, w.b + 1, 0);
+    } else {
+      ++w.k;
+      w.tile = w.begun = 0;
+      w.end = w.tiles;
+    }
     return true;
   }
 };
@@ -183,6 +238,134 @@ __device__ __forceinline__ bool any_not_finite(const char* p, int bytes, int lan
   return __any_sync(~0u, bad);
 }
 
+// --------------------------------------------------------------- joining
+// The four dims of row r of a joined or whole result, rounded to bf16 once.
+__device__ __forceinline__ void put_result(void* o, float* lse, int H, int r, int d, float4 x, float M,
+                                           float L, float vscale) {
+  const float f = L == 0.0f ? 0.0f : vscale / L;
+  const uint2 y = make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
+  *reinterpret_cast<uint2*>((char*)o + ((int64_t)r * H + d) * 2) = y;
+  if (d == 0) lse[r] = (M + log2f(L)) * 0.6931471805599453f;   // -inf with no key
+}
+__device__ __forceinline__ void put_partial(float* dst, int H, int R, int r, int d, float4 x, float M, float L) {
+  *reinterpret_cast<float4*>(dst + (int64_t)r * H + d) = x;
+  if (d == 0) {
+    dst[(int64_t)R * H + r] = M;
+    dst[(int64_t)R * (H + 1) + r] = L;
+  }
+}
+
+// Partials, or flags, of the CTAs that share an item: number p at base + p * step,
+// number 0 at + first instead of + other.
+template <class X>
+struct JoinList {
+  X* base;
+  int64_t step, first, other;
+  int n;
+  __device__ __forceinline__ X* operator()(int p) const { return base + p * step + (p == 0 ? first : other); }
+};
+
+// Whether all flags of the list hold `tag`; they are cleared then.  One warp,
+// after it set its own flag.  A word holds the call's tag from the arrival
+// until the join takes it back, so neither what it held before the call nor a
+// replay of the call matters.  Flags are set behind a fence that follows the
+// partials and read behind another: of CTAs that arrive together at least one
+// sees all, and where several do, they write the same result, or (claim) only
+// the one that takes the first flag goes on.
+__device__ __forceinline__ bool all_arrived(const JoinList<uint64_t>& flags, uint64_t tag, bool claim) {
+  const int lane = threadIdx.x & 31;
+  bool all = true;
+  for (int p = lane; p < flags.n; p += 32) all &= *reinterpret_cast<volatile uint64_t*>(flags(p)) == tag;
+  all = __all_sync(~0u, all);
+  if (all && claim) {
+    bool won = false;
+    if (lane == 0)
+      won = atomicCAS(reinterpret_cast<unsigned long long*>(flags(0)), (unsigned long long)tag, 0ull) == tag;
+    all = __shfl_sync(~0u, won, 0);
+  }
+  if (all) {
+    __threadfence();
+    for (int p = lane; p < flags.n; p += 32) *reinterpret_cast<volatile uint64_t*>(flags(p)) = 0;
+  }
+  return all;
+}
+
+// Sums the partials of a list in order, by the whole CTA, through `stage` (the
+// ring, with nothing in flight): into the partial `dst`, or where that is null
+// into o and lse.  All copies of a round are in flight at once: at the end of
+// the kernel what counts is the number of trips to L2.
+template <int H, int STAGE>
+__device__ __forceinline__ void join_partials(const JoinList<float>& src, int R, float* dst, void* o, float* lse,
+                                              float vscale, char* stage) {
+  constexpr int E = 4;   // float4 a thread
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const float* const all = reinterpret_cast<const float*>(stage);
+  const int ml = (2 * R + 3) / 4;                // 16-byte units of a partial's m and l
+  // rows at a time: 8 partials of them fit (ml <= 64, STAGE >= 16 KB: one row at least)
+  static_assert(STAGE / 128 - 64 >= H / 4, "");
+  const int rc = min(E * threads * 4 / H, (STAGE / 128 - ml) / (H / 4));
+  for (int r0 = 0; r0 < R; r0 += rc) {
+    const int rows = min(rc, R - r0);
+    const int unit = rows * (H / 4) + ml;        // 16-byte units staged of a partial
+    const int most = STAGE / 16 / unit;
+    float4 x[E];
+    float M[E], L[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      M[e] = -INFINITY;
+      L[e] = 0.0f;
+    }
+    for (int p0 = 0; p0 < src.n; p0 += most) {
+      const int n = min(most, src.n - p0);
+      __syncthreads();
+      for (int p = 0, j = tid, i = tid; i < n * unit; i += threads, j += threads) {
+        for (; j >= unit; j -= unit) ++p;
+        const int at = j < unit - ml ? r0 * H + j * 4 : R * H + (j - (unit - ml)) * 4;
+        cp_async16(smem_u32(stage) + i * 16, src(p0 + p) + at, 16);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int i = tid + e * threads, r = i / (H / 4), d = i % (H / 4) * 4;
+        if (r >= rows) continue;
+        const float* const mr = all + (unit - ml) * 4 + r0 + r;
+        float mn = M[e];
+        for (int p = 0; p < n; ++p) mn = fmaxf(mn, mr[p * unit * 4]);
+        const float low = mn == -INFINITY ? 0.0f : mn;
+        const float f0 = fast_exp2(M[e] - low);
+        M[e] = mn;
+        L[e] *= f0;
+        x[e].x *= f0; x[e].y *= f0; x[e].z *= f0; x[e].w *= f0;
+#pragma unroll 4
+        for (int p = 0; p < n; ++p) {
+          const float f = fast_exp2(mr[p * unit * 4] - low);
+          const float4 y = *reinterpret_cast<const float4*>(all + p * unit * 4 + r * H + d);
+          L[e] += mr[p * unit * 4 + R] * f;
+          x[e].x += y.x * f;
+          x[e].y += y.y * f;
+          x[e].z += y.z * f;
+          x[e].w += y.w * f;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int i = tid + e * threads, r = i / (H / 4), d = i % (H / 4) * 4;
+      if (r >= rows) continue;
+      if (dst) put_partial(dst, H, R, r0 + r, d, x[e], M[e], L[e]);
+      else put_result(o, lse, H, r0 + r, d, x[e], M[e], L[e], vscale);
+    }
+  }
+}
+
+// A partial that this CTA left, of an item that CTAs c0 .. c1 share.
+struct DecodeShare {
+  int b, k, c0, c1;   // c1 < c0: none
+};
+
 template <class C>
 __global__ void __launch_bounds__(C::TEAM ? 256 : kDecodeWarps * 32, C::MIN_CTAS)
 paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
@@ -192,18 +375,20 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
   extern __shared__ __align__(1024) char smem[];
   __shared__ float sh_m[kDecodeWarps][16], sh_l[kDecodeWarps][16];
   __shared__ long long sh_scan[9];
-  __shared__ int sh_b;
-  __shared__ long long sh_rem;
-  __shared__ int sh_last;
+  __shared__ DecodePlace sh_place[2];   // first and last unit
+  __shared__ int sh_last[2];
+  __shared__ DecodeShare sh_share[2];    // by the slot of its partial
+  __shared__ long long sh_t[3];          // first unit, one past the last, all units
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   const int g = lane >> 2, c = lane & 3;
   const int R = a.G * a.T;
   const DecodeShape<C> shape{a};
 
-  // ---- this CTA's part of the tiles
-  long long total;
+  // ---- this CTA's units
+  int ctas;
   {
+    long long total, t0, t1;
     const int per = (a.B + threads - 1) / threads;
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
     long long mine = 0;
@@ -212,7 +397,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         const int n = a.lens[b];
         if (n != shape.length(b)) atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
       }
-      mine += (long long)shape.tiles(shape.length(b)) * a.K;
+      mine += (long long)(shape.tiles(shape.length(b)) + kItemUnits) * a.K;
     }
     long long inc = mine;
 #pragma unroll
@@ -228,44 +413,57 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       if (w < warp) before += sh_scan[w];
       total += sh_scan[w];
     }
-    const long long n = min((long long)gridDim.x, total);
-    if (blockIdx.x >= n) return;
-    const long long t0 = blockIdx.x * total / n;
-    long long at = before + inc - mine;
-    if (t0 >= at && t0 < at + mine) {
+    ctas = (int)min((long long)gridDim.x, total);
+    if (blockIdx.x >= ctas) return;
+    t0 = quotient(blockIdx.x * total, ctas);
+    t1 = quotient((blockIdx.x + 1) * total, ctas);
+    const long long at = before + inc - mine;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {   // where this CTA's units begin and end
+      long long t = (i == 0 ? t0 : t1 - 1) - at;
+      if (t < 0 || t >= mine) continue;
       for (int b = b0; b < b1; ++b) {
-        const long long x = (long long)shape.tiles(shape.length(b)) * a.K;
-        if (t0 < at + x) {
-          sh_b = b;
-          sh_rem = t0 - at;
+        const int per_item = shape.tiles(shape.length(b)) + kItemUnits;
+        const long long x = (long long)per_item * a.K;
+        if (t < x) {
+          const int k = (int)quotient(t, per_item);
+          sh_place[i] = DecodePlace{b, k, (int)(t - (long long)k * per_item)};
           break;
         }
-        at += x;
+        t -= x;
       }
+    }
+    if (tid == 0) {
+      sh_t[0] = t0;
+      sh_t[1] = t1;
+      sh_t[2] = total;
+      sh_share[0].c0 = sh_share[1].c0 = 0;
+      sh_share[0].c1 = sh_share[1].c1 = -1;
     }
     __syncthreads();
   }
-  const long long ctas = min((long long)gridDim.x, total);
-  const long long t0 = blockIdx.x * total / ctas, t1 = (blockIdx.x + 1) * total / ctas;
   DecodeWalk walk;
-  walk.b = sh_b;
-  shape.enter(walk);
-  walk.k = (int)(sh_rem / walk.tiles);
-  walk.tile = (int)(sh_rem % walk.tiles);
-  walk.left = t1 - t0;
-  walk.end = (int)min((int64_t)walk.tiles, walk.tile + walk.left);
+  if (!shape.begin(walk, sh_place[0], sh_place[1])) return;
   DecodeWalk ahead = walk;   // where the copies are
-  int ahead_from = ahead.tile;
   bool more = true;
 
   // ---- copies: lane r looks up key r of the next slot one slot early, then all
   // lanes copy 16-byte units of it
   const int team = TEAM ? 0 : warp;
-  char* ring = smem + team * S * C::SLOT;
+  char* const ring = smem + team * S * C::SLOT;
   const uint32_t ring_u = smem_u32(ring);
   int64_t key_off = -1;   // lane r: byte offset of key r of the slot to come, -1: zeros
   int key_page = -1, key_in = 0, key_head = 0;
   bool key_live = false;
+  // this lane's unit of the first rows copied: where it is and where it goes
+  const int64_t lane_src = (lane / C::UPR) * a.lay.token + (lane % C::UPR) * 16;
+  const int64_t row_step = a.lay.token * (32 / C::UPR);
+  const uint32_t lane_dst = swz<C::UPR>(lane / C::UPR, lane % C::UPR);
+  // the swizzle of rows j * 32 / UPR on from that of the first rows
+  auto swz_step = [](int j) -> uint32_t {
+    constexpr int RPJ = 32 / C::UPR;
+    return C::UPR >= 8 ? ((j * RPJ) & 7) << 4 : ((j * RPJ >> 1) & 3) << 4;
+  };
   auto look_up = [&]() {
     key_live = false;
     if (!more) return;
@@ -283,13 +481,30 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       else
         atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
     }
-    if (__any_sync(~0u, key_live)) {
-      const uint32_t dst = ring_u + slot * C::SLOT;
-      constexpr int NJ = CK * C::UPR / 32;
+    const uint32_t dst = ring_u + slot * C::SLOT;
+    constexpr int NJ = CK * C::UPR / 32, RPJ = 32 / C::UPR;   // copies a lane, rows a copy
+    if (a.lay.page_shift >= 4 && __all_sync(~0u, key_off >= 0)) {
+      // whole slot, 16 keys or more a page: one offset per 16 keys, and steps
 #pragma unroll
-      for (int j0 = 0; j0 < NJ; ++j0) {
-        if (TEAM && j0 % (threads / 32) != warp) continue;
-        const int row = (j0 * 32 + lane) / C::UPR, u = (j0 * 32 + lane) % C::UPR;
+      for (int kt = 0; kt < KT; ++kt) {
+        const int64_t off = __shfl_sync(~0u, key_off, kt * 16) + lane_src;
+        const char *pk = (const char*)a.k_cache + off, *pv = (const char*)a.v_cache + off;
+#pragma unroll
+        for (int j = kt * NJ / KT; j < (kt + 1) * NJ / KT; ++j) {
+          if (!TEAM || j % (threads / 32) == warp) {
+            const uint32_t d = (dst + lane_dst ^ swz_step(j)) + j * RPJ * C::ROWB;
+            cp_async16(d, pk, 16);
+            cp_async16(d + C::HALF, pv, 16);
+          }
+          pk += row_step;
+          pv += row_step;
+        }
+      }
+    } else if (__any_sync(~0u, key_live)) {
+#pragma unroll 1
+      for (int j = 0; j < NJ; ++j) {
+        if (TEAM && j % (threads / 32) != warp) continue;
+        const int row = j * RPJ + lane / C::UPR, u = lane % C::UPR;
         const int64_t off = __shfl_sync(~0u, key_off, row);
         const uint32_t n = off >= 0 ? 16 : 0, d = dst + swz<C::UPR>(row, u);
         // nothing is read where n = 0 (q: an address that exists)
@@ -298,10 +513,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       }
     }
     cp_async_commit();
-    if (more && ++ahead.tile == ahead.end) {
-      more = shape.next_item(ahead, ahead_from);
-      ahead_from = 0;
-    }
+    if (more && ++ahead.tile == ahead.end) more = shape.next_item(ahead, sh_place[0]);
     look_up();
   };
   look_up();
@@ -310,65 +522,83 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
 
   // ---- items
   int cur = 0;
-  const int row0 = TEAM ? warp * 16 : 0;   // first query row of this warp
-  uint2* const q_sm = reinterpret_cast<uint2*>(smem + C::RING + warp * C::QBYTES);
+  const int row0 = TEAM ? warp * NT * 8 : 0;   // first query row of this warp
+  uint2* const q_sm = reinterpret_cast<uint2*>(smem + C::RING + (TEAM ? warp : 0) * C::QBYTES);
+  const uint32_t q_u = smem_u32(q_sm + lane);
+  // Query fragments: column n = lane / 4, dims as the key operand has them.
+  auto load_q = [&](const DecodeWalk& w, int nt, uint2 (&x)[KS]) {
+    const int r = row0 + nt * 8 + g;
+    const char* src = (const char*)a.q + (((int64_t)w.b * a.K + w.k) * R + r) * (H * 2);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      x[ks] = make_uint2(0, 0);
+      if (r < R) {
+        if (E4M3) {
+          x[ks] = __ldg(reinterpret_cast<const uint2*>(src + ks * 32 + c * 8));
+        } else {
+          x[ks].x = __ldg(reinterpret_cast<const uint32_t*>(src + ks * 32 + c * 4));
+          x[ks].y = __ldg(reinterpret_cast<const uint32_t*>(src + ks * 32 + 16 + c * 4));
+        }
+      }
+    }
+  };
+  // For 8-bit caches rows are scaled to [2^10, 2^11) and rounded to f16: exact for
+  // bf16 values down to 2^-27 of the row's largest.  Returns what undoes it.
+  auto scale_q = [&](uint2 (&x)[KS]) -> float {
+    float big = 0.0f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const float2 p = unpack_bf16x2(x[ks].x), q = unpack_bf16x2(x[ks].y);
+      big = fmaxf(fmaxf(big, fmaxf(fabsf(p.x), fabsf(p.y))), fmaxf(fabsf(q.x), fabsf(q.y)));
+    }
+    big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
+    big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
+    // 2^e with big * 2^e in [2^10, 2^11); 1 for rows of zeros or infinities
+    const int e = big > 0.0f && big < INFINITY
+                      ? min(10 - ((int)(__float_as_uint(big) >> 23) - 127), 126) : 0;
+    const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const float2 p = unpack_bf16x2(x[ks].x), q = unpack_bf16x2(x[ks].y);
+      x[ks] = make_uint2(pack_f16x2(p.x * up, p.y * up), pack_f16x2(q.x * up, q.y * up));
+    }
+    return __uint_as_float((uint32_t)(127 - e) << 23);
+  };
+  // The next item's queries are read while this one's results are written,
+  // where registers allow it.
+  constexpr bool EARLY = NT * KS <= 16;
+  uint2 q_next[EARLY ? NT : 1][KS];
+  if (EARLY) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) load_q(walk, nt, q_next[EARLY ? nt : 0]);
+  }
   while (true) {
-    const int begun = walk.tile;
     const int64_t item = (int64_t)walk.b * a.K + walk.k;
     uint2 qf[C::QSMEM ? 1 : KS][NT];
     float sl2[NT][2];      // score to log2 units, per column
-    // Query fragments: column n = lane / 4, dims as the key operand has them.
-    // For 8-bit caches rows are scaled to [2^10, 2^11) and rounded to f16: exact
-    // for bf16 values down to 2^-27 of the row's largest.
+    const float kscale = a.k_scale ? __ldg(a.k_scale + walk.k) : 1.0f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = row0 + nt * 8 + g;
-      const char* src = (const char*)a.q + (item * R + r) * (H * 2);
       uint2 x[KS];
+      if (EARLY) {
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        x[ks] = make_uint2(0, 0);
-        if (r < R) {
-          if (E4M3) {
-            x[ks] = __ldg(reinterpret_cast<const uint2*>(src + ks * 32 + c * 8));
-          } else {
-            x[ks].x = __ldg(reinterpret_cast<const uint32_t*>(src + ks * 32 + c * 4));
-            x[ks].y = __ldg(reinterpret_cast<const uint32_t*>(src + ks * 32 + 16 + c * 4));
-          }
-        }
-      }
-      if (E4M3) {
-        float big = 0.0f;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const float2 p = unpack_bf16x2(x[ks].x), q = unpack_bf16x2(x[ks].y);
-          big = fmaxf(fmaxf(big, fmaxf(fabsf(p.x), fabsf(p.y))), fmaxf(fabsf(q.x), fabsf(q.y)));
-        }
-        big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
-        // 2^e with big * 2^e in [2^10, 2^11); 1 for rows of zeros or infinities
-        const int e = big > 0.0f && big < INFINITY
-                          ? min(10 - ((int)(__float_as_uint(big) >> 23) - 127), 126) : 0;
-        const float up = __uint_as_float((uint32_t)(e + 127) << 23);
-        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const float2 p = unpack_bf16x2(x[ks].x), q = unpack_bf16x2(x[ks].y);
-          x[ks] = make_uint2(pack_f16x2(p.x * up, p.y * up), pack_f16x2(q.x * up, q.y * up));
-        }
-        const float kscale = a.k_scale ? __ldg(a.k_scale + walk.k) : 1.0f;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          sl2[nt][j] = __shfl_sync(~0u, down, (2 * c + j) * 4) * kscale * LOG2E;
+        for (int ks = 0; ks < KS; ++ks) x[ks] = q_next[EARLY ? nt : 0][ks];
       } else {
-        sl2[nt][0] = sl2[nt][1] = LOG2E;
+        load_q(walk, nt, x);
+      }
+      sl2[nt][0] = sl2[nt][1] = LOG2E;
+      if (E4M3) {
+        const float down = scale_q(x);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) sl2[nt][j] = __shfl_sync(~0u, down, (2 * c + j) * 4) * kscale * LOG2E;
       }
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        if (C::QSMEM) q_sm[(ks * NT + nt) * 32 + lane] = x[ks];
-        else qf[C::QSMEM ? 0 : ks][nt] = x[ks];
+        if (!C::QSMEM) qf[C::QSMEM ? 0 : ks][nt] = x[ks];
+        else if (TEAM || (ks * NT + nt) % kDecodeWarps == warp) q_sm[(ks * NT + nt) * 32 + lane] = x[ks];
       }
     }
+    if (C::QSMEM && !TEAM) __syncthreads();   // one copy for the CTA's warps
     // Keys that column (nt, j) keeps: [hi - window, hi)
     int col_hi[NT][2];
 #pragma unroll
@@ -410,11 +640,11 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[kt][nt][i] = s2[nt][i] = 0.0f;
-        const uint32_t row = kt * 16 + (lane & 15);
+        const uint32_t k_lane = ks_u + kt * 16 * C::ROWB + swz<C::UPR>(lane & 15, lane >> 4);
 #pragma unroll
         for (int ks = 0; ks < KS; ks += E4M3 ? 2 : 1) {
           uint32_t x[4];
-          ldsm4(ks_u + swz<C::UPR>(row, (E4M3 ? ks : 2 * ks) + (lane >> 4)), x);
+          ldsm4(k_lane ^ ((E4M3 ? ks : 2 * ks) << 4), x);
           if (E4M3) {
             uint32_t a0[4], a1[4];
             e4m3x4_to_f16(x[0], a0[0], a0[2]);
@@ -423,15 +653,15 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
             e4m3x4_to_f16(x[3], a1[1], a1[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const uint2 q0 = C::QSMEM ? q_sm[(ks * NT + nt) * 32 + lane] : qf[C::QSMEM ? 0 : ks][nt];
-              const uint2 q1 = C::QSMEM ? q_sm[((ks + 1) * NT + nt) * 32 + lane] : qf[C::QSMEM ? 0 : ks + 1][nt];
+              const uint2 q0 = C::QSMEM ? lds8(q_u + (ks * NT + nt) * 256) : qf[C::QSMEM ? 0 : ks][nt];
+              const uint2 q1 = C::QSMEM ? lds8(q_u + ((ks + 1) * NT + nt) * 256) : qf[C::QSMEM ? 0 : ks + 1][nt];
               mma16816<true>(s[kt][nt], a0, q0.x, q0.y);
               mma16816<true>(s2[nt], a1, q1.x, q1.y);
             }
           } else {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const uint2 q0 = C::QSMEM ? q_sm[(ks * NT + nt) * 32 + lane] : qf[C::QSMEM ? 0 : ks][nt];
+              const uint2 q0 = C::QSMEM ? lds8(q_u + (ks * NT + nt) * 256) : qf[C::QSMEM ? 0 : ks][nt];
               mma16816<false>(ks & 1 ? s2[nt] : s[kt][nt], x, q0.x, q0.y);
             }
           }
@@ -518,7 +748,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       auto load_v = [&](int kt, int ds, uint32_t (&v0)[4], uint32_t (&v1)[4]) {
         if (E4M3) {
           uint32_t x[4];
-          ldsm4_trans(vs_u + swz<C::UPR>(kt * 16 + (lane & 15), ds + (lane >> 4)), x);
+          ldsm4_trans((vs_u + kt * 16 * C::ROWB + swz<C::UPR>(lane & 15, lane >> 4)) ^ (ds << 4), x);
           // bytes (key 2c: dims 2g, 2g+1), (key 2c+1: the same) -> pairs of keys per dim
 #pragma unroll
           for (int i = 0; i < 4; ++i) x[i] = __byte_perm(x[i], 0, 0x3120);
@@ -527,8 +757,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
           e4m3x4_to_f16(x[2], v1[0], v1[1]);
           e4m3x4_to_f16(x[3], v1[2], v1[3]);
         } else {
-          ldsm4_trans(vs_u + swz<C::UPR>(kt * 16 + (lane & 7) + ((lane >> 4) << 3),
-                                         2 * ds + ((lane >> 3) & 1)), v0);
+          ldsm4_trans((vs_u + kt * 16 * C::ROWB +
+                       swz<C::UPR>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1)) ^ (ds << 5), v0);
         }
       };
       auto add_v = [&](float (&d)[4], const uint32_t (&v)[4], int kt, int nt) {
@@ -598,84 +828,84 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         l[nt][j] += __shfl_xor_sync(~0u, l[nt][j], 8);
         l[nt][j] += __shfl_xor_sync(~0u, l[nt][j], 16);
       }
-    const bool whole = begun == 0 && walk.end == walk.tiles;
+    const bool whole = walk.begun == 0 && walk.end == walk.tiles;
+    DecodeWalk then = walk;
+    const bool go_on = shape.next_item(then, sh_place[0]);
+    if (EARLY && go_on) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) load_q(then, nt, q_next[EARLY ? nt : 0]);
+    }
     const float vscale = a.v_scale ? __ldg(a.v_scale + walk.k) : 1.0f;
     const int64_t out_row = item * R;
     // Partials: slot 1 of a CTA holds the item that starts in it, slot 0 one
     // that started before.
-    const int64_t part = paged_partial_floats(R, H);
-    float* const mine = a.partials + ((int64_t)blockIdx.x * 2 + (begun == 0 ? 1 : 0)) * part;
+    float* const mine = a.partials + ((int64_t)blockIdx.x * 2 + (walk.begun == 0 ? 1 : 0)) * paged_partial_floats(R, H);
     auto put = [&](int r, int d, float4 x, float M, float L) {   // four dims of row r
-      if (whole) {
-        const float f = L == 0.0f ? 0.0f : vscale / L;
-        const uint2 y = make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
-        *reinterpret_cast<uint2*>((char*)a.o + ((out_row + r) * H + d) * 2) = y;
-        if (d == 0) a.lse[out_row + r] = (M + log2f(L)) * LN2;   // -inf with no key
-      } else {
-        *reinterpret_cast<float4*>(mine + (int64_t)r * H + d) = x;
-        if (d == 0) {
-          mine[(int64_t)R * H + r] = M;
-          mine[(int64_t)R * (H + 1) + r] = L;
-        }
-      }
+      if (whole) put_result((char*)a.o + out_row * H * 2, a.lse + out_row, H, r, d, x, M, L, vscale);
+      else put_partial(mine, H, R, r, d, x, M, L);
     };
     // O^T goes through shared memory: the slot just used, free until the next
     // copies are issued.  Four dims stay together; dims move by 8 with the column
-    // pair, against bank conflicts.
+    // pair, against bank conflicts.  16 rows at a time.
     float* const so = reinterpret_cast<float*>(ring + (cur == 0 ? S - 1 : cur - 1) * C::SLOT);
     if (!TEAM) {
-      __syncwarp();
+      constexpr int NR = NT < 2 ? NT : 2;   // n-tiles a round
 #pragma unroll
-      for (int ds = 0; ds < KS; ++ds)
+      for (int n0 = 0; n0 < NT; n0 += NR) {
+        if (n0 * 8 >= R) break;
+        __syncwarp();
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int ds = 0; ds < KS; ++ds)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float* const row = so + (nt * 8 + 2 * c + j) * H;
-            if (E4M3) {
-              *reinterpret_cast<float2*>(row + ((ds * 16 + 2 * g) ^ (c << 3))) =
-                  make_float2(o[ds][nt][j], o[ds][nt][j + 2]);
-            } else {
-              row[(ds * 16 + g) ^ (c << 3)] = o[ds][nt][j];
-              row[(ds * 16 + g + 8) ^ (c << 3)] = o[ds][nt][j + 2];
+          for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float* const row = so + (nt * 8 + 2 * c + j) * H;
+              if (E4M3) {
+                *reinterpret_cast<float2*>(row + ((ds * 16 + 2 * g) ^ (c << 3))) =
+                    make_float2(o[ds][n0 + nt][j], o[ds][n0 + nt][j + 2]);
+              } else {
+                row[(ds * 16 + g) ^ (c << 3)] = o[ds][n0 + nt][j];
+                row[(ds * 16 + g + 8) ^ (c << 3)] = o[ds][n0 + nt][j + 2];
+              }
             }
-          }
-      if (g == 0) {
+        if (g == 0) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            sh_m[warp][nt * 8 + 2 * c + j] = m[nt][j];
-            sh_l[warp][nt * 8 + 2 * c + j] = l[nt][j];
-          }
-      }
-      __syncthreads();
-      for (int i = tid; i < R * (H / 4); i += kDecodeWarps * 32) {
-        const int r = i / (H / 4), d = i % (H / 4) * 4;
-        float M = sh_m[0][r], L = 0.0f;
-#pragma unroll
-        for (int w = 1; w < kDecodeWarps; ++w) M = fmaxf(M, sh_m[w][r]);
-        const float base = M == -INFINITY ? 0.0f : M;
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        // every warp's ring has the same slot at the same place
-        const float* at = reinterpret_cast<const float*>(smem + ((const char*)so - ring)) + r * H +
-                          (d ^ (((r >> 1) & 3) << 3));
-#pragma unroll
-        for (int w = 0; w < kDecodeWarps; ++w) {
-          const float f = fast_exp2(sh_m[w][r] - base);
-          const float4 y = *reinterpret_cast<const float4*>(at + w * (S * C::SLOT / 4));
-          L += sh_l[w][r] * f;
-          x.x += y.x * f;
-          x.y += y.y * f;
-          x.z += y.z * f;
-          x.w += y.w * f;
+            for (int j = 0; j < 2; ++j) {
+              sh_m[warp][nt * 8 + 2 * c + j] = m[n0 + nt][j];
+              sh_l[warp][nt * 8 + 2 * c + j] = l[n0 + nt][j];
+            }
         }
-        put(r, d, x, M, L);
+        __syncthreads();
+        const int rows = min(NR * 8, R - n0 * 8);
+        for (int i = tid; i < rows * (H / 4); i += kDecodeWarps * 32) {
+          const int r = i / (H / 4), d = i % (H / 4) * 4;
+          float M = sh_m[0][r], L = 0.0f;
+#pragma unroll
+          for (int w = 1; w < kDecodeWarps; ++w) M = fmaxf(M, sh_m[w][r]);
+          const float base = M == -INFINITY ? 0.0f : M;
+          float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          // every warp's ring has the same slot at the same place
+          const float* at = reinterpret_cast<const float*>(smem + ((const char*)so - ring)) + r * H +
+                            (d ^ (((r >> 1) & 3) << 3));
+#pragma unroll
+          for (int w = 0; w < kDecodeWarps; ++w) {
+            const float f = fast_exp2(sh_m[w][r] - base);
+            const float4 y = *reinterpret_cast<const float4*>(at + w * (S * C::SLOT / 4));
+            L += sh_l[w][r] * f;
+            x.x += y.x * f;
+            x.y += y.y * f;
+            x.z += y.z * f;
+            x.w += y.w * f;
+          }
+          put(n0 * 8 + r, d, x, M, L);
+        }
+        __syncthreads();
       }
-      __syncthreads();
     } else {
-      // 16 rows of this warp, H dims, through 16 dims x 16 rows of shuffles: a
-      // transpose of four lanes' columns would cost more than these stores
+      // straight from the registers: the rows are this warp's alone
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -706,91 +936,101 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         }
     }
 
-    // ---- join of an item that several CTAs share, by the last of them
-    if (!whole) {
-      const int64_t at0 = t1 - walk.left - begun;   // the item's first tile in the list
-      const int c0 = (int)(((at0 + 1) * ctas - 1) / total);
-      const int c1 = (int)(((at0 + walk.tiles) * ctas - 1) / total);
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) {
-        // The counter's upper bits name the call, so what the word held before
-        // does not matter; the last arrival clears it for a replay of the call.
-        unsigned long long* const word = reinterpret_cast<unsigned long long*>(a.counters) + c0;
-        unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word), now;
-        while (true) {
-          const unsigned long long n = (old >> 16) == a.tag ? (old & 0xffff) + 1 : 1;
-          now = n;
-          const unsigned long long to = n == (unsigned long long)(c1 - c0 + 1) ? 0 : (a.tag << 16) | n;
-          const unsigned long long seen = atomicCAS(word, old, to);
-          if (seen == old) break;
-          old = seen;
-        }
-        sh_last = now == (unsigned long long)(c1 - c0 + 1);
-        __threadfence();
-      }
-      __syncthreads();
-      if (sh_last) {
-        for (int i = tid; i < R * (H / 4); i += threads) {
-          const int r = i / (H / 4), d = i % (H / 4) * 4;
-          float M = -INFINITY, L = 0.0f;
-          float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          constexpr int U = 8;   // partials read at once
-          for (int p0 = c0; p0 <= c1; p0 += U) {
-            float4 y[U];
-            float pm[U], pn[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              pm[u] = -INFINITY;
-              pn[u] = 0.0f;
-              y[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (p0 + u <= c1) {
-                const float* src = a.partials + ((int64_t)(p0 + u) * 2 + (p0 + u == c0 ? 1 : 0)) * part;
-                y[u] = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)r * H + d));
-                pm[u] = __ldcg(src + (int64_t)R * H + r);
-                pn[u] = __ldcg(src + (int64_t)R * (H + 1) + r);
-              }
-            }
-            float mn = M;
-#pragma unroll
-            for (int u = 0; u < U; ++u) mn = fmaxf(mn, pm[u]);
-            const float base = mn == -INFINITY ? 0.0f : mn;
-            const float f0 = fast_exp2(M - base);
-            M = mn;
-            L *= f0;
-            x.x *= f0; x.y *= f0; x.z *= f0; x.w *= f0;
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-              const float f = fast_exp2(pm[u] - base);
-              L += pn[u] * f;
-              x.x += y[u].x * f;
-              x.y += y[u].y * f;
-              x.z += y[u].z * f;
-              x.w += y[u].w * f;
-            }
-          }
-          const float f = L == 0.0f ? 0.0f : vscale / L;
-          const uint2 y = make_uint2(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f));
-          *reinterpret_cast<uint2*>((char*)a.o + ((out_row + r) * H + d) * 2) = y;
-          if (d == 0) a.lse[out_row + r] = (M + log2f(L)) * LN2;
-        }
-      }
+    if (!whole && tid == 0) {
+      // the item's first tile in the list: it is the one that this CTA's units
+      // begin in, or the one that they end in
+      const DecodePlace h = sh_place[0], e = sh_place[1];
+      const long long total = sh_t[2];
+      const long long at = (walk.b == h.b && walk.k == h.k ? sh_t[0] - h.rem : sh_t[1] - 1 - e.rem) + kItemUnits;
+      sh_share[walk.begun == 0 ? 1 : 0] =
+          DecodeShare{walk.b, walk.k, (int)quotient((at + 1) * ctas - 1, total),
+                      (int)quotient((at + walk.tiles) * ctas - 1, total)};
     }
-    if (!shape.next_item(walk, begun)) break;
+    if (!go_on) break;
+    walk = then;
   }
+
+  // ---- items that several CTAs share are joined by the last of them to get
+  // here; over kJoinMost partials in groups first, by the last of each group
   cp_async_wait<0>();
+  __syncthreads();
+  const int cta = (int)blockIdx.x;
+  const int64_t part = paged_partial_floats(R, H);
+  const DecodeShare share[2] = {sh_share[0], sh_share[1]};
+  if (share[0].c1 < 0 && share[1].c1 < 0) return;
+  auto in_groups = [&](const DecodeShare& x) { return x.c1 - x.c0 + 1 > kJoinMost; };
+  auto first_of = [&](const DecodeShare& x) {   // of the CTAs joined with this one
+    return in_groups(x) ? x.c0 + (cta - x.c0) / kJoinGroup * kJoinGroup : x.c0;
+  };
+  if (warp == 0) {
+    if (lane == 0) {
+      __threadfence();
+      for (int i = 0; i < 2; ++i)
+        if (share[i].c1 >= 0) *reinterpret_cast<volatile uint64_t*>(a.flags + cta * 4 + i) = a.tag;
+    }
+    __syncwarp();
+    asm volatile("fence.sc.gpu;" ::: "memory");
+    for (int i = 0; i < 2; ++i) {
+      if (share[i].c1 < 0) continue;
+      const int f = first_of(share[i]);
+      const int n = in_groups(share[i]) ? min(kJoinGroup, share[i].c1 + 1 - f) : share[i].c1 + 1 - f;
+      const bool last = all_arrived(JoinList<uint64_t>{a.flags + f * 4, 4, f == share[i].c0 ? 1 : 0, 0, n},
+                                    a.tag, in_groups(share[i]));
+      if (lane == 0) sh_last[i] = last;
+    }
+  }
+  __syncthreads();
+  for (int i = 0; i < 2; ++i) {
+    if (share[i].c1 < 0 || !sh_last[i]) continue;
+    const DecodeShare x = share[i];
+    const bool groups = in_groups(x);
+    const int f = first_of(x);
+    const int n = groups ? min(kJoinGroup, x.c1 + 1 - f) : x.c1 + 1 - f;
+    const int64_t item = (int64_t)x.b * a.K + x.k;
+    void* const o_out = (char*)a.o + item * R * H * 2;
+    float* const lse_out = a.lse + item * R;
+    const float vscale = a.v_scale ? __ldg(a.v_scale + x.k) : 1.0f;
+    // joined groups, by their first CTA: two of one kind (first of their item or
+    // not) are kJoinGroup CTAs apart or more
+    float* const first = a.group_partials + (int64_t)(x.c0 / kJoinGroup) * 2 * part;
+    JoinList<float> list{a.partials + (int64_t)f * 2 * part, 2 * part, f == x.c0 ? part : 0, 0, n};
+    float* dst = groups ? first + (int64_t)((f - x.c0) / kJoinGroup) * 2 * part + (f == x.c0 ? part : 0) : nullptr;
+    bool done = false;
+    while (true) {
+      join_partials<H, C::RING>(list, R, dst, o_out, lse_out, vscale, smem);
+      if (!groups || done) break;
+      const int m = (x.c1 - x.c0) / kJoinGroup + 1;
+      __syncthreads();
+      if (warp == 0) {
+        if (lane == 0) {
+          __threadfence();
+          *reinterpret_cast<volatile uint64_t*>(a.flags + f * 4 + (f == x.c0 ? 3 : 2)) = a.tag;
+        }
+        __syncwarp();
+        asm volatile("fence.sc.gpu;" ::: "memory");
+        const bool last = all_arrived(JoinList<uint64_t>{a.flags + x.c0 * 4, 4 * kJoinGroup, 3, 2, m}, a.tag, false);
+        if (lane == 0) sh_last[i] = last;
+      }
+      __syncthreads();
+      if (!sh_last[i]) break;
+      list = JoinList<float>{first, 2 * part, part, 0, m};
+      dst = nullptr;
+      done = true;
+    }
+    __syncthreads();
+  }
 }
 
 template <class C>
 cudaError_t launch_decode(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
-  const int warps = C::TEAM ? (a.G * a.T + 15) / 16 : kDecodeWarps;
-  const size_t smem = C::RING + (size_t)warps * C::QBYTES;
+  const int warps = C::TEAM ? (a.G * a.T + C::NT * 8 - 1) / (C::NT * 8) : kDecodeWarps;
+  const size_t smem = C::RING + (size_t)(C::TEAM ? warps : 1) * C::QBYTES;
   static bool ready[64] = {};   // per device; setting it twice is harmless
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !ready[dev]) {
-    const size_t most = C::RING + (size_t)(C::TEAM ? kMaxPagedRows / 16 : kDecodeWarps) * C::QBYTES;
+    const size_t most = C::RING + (size_t)(C::TEAM ? kMaxPagedRows / (C::NT * 8) : 1) * C::QBYTES;
     e = cudaFuncSetAttribute(paged_decode_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev] = true;
@@ -799,12 +1039,15 @@ cudaError_t launch_decode(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// Rows 1..8 and 9..16: warps on their own; more: a CTA's warps share the keys.
+// Up to 8, 16 and (H <= 128: registers) 32 rows: warps on their own; more: a CTA's
+// warps share the keys.
 template <int H, bool E4M3>
 cudaError_t launch_decode_rows(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
   const int R = a.G * a.T;
   if (R <= 8) return launch_decode<DecodeCfg<H, E4M3, 1, false>>(a, grid, st);
   if (R <= 16) return launch_decode<DecodeCfg<H, E4M3, 2, false>>(a, grid, st);
+  if constexpr (H <= 128)
+    if (R <= 32) return launch_decode<DecodeCfg<H, E4M3, 4, false>>(a, grid, st);
   return launch_decode<DecodeCfg<H, E4M3, 2, true>>(a, grid, st);
 }
 
