@@ -46,6 +46,13 @@ struct PagedAppendArgs {
   uint32_t* err;
 };
 
+// An item (b * K + k) whose tiles CTAs first .. last share; first < 0: none.  One
+// entry per item where there are no more of them than CTAs, else one per CTA,
+// for the item that begins in it.
+struct PagedDecodeSplit {
+  int item, first, last, pad;
+};
+
 struct PagedDecodeArgs {
   const void* q;               // bf16 [B, K, G, T, H]
   const void *k_cache, *v_cache;
@@ -58,23 +65,18 @@ struct PagedDecodeArgs {
   int B, K, G, T, H, max_pages;
   int window;                  // 0: none
   float* partials;             // workspace: [CTAs][2][paged_partial_floats] of split items
-  float* group_partials;       // workspace: [CTAs / kJoinGroup rounded up][2] joined groups
-  uint64_t* flags;             // workspace: [CTAs][4] arrivals
-  unsigned long long tag;      // names the call, never 0
+  PagedDecodeSplit* splits;    // workspace: [CTAs]
+  bool by_item;                // entries of splits are items
   uint32_t* err;
 };
 
-// CTAs whose partials of one item are joined first, where an item has many.
-constexpr int kJoinGroup = 16;
-
-// Workspace of a decode: flags, partials, joined groups, on a GPU with sm_count SMs.
+// Workspace of a decode: the splits, then partials, on a GPU with sm_count SMs.
 // CTAs an SM: as many as the rings leave room for.  Up to 16 query rows: two
 // up to H = 128, one at 256; more rows: two up to 64 rows (4 warps each) and H
 // = 128, else one.
 struct PagedDecodePlan {
   int ctas;
-  size_t partials;   // offsets
-  size_t groups;
+  size_t partials;   // offset
   size_t total;
 };
 // Floats of one partial: o [R, H], m [R], l [R], rounded up to 16 bytes.
@@ -84,10 +86,8 @@ __host__ __device__ inline int64_t paged_partial_floats(int R, int H) {
 inline PagedDecodePlan paged_decode_plan(int R, int H, int sm_count) {
   PagedDecodePlan p;
   p.ctas = sm_count * (H <= 128 && R <= 64 ? 2 : 1);
-  const size_t pair = 2 * paged_partial_floats(R, H) * 4;
-  p.partials = ((size_t)p.ctas * 32 + 255) & ~(size_t)255;
-  p.groups = p.partials + ((p.ctas * pair + 255) & ~(size_t)255);
-  p.total = p.groups + (((size_t)((p.ctas + kJoinGroup - 1) / kJoinGroup) * pair + 255) & ~(size_t)255);
+  p.partials = ((size_t)p.ctas * sizeof(PagedDecodeSplit) + 255) & ~(size_t)255;
+  p.total = p.partials + (((size_t)p.ctas * 2 * paged_partial_floats(R, H) * 4 + 255) & ~(size_t)255);
   return p;
 }
 

@@ -3,7 +3,6 @@
 // allocates device memory or synchronises.
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cstdint>
 
 #include "../../include/fa.h"
@@ -50,16 +49,6 @@ int make_layout(fa::PagedLayout* lay, int cache_type, int64_t page_stride, int64
 bool decode_shape_ok(int B, int K, int G, int T, int H) {
   return head_dim_ok(H) && (int64_t)G * T <= fa::kMaxPagedRows && B <= fa::kMaxPagedBatch &&
          (int64_t)B * K <= 65535;
-}
-
-// A number of its own for each decode call (never 0): a word that some other call
-// or program left in a workspace does not look like it.
-unsigned long long call_tag() {
-  static std::atomic<unsigned long long> calls{0};
-  unsigned long long x = calls.fetch_add(1) * 0x9e3779b97f4a7c15ull + 0x632be59bd9b4e019ull;
-  x = (x ^ (x >> 31)) * 0xd6e8feb86659fd93ull;
-  x ^= x >> 29;
-  return x ? x : 1;
 }
 
 int status(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
@@ -174,10 +163,9 @@ int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int
   a.B = B; a.K = K; a.G = G; a.T = T; a.H = H; a.max_pages = max_pages;
   // A window that reaches past the longest request is none.
   a.window = window >= max_pages * page_size ? 0 : window;
-  a.flags = static_cast<uint64_t*>(workspace);
+  a.splits = static_cast<fa::PagedDecodeSplit*>(workspace);
+  a.by_item = B * K <= plan.ctas;
   a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.partials);
-  a.group_partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.groups);
-  a.tag = call_tag();
   a.err = fa::device_error_word();
   if (!a.err || plan.ctas == 0) return FA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

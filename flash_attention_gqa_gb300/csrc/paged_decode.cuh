@@ -11,9 +11,9 @@
 // all items, in order, are dealt evenly to the CTAs (about one wave of them), so
 // ragged lengths and single long requests load the GPU alike.  The lengths
 // stay on the device: every CTA sums the tile counts for itself.  An item that
-// ends up in several CTAs leaves one partial (o, m, l) in each; the CTA that
-// arrives last (a counter per split item) joins them in key order, so the
-// result does not depend on timing.
+// ends up in several CTAs leaves one partial (o, m, l) in each, and a second
+// kernel, launched early and waiting for the first to end, joins them in key
+// order.  Nothing depends on timing.
 //
 // Products.  mma.sync with the keys as the 16-row operand: S^T = K Q^T and
 // O^T += V^T P^T waste nothing at R = 8 (tcgen05's 128-row tile would be
@@ -38,7 +38,6 @@
 namespace fa {
 
 constexpr int kDecodeWarps = 4;   // warps of a CTA whose warps stream alone
-constexpr int kJoinMost = 64;     // partials joined at once; more go in groups
 
 // ------------------------------------------------------------- primitives
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -238,7 +237,7 @@ __device__ __forceinline__ bool any_not_finite(const char* p, int bytes, int lan
   return __any_sync(~0u, bad);
 }
 
-// --------------------------------------------------------------- joining
+// --------------------------------------------------------------- results
 // The four dims of row r of a joined or whole result, rounded to bf16 once.
 __device__ __forceinline__ void put_result(void* o, float* lse, int H, int r, int d, float4 x, float M,
                                            float L, float vscale) {
@@ -255,117 +254,6 @@ __device__ __forceinline__ void put_partial(float* dst, int H, int R, int r, int
   }
 }
 
-// Partials, or flags, of the CTAs that share an item: number p at base + p * step,
-// number 0 at + first instead of + other.
-template <class X>
-struct JoinList {
-  X* base;
-  int64_t step, first, other;
-  int n;
-  __device__ __forceinline__ X* operator()(int p) const { return base + p * step + (p == 0 ? first : other); }
-};
-
-// Whether all flags of the list hold `tag`; they are cleared then.  One warp,
-// after it set its own flag.  A word holds the call's tag from the arrival
-// until the join takes it back, so neither what it held before the call nor a
-// replay of the call matters.  Flags are set behind a fence that follows the
-// partials and read behind another: of CTAs that arrive together at least one
-// sees all, and where several do, they write the same result, or (claim) only
-// the one that takes the first flag goes on.
-__device__ __forceinline__ bool all_arrived(const JoinList<uint64_t>& flags, uint64_t tag, bool claim) {
-  const int lane = threadIdx.x & 31;
-  bool all = true;
-  for (int p = lane; p < flags.n; p += 32) all &= *reinterpret_cast<volatile uint64_t*>(flags(p)) == tag;
-  all = __all_sync(~0u, all);
-  if (all && claim) {
-    bool won = false;
-    if (lane == 0)
-      won = atomicCAS(reinterpret_cast<unsigned long long*>(flags(0)), (unsigned long long)tag, 0ull) == tag;
-    all = __shfl_sync(~0u, won, 0);
-  }
-  if (all) {
-    __threadfence();
-    for (int p = lane; p < flags.n; p += 32) *reinterpret_cast<volatile uint64_t*>(flags(p)) = 0;
-  }
-  return all;
-}
-
-// Sums the partials of a list in order, by the whole CTA, through `stage` (the
-// ring, with nothing in flight): into the partial `dst`, or where that is null
-// into o and lse.  All copies of a round are in flight at once: at the end of
-// the kernel what counts is the number of trips to L2.
-template <int H, int STAGE>
-__device__ __forceinline__ void join_partials(const JoinList<float>& src, int R, float* dst, void* o, float* lse,
-                                              float vscale, char* stage) {
-  constexpr int E = 4;   // float4 a thread
-  const int tid = threadIdx.x, threads = blockDim.x;
-  const float* const all = reinterpret_cast<const float*>(stage);
-  const int ml = (2 * R + 3) / 4;                // 16-byte units of a partial's m and l
-  // rows at a time: 8 partials of them fit (ml <= 64, STAGE >= 16 KB: one row at least)
-  static_assert(STAGE / 128 - 64 >= H / 4, "");
-  const int rc = min(E * threads * 4 / H, (STAGE / 128 - ml) / (H / 4));
-  for (int r0 = 0; r0 < R; r0 += rc) {
-    const int rows = min(rc, R - r0);
-    const int unit = rows * (H / 4) + ml;        // 16-byte units staged of a partial
-    const int most = STAGE / 16 / unit;
-    float4 x[E];
-    float M[E], L[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      M[e] = -INFINITY;
-      L[e] = 0.0f;
-    }
-    for (int p0 = 0; p0 < src.n; p0 += most) {
-      const int n = min(most, src.n - p0);
-      __syncthreads();
-      for (int p = 0, j = tid, i = tid; i < n * unit; i += threads, j += threads) {
-        for (; j >= unit; j -= unit) ++p;
-        const int at = j < unit - ml ? r0 * H + j * 4 : R * H + (j - (unit - ml)) * 4;
-        cp_async16(smem_u32(stage) + i * 16, src(p0 + p) + at, 16);
-      }
-      cp_async_commit();
-      cp_async_wait<0>();
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int i = tid + e * threads, r = i / (H / 4), d = i % (H / 4) * 4;
-        if (r >= rows) continue;
-        const float* const mr = all + (unit - ml) * 4 + r0 + r;
-        float mn = M[e];
-        for (int p = 0; p < n; ++p) mn = fmaxf(mn, mr[p * unit * 4]);
-        const float low = mn == -INFINITY ? 0.0f : mn;
-        const float f0 = fast_exp2(M[e] - low);
-        M[e] = mn;
-        L[e] *= f0;
-        x[e].x *= f0; x[e].y *= f0; x[e].z *= f0; x[e].w *= f0;
-#pragma unroll 4
-        for (int p = 0; p < n; ++p) {
-          const float f = fast_exp2(mr[p * unit * 4] - low);
-          const float4 y = *reinterpret_cast<const float4*>(all + p * unit * 4 + r * H + d);
-          L[e] += mr[p * unit * 4 + R] * f;
-          x[e].x += y.x * f;
-          x[e].y += y.y * f;
-          x[e].z += y.z * f;
-          x[e].w += y.w * f;
-        }
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int i = tid + e * threads, r = i / (H / 4), d = i % (H / 4) * 4;
-      if (r >= rows) continue;
-      if (dst) put_partial(dst, H, R, r0 + r, d, x[e], M[e], L[e]);
-      else put_result(o, lse, H, r0 + r, d, x[e], M[e], L[e], vscale);
-    }
-  }
-}
-
-// A partial that this CTA left, of an item that CTAs c0 .. c1 share.
-struct DecodeShare {
-  int b, k, c0, c1;   // c1 < c0: none
-};
-
 template <class C>
 __global__ void __launch_bounds__(C::TEAM ? 256 : kDecodeWarps * 32, C::MIN_CTAS)
 paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
@@ -376,19 +264,17 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
   __shared__ float sh_m[kDecodeWarps][16], sh_l[kDecodeWarps][16];
   __shared__ long long sh_scan[9];
   __shared__ DecodePlace sh_place[2];   // first and last unit
-  __shared__ int sh_last[2];
-  __shared__ DecodeShare sh_share[2];    // by the slot of its partial
-  __shared__ long long sh_t[3];          // first unit, one past the last, all units
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   const int g = lane >> 2, c = lane & 3;
   const int R = a.G * a.T;
   const DecodeShape<C> shape{a};
 
+  // The join may be launched as soon as every CTA has got here; it waits.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
   // ---- this CTA's units
-  int ctas;
   {
-    long long total, t0, t1;
     const int per = (a.B + threads - 1) / threads;
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
     long long mine = 0;
@@ -407,38 +293,42 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     }
     if (lane == 31) sh_scan[warp] = inc;
     __syncthreads();
-    long long before = 0;
-    total = 0;
+    long long before = 0, total = 0;
     for (int w = 0; w < threads / 32; ++w) {
       if (w < warp) before += sh_scan[w];
       total += sh_scan[w];
     }
-    ctas = (int)min((long long)gridDim.x, total);
-    if (blockIdx.x >= ctas) return;
-    t0 = quotient(blockIdx.x * total, ctas);
-    t1 = quotient((blockIdx.x + 1) * total, ctas);
+    const int ctas = (int)min((long long)gridDim.x, total);
+    if (blockIdx.x >= ctas) {
+      if (tid == 0 && !a.by_item) a.splits[blockIdx.x] = PagedDecodeSplit{0, -1, 0, 0};
+      return;
+    }
+    const long long t0 = quotient(blockIdx.x * total, ctas), t1 = quotient((blockIdx.x + 1) * total, ctas);
     const long long at = before + inc - mine;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {   // where this CTA's units begin and end
       long long t = (i == 0 ? t0 : t1 - 1) - at;
       if (t < 0 || t >= mine) continue;
       for (int b = b0; b < b1; ++b) {
-        const int per_item = shape.tiles(shape.length(b)) + kItemUnits;
+        const int tiles = shape.tiles(shape.length(b)), per_item = tiles + kItemUnits;
         const long long x = (long long)per_item * a.K;
         if (t < x) {
           const int k = (int)quotient(t, per_item);
-          sh_place[i] = DecodePlace{b, k, (int)(t - (long long)k * per_item)};
+          const int rem = (int)(t - (long long)k * per_item);
+          sh_place[i] = DecodePlace{b, k, rem};
+          if (i == 1) {
+            // the item that the units end in, where it begins here and goes on
+            // in the next CTA: for the join, with its last CTA
+            const long long first = t1 - 1 - rem + kItemUnits;   // its first tile's unit
+            const bool split = rem >= kItemUnits && rem + 1 < per_item && first >= t0;
+            if (split || !a.by_item)
+              a.splits[a.by_item ? b * a.K + k : blockIdx.x] = PagedDecodeSplit{
+                  b * a.K + k, split ? (int)blockIdx.x : -1, (int)quotient((first + tiles) * ctas - 1, total), 0};
+          }
           break;
         }
         t -= x;
       }
-    }
-    if (tid == 0) {
-      sh_t[0] = t0;
-      sh_t[1] = t1;
-      sh_t[2] = total;
-      sh_share[0].c0 = sh_share[1].c0 = 0;
-      sh_share[0].c1 = sh_share[1].c1 = -1;
     }
     __syncthreads();
   }
@@ -936,89 +826,98 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         }
     }
 
-    if (!whole && tid == 0) {
-      // the item's first tile in the list: it is the one that this CTA's units
-      // begin in, or the one that they end in
-      const DecodePlace h = sh_place[0], e = sh_place[1];
-      const long long total = sh_t[2];
-      const long long at = (walk.b == h.b && walk.k == h.k ? sh_t[0] - h.rem : sh_t[1] - 1 - e.rem) + kItemUnits;
-      sh_share[walk.begun == 0 ? 1 : 0] =
-          DecodeShare{walk.b, walk.k, (int)quotient((at + 1) * ctas - 1, total),
-                      (int)quotient((at + walk.tiles) * ctas - 1, total)};
-    }
+    if (whole && a.by_item && tid == 0) a.splits[item] = PagedDecodeSplit{(int)item, -1, 0, 0};
     if (!go_on) break;
     walk = then;
   }
-
-  // ---- items that several CTAs share are joined by the last of them to get
-  // here; over kJoinMost partials in groups first, by the last of each group
   cp_async_wait<0>();
-  __syncthreads();
-  const int cta = (int)blockIdx.x;
+}
+
+// Joins the partials of an item that several CTAs of the first kernel share: a
+// thread per four dims of a row and share of the partials, `per` such elements a
+// CTA, kJoinThreads / per shares, whose results are then summed in order.
+constexpr int kJoinThreads = 512;
+
+template <int H>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedDecodeArgs a,
+                                                                  int per) {
+  __shared__ float4 sx[kJoinThreads];
+  __shared__ float2 sml[kJoinThreads];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // (L2 loads: this grid may have started before the first one wrote)
+  const int4 split = __ldcg(reinterpret_cast<const int4*>(a.splits) + blockIdx.x);
+  const int item = split.x, first = split.y, n = split.z - first + 1;   // n partials
+  if (first < 0) return;
+  const int R = a.G * a.T, shares = kJoinThreads / per;
+  const int share = threadIdx.x / per, at = threadIdx.x % per;
+  const int i = blockIdx.y * per + at;
+  const int r = i / (H / 4), d = i % (H / 4) * 4;
   const int64_t part = paged_partial_floats(R, H);
-  const DecodeShare share[2] = {sh_share[0], sh_share[1]};
-  if (share[0].c1 < 0 && share[1].c1 < 0) return;
-  auto in_groups = [&](const DecodeShare& x) { return x.c1 - x.c0 + 1 > kJoinMost; };
-  auto first_of = [&](const DecodeShare& x) {   // of the CTAs joined with this one
-    return in_groups(x) ? x.c0 + (cta - x.c0) / kJoinGroup * kJoinGroup : x.c0;
-  };
-  if (warp == 0) {
-    if (lane == 0) {
-      __threadfence();
-      for (int i = 0; i < 2; ++i)
-        if (share[i].c1 >= 0) *reinterpret_cast<volatile uint64_t*>(a.flags + cta * 4 + i) = a.tag;
-    }
-    __syncwarp();
-    asm volatile("fence.sc.gpu;" ::: "memory");
-    for (int i = 0; i < 2; ++i) {
-      if (share[i].c1 < 0) continue;
-      const int f = first_of(share[i]);
-      const int n = in_groups(share[i]) ? min(kJoinGroup, share[i].c1 + 1 - f) : share[i].c1 + 1 - f;
-      const bool last = all_arrived(JoinList<uint64_t>{a.flags + f * 4, 4, f == share[i].c0 ? 1 : 0, 0, n},
-                                    a.tag, in_groups(share[i]));
-      if (lane == 0) sh_last[i] = last;
-    }
-  }
-  __syncthreads();
-  for (int i = 0; i < 2; ++i) {
-    if (share[i].c1 < 0 || !sh_last[i]) continue;
-    const DecodeShare x = share[i];
-    const bool groups = in_groups(x);
-    const int f = first_of(x);
-    const int n = groups ? min(kJoinGroup, x.c1 + 1 - f) : x.c1 + 1 - f;
-    const int64_t item = (int64_t)x.b * a.K + x.k;
-    void* const o_out = (char*)a.o + item * R * H * 2;
-    float* const lse_out = a.lse + item * R;
-    const float vscale = a.v_scale ? __ldg(a.v_scale + x.k) : 1.0f;
-    // joined groups, by their first CTA: two of one kind (first of their item or
-    // not) are kJoinGroup CTAs apart or more
-    float* const first = a.group_partials + (int64_t)(x.c0 / kJoinGroup) * 2 * part;
-    JoinList<float> list{a.partials + (int64_t)f * 2 * part, 2 * part, f == x.c0 ? part : 0, 0, n};
-    float* dst = groups ? first + (int64_t)((f - x.c0) / kJoinGroup) * 2 * part + (f == x.c0 ? part : 0) : nullptr;
-    bool done = false;
-    while (true) {
-      join_partials<H, C::RING>(list, R, dst, o_out, lse_out, vscale, smem);
-      if (!groups || done) break;
-      const int m = (x.c1 - x.c0) / kJoinGroup + 1;
-      __syncthreads();
-      if (warp == 0) {
-        if (lane == 0) {
-          __threadfence();
-          *reinterpret_cast<volatile uint64_t*>(a.flags + f * 4 + (f == x.c0 ? 3 : 2)) = a.tag;
+  // partial 0 in slot 1 of its CTA, the others in slot 0 of theirs
+  const float* const base = a.partials + (int64_t)first * 2 * part;
+  float M = -INFINITY, L = 0.0f;
+  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (r < R) {
+    constexpr int U = 8;   // partials in flight
+    for (int p0 = share; p0 < n; p0 += U * shares) {
+      float4 y[U];
+      float m[U], l[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int p = p0 + u * shares;
+        m[u] = -INFINITY;
+        if (p < n) {
+          const float* const src = base + (p ? p * 2 : 1) * part;
+          y[u] = __ldcg(reinterpret_cast<const float4*>(src + r * H + d));
+          m[u] = __ldcg(src + R * H + r);
+          l[u] = __ldcg(src + R * H + R + r);
         }
-        __syncwarp();
-        asm volatile("fence.sc.gpu;" ::: "memory");
-        const bool last = all_arrived(JoinList<uint64_t>{a.flags + x.c0 * 4, 4 * kJoinGroup, 3, 2, m}, a.tag, false);
-        if (lane == 0) sh_last[i] = last;
       }
-      __syncthreads();
-      if (!sh_last[i]) break;
-      list = JoinList<float>{first, 2 * part, part, 0, m};
-      dst = nullptr;
-      done = true;
+      float mn = M;
+#pragma unroll
+      for (int u = 0; u < U; ++u) mn = fmaxf(mn, m[u]);
+      const float low = mn == -INFINITY ? 0.0f : mn, f0 = fast_exp2(M - low);
+      M = mn;
+      L *= f0;
+      x.x *= f0; x.y *= f0; x.z *= f0; x.w *= f0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (p0 + u * shares < n) {
+          const float f = fast_exp2(m[u] - low);
+          L += l[u] * f;
+          x.x += y[u].x * f;
+          x.y += y[u].y * f;
+          x.z += y[u].z * f;
+          x.w += y[u].w * f;
+        }
+      }
     }
-    __syncthreads();
   }
+  if (shares > 1) {
+    sx[threadIdx.x] = x;
+    sml[threadIdx.x] = make_float2(M, L);
+    __syncthreads();
+    if (share == 0) {
+      for (int w = 1; w < shares; ++w) M = fmaxf(M, sml[w * per + at].x);
+      const float low = M == -INFINITY ? 0.0f : M;
+      L = 0.0f;
+      x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int w = 0; w < shares; ++w) {
+        const float2 ml = sml[w * per + at];
+        const float4 y = sx[w * per + at];
+        const float f = fast_exp2(ml.x - low);
+        L += ml.y * f;
+        x.x += y.x * f;
+        x.y += y.y * f;
+        x.z += y.z * f;
+        x.w += y.w * f;
+      }
+    }
+  }
+  if (share == 0 && r < R)
+    put_result((char*)a.o + (int64_t)item * R * H * 2, a.lse + (int64_t)item * R, H, r, d, x, M, L,
+               a.v_scale ? a.v_scale[item % a.K] : 1.0f);
 }
 
 template <class C>
@@ -1036,7 +935,23 @@ cudaError_t launch_decode(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
     if (dev < 64) ready[dev] = true;
   }
   paged_decode_kernel<C><<<grid, warps * 32, smem, st>>>(a);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // Shares of an item's partials: enough that each has about eight, in flight at
+  // once (one kv head of 131072 keys, 304 partials: 47 us with two, 24 with 16).
+  const int items = a.B * a.K, partials = grid / items + 2;
+  int per = kJoinThreads;
+  while (per > 32 && kJoinThreads / per * 8 < partials) per /= 2;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(a.by_item ? items : grid, (a.G * a.T * (C::H / 4) + per - 1) / per);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<C::H>, a, per);
 }
 
 // Up to 8, 16 and (H <= 128: registers) 32 rows: warps on their own; more: a CTA's
