@@ -15,9 +15,14 @@ constexpr int kTablesThreads = 1024;
 
 // Request b holds ceil(c_b / P) pages and needs ceil((c_b + n_b) / P): two
 // exclusive sums over the requests (tokens, opened pages) place every token
-// and every page.  All lengths are read before anything is written, so the
-// outputs may replace the inputs; a call that cannot be met changes nothing.
-__global__ void __launch_bounds__(kTablesThreads) paged_tables_kernel(const PagedTablesArgs a) {
+// and every page.  A call that cannot be met changes nothing.
+//
+// Every CTA forms the sums for itself (8 bytes a request, a few microseconds at
+// 8192 requests) and then fills its share of the tokens; nothing is exchanged.
+// Where the outputs replace the inputs, all lengths have to be read before
+// anything is written: the CTAs are then one cluster, with its barrier between.
+template <bool IN_PLACE>
+__global__ void __launch_bounds__(kTablesThreads) paged_tables_kernel(const __grid_constant__ PagedTablesArgs a) {
   extern __shared__ int sm[];
   int* starts = sm;               // [B + 1] first token of each request
   int* cached = sm + a.B + 1;     // [B]
@@ -74,8 +79,12 @@ __global__ void __launch_bounds__(kTablesThreads) paged_tables_kernel(const Page
     }
     if (tid == 0) starts[a.B] = (int)all_tok;
   }
-  __syncthreads();
-  if (fail) {
+  if (IN_PLACE)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else
+    __syncthreads();
+  if (blockIdx.x != 0) {
+  } else if (fail) {
     for (int b = tid; b < a.B; b += kTablesThreads) a.total_lens[b] = a.cached_lens[b];
     for (int b = tid; b <= a.B; b += kTablesThreads) a.token_starts[b] = 0;
     if (tid == 0) {
@@ -88,7 +97,8 @@ __global__ void __launch_bounds__(kTablesThreads) paged_tables_kernel(const Page
     if (tid == 0) *a.free_used_out = used + (int)all_pg;
   }
   const int tokens = fail ? 0 : (int)all_tok;
-  for (int i = tid; i < a.max_tokens; i += kTablesThreads) {
+#pragma unroll 2
+  for (int i = blockIdx.x * kTablesThreads + tid; i < a.max_tokens; i += gridDim.x * kTablesThreads) {
     if (i >= tokens) {
       a.slots[i] = -1;
       if (a.positions) a.positions[i] = -1;
@@ -131,59 +141,102 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
-// One thread per 8 head dims of a key and of the value beside it.
-template <bool E4M3>
-__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const PagedAppendArgs a) {
-  const int vecs = a.H / 8;
-  const int64_t i = (int64_t)blockIdx.x * kAppendThreads + threadIdx.x;
-  if (i >= (int64_t)a.N * a.K * vecs) return;
-  const int u = (int)(i % vecs);
-  const int k = (int)(i / vecs % a.K);
-  const int64_t n = i / vecs / a.K;
-  const int64_t slot = a.slots[n];
-  if (slot < 0) return;   // padding
-  if (slot >> a.lay.page_shift >= a.lay.n_pages) {
-    atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
-    return;
-  }
-  const int64_t page = slot >> a.lay.page_shift, in = slot & ((1 << a.lay.page_shift) - 1);
-  const int64_t dst = page * a.lay.page + k * a.lay.head + in * a.lay.token;
-  const uint4 xk = *reinterpret_cast<const uint4*>((const char*)a.k + n * a.k_token + k * a.k_head + u * 16);
-  const uint4 xv = *reinterpret_cast<const uint4*>((const char*)a.v + n * a.v_token + k * a.v_head + u * 16);
-  if (!E4M3) {
-    *reinterpret_cast<uint4*>((char*)a.k_cache + dst + u * 16) = xk;
-    *reinterpret_cast<uint4*>((char*)a.v_cache + dst + u * 16) = xv;
-  } else {
-    auto squeeze = [](uint4 x, float s) {
-      const float2 p = unpack_bf16x2(x.x), q = unpack_bf16x2(x.y), r = unpack_bf16x2(x.z), t = unpack_bf16x2(x.w);
-      return make_uint2(pack_e4m3x4(p.x / s, p.y / s, q.x / s, q.y / s),
-                        pack_e4m3x4(r.x / s, r.y / s, t.x / s, t.y / s));
-    };
-    const float sk = a.k_scale ? a.k_scale[k] : 1.0f, sv = a.v_scale ? a.v_scale[k] : 1.0f;
-    *reinterpret_cast<uint2*>((char*)a.k_cache + dst + u * 8) = squeeze(xk, sk);
-    *reinterpret_cast<uint2*>((char*)a.v_cache + dst + u * 8) = squeeze(xv, sv);
+// A thread takes 8 head dims of a key and of the value beside it, `PER` of them
+// with all loads in flight before the first store; a CTA takes `tokens` tokens.
+template <bool E4M3, int PER>
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __grid_constant__ PagedAppendArgs a,
+                                                                      int tokens) {
+  const uint32_t vecs = a.H / 8, units = a.K * vecs;      // 16-byte units of a token
+  const int shift = a.H == 64 ? 3 : a.H == 128 ? 4 : 5;   // log2(vecs)
+  const int64_t n0 = (int64_t)blockIdx.x * tokens;
+  const uint32_t all = (uint32_t)min((int64_t)tokens, a.N - n0) * units;
+  for (uint32_t i0 = threadIdx.x; i0 < all; i0 += PER * kAppendThreads) {
+    uint4 xk[PER], xv[PER];
+    int64_t slot[PER];
+    uint32_t k[PER], u[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const uint32_t i = i0 + j * kAppendThreads;
+      slot[j] = -1;
+      if (i >= all) continue;
+      const uint32_t t = i / units, rest = i - t * units;
+      const int64_t n = n0 + t;
+      k[j] = rest >> shift;
+      u[j] = rest & (vecs - 1);
+      slot[j] = a.slots[n];
+      xk[j] = __ldg(reinterpret_cast<const uint4*>((const char*)a.k + n * a.k_token + k[j] * a.k_head + u[j] * 16));
+      xv[j] = __ldg(reinterpret_cast<const uint4*>((const char*)a.v + n * a.v_token + k[j] * a.v_head + u[j] * 16));
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      if (slot[j] < 0) continue;   // padding
+      const int64_t page = slot[j] >> a.lay.page_shift, in = slot[j] & ((1 << a.lay.page_shift) - 1);
+      if (page >= a.lay.n_pages) {
+        atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+        continue;
+      }
+      const int64_t dst = page * a.lay.page + k[j] * a.lay.head + in * a.lay.token;
+      if (!E4M3) {
+        *reinterpret_cast<uint4*>((char*)a.k_cache + dst + u[j] * 16) = xk[j];
+        *reinterpret_cast<uint4*>((char*)a.v_cache + dst + u[j] * 16) = xv[j];
+      } else {
+        auto squeeze = [](uint4 x, float s) {
+          const float2 p = unpack_bf16x2(x.x), q = unpack_bf16x2(x.y);
+          const float2 r = unpack_bf16x2(x.z), t = unpack_bf16x2(x.w);
+          return make_uint2(pack_e4m3x4(p.x / s, p.y / s, q.x / s, q.y / s),
+                            pack_e4m3x4(r.x / s, r.y / s, t.x / s, t.y / s));
+        };
+        const float sk = a.k_scale ? a.k_scale[k[j]] : 1.0f, sv = a.v_scale ? a.v_scale[k[j]] : 1.0f;
+        *reinterpret_cast<uint2*>((char*)a.k_cache + dst + u[j] * 8) = squeeze(xk[j], sk);
+        *reinterpret_cast<uint2*>((char*)a.v_cache + dst + u[j] * 8) = squeeze(xv[j], sv);
+      }
+    }
   }
 }
 
 }  // namespace
 
 cudaError_t launch_paged_tables(const PagedTablesArgs& a, cudaStream_t st) {
+  const bool in_place = a.total_lens == a.cached_lens || a.free_used_out == a.free_used;
+  auto* const kernel = in_place ? paged_tables_kernel<true> : paged_tables_kernel<false>;
   const size_t smem = (3 * (size_t)a.B + 1) * sizeof(int);
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        paged_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  paged_tables_kernel<<<1, kTablesThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  // Two tokens a thread: the searches and look-ups of a token are a chain of
+  // latencies (94000 tokens: 76 us in one CTA).  A cluster has at most 8 CTAs.
+  int ctas = 1;
+  while (ctas < (in_place ? 8 : 128) && ctas * 2 * kTablesThreads < a.max_tokens) ctas *= 2;
+  cudaLaunchAttribute cluster{};
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = in_place ? ctas : 1;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kTablesThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t st) {
-  const int64_t n = (int64_t)a.N * a.K * (a.H / 8);
-  const int64_t blocks = (n + kAppendThreads - 1) / kAppendThreads;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  if (a.e4m3) paged_append_kernel<true><<<(unsigned)blocks, kAppendThreads, 0, st>>>(a);
-  else paged_append_kernel<false><<<(unsigned)blocks, kAppendThreads, 0, st>>>(a);
+  const int64_t units = (int64_t)a.K * (a.H / 8), all = a.N * units;
+  // Four 16-byte pairs a thread once that fills the GPU (8 CTAs on each of its
+  // SMs), one below.
+  const bool four = all >= (int64_t)4 * kAppendThreads * 1216;
+  int64_t tokens = (four ? 4 : 1) * kAppendThreads / units;
+  if (tokens < 1) tokens = 1;
+  const unsigned blocks = (unsigned)((a.N + tokens - 1) / tokens);
+  if (a.e4m3) {
+    if (four) paged_append_kernel<true, 4><<<blocks, kAppendThreads, 0, st>>>(a, (int)tokens);
+    else paged_append_kernel<true, 1><<<blocks, kAppendThreads, 0, st>>>(a, (int)tokens);
+  } else {
+    if (four) paged_append_kernel<false, 4><<<blocks, kAppendThreads, 0, st>>>(a, (int)tokens);
+    else paged_append_kernel<false, 1><<<blocks, kAppendThreads, 0, st>>>(a, (int)tokens);
+  }
   return cudaGetLastError();
 }
 
