@@ -141,6 +141,12 @@ struct DecodePlace {
   int b, k, rem;
 };
 
+// Unit t of request b's.
+struct DecodeEnd {
+  int b, len;
+  long long t;
+};
+
 // The part of an item that a CTA does: tiles [begun, end) of its `tiles`.
 struct DecodeWalk {
   int b, k, len, first, tiles;   // first: key of tile 0, a multiple of CK
@@ -163,6 +169,10 @@ struct DecodeShape {
   __device__ __forceinline__ int first(int len) const { return low(len) & ~(C::CK - 1); }
   __device__ __forceinline__ int tiles(int len) const {
     return max(1, (len - first(len) + C::TK - 1) / C::TK);   // an empty item writes its zeros
+  }
+  __device__ __forceinline__ DecodePlace place(const DecodeEnd& e) const {
+    const int per_item = tiles(e.len) + kItemUnits, k = (int)quotient(e.t, per_item);
+    return DecodePlace{e.b, k, (int)(e.t - (long long)k * per_item)};
   }
   __device__ __forceinline__ void enter(DecodeWalk& w, int b, int k) const {
     w.b = b;
@@ -262,8 +272,9 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
   constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
   extern __shared__ __align__(1024) char smem[];
   __shared__ float sh_m[kDecodeWarps][16], sh_l[kDecodeWarps][16];
-  __shared__ long long sh_scan[9];
-  __shared__ DecodePlace sh_place[2];   // first and last unit
+  __shared__ long long sh_scan[8];
+  __shared__ float sh_down[NT * 8];     // what undoes the scaling of a query row
+  __shared__ DecodeEnd sh_ends[2];      // first and last unit
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   const int g = lane >> 2, c = lane & 3;
@@ -274,6 +285,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- this CTA's units
+  DecodePlace head;
+  DecodeWalk walk;
   {
     const int per = (a.B + threads - 1) / threads;
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
@@ -298,42 +311,43 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       if (w < warp) before += sh_scan[w];
       total += sh_scan[w];
     }
-    const int ctas = (int)min((long long)gridDim.x, total);
-    if (blockIdx.x >= ctas) {
-      if (tid == 0 && !a.by_item) a.splits[blockIdx.x] = PagedDecodeSplit{0, -1, 0, 0};
+    // CTA i: total / ctas units, and one more where i < total % ctas
+    const int ctas = (int)min((long long)gridDim.x, total), i = blockIdx.x;
+    if (i >= ctas) {
+      if (tid == 0 && !a.by_item) a.splits[i] = PagedDecodeSplit{0, -1, 0, 0};
       return;
     }
-    const long long t0 = quotient(blockIdx.x * total, ctas), t1 = quotient((blockIdx.x + 1) * total, ctas);
+    const long long each = quotient(total, ctas), over = total - each * ctas;
+    const long long t0 = i * each + min((long long)i, over), t1 = t0 + each + (i < over ? 1 : 0);
     const long long at = before + inc - mine;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {   // where this CTA's units begin and end
-      long long t = (i == 0 ? t0 : t1 - 1) - at;
-      if (t < 0 || t >= mine) continue;
+    if (t0 < at + mine && t1 - 1 >= at) {   // the requests that hold the first and the last unit
+      long long x = at;
       for (int b = b0; b < b1; ++b) {
-        const int tiles = shape.tiles(shape.length(b)), per_item = tiles + kItemUnits;
-        const long long x = (long long)per_item * a.K;
-        if (t < x) {
-          const int k = (int)quotient(t, per_item);
-          const int rem = (int)(t - (long long)k * per_item);
-          sh_place[i] = DecodePlace{b, k, rem};
-          if (i == 1) {
-            // the item that the units end in, where it begins here and goes on
-            // in the next CTA: for the join, with its last CTA
-            const long long first = t1 - 1 - rem + kItemUnits;   // its first tile's unit
-            const bool split = rem >= kItemUnits && rem + 1 < per_item && first >= t0;
-            if (split || !a.by_item)
-              a.splits[a.by_item ? b * a.K + k : blockIdx.x] = PagedDecodeSplit{
-                  b * a.K + k, split ? (int)blockIdx.x : -1, (int)quotient((first + tiles) * ctas - 1, total), 0};
-          }
-          break;
-        }
-        t -= x;
+        const int len = shape.length(b);
+        const long long next = x + (long long)(shape.tiles(len) + kItemUnits) * a.K;
+        if (t0 >= x && t0 < next) sh_ends[0] = DecodeEnd{b, len, t0 - x};
+        if (t1 - 1 >= x && t1 - 1 < next) sh_ends[1] = DecodeEnd{b, len, t1 - 1 - x};
+        x = next;
       }
     }
     __syncthreads();
+    head = shape.place(sh_ends[0]);
+    const DecodePlace tail = shape.place(sh_ends[1]);
+    if (tid == 32) {
+      // the item that the units end in, where it begins here and goes on in the
+      // next CTA: for the join, with its last CTA
+      const int tiles = shape.tiles(sh_ends[1].len);
+      const long long first = t1 - 1 - tail.rem + kItemUnits;   // its first tile's unit
+      const bool split = tail.rem >= kItemUnits && tail.rem + 1 < tiles + kItemUnits && first >= t0;
+      if (split || !a.by_item) {
+        const long long unit = first + tiles - 1, cut = over * (each + 1);
+        const long long last = unit < cut ? quotient(unit, each + 1) : over + quotient(unit - cut, each);
+        const int item = tail.b * a.K + tail.k;
+        a.splits[a.by_item ? item : i] = PagedDecodeSplit{item, split ? i : -1, (int)last, 0};
+      }
+    }
+    if (!shape.begin(walk, head, tail)) return;
   }
-  DecodeWalk walk;
-  if (!shape.begin(walk, sh_place[0], sh_place[1])) return;
   DecodeWalk ahead = walk;   // where the copies are
   bool more = true;
 
@@ -403,7 +417,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       }
     }
     cp_async_commit();
-    if (more && ++ahead.tile == ahead.end) more = shape.next_item(ahead, sh_place[0]);
+    if (more && ++ahead.tile == ahead.end) more = shape.next_item(ahead, head);
     look_up();
   };
   look_up();
@@ -468,27 +482,54 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     float sl2[NT][2];      // score to log2 units, per column
     const float kscale = a.k_scale ? __ldg(a.k_scale + walk.k) : 1.0f;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      uint2 x[KS];
-      if (EARLY) {
+    for (int nt = 0; nt < NT; ++nt) sl2[nt][0] = sl2[nt][1] = LOG2E;
+    if constexpr (C::QSMEM && !TEAM) {
+      // one copy for the CTA's warps, which take its n-tiles in turn
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) x[ks] = q_next[EARLY ? nt : 0][ks];
-      } else {
+      for (int nt = 0; nt < NT; ++nt) {
+        if (nt % kDecodeWarps != warp) continue;
+        uint2 x[KS];
         load_q(walk, nt, x);
+        if (E4M3) {
+          const float down = scale_q(x);
+          if (c == 0) sh_down[nt * 8 + g] = down;
+        }
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) q_sm[(ks * NT + nt) * 32 + lane] = x[ks];
       }
-      sl2[nt][0] = sl2[nt][1] = LOG2E;
+      __syncthreads();
       if (E4M3) {
-        const float down = scale_q(x);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) sl2[nt][j] = __shfl_sync(~0u, down, (2 * c + j) * 4) * kscale * LOG2E;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) sl2[nt][j] = sh_down[nt * 8 + 2 * c + j] * kscale * LOG2E;
+      }
+    } else {
+      uint2 x[NT][KS];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (EARLY) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) x[nt][ks] = q_next[EARLY ? nt : 0][ks];
+        } else {
+          load_q(walk, nt, x[nt]);
+        }
       }
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        if (!C::QSMEM) qf[C::QSMEM ? 0 : ks][nt] = x[ks];
-        else if (TEAM || (ks * NT + nt) % kDecodeWarps == warp) q_sm[(ks * NT + nt) * 32 + lane] = x[ks];
+      for (int nt = 0; nt < NT; ++nt) {
+        if (E4M3) {
+          const float down = scale_q(x[nt]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            sl2[nt][j] = __shfl_sync(~0u, down, (2 * c + j) * 4) * kscale * LOG2E;
+        }
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          if (C::QSMEM) q_sm[(ks * NT + nt) * 32 + lane] = x[nt][ks];
+          else qf[C::QSMEM ? 0 : ks][nt] = x[nt][ks];
+        }
       }
     }
-    if (C::QSMEM && !TEAM) __syncthreads();   // one copy for the CTA's warps
     // Keys that column (nt, j) keeps: [hi - window, hi)
     int col_hi[NT][2];
 #pragma unroll
@@ -720,7 +761,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       }
     const bool whole = walk.begun == 0 && walk.end == walk.tiles;
     DecodeWalk then = walk;
-    const bool go_on = shape.next_item(then, sh_place[0]);
+    const bool go_on = shape.next_item(then, head);
     if (EARLY && go_on) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) load_q(then, nt, q_next[EARLY ? nt : 0]);
