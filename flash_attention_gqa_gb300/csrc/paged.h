@@ -71,9 +71,8 @@ struct PagedDecodeArgs {
 };
 
 // Workspace of a decode: the splits, then partials, on a GPU with sm_count SMs.
-// CTAs an SM: as many as the rings leave room for.  Up to 16 query rows: two
-// up to H = 128, one at 256; more rows: two up to 64 rows (4 warps each) and H
-// = 128, else one.
+// CTAs an SM: two of 4 warps up to H = 128 and 32 query rows, else one (of 4 warps
+// at H = 256 up to 16 rows, of 8 with more rows): what rings and registers allow.
 struct PagedDecodePlan {
   int ctas;
   size_t partials;   // offset
@@ -85,7 +84,7 @@ __host__ __device__ inline int64_t paged_partial_floats(int R, int H) {
 }
 inline PagedDecodePlan paged_decode_plan(int R, int H, int sm_count) {
   PagedDecodePlan p;
-  p.ctas = sm_count * (H <= 128 && R <= 64 ? 2 : 1);
+  p.ctas = sm_count * (H <= 128 && R <= 32 ? 2 : 1);
   p.partials = ((size_t)p.ctas * sizeof(PagedDecodeSplit) + 255) & ~(size_t)255;
   p.total = p.partials + (((size_t)p.ctas * 2 * paged_partial_floats(R, H) * 4 + 255) & ~(size_t)255);
   return p;

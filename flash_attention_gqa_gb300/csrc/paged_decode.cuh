@@ -37,7 +37,6 @@
 
 namespace fa {
 
-constexpr int kDecodeWarps = 4;   // warps of a CTA whose warps stream alone
 
 // ------------------------------------------------------------- primitives
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -94,26 +93,33 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t
 }
 
 // ------------------------------------------------------------ configuration
-// NT: n-tiles of 8 query rows per warp.  TEAM: the CTA's warps share a ring.
-template <int H_, bool E4M3_, int NT_, bool TEAM_>
+// NT: n-tiles of 8 query rows per warp.  WR: warps of a team, which share a ring
+// and the keys in it, NT * 8 rows each.
+template <int H_, bool E4M3_, int NT_, int WR_>
 struct DecodeCfg {
-  static constexpr int H = H_, NT = NT_;
-  static constexpr bool E4M3 = E4M3_, TEAM = TEAM_;
+  static constexpr int H = H_, NT = NT_, WR = WR_;
+  static constexpr bool E4M3 = E4M3_, TEAM = WR > 1;
   static constexpr int ROWB = E4M3 ? H : 2 * H;        // bytes of a key
   static constexpr int UPR = ROWB / 16;                // 16-byte units of a key
-  static constexpr int CK = TEAM || E4M3 || H == 64 ? 32 : 16;   // keys of a ring slot
+  static constexpr int CK = E4M3 || H == 64 ? 32 : 16; // keys of a ring slot
   static constexpr int HALF = CK * ROWB;               // a slot holds K, then V
   static constexpr int SLOT = 2 * HALF;
-  static constexpr int TEAMS = TEAM ? 1 : kDecodeWarps;
+  static constexpr int WARPS = TEAM ? 8 : 4;
+  static constexpr int THREADS = WARPS * 32;
+  static constexpr int TEAMS = WARPS / WR;
   static constexpr int TK = TEAMS * CK;                // keys of a tile
+  static constexpr int ITEM_UNITS = 8 / TEAMS;         // an item's fixed cost, in tiles (below)
+  static constexpr bool QSMEM = TEAM || H * NT > 256;  // query fragments in shared memory
+  static constexpr int QTILES = WR * NT;
+  static constexpr int QBYTES = QSMEM ? H / 16 * QTILES * 32 * 8 : 0;
   // Streams of one warp: 24 KB of ring a warp up to H = 128 (two CTAs an SM,
-  // up to 128 KB of copies in flight on it), 48 KB at H = 256 (one CTA).
-  static constexpr int STAGES = TEAM ? 4 : (H == 256 ? 48 : 24) * 1024 / SLOT;
+  // up to 128 KB of copies in flight on it), 48 KB at H = 256 (one CTA).  Teams:
+  // what the queries leave of 212 KB.
+  static constexpr int STAGES = TEAM ? (212 * 1024 - QBYTES) / (TEAMS * SLOT) : (H == 256 ? 48 : 24) * 1024 / SLOT;
   static constexpr int RING = TEAMS * STAGES * SLOT;
-  static constexpr bool QSMEM = H * NT > 256;          // query fragments in shared memory
-  static constexpr int QBYTES = QSMEM ? H / 16 * NT * 32 * 8 : 0;   // TEAM: per warp
   static constexpr int MIN_CTAS = !TEAM && H <= 128 ? 2 : 1;
   static_assert(TEAM || (NT < 2 ? NT : 2) * 8 * H * 4 <= SLOT, "16 rows of a warp's O^T fit in a ring slot");
+  static_assert(!TEAM || 2 * 32 * H <= SLOT, "8 rows of two warps' O^T fit in a ring slot");
   static_assert(STAGES >= 3, "");
 };
 
@@ -127,10 +133,8 @@ __device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t u) {
 }
 
 // ------------------------------------------------------------------ the walk
-// The list that is dealt to the CTAs: per item (b, k) kItemUnits units that
+// The list that is dealt to the CTAs: per item (b, k) ITEM_UNITS units that
 // stand for its start and end, then one unit per tile.
-constexpr int kItemUnits = 2;
-
 // a / b for a, b >= 0: mostly in 32 bits, which takes a fraction of the time.
 __device__ __forceinline__ long long quotient(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
@@ -171,7 +175,7 @@ struct DecodeShape {
     return max(1, (len - first(len) + C::TK - 1) / C::TK);   // an empty item writes its zeros
   }
   __device__ __forceinline__ DecodePlace place(const DecodeEnd& e) const {
-    const int per_item = tiles(e.len) + kItemUnits, k = (int)quotient(e.t, per_item);
+    const int per_item = tiles(e.len) + C::ITEM_UNITS, k = (int)quotient(e.t, per_item);
     return DecodePlace{e.b, k, (int)(e.t - (long long)k * per_item)};
   }
   __device__ __forceinline__ void enter(DecodeWalk& w, int b, int k) const {
@@ -189,9 +193,9 @@ struct DecodeShape {
   __device__ __forceinline__ bool begin(DecodeWalk& w, const DecodePlace& h, const DecodePlace& e) const {
     const int between = (e.b - h.b) * a.K + e.k - h.k;   // items
     enter(w, e.b, e.k);
-    const int end = min(w.tiles, e.rem + 1 - kItemUnits);
+    const int end = min(w.tiles, e.rem + 1 - C::ITEM_UNITS);
     if (between == 0) {
-      w.tile = w.begun = max(0, h.rem - kItemUnits);
+      w.tile = w.begun = max(0, h.rem - C::ITEM_UNITS);
       w.end = end;
       w.todo = 0;
       w.tail = false;
@@ -205,7 +209,7 @@ struct DecodeShape {
   }
   __device__ __forceinline__ void head(DecodeWalk& w, const DecodePlace& h) const {
     enter(w, h.b, h.k);
-    w.tile = w.begun = max(0, h.rem - kItemUnits);
+    w.tile = w.begun = max(0, h.rem - C::ITEM_UNITS);
   }
   __device__ __forceinline__ bool next_item(DecodeWalk& w, const DecodePlace& h) const {
     if (w.tail) {
@@ -265,18 +269,20 @@ __device__ __forceinline__ void put_partial(float* dst, int H, int R, int r, int
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::TEAM ? 256 : kDecodeWarps * 32, C::MIN_CTAS)
+__global__ void __launch_bounds__(C::THREADS, C::MIN_CTAS)
 paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
   constexpr int H = C::H, NT = C::NT, CK = C::CK, KT = CK / 16, KS = H / 16, S = C::STAGES;
+  constexpr int WR = C::WR, WARPS = C::WARPS, threads = C::THREADS;
   constexpr bool E4M3 = C::E4M3, TEAM = C::TEAM;
   constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
   extern __shared__ __align__(1024) char smem[];
-  __shared__ float sh_m[kDecodeWarps][16], sh_l[kDecodeWarps][16];
+  __shared__ float sh_m[WARPS][16], sh_l[WARPS][16];
+  __shared__ float4 sh_ml[TEAM ? WARPS : 1][32];
   __shared__ long long sh_scan[8];
-  __shared__ float sh_down[NT * 8];     // what undoes the scaling of a query row
+  __shared__ float sh_down[C::QTILES * 8];     // what undoes the scaling of a query row
   __shared__ DecodeEnd sh_ends[2];      // first and last unit
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
   const int R = a.G * a.T;
   const DecodeShape<C> shape{a};
@@ -296,7 +302,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         const int n = a.lens[b];
         if (n != shape.length(b)) atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
       }
-      mine += (long long)(shape.tiles(shape.length(b)) + kItemUnits) * a.K;
+      mine += (long long)(shape.tiles(shape.length(b)) + C::ITEM_UNITS) * a.K;
     }
     long long inc = mine;
 #pragma unroll
@@ -324,7 +330,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       long long x = at;
       for (int b = b0; b < b1; ++b) {
         const int len = shape.length(b);
-        const long long next = x + (long long)(shape.tiles(len) + kItemUnits) * a.K;
+        const long long next = x + (long long)(shape.tiles(len) + C::ITEM_UNITS) * a.K;
         if (t0 >= x && t0 < next) sh_ends[0] = DecodeEnd{b, len, t0 - x};
         if (t1 - 1 >= x && t1 - 1 < next) sh_ends[1] = DecodeEnd{b, len, t1 - 1 - x};
         x = next;
@@ -337,8 +343,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       // the item that the units end in, where it begins here and goes on in the
       // next CTA: for the join, with its last CTA
       const int tiles = shape.tiles(sh_ends[1].len);
-      const long long first = t1 - 1 - tail.rem + kItemUnits;   // its first tile's unit
-      const bool split = tail.rem >= kItemUnits && tail.rem + 1 < tiles + kItemUnits && first >= t0;
+      const long long first = t1 - 1 - tail.rem + C::ITEM_UNITS;   // its first tile's unit
+      const bool split = tail.rem >= C::ITEM_UNITS && tail.rem + 1 < tiles + C::ITEM_UNITS && first >= t0;
       if (split || !a.by_item) {
         const long long unit = first + tiles - 1, cut = over * (each + 1);
         const long long last = unit < cut ? quotient(unit, each + 1) : over + quotient(unit - cut, each);
@@ -353,7 +359,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
 
   // ---- copies: lane r looks up key r of the next slot one slot early, then all
   // lanes copy 16-byte units of it
-  const int team = TEAM ? 0 : warp;
+  const int team = warp / WR, wr = warp % WR;
   char* const ring = smem + team * S * C::SLOT;
   const uint32_t ring_u = smem_u32(ring);
   int64_t key_off = -1;   // lane r: byte offset of key r of the slot to come, -1: zeros
@@ -395,7 +401,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         const char *pk = (const char*)a.k_cache + off, *pv = (const char*)a.v_cache + off;
 #pragma unroll
         for (int j = kt * NJ / KT; j < (kt + 1) * NJ / KT; ++j) {
-          if (!TEAM || j % (threads / 32) == warp) {
+          if (j % WR == wr) {
             const uint32_t d = (dst + lane_dst ^ swz_step(j)) + j * RPJ * C::ROWB;
             cp_async16(d, pk, 16);
             cp_async16(d + C::HALF, pv, 16);
@@ -407,7 +413,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     } else if (__any_sync(~0u, key_live)) {
 #pragma unroll 1
       for (int j = 0; j < NJ; ++j) {
-        if (TEAM && j % (threads / 32) != warp) continue;
+        if (j % WR != wr) continue;
         const int row = j * RPJ + lane / C::UPR, u = lane % C::UPR;
         const int64_t off = __shfl_sync(~0u, key_off, row);
         const uint32_t n = off >= 0 ? 16 : 0, d = dst + swz<C::UPR>(row, u);
@@ -426,12 +432,12 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
 
   // ---- items
   int cur = 0;
-  const int row0 = TEAM ? warp * NT * 8 : 0;   // first query row of this warp
-  uint2* const q_sm = reinterpret_cast<uint2*>(smem + C::RING + (TEAM ? warp : 0) * C::QBYTES);
-  const uint32_t q_u = smem_u32(q_sm + lane);
+  const int row0 = wr * NT * 8;   // first query row of this warp
+  uint2* const q_sm = reinterpret_cast<uint2*>(smem + C::RING);   // [ks][n-tile][lane]
+  const uint32_t q_u = smem_u32(q_sm + wr * NT * 32 + lane);
   // Query fragments: column n = lane / 4, dims as the key operand has them.
   auto load_q = [&](const DecodeWalk& w, int nt, uint2 (&x)[KS]) {
-    const int r = row0 + nt * 8 + g;
+    const int r = nt * 8 + g;
     const char* src = (const char*)a.q + (((int64_t)w.b * a.K + w.k) * R + r) * (H * 2);
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -470,7 +476,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
   };
   // The next item's queries are read while this one's results are written,
   // where registers allow it.
-  constexpr bool EARLY = NT * KS <= 16;
+  constexpr bool EARLY = !C::QSMEM && NT * KS <= 16;
   uint2 q_next[EARLY ? NT : 1][KS];
   if (EARLY) {
 #pragma unroll
@@ -483,11 +489,12 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     const float kscale = a.k_scale ? __ldg(a.k_scale + walk.k) : 1.0f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) sl2[nt][0] = sl2[nt][1] = LOG2E;
-    if constexpr (C::QSMEM && !TEAM) {
+    if constexpr (C::QSMEM) {
       // one copy for the CTA's warps, which take its n-tiles in turn
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        if (nt % kDecodeWarps != warp) continue;
+      for (int nt0 = 0; nt0 < C::QTILES; nt0 += WARPS) {
+        const int nt = nt0 + warp;
+        if (nt >= C::QTILES) continue;
         uint2 x[KS];
         load_q(walk, nt, x);
         if (E4M3) {
@@ -495,14 +502,14 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
           if (c == 0) sh_down[nt * 8 + g] = down;
         }
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) q_sm[(ks * NT + nt) * 32 + lane] = x[ks];
+        for (int ks = 0; ks < KS; ++ks) q_sm[(ks * C::QTILES + nt) * 32 + lane] = x[ks];
       }
       __syncthreads();
       if (E4M3) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) sl2[nt][j] = sh_down[nt * 8 + 2 * c + j] * kscale * LOG2E;
+          for (int j = 0; j < 2; ++j) sl2[nt][j] = sh_down[row0 + nt * 8 + 2 * c + j] * kscale * LOG2E;
       }
     } else {
       uint2 x[NT][KS];
@@ -525,8 +532,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         }
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          if (C::QSMEM) q_sm[(ks * NT + nt) * 32 + lane] = x[nt][ks];
-          else qf[C::QSMEM ? 0 : ks][nt] = x[nt][ks];
+          qf[C::QSMEM ? 0 : ks][nt] = x[nt][ks];
         }
       }
     }
@@ -551,7 +557,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
 
     for (; walk.tile < walk.end; ++walk.tile) {
       cp_async_wait<S - 2>();
-      if (TEAM) __syncthreads(); else __syncwarp();
+      if (TEAM) named_bar_sync(1 + team, WR * 32); else __syncwarp();
       {
         const int next = cur == 0 ? S - 1 : cur - 1;   // the slot of the chunk before: free
         issue(next);
@@ -562,191 +568,202 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       const int key0 = walk.first + (walk.tile * C::TEAMS + team) * CK;
       if (key0 >= walk.len) continue;   // this team has no keys in the tile
 
-      // S^T = K Q^T
-      float s[KT][NT][4];
+      // A slot's keys at once, or with many rows (registers) 16 at a time.
+      constexpr int KT2 = NT < 4 ? KT : 1;
+      constexpr bool TWO = NT < 4;
+#pragma unroll 1
+      for (int k0 = 0; k0 < CK; k0 += KT2 * 16) {
+        const int key1 = key0 + k0;
+        if (k0 && key1 >= walk.len) break;
+        const uint32_t k_u = ks_u + k0 * C::ROWB, v_u = vs_u + k0 * C::ROWB;
+        // S^T = K Q^T
+        float s[KT2][NT][4];
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        float s2[NT][4];   // a second chain of products where there is only one
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[kt][nt][i] = s2[nt][i] = 0.0f;
-        const uint32_t k_lane = ks_u + kt * 16 * C::ROWB + swz<C::UPR>(lane & 15, lane >> 4);
-#pragma unroll
-        for (int ks = 0; ks < KS; ks += E4M3 ? 2 : 1) {
-          uint32_t x[4];
-          ldsm4(k_lane ^ ((E4M3 ? ks : 2 * ks) << 4), x);
-          if (E4M3) {
-            uint32_t a0[4], a1[4];
-            e4m3x4_to_f16(x[0], a0[0], a0[2]);
-            e4m3x4_to_f16(x[1], a0[1], a0[3]);
-            e4m3x4_to_f16(x[2], a1[0], a1[2]);
-            e4m3x4_to_f16(x[3], a1[1], a1[3]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint2 q0 = C::QSMEM ? lds8(q_u + (ks * NT + nt) * 256) : qf[C::QSMEM ? 0 : ks][nt];
-              const uint2 q1 = C::QSMEM ? lds8(q_u + ((ks + 1) * NT + nt) * 256) : qf[C::QSMEM ? 0 : ks + 1][nt];
-              mma16816<true>(s[kt][nt], a0, q0.x, q0.y);
-              mma16816<true>(s2[nt], a1, q1.x, q1.y);
-            }
-          } else {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const uint2 q0 = C::QSMEM ? lds8(q_u + (ks * NT + nt) * 256) : qf[C::QSMEM ? 0 : ks][nt];
-              mma16816<false>(ks & 1 ? s2[nt] : s[kt][nt], x, q0.x, q0.y);
-            }
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[kt][nt][i] += s2[nt][i];
-      }
-      const bool masked = key0 < full_lo || key0 + CK > full_hi;
-      if (masked) {
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
+        for (int kt = 0; kt < KT2; ++kt) {
+          float s2[TWO ? NT : 1][4];   // a second chain of products where there are few
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int key = key0 + kt * 16 + g + (i >> 1) * 8, hi = col_hi[nt][i & 1];
-              if (key >= hi || (a.window > 0 && key < hi - a.window)) s[kt][nt][i] = -INFINITY;
+            for (int i = 0; i < 4; ++i) s[kt][nt][i] = s2[TWO ? nt : 0][i] = 0.0f;
+          const uint32_t k_lane = k_u + kt * 16 * C::ROWB + swz<C::UPR>(lane & 15, lane >> 4);
+#pragma unroll
+          for (int ks = 0; ks < KS; ks += E4M3 ? 2 : 1) {
+            uint32_t x[4];
+            ldsm4(k_lane ^ ((E4M3 ? ks : 2 * ks) << 4), x);
+            if (E4M3) {
+              uint32_t a0[4], a1[4];
+              e4m3x4_to_f16(x[0], a0[0], a0[2]);
+              e4m3x4_to_f16(x[1], a0[1], a0[3]);
+              e4m3x4_to_f16(x[2], a1[0], a1[2]);
+              e4m3x4_to_f16(x[3], a1[1], a1[3]);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint2 q0 = C::QSMEM ? lds8(q_u + (ks * C::QTILES + nt) * 256) : qf[C::QSMEM ? 0 : ks][nt];
+                const uint2 q1 = C::QSMEM ? lds8(q_u + ((ks + 1) * C::QTILES + nt) * 256) : qf[C::QSMEM ? 0 : ks + 1][nt];
+                mma16816<true>(s[kt][nt], a0, q0.x, q0.y);
+                mma16816<true>(TWO ? s2[TWO ? nt : 0] : s[kt][nt], a1, q1.x, q1.y);
+              }
+            } else {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint2 q0 = C::QSMEM ? lds8(q_u + (ks * C::QTILES + nt) * 256) : qf[C::QSMEM ? 0 : ks][nt];
+                mma16816<false>(TWO && (ks & 1) ? s2[TWO ? nt : 0] : s[kt][nt], x, q0.x, q0.y);
+              }
             }
-      }
-
-      // online softmax, per column
-      float alpha[NT][2];
-      bool moved = false;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float mx = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
-#pragma unroll
-          for (int kt = 1; kt < KT; ++kt) mx = fmaxf(mx, fmaxf(s[kt][nt][j], s[kt][nt][j + 2]));
-          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
-          const float mn = fmaxf(m[nt][j], mx * sl2[nt][j]);
-          const float base = mn == -INFINITY ? 0.0f : mn;
-          alpha[nt][j] = fast_exp2(m[nt][j] - base);
-          moved |= mn != m[nt][j];
-          m[nt][j] = mn;
-          float sum = 0.0f;
-#pragma unroll
-          for (int kt = 0; kt < KT; ++kt) {
-            s[kt][nt][j] = fast_exp2(fmaf(s[kt][nt][j], sl2[nt][j], -base));
-            s[kt][nt][j + 2] = fast_exp2(fmaf(s[kt][nt][j + 2], sl2[nt][j], -base));
-            sum += s[kt][nt][j] + s[kt][nt][j + 2];
           }
-          l[nt][j] = l[nt][j] * alpha[nt][j] + sum;
+          if (TWO) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s[kt][nt][i] += s2[TWO ? nt : 0][i];
+          }
         }
-      if (__any_sync(~0u, moved)) {
+        const bool masked = key1 < full_lo || key1 + KT2 * 16 > full_hi;
+        if (masked) {
 #pragma unroll
-        for (int ds = 0; ds < KS; ++ds)
+          for (int kt = 0; kt < KT2; ++kt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            o[ds][nt][0] *= alpha[nt][0];
-            o[ds][nt][1] *= alpha[nt][1];
-            o[ds][nt][2] *= alpha[nt][0];
-            o[ds][nt][3] *= alpha[nt][1];
-          }
-      }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int key = key1 + kt * 16 + g + (i >> 1) * 8, hi = col_hi[nt][i & 1];
+                if (key >= hi || (a.window > 0 && key < hi - a.window)) s[kt][nt][i] = -INFINITY;
+              }
+        }
 
-      // O^T += V^T P^T.  bf16 caches: the weights go in as two bf16 terms (their
-      // sum is off by 2^-17), so that o is rounded to bf16 once, at the end; the
-      // products are a quarter of the issue slots either way.  8-bit caches:
-      // one f16 term, off by 2^-12, against values of 2^-4.
-      uint32_t p[KT][NT][2], pl[KT][NT][2];
-#pragma unroll
-      for (int kt = 0; kt < KT; ++kt)
+        // online softmax, per column
+        float alpha[NT][2];
+        bool moved = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float x = s[kt][nt][2 * h], y = s[kt][nt][2 * h + 1];
-            if (E4M3) {
-              p[kt][nt][h] = transpose8x8(pack_f16x2(x, y));
-            } else {
-              const uint32_t hi = pack_bf16x2(x, y);
-              const float2 r = unpack_bf16x2(hi);
-              p[kt][nt][h] = transpose8x8(hi);
-              pl[kt][nt][h] = transpose8x8(pack_bf16x2(x - r.x, y - r.y));
+          for (int j = 0; j < 2; ++j) {
+            float mx = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
+#pragma unroll
+            for (int kt = 1; kt < KT2; ++kt) mx = fmaxf(mx, fmaxf(s[kt][nt][j], s[kt][nt][j + 2]));
+            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
+            const float mn = fmaxf(m[nt][j], mx * sl2[nt][j]);
+            const float base = mn == -INFINITY ? 0.0f : mn;
+            alpha[nt][j] = fast_exp2(m[nt][j] - base);
+            moved |= mn != m[nt][j];
+            m[nt][j] = mn;
+            float sum = 0.0f;
+#pragma unroll
+            for (int kt = 0; kt < KT2; ++kt) {
+              s[kt][nt][j] = fast_exp2(fmaf(s[kt][nt][j], sl2[nt][j], -base));
+              s[kt][nt][j + 2] = fast_exp2(fmaf(s[kt][nt][j + 2], sl2[nt][j], -base));
+              sum += s[kt][nt][j] + s[kt][nt][j + 2];
             }
+            l[nt][j] = l[nt][j] * alpha[nt][j] + sum;
           }
-      // Operand V^T of 16 keys and 16 dims (8-bit: 32 dims, two operands).
-      auto load_v = [&](int kt, int ds, uint32_t (&v0)[4], uint32_t (&v1)[4]) {
-        if (E4M3) {
-          uint32_t x[4];
-          ldsm4_trans((vs_u + kt * 16 * C::ROWB + swz<C::UPR>(lane & 15, lane >> 4)) ^ (ds << 4), x);
-          // bytes (key 2c: dims 2g, 2g+1), (key 2c+1: the same) -> pairs of keys per dim
+        if (__any_sync(~0u, moved)) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = __byte_perm(x[i], 0, 0x3120);
-          e4m3x4_to_f16(x[0], v0[0], v0[1]);
-          e4m3x4_to_f16(x[1], v0[2], v0[3]);
-          e4m3x4_to_f16(x[2], v1[0], v1[1]);
-          e4m3x4_to_f16(x[3], v1[2], v1[3]);
-        } else {
-          ldsm4_trans((vs_u + kt * 16 * C::ROWB +
-                       swz<C::UPR>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1)) ^ (ds << 5), v0);
+          for (int ds = 0; ds < KS; ++ds)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              o[ds][nt][0] *= alpha[nt][0];
+              o[ds][nt][1] *= alpha[nt][1];
+              o[ds][nt][2] *= alpha[nt][0];
+              o[ds][nt][3] *= alpha[nt][1];
+            }
         }
-      };
-      auto add_v = [&](float (&d)[4], const uint32_t (&v)[4], int kt, int nt) {
-        mma16816<E4M3>(d, v, p[kt][nt][0], p[kt][nt][1]);
-        if (!E4M3) mma16816<E4M3>(d, v, pl[kt][nt][0], pl[kt][nt][1]);
-      };
-      if (masked && a.T > 1 && any_not_finite<E4M3>(vs_p, C::HALF, lane)) {
-        // Some column does not keep a key whose value is an infinity or NaN, and
-        // 0 x inf would reach it: each query position gets its own products, the
-        // keys that it does not keep zeroed, and takes its columns of them.
-#pragma unroll 1
-        for (int t = 0; t < a.T; ++t) {
-          const int hi = full_hi + t, lo = a.window > 0 ? hi - a.window : 0;
+
+        // O^T += V^T P^T.  bf16 caches: the weights go in as two bf16 terms (their
+        // sum is off by 2^-17), so that o is rounded to bf16 once, at the end; the
+        // products are a quarter of the issue slots either way.  8-bit caches:
+        // one f16 term, off by 2^-12, against values of 2^-4.
+        uint32_t p[KT2][NT][2], pl[KT2][NT][2];
 #pragma unroll
-          for (int kt = 0; kt < KT; ++kt) {
-            uint32_t keep[2];   // of keys 2c, 2c + 1 and those + 8, as halves
+        for (int kt = 0; kt < KT2; ++kt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const int key = key0 + kt * 16 + 2 * c + 8 * h;
-              keep[h] = (key >= lo && key < hi ? 0xffffu : 0u) |
-                        (key + 1 >= lo && key + 1 < hi ? 0xffff0000u : 0u);
+              const float x = s[kt][nt][2 * h], y = s[kt][nt][2 * h + 1];
+              if (E4M3) {
+                p[kt][nt][h] = transpose8x8(pack_f16x2(x, y));
+              } else {
+                const uint32_t hi = pack_bf16x2(x, y);
+                const float2 r = unpack_bf16x2(hi);
+                p[kt][nt][h] = transpose8x8(hi);
+                pl[kt][nt][h] = transpose8x8(pack_bf16x2(x - r.x, y - r.y));
+              }
             }
+        // Operand V^T of 16 keys and 16 dims (8-bit: 32 dims, two operands).
+        auto load_v = [&](int kt, int ds, uint32_t (&v0)[4], uint32_t (&v1)[4]) {
+          if (E4M3) {
+            uint32_t x[4];
+            ldsm4_trans((v_u + kt * 16 * C::ROWB + swz<C::UPR>(lane & 15, lane >> 4)) ^ (ds << 4), x);
+            // bytes (key 2c: dims 2g, 2g+1), (key 2c+1: the same) -> pairs of keys per dim
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = __byte_perm(x[i], 0, 0x3120);
+            e4m3x4_to_f16(x[0], v0[0], v0[1]);
+            e4m3x4_to_f16(x[1], v0[2], v0[3]);
+            e4m3x4_to_f16(x[2], v1[0], v1[1]);
+            e4m3x4_to_f16(x[3], v1[2], v1[3]);
+          } else {
+            ldsm4_trans((v_u + kt * 16 * C::ROWB +
+                         swz<C::UPR>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1)) ^ (ds << 5), v0);
+          }
+        };
+        auto add_v = [&](float (&d)[4], const uint32_t (&v)[4], int kt, int nt) {
+          mma16816<E4M3>(d, v, p[kt][nt][0], p[kt][nt][1]);
+          if (!E4M3) mma16816<E4M3>(d, v, pl[kt][nt][0], pl[kt][nt][1]);
+        };
+        if (masked && a.T > 1 && any_not_finite<E4M3>(vs_p + k0 * C::ROWB, KT2 * 16 * C::ROWB, lane)) {
+          // Some column does not keep a key whose value is an infinity or NaN, and
+          // 0 x inf would reach it: each query position gets its own products, the
+          // keys that it does not keep zeroed, and takes its columns of them.
+#pragma unroll 1
+          for (int t = 0; t < a.T; ++t) {
+            const int hi = full_hi + t, lo = a.window > 0 ? hi - a.window : 0;
+#pragma unroll
+            for (int kt = 0; kt < KT2; ++kt) {
+              uint32_t keep[2];   // of keys 2c, 2c + 1 and those + 8, as halves
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int key = key1 + kt * 16 + 2 * c + 8 * h;
+                keep[h] = (key >= lo && key < hi ? 0xffffu : 0u) |
+                          (key + 1 >= lo && key + 1 < hi ? 0xffff0000u : 0u);
+              }
+#pragma unroll
+              for (int ds = 0; ds < KS; ds += E4M3 ? 2 : 1) {
+                uint32_t v[2][4];
+                load_v(kt, ds, v[0], v[1]);
+#pragma unroll
+                for (int i = 0; i < (E4M3 ? 2 : 1); ++i) {
+                  v[i][0] &= keep[0];
+                  v[i][1] &= keep[0];
+                  v[i][2] &= keep[1];
+                  v[i][3] &= keep[1];
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) {
+                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    add_v(d, v[i], kt, nt);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                      if (col_hi[nt][e & 1] == hi) o[ds + i][nt][e] += d[e];
+                  }
+                }
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int kt = 0; kt < KT2; ++kt)
 #pragma unroll
             for (int ds = 0; ds < KS; ds += E4M3 ? 2 : 1) {
               uint32_t v[2][4];
               load_v(kt, ds, v[0], v[1]);
 #pragma unroll
-              for (int i = 0; i < (E4M3 ? 2 : 1); ++i) {
-                v[i][0] &= keep[0];
-                v[i][1] &= keep[0];
-                v[i][2] &= keep[1];
-                v[i][3] &= keep[1];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                  add_v(d, v[i], kt, nt);
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    if (col_hi[nt][e & 1] == hi) o[ds + i][nt][e] += d[e];
-                }
+              for (int nt = 0; nt < NT; ++nt) {
+                add_v(o[ds][nt], v[0], kt, nt);
+                if (E4M3) add_v(o[ds + (E4M3 ? 1 : 0)][nt], v[1], kt, nt);
               }
             }
-          }
         }
-      } else {
-#pragma unroll
-        for (int kt = 0; kt < KT; ++kt)
-#pragma unroll
-          for (int ds = 0; ds < KS; ds += E4M3 ? 2 : 1) {
-            uint32_t v[2][4];
-            load_v(kt, ds, v[0], v[1]);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              add_v(o[ds][nt], v[0], kt, nt);
-              if (E4M3) add_v(o[ds + (E4M3 ? 1 : 0)][nt], v[1], kt, nt);
-            }
-          }
       }
     }
 
@@ -811,18 +828,18 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         }
         __syncthreads();
         const int rows = min(NR * 8, R - n0 * 8);
-        for (int i = tid; i < rows * (H / 4); i += kDecodeWarps * 32) {
+        for (int i = tid; i < rows * (H / 4); i += threads) {
           const int r = i / (H / 4), d = i % (H / 4) * 4;
           float M = sh_m[0][r], L = 0.0f;
 #pragma unroll
-          for (int w = 1; w < kDecodeWarps; ++w) M = fmaxf(M, sh_m[w][r]);
+          for (int w = 1; w < WARPS; ++w) M = fmaxf(M, sh_m[w][r]);
           const float base = M == -INFINITY ? 0.0f : M;
           float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           // every warp's ring has the same slot at the same place
           const float* at = reinterpret_cast<const float*>(smem + ((const char*)so - ring)) + r * H +
                             (d ^ (((r >> 1) & 3) << 3));
 #pragma unroll
-          for (int w = 0; w < kDecodeWarps; ++w) {
+          for (int w = 0; w < WARPS; ++w) {
             const float f = fast_exp2(sh_m[w][r] - base);
             const float4 y = *reinterpret_cast<const float4*>(at + w * (S * C::SLOT / 4));
             L += sh_l[w][r] * f;
@@ -836,35 +853,95 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         __syncthreads();
       }
     } else {
-      // straight from the registers: the rows are this warp's alone
+      // Teams are joined in pairs, an n-tile at a time: a lane of the one adds
+      // what the same lane of the other left in the slots just used.
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int step = C::TEAMS / 2; step; step /= 2) {
+        const int index = (team - step) * WR + wr, from = index + step * WR;   // of the writer, here and there
+        auto area = [&](int i) {
+          return reinterpret_cast<float4*>(smem + (step + i / 2) % (2 * step) * S * C::SLOT + ((char*)so - ring) +
+                                           i % 2 * 32 * H) + lane;
+        };
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int r = row0 + nt * 8 + 2 * c + j;
-          if (r >= R) continue;
-          const float L = l[nt][j], M = m[nt][j], f = L == 0.0f ? 0.0f : vscale / L;
+        for (int nt = 0; nt < NT; ++nt) {
+          __syncthreads();
+          if (team >= step && team < 2 * step) {
+            float4* const dst = area(index);
 #pragma unroll
-          for (int ds = 0; ds < KS; ++ds) {
-            const int d0 = ds * 16 + (E4M3 ? 2 * g : g), d1 = d0 + (E4M3 ? 1 : 8);
-            if (whole) {
-              __nv_bfloat16* const dst = (__nv_bfloat16*)a.o + (out_row + r) * H;
-              dst[d0] = __float2bfloat16(o[ds][nt][j] * f);
-              dst[d1] = __float2bfloat16(o[ds][nt][j + 2] * f);
-            } else {
-              mine[(int64_t)r * H + d0] = o[ds][nt][j];
-              mine[(int64_t)r * H + d1] = o[ds][nt][j + 2];
-            }
+            for (int ds = 0; ds < KS; ++ds)
+              dst[ds * 32] = make_float4(o[ds][nt][0], o[ds][nt][1], o[ds][nt][2], o[ds][nt][3]);
+            sh_ml[warp][lane] = make_float4(m[nt][0], m[nt][1], l[nt][0], l[nt][1]);
           }
-          if (g == 0) {
-            if (whole) {
-              a.lse[out_row + r] = (M + log2f(L)) * LN2;
-            } else {
-              mine[(int64_t)R * H + r] = M;
-              mine[(int64_t)R * (H + 1) + r] = L;
+          __syncthreads();
+          if (team < step) {
+            const float4* const src = area(from);
+            const float4 ml = sh_ml[warp + step * WR][lane];
+            const float other[2] = {ml.x, ml.y}, sum[2] = {ml.z, ml.w};
+            float f[2], h[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float mn = fmaxf(m[nt][j], other[j]), base = mn == -INFINITY ? 0.0f : mn;
+              f[j] = fast_exp2(m[nt][j] - base);
+              h[j] = fast_exp2(other[j] - base);
+              m[nt][j] = mn;
+              l[nt][j] = l[nt][j] * f[j] + sum[j] * h[j];
+            }
+#pragma unroll
+            for (int ds = 0; ds < KS; ++ds) {
+              const float4 y = src[ds * 32];
+              o[ds][nt][0] = o[ds][nt][0] * f[0] + y.x * h[0];
+              o[ds][nt][1] = o[ds][nt][1] * f[1] + y.y * h[1];
+              o[ds][nt][2] = o[ds][nt][2] * f[0] + y.z * h[0];
+              o[ds][nt][3] = o[ds][nt][3] * f[1] + y.w * h[1];
             }
           }
         }
+      }
+      __syncthreads();
+      if (team == 0) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float f[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int r = row0 + nt * 8 + 2 * c + j;
+            const float L = l[nt][j], M = m[nt][j];
+            f[j] = L == 0.0f ? 0.0f : vscale / L;
+            if (r >= R) continue;
+            if (whole) {
+              if (g == 0) a.lse[out_row + r] = (M + log2f(L)) * LN2;
+            } else {
+              if (g == 0) {
+                mine[(int64_t)R * H + r] = M;
+                mine[(int64_t)R * (H + 1) + r] = L;
+              }
+#pragma unroll
+              for (int ds = 0; ds < KS; ++ds) {
+                const int d0 = ds * 16 + (E4M3 ? 2 * g : g), d1 = d0 + (E4M3 ? 1 : 8);
+                mine[(int64_t)r * H + d0] = o[ds][nt][j];
+                mine[(int64_t)r * H + d1] = o[ds][nt][j + 2];
+              }
+            }
+          }
+          if (whole) {   // transposed: row g, dims in pairs
+            const int r = row0 + nt * 8 + g;
+            char* const dst = (char*)a.o + (out_row + r) * (H * 2);
+#pragma unroll
+            for (int ds = 0; ds < KS; ++ds) {
+              const uint32_t x = transpose8x8(pack_bf16x2(o[ds][nt][0] * f[0], o[ds][nt][1] * f[1]));
+              const uint32_t y = transpose8x8(pack_bf16x2(o[ds][nt][2] * f[0], o[ds][nt][3] * f[1]));
+              if (r >= R) continue;
+              if (E4M3) {   // x: dims 4c and 4c + 2, y: dims 4c + 1 and 4c + 3
+                *reinterpret_cast<uint2*>(dst + ds * 32 + c * 8) =
+                    make_uint2(__byte_perm(x, y, 0x5410), __byte_perm(x, y, 0x7632));
+              } else {
+                *reinterpret_cast<uint32_t*>(dst + ds * 32 + c * 4) = x;
+                *reinterpret_cast<uint32_t*>(dst + ds * 32 + 16 + c * 4) = y;
+              }
+            }
+          }
+        }
+      }
     }
 
     if (whole && a.by_item && tid == 0) a.splits[item] = PagedDecodeSplit{(int)item, -1, 0, 0};
@@ -963,19 +1040,17 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 
 template <class C>
 cudaError_t launch_decode(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
-  const int warps = C::TEAM ? (a.G * a.T + C::NT * 8 - 1) / (C::NT * 8) : kDecodeWarps;
-  const size_t smem = C::RING + (size_t)(C::TEAM ? warps : 1) * C::QBYTES;
+  constexpr size_t smem = C::RING + C::QBYTES;
   static bool ready[64] = {};   // per device; setting it twice is harmless
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !ready[dev]) {
-    const size_t most = C::RING + (size_t)(C::TEAM ? kMaxPagedRows / (C::NT * 8) : 1) * C::QBYTES;
-    e = cudaFuncSetAttribute(paged_decode_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    e = cudaFuncSetAttribute(paged_decode_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev] = true;
   }
-  paged_decode_kernel<C><<<grid, warps * 32, smem, st>>>(a);
+  paged_decode_kernel<C><<<grid, C::THREADS, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // Shares of an item's partials: enough that each has about eight, in flight at
@@ -995,16 +1070,21 @@ cudaError_t launch_decode(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, paged_join_kernel<C::H>, a, per);
 }
 
-// Up to 8, 16 and (H <= 128: registers) 32 rows: warps on their own; more: a CTA's
-// warps share the keys.
+// Up to 8, 16 and (H <= 128: registers) 32 rows: warps on their own; more: teams.
 template <int H, bool E4M3>
 cudaError_t launch_decode_rows(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
   const int R = a.G * a.T;
-  if (R <= 8) return launch_decode<DecodeCfg<H, E4M3, 1, false>>(a, grid, st);
-  if (R <= 16) return launch_decode<DecodeCfg<H, E4M3, 2, false>>(a, grid, st);
-  if constexpr (H <= 128)
-    if (R <= 32) return launch_decode<DecodeCfg<H, E4M3, 4, false>>(a, grid, st);
-  return launch_decode<DecodeCfg<H, E4M3, 2, true>>(a, grid, st);
+  if (R <= 8) return launch_decode<DecodeCfg<H, E4M3, 1, 1>>(a, grid, st);
+  if (R <= 16) return launch_decode<DecodeCfg<H, E4M3, 2, 1>>(a, grid, st);
+  if constexpr (H <= 128) {
+    if (R <= 32) return launch_decode<DecodeCfg<H, E4M3, 4, 1>>(a, grid, st);
+    if (R <= 64) return launch_decode<DecodeCfg<H, E4M3, 4, 2>>(a, grid, st);
+    return launch_decode<DecodeCfg<H, E4M3, 4, 4>>(a, grid, st);
+  } else {
+    if (R <= 32) return launch_decode<DecodeCfg<H, E4M3, 2, 2>>(a, grid, st);
+    if (R <= 64) return launch_decode<DecodeCfg<H, E4M3, 2, 4>>(a, grid, st);
+    return launch_decode<DecodeCfg<H, E4M3, 2, 8>>(a, grid, st);
+  }
 }
 
 }  // namespace fa
