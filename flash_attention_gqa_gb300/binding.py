@@ -277,48 +277,49 @@ def fa_bwd_masked(q, k, v, o, lse, dO, seg_q, seg_kv, causal, mask, dq, dk, dv, 
 # strides whose innermost is 1; [n_pages, page_size, K, H] memory is passed as its
 # transpose(1, 2).  Work goes to the tensors' own device.
 
-def _dense(t: torch.Tensor, dtype, shape, index: int, name: str) -> int:
-    """Address of a dense tensor of the given type and shape on CUDA device `index`."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
-                         f"on cuda:{index}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+# These calls are a few microseconds of GPU work, so their checks are written for
+# few Python operations: sizes by numel of contiguous tensors, types by identity.
+
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream   # its address; a Stream object costs 2 us
+_BF16, _I32, _I64, _F32, _E4M3 = (torch.bfloat16, torch.int32, torch.int64, torch.float32,
+                                  torch.float8_e4m3fn)
+
+
+def _dense(t: torch.Tensor, dtype, n: int, index: int, name: str) -> int:
+    """Address of a contiguous tensor of n values of `dtype` on CUDA device `index`."""
+    if (t.dtype is not dtype or t.numel() != n or t.get_device() != index
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} values on "
+                         f"cuda:{index}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
 def _paged_cache(k_cache, v_cache, k_scale, v_scale, K: int, H: int, index: int):
-    """(cache type, strides, k_scale address, v_scale address) of a checked cache pair."""
-    P, Kc, page, Hc = k_cache.shape
-    if (Kc, Hc) != (K, H) or v_cache.shape != k_cache.shape:
+    """(cache type, shape, strides, k_scale and v_scale addresses) of a checked cache pair."""
+    shape, stride, dtype = k_cache.shape, k_cache.stride(), k_cache.dtype
+    if len(shape) != 4 or shape[1] != K or shape[3] != H or v_cache.shape != shape:
         raise ValueError(f"k_cache and v_cache must be [n_pages, {K}, page_size, {H}], "
-                         f"got {tuple(k_cache.shape)} and {tuple(v_cache.shape)}")
-    stride = k_cache.stride()
+                         f"got {tuple(shape)} and {tuple(v_cache.shape)}")
     if (stride[3] != 1 or v_cache.stride() != stride) and k_cache.numel():
         raise ValueError("k_cache and v_cache must have the same strides, innermost 1")
     if k_cache.get_device() != index or v_cache.get_device() != index or index < 0:
         raise ValueError("k_cache and v_cache must be on the CUDA device of the other tensors")
-    dtype = k_cache.dtype
     if v_cache.dtype is not dtype:
         raise ValueError("k_cache and v_cache must have one type")
-    if dtype is torch.bfloat16:
+    if dtype is _BF16:
         if k_scale is not None or v_scale is not None:
             raise ValueError("a bfloat16 cache takes no scales")
-        return FA_CACHE_BF16, stride, None, None
-    if dtype is not torch.float8_e4m3fn:
+        return FA_CACHE_BF16, shape, stride, None, None
+    if dtype is not _E4M3:
         raise ValueError(f"the cache must be bfloat16 or float8_e4m3fn, got {dtype}")
-    return (FA_CACHE_E4M3, stride,
-            None if k_scale is None else _dense(k_scale, torch.float32, (K,), index, "k_scale"),
-            None if v_scale is None else _dense(v_scale, torch.float32, (K,), index, "v_scale"))
+    return (FA_CACHE_E4M3, shape, stride,
+            None if k_scale is None else _dense(k_scale, _F32, K, index, "k_scale"),
+            None if v_scale is None else _dense(v_scale, _F32, K, index, "v_scale"))
 
 
-def _raw_stream(stream, index: int) -> int:
-    if stream is None:   # the address alone: a Stream object costs 2 us
-        return torch._C._cuda_getCurrentRawStream(index)
+def _raw_stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _elsewhere(index: int) -> bool:
-    """Whether CUDA device `index` is not the current one."""
-    return index >= 0 and index != torch.cuda.current_device()
 
 
 def fa_paged_tables(cached_lens, new_lens, free_pages, free_used, block_table, total_lens,
@@ -329,28 +330,28 @@ def fa_paged_tables(cached_lens, new_lens, free_pages, free_used, block_table, t
     dev = cached_lens.get_device()
     if dev < 0:
         raise ValueError("cached_lens must be a CUDA tensor")
-    if _elsewhere(dev):
+    if dev != _current_device():
         with torch.cuda.device(dev):
             return fa_paged_tables(cached_lens, new_lens, free_pages, free_used, block_table,
                                    total_lens, token_starts, slots, positions, free_used_out,
                                    n_pages, page_size, stream, check)
-    i32, one = torch.int32, (1,)
-    B, tokens, n_free = cached_lens.shape[0], slots.shape[0], free_pages.shape[0]
-    max_pages = block_table.shape[1]
-    rows = (B,)
+    B, tokens, n_free = cached_lens.numel(), slots.numel(), free_pages.numel()
+    rows, max_pages = block_table.shape
+    if rows != B:
+        raise ValueError(f"block_table must have {B} rows, got {rows}")
     rc = (_lib or load()).fa_paged_tables(
-        _dense(cached_lens, i32, rows, dev, "cached_lens"),
-        _dense(new_lens, i32, rows, dev, "new_lens"),
-        _dense(free_pages, i32, (n_free,), dev, "free_pages"), n_free,
-        _dense(free_used, i32, one, dev, "free_used"),
-        _dense(block_table, i32, (B, max_pages), dev, "block_table"), max_pages,
-        _dense(total_lens, i32, rows, dev, "total_lens"),
-        _dense(token_starts, i32, (B + 1,), dev, "token_starts"),
-        _dense(slots, torch.int64, (tokens,), dev, "slots"),
-        None if positions is None else _dense(positions, i32, (tokens,), dev, "positions"), tokens,
-        _dense(free_used_out, i32, one, dev, "free_used_out"),
-        B, n_pages, page_size, _raw_stream(stream, dev))
-    if check:
+        _dense(cached_lens, _I32, B, dev, "cached_lens"),
+        _dense(new_lens, _I32, B, dev, "new_lens"),
+        _dense(free_pages, _I32, n_free, dev, "free_pages"), n_free,
+        _dense(free_used, _I32, 1, dev, "free_used"),
+        _dense(block_table, _I32, B * max_pages, dev, "block_table"), max_pages,
+        _dense(total_lens, _I32, B, dev, "total_lens"),
+        _dense(token_starts, _I32, B + 1, dev, "token_starts"),
+        _dense(slots, _I64, tokens, dev, "slots"),
+        None if positions is None else _dense(positions, _I32, tokens, dev, "positions"), tokens,
+        _dense(free_used_out, _I32, 1, dev, "free_used_out"), B, n_pages, page_size,
+        _current_stream(dev) if stream is None else _raw_stream(stream))
+    if rc and check:
         _check("fa_paged_tables", rc)
     return rc
 
@@ -359,22 +360,22 @@ def fa_paged_append(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, s
                     check=True) -> int:
     """Write k, v [N, K, H] (bf16, any token and head strides) into the pages of `slots`."""
     dev = k.get_device()
-    if _elsewhere(dev):
+    if dev >= 0 and dev != _current_device():
         with torch.cuda.device(dev):
             return fa_paged_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream, check)
     N, K, H = shape = k.shape
-    sk, sv, bf16 = k.stride(), v.stride(), torch.bfloat16
-    if (k.dtype is not bf16 or v.dtype is not bf16 or v.shape != shape or v.get_device() != dev
+    sk, sv = k.stride(), v.stride()
+    if (k.dtype is not _BF16 or v.dtype is not _BF16 or v.shape != shape or v.get_device() != dev
             or ((sk[2] != 1 or sv[2] != 1) and k.numel())):
         raise ValueError("k and v must be bfloat16 tensors of one shape [N, K, H] on one device, "
                          "innermost stride 1")
-    kind, st, ks, vs = _paged_cache(k_cache, v_cache, k_scale, v_scale, K, H, dev)
-    n_pages, _, page, _ = k_cache.shape
+    kind, cs, st, ks, vs = _paged_cache(k_cache, v_cache, k_scale, v_scale, K, H, dev)
     rc = (_lib or load()).fa_paged_append(
         k.data_ptr(), v.data_ptr(), sk[0], sk[1], sv[0], sv[1],
-        _dense(slots, torch.int64, (N,), dev, "slots"), k_cache.data_ptr(), v_cache.data_ptr(),
-        kind, ks, vs, st[0], st[1], st[2], N, K, H, n_pages, page, _raw_stream(stream, dev))
-    if check:
+        _dense(slots, _I64, N, dev, "slots"), k_cache.data_ptr(), v_cache.data_ptr(), kind, ks, vs,
+        st[0], st[1], st[2], N, K, H, cs[0], cs[2],
+        _current_stream(dev) if stream is None else _raw_stream(stream))
+    if rc and check:
         _check("fa_paged_append", rc)
     return rc
 
@@ -383,27 +384,28 @@ def fa_paged_decode(q, k_cache, v_cache, block_table, lens, o, lse, workspace, k
                     v_scale=None, window=0, stream=None, check=True) -> int:
     """Attention of q [B, K, G, T, H], each request's T newest tokens, over its pages."""
     dev = q.get_device()
-    if _elsewhere(dev):
+    if dev >= 0 and dev != _current_device():
         with torch.cuda.device(dev):
             return fa_paged_decode(q, k_cache, v_cache, block_table, lens, o, lse, workspace,
                                    k_scale, v_scale, window, stream, check)
-    B, K, G, T, H = shape = q.shape
-    kind, st, ks, vs = _paged_cache(k_cache, v_cache, k_scale, v_scale, K, H, dev)
-    n_pages, _, page, _ = k_cache.shape
-    max_pages = block_table.shape[1]
+    B, K, G, T, H = q.shape
+    rows = B * K * G * T
+    kind, cs, st, ks, vs = _paged_cache(k_cache, v_cache, k_scale, v_scale, K, H, dev)
+    requests, max_pages = block_table.shape
+    if requests != B:
+        raise ValueError(f"block_table must have {B} rows, got {requests}")
     ws, ws_bytes = None, 0
     if workspace is not None:
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    bf16, i32 = torch.bfloat16, torch.int32
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
     rc = (_lib or load()).fa_paged_decode(
-        _dense(q, bf16, shape, dev, "q"), k_cache.data_ptr(), v_cache.data_ptr(), kind,
-        ks, vs, st[0], st[1], st[2], _dense(block_table, i32, (B, max_pages), dev, "block_table"),
-        _dense(lens, i32, (B,), dev, "lens"), window, _dense(o, bf16, shape, dev, "o"),
-        _dense(lse, torch.float32, (B, K, G, T), dev, "lse"), ws, ws_bytes,
-        B, K, G, T, H, n_pages, page, max_pages, _raw_stream(stream, dev))
-    if check:
+        _dense(q, _BF16, rows * H, dev, "q"), k_cache.data_ptr(), v_cache.data_ptr(), kind, ks, vs,
+        st[0], st[1], st[2], _dense(block_table, _I32, B * max_pages, dev, "block_table"),
+        _dense(lens, _I32, B, dev, "lens"), window, _dense(o, _BF16, rows * H, dev, "o"),
+        _dense(lse, _F32, rows, dev, "lse"), ws, ws_bytes, B, K, G, T, H, cs[0], cs[2], max_pages,
+        _current_stream(dev) if stream is None else _raw_stream(stream))
+    if rc and check:
         _check("fa_paged_decode", rc)
     return rc
 

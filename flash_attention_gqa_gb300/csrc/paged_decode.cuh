@@ -670,10 +670,10 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
             }
         }
 
-        // O^T += V^T P^T.  bf16 caches: the weights go in as two bf16 terms (their
-        // sum is off by 2^-17), so that o is rounded to bf16 once, at the end; the
-        // products are a quarter of the issue slots either way.  8-bit caches:
-        // one f16 term, off by 2^-12, against values of 2^-4.
+        // O^T += V^T P^T.  bf16 caches: the weights go in as two bf16 terms, cut
+        // and rest (off by 2^-16 in all), so that o is rounded to bf16 once, at the
+        // end.  The rest is kept above zero, or an infinite value would give
+        // 0 x inf.  8-bit caches: one f16 term, off by 2^-12, against values of 2^-4.
         uint32_t p[KT2][NT][2], pl[KT2][NT][2];
 #pragma unroll
         for (int kt = 0; kt < KT2; ++kt)
@@ -685,10 +685,10 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
               if (E4M3) {
                 p[kt][nt][h] = transpose8x8(pack_f16x2(x, y));
               } else {
-                const uint32_t hi = pack_bf16x2(x, y);
-                const float2 r = unpack_bf16x2(hi);
-                p[kt][nt][h] = transpose8x8(hi);
-                pl[kt][nt][h] = transpose8x8(pack_bf16x2(x - r.x, y - r.y));
+                const float hx = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+                const float hy = __uint_as_float(__float_as_uint(y) & 0xffff0000u);
+                p[kt][nt][h] = transpose8x8(__byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632));
+                pl[kt][nt][h] = transpose8x8(pack_bf16x2(fmaf(x, 0x1p-20f, x - hx), fmaf(y, 0x1p-20f, y - hy)));
               }
             }
         // Operand V^T of 16 keys and 16 dims (8-bit: 32 dims, two operands).

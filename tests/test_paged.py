@@ -241,12 +241,13 @@ def test_decode(lib, heads, H, dtype):
     _check(P.problem(G, B=len(LENS), K=K, G=G, T=1, H=H, lens=LENS, page=16, dtype=dtype))
 
 
-@pytest.mark.parametrize("page", [1, 2, 4, 8, 32, 64, 256, 1024])
+@pytest.mark.parametrize("page", [1, 2, 4, 8, 32, 64, 256, 1024, 65536])
 @pytest.mark.parametrize("layout", ["head", "token"])
 def test_decode_page_sizes_and_layouts(lib, page, layout):
     dtype, H = (BF16, 128) if page in (1, 8, 64, 1024) else (E4M3, 64)
     _check(P.problem(page, B=5, K=3, G=4, T=1, H=H, lens=[5, 0, 331, 64, 190], page=page,
-                     dtype=dtype, layout=layout, pad=32 if page > 1 else 0))
+                     dtype=dtype, layout=layout, pad=32 if page > 1 else 0,
+                     spare=3 if page < 65536 else 0))
 
 
 @pytest.mark.parametrize("dtype", [BF16, E4M3], ids=["bf16", "e4m3"])
@@ -330,6 +331,37 @@ def test_decode_infinities_and_nan_of_masked_keys_stay_there(lib):
         fine = ~bo
         P.check_decode(torch.where(fine, o, want[0].float()), torch.where(torch.isnan(lse), want[1].float(), lse),
                        want, 64, dtype == E4M3, 40)
+
+
+def test_decode_infinities_of_kept_keys(lib):
+    """An infinite value that a query keeps is in its result as such; scores of -inf have no weight,
+    and one of +inf leaves no number."""
+    p = P.problem(21, B=3, K=1, G=4, T=1, H=64, lens=[300, 1, 40], page=16)
+    q, kc, vc, table, lens, *_ = p
+    q.abs_().clamp_(min=1e-3)
+    at = lambda b, s: (int(table[b, s // 16]), 0, s % 16)
+    vc[at(0, 17)][2], vc[at(0, 290)][3], vc[at(1, 0)][4] = math.inf, -math.inf, math.inf
+    vc[at(0, 5)][6], vc[at(0, 200)][6] = math.inf, -math.inf          # both: no number
+    kc[at(2, 7)] = -math.inf
+    o, lse = (x.cpu() for x in _decode(p))
+    _ok()
+    inf, none = torch.isinf(o[..., 0, :]), torch.isnan(o[..., 0, :])
+    assert (o[0, 0, :, 0, 2] == math.inf).all() and (o[0, 0, :, 0, 3] == -math.inf).all()
+    assert (o[1, 0, :, 0, 4] == math.inf).all() and none[0, 0, :, 6].all()
+    assert inf.sum() == 12 and none.sum() == 4
+    # the key of -inf scores counts as absent
+    n = 40
+    keep = [s for s in range(n) if s != 7]
+    k, v = (torch.stack([c[at(2, s)] for s in keep]).double() for c in (kc, vc))
+    x = q[2, 0, :, 0].double() @ k.T
+    w = torch.softmax(x, -1)
+    assert ((o[2, 0, :, 0].double() - w @ v).abs()
+            <= 2.0 ** -8 * (w @ v).abs() + 2.0 ** -13 * (w @ v.abs())).all()
+    assert (lse[2, 0, :, 0].double() - torch.logsumexp(x, -1)).abs().max() <= 2.0 ** -14
+    kc[at(2, 7)] = math.inf
+    o, lse = (x.cpu() for x in _decode(p))
+    _ok()
+    assert torch.isnan(o[2]).all() and not torch.isnan(lse[0]).any()
 
 
 def test_decode_bad_pages_and_lengths_are_reported(lib):
