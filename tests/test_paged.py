@@ -261,6 +261,16 @@ def test_decode_many_rows(lib, rows, dtype):
                          dtype=dtype))
 
 
+@pytest.mark.parametrize("dtype", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("rows", [(16, 2), (8, 6), (12, 8), (128, 1)], ids=lambda r: "G%d_T%d" % r)
+def test_decode_many_rows_of_long_requests(lib, rows, dtype):
+    """The same, split over many CTAs, whose teams of warps and partials are joined."""
+    G, T = rows
+    for H in (64, 128, 256):
+        _check(P.problem(H, B=3, K=2, G=G, T=T, H=H, lens=[2500, 17, 800], page=16, dtype=dtype))
+        _check(P.problem(H, B=2, K=1, G=G, T=T, H=H, lens=[1100, 900], page=64, dtype=dtype), 333)
+
+
 @pytest.mark.parametrize("T", [1, 3])
 @pytest.mark.parametrize("window", [1, 2, 16, 50, 128, 10 ** 6, 2 ** 31 - 1])
 def test_decode_window(lib, window, T):
@@ -304,11 +314,12 @@ def test_decode_8bit_query_range(lib):
     _check(tuple(p))
 
 
-def test_decode_infinities_and_nan_of_masked_keys_stay_there(lib):
+@pytest.mark.parametrize("G", [2, 5, 10, 20, 40], ids=lambda g: "G%d" % g)
+def test_decode_infinities_and_nan_of_masked_keys_stay_there(lib, G):
     """Tokens past a query and before its window never reach it, whatever they hold; the query
     that sees one has it in its result."""
     for dtype in (BF16, E4M3):
-        p = P.problem(11, B=2, K=2, G=2, T=3, H=64, lens=[40, 35], page=16, dtype=dtype)
+        p = P.problem(11, B=2, K=2, G=G, T=3, H=64, lens=[40, 35], page=16, dtype=dtype)
         q, kc, vc, table, lens, ks, vs = p
         bad = math.nan if dtype == E4M3 else math.inf
         last = 39                                   # request 0's last key: only t = 2 sees it
@@ -322,7 +333,7 @@ def test_decode_infinities_and_nan_of_masked_keys_stay_there(lib):
         bo = ~torch.isfinite(o)
         assert bo[0, 0, :, 2, 3].all() and bo[0, 1, :, 2].all() and bo[1, 1, :, 0, 5].all()
         assert torch.isnan(lse[0, 1, :, 2]).all()
-        assert bo.sum() == 2 + 2 * 64 + 2
+        assert bo.sum() == G + G * 64 + G
         clean = [x.clone() for x in (kc, vc)]
         for c in clean:
             c.copy_(torch.nan_to_num(c.float(), 0.0, 0.0, 0.0).to(dtype))
