@@ -56,9 +56,9 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 // Not to be hoisted out of the loop that it stands in: that would take registers.
-__device__ __forceinline__ uint2 lds8(uint32_t addr) {
-  uint2 x;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(addr));
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 x;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(addr));
   return x;
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -91,6 +91,10 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t
       "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
       : "=r"(lo), "=r"(hi) : "r"(x));
 }
+
+// The base of a column that has met no score: finite, so that masked scores
+// (-inf) have no weight against it.
+constexpr float kNoScore = -3e38f;
 
 // ------------------------------------------------------------ configuration
 // NT: n-tiles of 8 query rows per warp.  WR: warps of a team, which share a ring
@@ -433,7 +437,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
   // ---- items
   int cur = 0;
   const int row0 = wr * NT * 8;   // first query row of this warp
-  uint2* const q_sm = reinterpret_cast<uint2*>(smem + C::RING);   // [ks][n-tile][lane]
+  uint4* const q_sm = reinterpret_cast<uint4*>(smem + C::RING);   // [pair of ks][n-tile][lane]
   const uint32_t q_u = smem_u32(q_sm + wr * NT * 32 + lane);
   // Query fragments: column n = lane / 4, dims as the key operand has them.
   auto load_q = [&](const DecodeWalk& w, int nt, uint2 (&x)[KS]) {
@@ -502,7 +506,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
           if (c == 0) sh_down[nt * 8 + g] = down;
         }
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) q_sm[(ks * C::QTILES + nt) * 32 + lane] = x[ks];
+        for (int ks = 0; ks < KS; ks += 2)
+          q_sm[(ks / 2 * C::QTILES + nt) * 32 + lane] = make_uint4(x[ks].x, x[ks].y, x[ks + 1].x, x[ks + 1].y);
       }
       __syncthreads();
       if (E4M3) {
@@ -549,7 +554,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     float o[KS][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = kNoScore;
       l[nt][0] = l[nt][1] = 0.0f;
 #pragma unroll
       for (int ds = 0; ds < KS; ++ds) o[ds][nt][0] = o[ds][nt][1] = o[ds][nt][2] = o[ds][nt][3] = 0.0f;
@@ -587,28 +592,30 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
             for (int i = 0; i < 4; ++i) s[kt][nt][i] = s2[TWO ? nt : 0][i] = 0.0f;
           const uint32_t k_lane = k_u + kt * 16 * C::ROWB + swz<C::UPR>(lane & 15, lane >> 4);
 #pragma unroll
-          for (int ks = 0; ks < KS; ks += E4M3 ? 2 : 1) {
-            uint32_t x[4];
-            ldsm4(k_lane ^ ((E4M3 ? ks : 2 * ks) << 4), x);
+          for (int ks = 0; ks < KS; ks += 2) {
+            uint32_t a0[4], a1[4];   // the keys' dims of two steps
             if (E4M3) {
-              uint32_t a0[4], a1[4];
+              uint32_t x[4];
+              ldsm4(k_lane ^ (ks << 4), x);
               e4m3x4_to_f16(x[0], a0[0], a0[2]);
               e4m3x4_to_f16(x[1], a0[1], a0[3]);
               e4m3x4_to_f16(x[2], a1[0], a1[2]);
               e4m3x4_to_f16(x[3], a1[1], a1[3]);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const uint2 q0 = C::QSMEM ? lds8(q_u + (ks * C::QTILES + nt) * 256) : qf[C::QSMEM ? 0 : ks][nt];
-                const uint2 q1 = C::QSMEM ? lds8(q_u + ((ks + 1) * C::QTILES + nt) * 256) : qf[C::QSMEM ? 0 : ks + 1][nt];
-                mma16816<true>(s[kt][nt], a0, q0.x, q0.y);
-                mma16816<true>(TWO ? s2[TWO ? nt : 0] : s[kt][nt], a1, q1.x, q1.y);
-              }
             } else {
+              ldsm4(k_lane ^ (ks << 5), a0);
+              ldsm4(k_lane ^ (ks << 5) ^ 32, a1);
+            }
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const uint2 q0 = C::QSMEM ? lds8(q_u + (ks * C::QTILES + nt) * 256) : qf[C::QSMEM ? 0 : ks][nt];
-                mma16816<false>(TWO && (ks & 1) ? s2[TWO ? nt : 0] : s[kt][nt], x, q0.x, q0.y);
+            for (int nt = 0; nt < NT; ++nt) {
+              uint4 q;
+              if (C::QSMEM) {
+                q = lds16(q_u + (ks / 2 * C::QTILES + nt) * 512);
+              } else {
+                const uint2 q0 = qf[C::QSMEM ? 0 : ks][nt], q1 = qf[C::QSMEM ? 0 : ks + 1][nt];
+                q = make_uint4(q0.x, q0.y, q1.x, q1.y);
               }
+              mma16816<E4M3>(s[kt][nt], a0, q.x, q.y);
+              mma16816<E4M3>(TWO ? s2[TWO ? nt : 0] : s[kt][nt], a1, q.z, q.w);
             }
           }
           if (TWO) {
@@ -631,9 +638,11 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
               }
         }
 
-        // online softmax, per column
-        float alpha[NT][2];
-        bool moved = false;
+        // Online softmax, per column.  The base m of the exponents is raised only
+        // where a score passes it by 8 (in log2 units: weights stay below 2^8), so
+        // that most slots need neither the maximum over the lanes nor a rescaling
+        // of o: exact, as m cancels in o / l.
+        bool high = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -641,34 +650,47 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
             float mx = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
 #pragma unroll
             for (int kt = 1; kt < KT2; ++kt) mx = fmaxf(mx, fmaxf(s[kt][nt][j], s[kt][nt][j + 2]));
-            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
-            const float mn = fmaxf(m[nt][j], mx * sl2[nt][j]);
-            const float base = mn == -INFINITY ? 0.0f : mn;
-            alpha[nt][j] = fast_exp2(m[nt][j] - base);
-            moved |= mn != m[nt][j];
-            m[nt][j] = mn;
+            high |= fmaf(mx, sl2[nt][j], -m[nt][j]) > 8.0f;
+          }
+        if (__any_sync(~0u, high)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float alpha[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float mx = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
+#pragma unroll
+              for (int kt = 1; kt < KT2; ++kt) mx = fmaxf(mx, fmaxf(s[kt][nt][j], s[kt][nt][j + 2]));
+              mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
+              const float mn = fmaxf(m[nt][j], mx * sl2[nt][j]);
+              alpha[j] = fast_exp2(m[nt][j] - mn);
+              m[nt][j] = mn;
+              l[nt][j] *= alpha[j];
+            }
+#pragma unroll
+            for (int ds = 0; ds < KS; ++ds) {
+              o[ds][nt][0] *= alpha[0];
+              o[ds][nt][1] *= alpha[1];
+              o[ds][nt][2] *= alpha[0];
+              o[ds][nt][3] *= alpha[1];
+            }
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
             float sum = 0.0f;
 #pragma unroll
             for (int kt = 0; kt < KT2; ++kt) {
-              s[kt][nt][j] = fast_exp2(fmaf(s[kt][nt][j], sl2[nt][j], -base));
-              s[kt][nt][j + 2] = fast_exp2(fmaf(s[kt][nt][j + 2], sl2[nt][j], -base));
+              s[kt][nt][j] = fast_exp2(fmaf(s[kt][nt][j], sl2[nt][j], -m[nt][j]));
+              s[kt][nt][j + 2] = fast_exp2(fmaf(s[kt][nt][j + 2], sl2[nt][j], -m[nt][j]));
               sum += s[kt][nt][j] + s[kt][nt][j + 2];
             }
-            l[nt][j] = l[nt][j] * alpha[nt][j] + sum;
+            l[nt][j] += sum;
           }
-        if (__any_sync(~0u, moved)) {
-#pragma unroll
-          for (int ds = 0; ds < KS; ++ds)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              o[ds][nt][0] *= alpha[nt][0];
-              o[ds][nt][1] *= alpha[nt][1];
-              o[ds][nt][2] *= alpha[nt][0];
-              o[ds][nt][3] *= alpha[nt][1];
-            }
-        }
 
         // O^T += V^T P^T.  bf16 caches: the weights go in as two bf16 terms, cut
         // and rest (off by 2^-16 in all), so that o is rounded to bf16 once, at the
@@ -772,6 +794,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
+        if (m[nt][j] == kNoScore) m[nt][j] = -INFINITY;
         l[nt][j] += __shfl_xor_sync(~0u, l[nt][j], 4);
         l[nt][j] += __shfl_xor_sync(~0u, l[nt][j], 8);
         l[nt][j] += __shfl_xor_sync(~0u, l[nt][j], 16);
