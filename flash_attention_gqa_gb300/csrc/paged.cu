@@ -17,8 +17,10 @@ constexpr int kTablesThreads = 1024;
 // exclusive sums over the requests (tokens, opened pages) place every token
 // and every page.  A call that cannot be met changes nothing.
 //
-// Every CTA forms the sums for itself (8 bytes a request, a few microseconds at
-// 8192 requests) and then fills its share of the tokens; nothing is exchanged.
+// Every CTA forms the sums for itself (8 bytes a request) and then fills its
+// share of the tokens; nothing is exchanged.  Latency bounds it: lengths, sums,
+// a search per token, its table entry, its slot (64 requests of one token 3.4 us,
+// 128 with 94000 tokens 4.6 us).
 // Where the outputs replace the inputs, all lengths have to be read before
 // anything is written: the CTAs are then one cluster, with its barrier between.
 template <bool IN_PLACE>
@@ -143,6 +145,8 @@ __device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float
 
 // A thread takes 8 head dims of a key and of the value beside it, `PER` of them
 // with all loads in flight before the first store; a CTA takes `tokens` tokens.
+// Bound by memory: 16000 tokens x 8 heads x 128 dims 21.6 us, 6.1 TB/s read and
+// written; 64 tokens 1.5 us, a launch.
 template <bool E4M3, int PER>
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const __grid_constant__ PagedAppendArgs a,
                                                                       int tokens) {

@@ -3,29 +3,40 @@
 //   x[r, s] = q[r] . k[s],  w = softmax over the keys that row r keeps,  o[r] = sum_s w[r, s] v[s]
 //
 // for the R = G * T query rows of a kv head, which share its keys.  Every key
-// and value byte is needed once and meets R rows: R FLOP per byte in bf16, so
-// memory bandwidth is the bound up to R ~ 100, and the kernel is built around
-// keeping copies in flight.
+// and value byte is needed once and meets R rows, R FLOP per byte in bf16: the
+// bound is memory, and the kernel is built around keeping copies in flight.
+// Measured (device time): 8 requests x 8 kv heads x 32768 keys, R = 8, H = 128:
+// 161 us, 6.65 TB/s; from there on 7.1 TB/s for every further byte, over a fixed
+// 9.5 us (3 us until the first copies are out, 1 us of latency, 2 us in which
+// CTAs end at different times, 3 us of joining).
 //
 // Split.  The (request, kv head) items are cut into tiles of keys; all tiles of
-// all items, in order, are dealt evenly to the CTAs (about one wave of them), so
-// ragged lengths and single long requests load the GPU alike.  The lengths
-// stay on the device: every CTA sums the tile counts for itself.  An item that
-// ends up in several CTAs leaves one partial (o, m, l) in each, and a second
-// kernel, launched early and waiting for the first to end, joins them in key
-// order.  Nothing depends on timing.
+// all items, in order, are dealt evenly to about one wave of CTAs, so ragged
+// lengths and single long requests load the GPU alike (two or three waves of
+// smaller parts cost more in starts than they gain in balance: 64 ragged
+// requests 74 us in one, 78 and 80 us in two and three).  The lengths stay on
+// the device: every CTA sums the tile counts for itself.  An item that ends up
+// in several CTAs leaves one partial (o, m, l) in each, and a second kernel,
+// launched early and waiting for the first to end, joins them in key order
+// (a join by the last CTA to arrive took 4 to 20 us: it has one SM's loads).
+// Nothing depends on timing.
 //
 // Products.  mma.sync with the keys as the 16-row operand: S^T = K Q^T and
-// O^T += V^T P^T waste nothing at R = 8 (tcgen05's 128-row tile would be
-// mostly padding there, and its operands would have to pass through tensor
-// memory and barriers for work that takes a quarter of the issue slots here).
-// The S^T accumulator becomes the P^T operand by one 8x8 transpose
-// (movmatrix), and running maxima live in the lanes that own the columns.
+// O^T += V^T P^T waste nothing at R = 8, where tcgen05's 128-row tile would be
+// mostly padding and its operands would pass through tensor memory and
+// barriers.  The issue slots are 23% used at R = 8 in bf16 and 38% with 8-bit
+// caches, 41% at R = 32.  mma.sync runs at one m16n8k16 per 8 cycles and
+// sub-core here (640 TFLOP/s), so from R = 64 on it and the instructions around
+// it are the bound (102 us for 64 rows, 181 us for 128, where 32 take 56 us and
+// 8 take 47 us: 16 requests x 4 kv heads x 8192 keys).  The S^T accumulator
+// becomes the P^T operand by one 8x8 transpose (movmatrix), and maxima and sums
+// live in the lanes that own the columns.
 //
-// Streams.  With R <= 16 each warp is on its own: it copies its keys (16-byte
-// cp.async, swizzled so that ldmatrix is conflict-free) into its own ring, and
-// waits for nobody until its CTA's part of the item ends; the ring runs ahead
-// across items.  With more rows the CTA's warps share one ring, 16 rows each.
+// Streams.  Up to 32 rows (16 at H = 256) each warp is on its own: it copies its
+// keys (16-byte cp.async, swizzled so that ldmatrix is conflict-free) into its
+// own ring, and waits for nobody until its CTA's part of the item ends; the
+// ring runs ahead across items.  With more rows, teams of 2 to 8 warps share a
+// ring and hold 32 rows (16) each.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -36,7 +47,6 @@
 #include "ptx.cuh"
 
 namespace fa {
-
 
 // ------------------------------------------------------------- primitives
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
@@ -137,13 +147,15 @@ __device__ __forceinline__ uint32_t swz(uint32_t r, uint32_t u) {
 }
 
 // ------------------------------------------------------------------ the walk
-// The list that is dealt to the CTAs: per item (b, k) ITEM_UNITS units that
-// stand for its start and end, then one unit per tile.
 // a / b for a, b >= 0: mostly in 32 bits, which takes a fraction of the time.
 __device__ __forceinline__ long long quotient(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
+// The list that is dealt to the CTAs: per item (b, k) ITEM_UNITS units that
+// stand for its start and end (about the time of two tiles of four warps), then
+// one unit per tile.  64 requests of 1 to 16384 tokens: 108 us without those
+// units, 75.0, 74.4, 75.3 and 76.8 us with 1, 2, 3 and 6.
 // A place in the list: unit `rem` of item (b, k).
 struct DecodePlace {
   int b, k, rem;
@@ -1077,7 +1089,7 @@ cudaError_t launch_decode(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // Shares of an item's partials: enough that each has about eight, in flight at
-  // once (one kv head of 131072 keys, 304 partials: 47 us with two, 24 with 16).
+  // once (one kv head of 131072 keys, 304 partials: 47 us with two, 22 with 16).
   const int items = a.B * a.K, partials = grid / items + 2;
   int per = kJoinThreads;
   while (per > 32 && kJoinThreads / per * 8 < partials) per /= 2;

@@ -633,6 +633,30 @@ def test_paged_tables_helper(lib):
         assert np.array_equal(g.cpu().numpy().ravel(), np.asarray(w).ravel())
 
 
+def test_serving_step_through_the_helpers(lib):
+    """The helpers that allocate, as in the README: two steps from an empty cache."""
+    B, K, G, H, page, n_pages = 3, 2, 4, 64, 16, 32
+    gen = torch.Generator().manual_seed(3)
+    caches = [torch.empty((n_pages, K, page, H), dtype=BF16, device="cuda") for _ in range(2)]
+    lens, used, free = _i32([0] * B), _i32([0]), _i32(np.arange(n_pages)[::-1].copy())
+    table = torch.zeros((B, 8), dtype=torch.int32, device="cuda")
+    past = [torch.zeros((B, 0, K, H)) for _ in range(2)]
+    for n in (21, 1):
+        kv = torch.randn((2, B, n, K, H), generator=gen).bfloat16()
+        q = (torch.randn((B, K, G, 1, H), generator=gen) / 8).bfloat16()
+        past = [torch.cat([p, x.float()], 1) for p, x in zip(past, kv)]
+        lens, starts, slots, positions, used = binding.paged_tables(
+            lens, _i32([n] * B), free, used, table, n_pages=n_pages, page_size=page, max_tokens=B * n)
+        k, v = (x.reshape(B * n, K, H).cuda() for x in kv)
+        binding.fa_paged_append(k, v, slots, *caches)
+        o, lse = binding.paged_attention_decode(q.cuda(), *caches, table, lens)
+        _ok()
+        ro, rl = oracle.attention_forward(q.double().numpy(), *(x.transpose(1, 2).double().numpy() for x in past))
+        assert np.abs(o.float().cpu().numpy() - ro).max() <= 2e-2
+        assert np.abs(lse.cpu().numpy() - rl).max() <= 1e-3
+    assert lens.tolist() == [22] * B and used.tolist() == [6]
+
+
 @pytest.mark.parametrize("what", ["lens", "table", "o", "dtype", "scale", "strides"])
 def test_binding_refuses_wrong_gpu_tensors(lib, what):
     q = torch.zeros((2, 2, 4, 1, 64), dtype=BF16, device="cuda")
