@@ -988,20 +988,19 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
 
 // Joins the partials of an item that several CTAs of the first kernel share: a
 // thread per four dims of a row and share of the partials, `per` such elements a
-// CTA, kJoinThreads / per shares, whose results are then summed in order.
-constexpr int kJoinThreads = 512;
-
-template <int H>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedDecodeArgs a,
-                                                                  int per) {
-  __shared__ float4 sx[kJoinThreads];
-  __shared__ float2 sml[kJoinThreads];
+// CTA, whose shares are then summed in order.  U: partials in flight a thread.
+// Few registers and threads a CTA, so that the whole grid starts at once as the
+// first one ends (512 threads of 75 registers, one CTA an SM, took 4 us).
+template <int H, int U, int THREADS>
+__global__ void __launch_bounds__(THREADS) paged_join_kernel(const __grid_constant__ PagedDecodeArgs a, int per) {
+  __shared__ float4 sx[THREADS];
+  __shared__ float2 sml[THREADS];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // (L2 loads: this grid may have started before the first one wrote)
   const int4 split = __ldcg(reinterpret_cast<const int4*>(a.splits) + blockIdx.x);
   const int item = split.x, first = split.y, n = split.z - first + 1;   // n partials
   if (first < 0) return;
-  const int R = a.G * a.T, shares = kJoinThreads / per;
+  const int R = a.G * a.T, shares = blockDim.x / per;
   const int share = threadIdx.x / per, at = threadIdx.x % per;
   const int i = blockIdx.y * per + at;
   const int r = i / (H / 4), d = i % (H / 4) * 4;
@@ -1011,7 +1010,6 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   float M = -INFINITY, L = 0.0f;
   float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (r < R) {
-    constexpr int U = 8;   // partials in flight
     for (int p0 = share; p0 < n; p0 += U * shares) {
       float4 y[U];
       float m[U], l[U];
@@ -1088,21 +1086,27 @@ cudaError_t launch_decode(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
   paged_decode_kernel<C><<<grid, C::THREADS, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // Shares of an item's partials: enough that each has about eight, in flight at
-  // once (one kv head of 131072 keys, 304 partials: 47 us with two, 22 with 16).
-  const int items = a.B * a.K, partials = grid / items + 2;
-  int per = kJoinThreads;
-  while (per > 32 && kJoinThreads / per * 8 < partials) per /= 2;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a.by_item ? items : grid, (a.G * a.T * (C::H / 4) + per - 1) / per);
-  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cfg.attrs = &early;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<C::H>, a, per);
+  // Partials of an item: about grid / items, two more at most.  Up to 4: all in
+  // flight in one thread; up to 16: two shares of 8; more (one kv head of 131072
+  // keys: 304): 16 shares, 8 in flight each.
+  const int items = a.B * a.K, elements = a.G * a.T * (C::H / 4), partials = grid / items + 2;
+  const int shares = partials <= 4 ? 1 : partials <= 16 ? 2 : 16;
+  int per = shares == 16 ? 32 : 256 / shares;
+  while (per > 32 && per / 2 >= elements) per /= 2;
+  cfg.gridDim = dim3(a.by_item ? items : grid, (elements + per - 1) / per);
+  cfg.blockDim = dim3(shares * per);
+  switch (shares) {
+    case 1: return cudaLaunchKernelEx(&cfg, paged_join_kernel<C::H, 4, 256>, a, per);
+    case 2: return cudaLaunchKernelEx(&cfg, paged_join_kernel<C::H, 8, 256>, a, per);
+    default: return cudaLaunchKernelEx(&cfg, paged_join_kernel<C::H, 8, 512>, a, per);
+  }
 }
 
 // Up to 8, 16 and (H <= 128: registers) 32 rows: warps on their own; more: teams.
