@@ -156,6 +156,7 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 // stand for its start and end (about the time of two tiles of four warps), then
 // one unit per tile.  64 requests of 1 to 16384 tokens: 108 us without those
 // units, 75.0, 74.4, 75.3 and 76.8 us with 1, 2, 3 and 6.
+
 // A place in the list: unit `rem` of item (b, k).
 struct DecodePlace {
   int b, k, rem;
@@ -171,8 +172,7 @@ struct DecodeEnd {
 struct DecodeWalk {
   int b, k, len, first, tiles;   // first: key of tile 0, a multiple of CK
   int tile, begun, end;
-  int todo;                      // whole items that follow
-  bool tail;                     // this is the CTA's last item, done first
+  int todo;                      // items that follow
 };
 
 template <class C>
@@ -203,37 +203,21 @@ struct DecodeShape {
     w.tile = w.begun = 0;
     w.end = w.tiles;
   }
-  // The CTA's items: the one its units end in first, where that goes on in
-  // the next CTA, so that by the end of the kernel most joins are over; then
-  // from the one that its units begin in.  False where it has no tile at all.
+  // From the item that the CTA's units begin in to the one that they end in.
+  // False where they hold no tile at all.
   __device__ __forceinline__ bool begin(DecodeWalk& w, const DecodePlace& h, const DecodePlace& e) const {
     const int between = (e.b - h.b) * a.K + e.k - h.k;   // items
-    enter(w, e.b, e.k);
-    const int end = min(w.tiles, e.rem + 1 - C::ITEM_UNITS);
-    if (between == 0) {
-      w.tile = w.begun = max(0, h.rem - C::ITEM_UNITS);
-      w.end = end;
-      w.todo = 0;
-      w.tail = false;
-      return w.end > w.begun;
-    }
-    w.tail = end > 0 && end < w.tiles;
-    w.todo = between - (w.tail || end <= 0 ? 1 : 0);
-    if (w.tail) w.end = end;
-    else head(w, h);
-    return true;
-  }
-  __device__ __forceinline__ void head(DecodeWalk& w, const DecodePlace& h) const {
     enter(w, h.b, h.k);
     w.tile = w.begun = max(0, h.rem - C::ITEM_UNITS);
+    const int last_end = e.rem + 1 - C::ITEM_UNITS;   // of the last item
+    w.todo = last_end > 0 ? between : between - 1;
+    if (between == 0) w.end = min(w.end, last_end);
+    return w.end > w.begun;
   }
-  __device__ __forceinline__ bool next_item(DecodeWalk& w, const DecodePlace& h) const {
-    if (w.tail) {
-      head(w, h);
-      w.tail = false;
-      return true;
-    }
-    if (w.todo == 0) return false;
+  // `last`: of the CTA's last unit (read again: once an item costs less than a
+  // register).
+  __device__ __forceinline__ bool next_item(DecodeWalk& w, const DecodeEnd& last) const {
+    if (w.todo <= 0) return false;
     --w.todo;
     if (w.k + 1 == a.K) {
       enter(w, w.b + 1, 0);
@@ -241,6 +225,10 @@ struct DecodeShape {
       ++w.k;
       w.tile = w.begun = 0;
       w.end = w.tiles;
+    }
+    if (w.todo == 0) {
+      const int last_end = place(last).rem + 1 - C::ITEM_UNITS;
+      if (last_end > 0) w.end = min(w.end, last_end);
     }
     return true;
   }
@@ -307,7 +295,6 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- this CTA's units
-  DecodePlace head;
   DecodeWalk walk;
   {
     const int per = (a.B + threads - 1) / threads;
@@ -353,8 +340,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       }
     }
     __syncthreads();
-    head = shape.place(sh_ends[0]);
-    const DecodePlace tail = shape.place(sh_ends[1]);
+    const DecodePlace head = shape.place(sh_ends[0]), tail = shape.place(sh_ends[1]);
     if (tid == 32) {
       // the item that the units end in, where it begins here and goes on in the
       // next CTA: for the join, with its last CTA
@@ -439,7 +425,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       }
     }
     cp_async_commit();
-    if (more && ++ahead.tile == ahead.end) more = shape.next_item(ahead, head);
+    if (more && ++ahead.tile == ahead.end) more = shape.next_item(ahead, sh_ends[1]);
     look_up();
   };
   look_up();
@@ -813,7 +799,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       }
     const bool whole = walk.begun == 0 && walk.end == walk.tiles;
     DecodeWalk then = walk;
-    const bool go_on = shape.next_item(then, head);
+    const bool go_on = shape.next_item(then, sh_ends[1]);
     if (EARLY && go_on) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) load_q(then, nt, q_next[EARLY ? nt : 0]);
