@@ -278,7 +278,8 @@ def fa_bwd_masked(q, k, v, o, lse, dO, seg_q, seg_kv, causal, mask, dq, dk, dv, 
 # transpose(1, 2).  Work goes to the tensors' own device.
 
 # These calls are a few microseconds of GPU work, so their checks are written for
-# few Python operations: sizes by numel of contiguous tensors, types by identity.
+# few Python operations: all in one condition, sizes by numel of contiguous tensors, types
+# by identity.  Where it fails, _dense names the tensor that is wrong.
 
 _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream   # its address; a Stream object costs 2 us
@@ -339,17 +340,32 @@ def fa_paged_tables(cached_lens, new_lens, free_pages, free_used, block_table, t
     rows, max_pages = block_table.shape
     if rows != B:
         raise ValueError(f"block_table must have {B} rows, got {rows}")
+    if not (_I32 is cached_lens.dtype is new_lens.dtype is free_pages.dtype is free_used.dtype
+            is block_table.dtype is total_lens.dtype is token_starts.dtype is free_used_out.dtype
+            and slots.dtype is _I64
+            and dev == new_lens.get_device() == free_pages.get_device() == free_used.get_device()
+            == block_table.get_device() == total_lens.get_device() == token_starts.get_device()
+            == slots.get_device() == free_used_out.get_device()
+            and B == new_lens.numel() == total_lens.numel() == token_starts.numel() - 1
+            and 1 == free_used.numel() == free_used_out.numel()
+            and cached_lens.is_contiguous() and new_lens.is_contiguous()
+            and free_pages.is_contiguous() and block_table.is_contiguous()
+            and total_lens.is_contiguous() and token_starts.is_contiguous()
+            and slots.is_contiguous()):
+        for t, dtype, n, name in (
+                (cached_lens, _I32, B, "cached_lens"), (new_lens, _I32, B, "new_lens"),
+                (free_pages, _I32, n_free, "free_pages"), (free_used, _I32, 1, "free_used"),
+                (block_table, _I32, B * max_pages, "block_table"),
+                (total_lens, _I32, B, "total_lens"),
+                (token_starts, _I32, B + 1, "token_starts"), (slots, _I64, tokens, "slots"),
+                (free_used_out, _I32, 1, "free_used_out")):
+            _dense(t, dtype, n, dev, name)
     rc = (_lib or load()).fa_paged_tables(
-        _dense(cached_lens, _I32, B, dev, "cached_lens"),
-        _dense(new_lens, _I32, B, dev, "new_lens"),
-        _dense(free_pages, _I32, n_free, dev, "free_pages"), n_free,
-        _dense(free_used, _I32, 1, dev, "free_used"),
-        _dense(block_table, _I32, B * max_pages, dev, "block_table"), max_pages,
-        _dense(total_lens, _I32, B, dev, "total_lens"),
-        _dense(token_starts, _I32, B + 1, dev, "token_starts"),
-        _dense(slots, _I64, tokens, dev, "slots"),
+        cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), n_free,
+        free_used.data_ptr(), block_table.data_ptr(), max_pages, total_lens.data_ptr(),
+        token_starts.data_ptr(), slots.data_ptr(),
         None if positions is None else _dense(positions, _I32, tokens, dev, "positions"), tokens,
-        _dense(free_used_out, _I32, 1, dev, "free_used_out"), B, n_pages, page_size,
+        free_used_out.data_ptr(), B, n_pages, page_size,
         _current_stream(dev) if stream is None else _raw_stream(stream))
     if rc and check:
         _check("fa_paged_tables", rc)
@@ -399,11 +415,21 @@ def fa_paged_decode(q, k_cache, v_cache, block_table, lens, o, lse, workspace, k
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
         ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    if not (_BF16 is q.dtype is o.dtype and _I32 is block_table.dtype is lens.dtype
+            and lse.dtype is _F32
+            and dev == o.get_device() == lse.get_device() == block_table.get_device()
+            == lens.get_device()
+            and rows * H == o.numel() and rows == lse.numel() and B == lens.numel()
+            and q.is_contiguous() and o.is_contiguous() and lse.is_contiguous()
+            and block_table.is_contiguous() and lens.is_contiguous()):
+        for t, dtype, n, name in (
+                (q, _BF16, rows * H, "q"), (block_table, _I32, B * max_pages, "block_table"),
+                (lens, _I32, B, "lens"), (o, _BF16, rows * H, "o"), (lse, _F32, rows, "lse")):
+            _dense(t, dtype, n, dev, name)
     rc = (_lib or load()).fa_paged_decode(
-        _dense(q, _BF16, rows * H, dev, "q"), k_cache.data_ptr(), v_cache.data_ptr(), kind, ks, vs,
-        st[0], st[1], st[2], _dense(block_table, _I32, B * max_pages, dev, "block_table"),
-        _dense(lens, _I32, B, dev, "lens"), window, _dense(o, _BF16, rows * H, dev, "o"),
-        _dense(lse, _F32, rows, dev, "lse"), ws, ws_bytes, B, K, G, T, H, cs[0], cs[2], max_pages,
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kind, ks, vs, st[0], st[1], st[2],
+        block_table.data_ptr(), lens.data_ptr(), window, o.data_ptr(), lse.data_ptr(), ws, ws_bytes,
+        B, K, G, T, H, cs[0], cs[2], max_pages,
         _current_stream(dev) if stream is None else _raw_stream(stream))
     if rc and check:
         _check("fa_paged_decode", rc)

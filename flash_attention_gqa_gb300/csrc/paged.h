@@ -67,6 +67,7 @@ struct PagedDecodeArgs {
   float* partials;             // workspace: [CTAs][2][paged_partial_floats] of split items
   PagedDecodeSplit* splits;    // workspace: [CTAs]
   bool by_item;                // entries of splits are items
+  bool unsplit;                // no item is shared: no splits, no partials (set by the launch)
   uint32_t* err;
 };
 

@@ -208,6 +208,10 @@ struct DecodeShape {
   __device__ __forceinline__ bool begin(DecodeWalk& w, const DecodePlace& h, const DecodePlace& e) const {
     const int between = (e.b - h.b) * a.K + e.k - h.k;   // items
     enter(w, h.b, h.k);
+    if (a.unsplit) {   // an item is done whole by the CTA that its first unit is in
+      w.todo = between;
+      return h.rem == 0 || next_item(w, DecodeEnd{});
+    }
     w.tile = w.begun = max(0, h.rem - C::ITEM_UNITS);
     const int last_end = e.rem + 1 - C::ITEM_UNITS;   // of the last item
     w.todo = last_end > 0 ? between : between - 1;
@@ -226,7 +230,7 @@ struct DecodeShape {
       w.tile = w.begun = 0;
       w.end = w.tiles;
     }
-    if (w.todo == 0) {
+    if (w.todo == 0 && !a.unsplit) {
       const int last_end = place(last).rem + 1 - C::ITEM_UNITS;
       if (last_end > 0) w.end = min(w.end, last_end);
     }
@@ -323,7 +327,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     // CTA i: total / ctas units, and one more where i < total % ctas
     const int ctas = (int)min((long long)gridDim.x, total), i = blockIdx.x;
     if (i >= ctas) {
-      if (tid == 0 && !a.by_item) a.splits[i] = PagedDecodeSplit{0, -1, 0, 0};
+      if (tid == 0 && !a.by_item && !a.unsplit) a.splits[i] = PagedDecodeSplit{0, -1, 0, 0};
       return;
     }
     const long long each = quotient(total, ctas), over = total - each * ctas;
@@ -341,7 +345,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     }
     __syncthreads();
     const DecodePlace head = shape.place(sh_ends[0]), tail = shape.place(sh_ends[1]);
-    if (tid == 32) {
+    if (tid == 32 && !a.unsplit) {
       // the item that the units end in, where it begins here and goes on in the
       // next CTA: for the join, with its last CTA
       const int tiles = shape.tiles(sh_ends[1].len);
@@ -965,7 +969,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       }
     }
 
-    if (whole && a.by_item && tid == 0) a.splits[item] = PagedDecodeSplit{(int)item, -1, 0, 0};
+    if (whole && a.by_item && !a.unsplit && tid == 0) a.splits[item] = PagedDecodeSplit{(int)item, -1, 0, 0};
     if (!go_on) break;
     walk = then;
   }
@@ -1057,8 +1061,22 @@ __global__ void __launch_bounds__(THREADS) paged_join_kernel(const __grid_consta
                a.v_scale ? a.v_scale[item % a.K] : 1.0f);
 }
 
+// The most tiles that a request can have.
 template <class C>
-cudaError_t launch_decode(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
+int64_t decode_most_tiles(const PagedDecodeArgs& a) {
+  int64_t keys = (int64_t)a.max_pages << a.lay.page_shift;
+  const int64_t seen = (int64_t)a.window + a.T - 1 + C::CK - 1;   // from a multiple of CK on
+  if (a.window > 0 && seen < keys) keys = seen;
+  return (keys + C::TK - 1) / C::TK;
+}
+// Requests of few tiles are not split, which saves the second launch: up to 4
+// tiles (64 requests x 8 kv heads x 256 keys: 20.0 us split, 17.5 whole; 8 x 8:
+// 8.2 and 7.8; 1 x 2 at H = 256: 8.1 and 8.9, and 2 us of the host), with items
+// for every CTA up to 8 (64 x 8 x 512 keys: 29.7 and 27.7 us; 1 x 2: 8.1 and 12.7).
+inline int64_t decode_whole_tiles(int64_t items, int ctas) { return items >= ctas ? 8 : 4; }
+
+template <class C>
+cudaError_t launch_decode(PagedDecodeArgs a, int grid, cudaStream_t st) {
   constexpr size_t smem = C::RING + C::QBYTES;
   static bool ready[64] = {};   // per device; setting it twice is harmless
   int dev = 0;
@@ -1069,9 +1087,10 @@ cudaError_t launch_decode(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev] = true;
   }
+  a.unsplit = decode_most_tiles<C>(a) <= decode_whole_tiles((int64_t)a.B * a.K, grid);
   paged_decode_kernel<C><<<grid, C::THREADS, smem, st>>>(a);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.unsplit) return e;
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;

@@ -294,6 +294,19 @@ def test_decode_ragged_batch(lib):
     _check(P.problem(4, B=300, K=2, G=4, T=1, H=64, lens=lens, page=16))
 
 
+@pytest.mark.parametrize("dtype", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("B", [3, 200])
+@pytest.mark.parametrize("longest", [64, 256, 272, 512, 528])
+def test_decode_short_tables(lib, B, longest, dtype):
+    """Around the lengths up to which a request is not split, whose rule goes by the columns of
+    the table; few and many requests."""
+    rng = np.random.default_rng(longest)
+    lens = [longest, 0, 1] + [int(x) for x in rng.integers(0, longest + 1, B - 3)]
+    for H, G in ((64, 3), (128, 12)):
+        _check(P.problem(5, B=B, K=2, G=G, T=1, H=H, lens=lens, page=16, dtype=dtype, extra_cols=0))
+    _check(P.problem(6, B=B, K=2, G=8, T=2, H=64, lens=lens, page=16, dtype=dtype, extra_cols=90), 100)
+
+
 def test_decode_large_scores(lib):
     """Scores in the hundreds: the running maximum carries them."""
     p = P.problem(9, B=3, K=2, G=4, T=1, H=128, lens=[700, 64, 1], page=16)
@@ -657,7 +670,27 @@ def test_serving_step_through_the_helpers(lib):
     assert lens.tolist() == [22] * B and used.tolist() == [6]
 
 
-@pytest.mark.parametrize("what", ["lens", "table", "o", "dtype", "scale", "strides"])
+@pytest.mark.parametrize("wrong", range(11))
+def test_binding_refuses_wrong_tables_tensors(lib, wrong):
+    """Each tensor in turn of another type, another size, not contiguous, or on the CPU."""
+    def good():
+        return [_i32([1, 2]), _i32([1, 1]), _i32(range(8)), _i32([0]), _i32(np.zeros((2, 4), int)),
+                _i32([0, 0]), _i32([0, 0, 0]), torch.zeros(4, dtype=torch.int64, device="cuda"),
+                _i32([0] * 4), _i32([0])]
+    if wrong == 10:
+        binding.fa_paged_tables(*good(), 8, 16)
+        return _ok()
+    for spoil in (lambda t: t.float(), lambda t: torch.cat([t, t]) if wrong in (0, 1, 3, 4, 5, 6, 8, 9) else t.float(),
+                  lambda t: torch.stack([t, t], -1)[..., 0] if t.numel() > 1 else t.float(), lambda t: t.cpu()):
+        args = good()
+        args[wrong] = spoil(args[wrong])
+        with pytest.raises(ValueError):
+            binding.fa_paged_tables(*args, 8, 16)
+    _ok()
+
+
+@pytest.mark.parametrize("what", ["lens", "table", "o", "dtype", "scale", "strides", "lse", "sizes",
+                                  "apart", "cpu"])
 def test_binding_refuses_wrong_gpu_tensors(lib, what):
     q = torch.zeros((2, 2, 4, 1, 64), dtype=BF16, device="cuda")
     kc = torch.zeros((3, 2, 16, 64), dtype=BF16, device="cuda")
@@ -673,6 +706,14 @@ def test_binding_refuses_wrong_gpu_tensors(lib, what):
         kc, vc = kc.half(), vc.half()
     elif what == "scale":
         ks = torch.ones(2, device="cuda")
+    elif what == "lse":
+        lse = lse.double()
+    elif what == "sizes":
+        lens = _i32([1, 1, 1])
+    elif what == "apart":
+        q = torch.stack([q, q], -1)[..., 0]
+    elif what == "cpu":
+        table = table.cpu()
     else:
         vc = vc.transpose(1, 2).contiguous().transpose(1, 2)
     with pytest.raises(ValueError):
