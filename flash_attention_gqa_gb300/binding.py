@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -55,6 +56,9 @@ SIGNATURES = {
     "fa_paged_decode": (_I, [_P, _P, _P, _I, _P, _P, _L, _L, _L, _P, _P, _I, _P, _P, _P,
                              ctypes.c_size_t, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
     "fa_paged_decode_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
+    "fa_paged_tables_packed": (_I, [ctypes.c_char_p]),
+    "fa_paged_append_packed": (_I, [ctypes.c_char_p]),
+    "fa_paged_decode_packed": (_I, [ctypes.c_char_p]),
     "fa_check_status": (_I, [_P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_set_wait_limit_ns": (_I, [ctypes.c_uint64]),
@@ -283,6 +287,8 @@ def fa_bwd_masked(q, k, v, o, lse, dO, seg_q, seg_kv, causal, mask, dq, dk, dv, 
 
 _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream   # its address; a Stream object costs 2 us
+# The packed calls' records: ctypes takes 2 us for two dozen arguments, and a sixth of it here.
+_TABLES, _APPEND, _DECODE = (struct.Struct(f"{n}q").pack for n in (17, 21, 25))
 _BF16, _I32, _I64, _F32, _E4M3 = (torch.bfloat16, torch.int32, torch.int64, torch.float32,
                                   torch.float8_e4m3fn)
 
@@ -311,12 +317,12 @@ def _paged_cache(k_cache, v_cache, k_scale, v_scale, K: int, H: int, index: int)
     if dtype is _BF16:
         if k_scale is not None or v_scale is not None:
             raise ValueError("a bfloat16 cache takes no scales")
-        return FA_CACHE_BF16, shape, stride, None, None
+        return FA_CACHE_BF16, shape, stride, 0, 0
     if dtype is not _E4M3:
         raise ValueError(f"the cache must be bfloat16 or float8_e4m3fn, got {dtype}")
     return (FA_CACHE_E4M3, shape, stride,
-            None if k_scale is None else _dense(k_scale, _F32, K, index, "k_scale"),
-            None if v_scale is None else _dense(v_scale, _F32, K, index, "v_scale"))
+            0 if k_scale is None else _dense(k_scale, _F32, K, index, "k_scale"),
+            0 if v_scale is None else _dense(v_scale, _F32, K, index, "v_scale"))
 
 
 def _raw_stream(stream) -> int:
@@ -360,13 +366,13 @@ def fa_paged_tables(cached_lens, new_lens, free_pages, free_used, block_table, t
                 (token_starts, _I32, B + 1, "token_starts"), (slots, _I64, tokens, "slots"),
                 (free_used_out, _I32, 1, "free_used_out")):
             _dense(t, dtype, n, dev, name)
-    rc = (_lib or load()).fa_paged_tables(
+    rc = (_lib or load()).fa_paged_tables_packed(_TABLES(
         cached_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(), n_free,
         free_used.data_ptr(), block_table.data_ptr(), max_pages, total_lens.data_ptr(),
         token_starts.data_ptr(), slots.data_ptr(),
-        None if positions is None else _dense(positions, _I32, tokens, dev, "positions"), tokens,
+        0 if positions is None else _dense(positions, _I32, tokens, dev, "positions"), tokens,
         free_used_out.data_ptr(), B, n_pages, page_size,
-        _current_stream(dev) if stream is None else _raw_stream(stream))
+        _current_stream(dev) if stream is None else _raw_stream(stream)))
     if rc and check:
         _check("fa_paged_tables", rc)
     return rc
@@ -386,11 +392,11 @@ def fa_paged_append(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, s
         raise ValueError("k and v must be bfloat16 tensors of one shape [N, K, H] on one device, "
                          "innermost stride 1")
     kind, cs, st, ks, vs = _paged_cache(k_cache, v_cache, k_scale, v_scale, K, H, dev)
-    rc = (_lib or load()).fa_paged_append(
+    rc = (_lib or load()).fa_paged_append_packed(_APPEND(
         k.data_ptr(), v.data_ptr(), sk[0], sk[1], sv[0], sv[1],
         _dense(slots, _I64, N, dev, "slots"), k_cache.data_ptr(), v_cache.data_ptr(), kind, ks, vs,
         st[0], st[1], st[2], N, K, H, cs[0], cs[2],
-        _current_stream(dev) if stream is None else _raw_stream(stream))
+        _current_stream(dev) if stream is None else _raw_stream(stream)))
     if rc and check:
         _check("fa_paged_append", rc)
     return rc
@@ -410,7 +416,7 @@ def fa_paged_decode(q, k_cache, v_cache, block_table, lens, o, lse, workspace, k
     requests, max_pages = block_table.shape
     if requests != B:
         raise ValueError(f"block_table must have {B} rows, got {requests}")
-    ws, ws_bytes = None, 0
+    ws = ws_bytes = 0
     if workspace is not None:
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
@@ -426,11 +432,11 @@ def fa_paged_decode(q, k_cache, v_cache, block_table, lens, o, lse, workspace, k
                 (q, _BF16, rows * H, "q"), (block_table, _I32, B * max_pages, "block_table"),
                 (lens, _I32, B, "lens"), (o, _BF16, rows * H, "o"), (lse, _F32, rows, "lse")):
             _dense(t, dtype, n, dev, name)
-    rc = (_lib or load()).fa_paged_decode(
+    rc = (_lib or load()).fa_paged_decode_packed(_DECODE(
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kind, ks, vs, st[0], st[1], st[2],
         block_table.data_ptr(), lens.data_ptr(), window, o.data_ptr(), lse.data_ptr(), ws, ws_bytes,
         B, K, G, T, H, cs[0], cs[2], max_pages,
-        _current_stream(dev) if stream is None else _raw_stream(stream))
+        _current_stream(dev) if stream is None else _raw_stream(stream)))
     if rc and check:
         _check("fa_paged_decode", rc)
     return rc

@@ -184,3 +184,94 @@ int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int
 }
 
 }  // extern "C"
+
+namespace {
+
+// Reads a record of 8-byte arguments in order; `ok` falls where a size does not
+// fit an int.
+struct Record {
+  const int64_t* at;
+  bool ok = true;
+  template <class T>
+  T* ptr() { return reinterpret_cast<T*>(static_cast<uintptr_t>(*at++)); }
+  int64_t wide() { return *at++; }
+  int size() {
+    const int64_t x = *at++;
+    if (x < INT32_MIN || x > INT32_MAX) ok = false;
+    return static_cast<int>(x);
+  }
+};
+
+}  // namespace
+
+extern "C" {
+
+int fa_paged_tables_packed(const int64_t* args) {
+  if (!args) return FA_ERR_INVALID_ARG;
+  Record r{args};
+  const auto* cached = r.ptr<const int32_t>();
+  const auto* fresh = r.ptr<const int32_t>();
+  const auto* free_pages = r.ptr<const int32_t>();
+  const int n_free = r.size();
+  const auto* used = r.ptr<const int32_t>();
+  auto* table = r.ptr<int32_t>();
+  const int max_pages = r.size();
+  auto* total = r.ptr<int32_t>();
+  auto* starts = r.ptr<int32_t>();
+  auto* slots = r.ptr<int64_t>();
+  auto* positions = r.ptr<int32_t>();
+  const int max_tokens = r.size();
+  auto* used_out = r.ptr<int32_t>();
+  const int B = r.size(), n_pages = r.size(), page_size = r.size();
+  void* stream = r.ptr<void>();
+  if (!r.ok) return FA_ERR_INVALID_ARG;
+  return fa_paged_tables(cached, fresh, free_pages, n_free, used, table, max_pages, total, starts, slots,
+                         positions, max_tokens, used_out, B, n_pages, page_size, stream);
+}
+
+int fa_paged_append_packed(const int64_t* args) {
+  if (!args) return FA_ERR_INVALID_ARG;
+  Record r{args};
+  const void* k = r.ptr<const void>();
+  const void* v = r.ptr<const void>();
+  const int64_t kt = r.wide(), kh = r.wide(), vt = r.wide(), vh = r.wide();
+  const auto* slots = r.ptr<const int64_t>();
+  void* kc = r.ptr<void>();
+  void* vc = r.ptr<void>();
+  const int type = r.size();
+  const auto* ks = r.ptr<const float>();
+  const auto* vs = r.ptr<const float>();
+  const int64_t page = r.wide(), head = r.wide(), token = r.wide();
+  const int N = r.size(), K = r.size(), H = r.size(), n_pages = r.size(), page_size = r.size();
+  void* stream = r.ptr<void>();
+  if (!r.ok) return FA_ERR_INVALID_ARG;
+  return fa_paged_append(k, v, kt, kh, vt, vh, slots, kc, vc, type, ks, vs, page, head, token, N, K, H,
+                         n_pages, page_size, stream);
+}
+
+int fa_paged_decode_packed(const int64_t* args) {
+  if (!args) return FA_ERR_INVALID_ARG;
+  Record r{args};
+  const void* q = r.ptr<const void>();
+  const void* kc = r.ptr<const void>();
+  const void* vc = r.ptr<const void>();
+  const int type = r.size();
+  const auto* ks = r.ptr<const float>();
+  const auto* vs = r.ptr<const float>();
+  const int64_t page = r.wide(), head = r.wide(), token = r.wide();
+  const auto* table = r.ptr<const int32_t>();
+  const auto* lens = r.ptr<const int32_t>();
+  const int window = r.size();
+  void* o = r.ptr<void>();
+  auto* lse = r.ptr<float>();
+  void* workspace = r.ptr<void>();
+  const size_t bytes = static_cast<size_t>(r.wide());
+  const int B = r.size(), K = r.size(), G = r.size(), T = r.size(), H = r.size();
+  const int n_pages = r.size(), page_size = r.size(), max_pages = r.size();
+  void* stream = r.ptr<void>();
+  if (!r.ok) return FA_ERR_INVALID_ARG;
+  return fa_paged_decode(q, kc, vc, type, ks, vs, page, head, token, table, lens, window, o, lse, workspace,
+                         bytes, B, K, G, T, H, n_pages, page_size, max_pages, stream);
+}
+
+}  // extern "C"

@@ -329,6 +329,18 @@ int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int
 size_t fa_paged_decode_workspace_size(int B, int K, int G, int T, int H);
 
 /*
+ * The three calls above with their arguments in one record, for callers that
+ * pay for each argument (foreign-function interfaces: two dozen of them cost
+ * more than the rest of a small call).  The record holds the plain call's
+ * arguments in order, 8 bytes each: addresses as integers, sizes as signed
+ * integers.  A size that does not fit its plain argument's type is
+ * FA_ERR_INVALID_ARG; all else is as in the plain call.
+ */
+int fa_paged_tables_packed(const int64_t* args);   /* 17 */
+int fa_paged_append_packed(const int64_t* args);   /* 21 */
+int fa_paged_decode_packed(const int64_t* args);   /* 25 */
+
+/*
  * Synchronises `stream`, then reads and clears the device error word of the
  * current device.  Returns FA_OK, FA_ERR_DEVICE_TIMEOUT, FA_ERR_DEVICE_VALUE (a
  * timeout comes before it) or FA_ERR_CUDA.

@@ -1,6 +1,7 @@
 """The paged cache operators without a GPU: argument checks of the C ABI (fake pointers: every
 call is refused, or has nothing to do, before any launch) and of the binding."""
 import ctypes
+import struct
 
 import pytest
 import torch
@@ -11,11 +12,19 @@ from test_boundary import clib  # noqa: F401  (fixture)
 BAD, UNSUP, OK = binding.FA_ERR_INVALID_ARG, binding.FA_ERR_UNSUPPORTED, binding.FA_OK
 
 
+def _both(lib, name, *args):
+    """The status of a call with plain arguments, which its packed form has to give too."""
+    rc = getattr(lib, name)(*args)
+    record = struct.pack(f"{len(args)}q", *(0 if x is None else x for x in args))
+    assert getattr(lib, name + "_packed")(record) == rc
+    return rc
+
+
 def _tables(lib, cached=16, new=16, free=16, n_free=10, used=16, table=16, max_pages=8, total=16,
             starts=16, slots=16, positions=16, max_tokens=64, used_out=16, B=4, n_pages=100,
             page=16):
-    return lib.fa_paged_tables(cached, new, free, n_free, used, table, max_pages, total, starts,
-                               slots, positions, max_tokens, used_out, B, n_pages, page, None)
+    return _both(lib, "fa_paged_tables", cached, new, free, n_free, used, table, max_pages, total, starts,
+                 slots, positions, max_tokens, used_out, B, n_pages, page, None)
 
 
 @pytest.mark.parametrize("kw,rc", [
@@ -33,8 +42,8 @@ def test_tables_refusals(clib, kw, rc):  # noqa: F811
 
 def _append(lib, k=16, v=16, kt=1024, kh=128, vt=1024, vh=128, slots=16, kc=16, vc=16, kind=0,
             ks=None, vs=None, sp=16384, sh=2048, st=128, N=4, K=8, H=128, n_pages=10, page=16):
-    return lib.fa_paged_append(k, v, kt, kh, vt, vh, slots, kc, vc, kind, ks, vs, sp, sh, st, N, K,
-                               H, n_pages, page, None)
+    return _both(lib, "fa_paged_append", k, v, kt, kh, vt, vh, slots, kc, vc, kind, ks, vs, sp, sh, st, N, K,
+                 H, n_pages, page, None)
 
 
 @pytest.mark.parametrize("kw,rc", [
@@ -53,8 +62,8 @@ def test_append_refusals(clib, kw, rc):  # noqa: F811
 def _decode(lib, q=16, kc=16, vc=16, kind=0, ks=None, vs=None, sp=16384, sh=2048, st=128, table=16,
             lens=16, window=0, o=16, lse=16, ws=256, ws_bytes=1 << 30, B=4, K=8, G=4, T=1, H=128,
             n_pages=10, page=16, max_pages=8):
-    return lib.fa_paged_decode(q, kc, vc, kind, ks, vs, sp, sh, st, table, lens, window, o, lse,
-                               ws, ws_bytes, B, K, G, T, H, n_pages, page, max_pages, None)
+    return _both(lib, "fa_paged_decode", q, kc, vc, kind, ks, vs, sp, sh, st, table, lens, window, o, lse,
+                 ws, ws_bytes, B, K, G, T, H, n_pages, page, max_pages, None)
 
 
 @pytest.mark.parametrize("kw,rc", [
@@ -107,6 +116,17 @@ def test_binding_refuses_wrong_tensors():
     with pytest.raises(ValueError):
         binding.fa_paged_decode(bf(1, 4, 2, 1, 128), bf(3, 4, 16, 128), bf(3, 4, 16, 128),
                                 i32(1, 2), i32(1), bf(1, 4, 2, 1, 128), torch.zeros(1, 4, 2, 1), None)
+
+
+@pytest.mark.parametrize("name,n", [("tables", 17), ("append", 21), ("decode", 25)])
+def test_packed_sizes_have_to_fit(clib, name, n):  # noqa: F811
+    # the second size argument from the end, past an int (and null pointers elsewhere)
+    call = getattr(clib, f"fa_paged_{name}_packed")
+    for big in (2 ** 31, 2 ** 32 + 1, -2 ** 31 - 1):
+        record = [0] * n
+        record[-3] = big
+        assert call(struct.pack(f"{n}q", *record)) == BAD
+    assert call(None) == BAD
 
 
 def test_argument_types_are_plain(clib):  # noqa: F811
