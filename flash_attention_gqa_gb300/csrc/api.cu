@@ -216,6 +216,8 @@ int fwd_common(const void* q, const void* k, const void* v, const int32_t* seg_q
 
 }  // namespace
 
+uint64_t fa::device_wait_limit_ns() { return wait_limit(); }
+
 extern "C" {
 
 int fa_fwd(const void* q, const void* k, const void* v, const int32_t* seg_q,

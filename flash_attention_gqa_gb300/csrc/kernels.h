@@ -98,6 +98,8 @@ cudaError_t launch_wait_selftest(uint32_t* err, uint64_t limit_ns, cudaStream_t 
 
 // Device address of the error word on the current device (null on failure).
 uint32_t* device_error_word();
+// Time limit of bounded device waits of kernels launched from now on.
+uint64_t device_wait_limit_ns();
 
 // KV rows per tile of the backward kernels.  H = 256 always takes 64 (a
 // 128-key K/V pair does not fit in shared memory next to the Q/dO tiles); H <=

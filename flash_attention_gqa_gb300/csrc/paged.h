@@ -65,6 +65,7 @@ struct PagedDecodeArgs {
   int B, K, G, T, H, max_pages;
   int window;                  // 0: none
   float* partials;             // workspace: [CTAs][2][paged_partial_floats] of split items
+  uint64_t wait_limit_ns;      // of the waits on barriers (the tcgen05 kernel)
   PagedDecodeSplit* splits;    // workspace: [CTAs]
   bool by_item;                // entries of splits are items
   bool unsplit;                // no item is shared: no splits, no partials (set by the launch)

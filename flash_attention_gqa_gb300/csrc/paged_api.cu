@@ -166,6 +166,7 @@ int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int
   a.splits = static_cast<fa::PagedDecodeSplit*>(workspace);
   a.by_item = B * K <= plan.ctas;
   a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.partials);
+  a.wait_limit_ns = fa::device_wait_limit_ns();
   a.err = fa::device_error_word();
   if (!a.err || plan.ctas == 0) return FA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

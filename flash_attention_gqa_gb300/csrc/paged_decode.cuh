@@ -131,6 +131,7 @@ struct DecodeCfg {
   // what the queries leave of 212 KB.
   static constexpr int STAGES = TEAM ? (212 * 1024 - QBYTES) / (TEAMS * SLOT) : (H == 256 ? 48 : 24) * 1024 / SLOT;
   static constexpr int RING = TEAMS * STAGES * SLOT;
+  static constexpr int SMEM = RING + QBYTES;
   static constexpr int MIN_CTAS = !TEAM && H <= 128 ? 2 : 1;
   static_assert(TEAM || (NT < 2 ? NT : 2) * 8 * H * 4 <= SLOT, "16 rows of a warp's O^T fit in a ring slot");
   static_assert(!TEAM || 2 * 32 * H <= SLOT, "8 rows of two warps' O^T fit in a ring slot");
@@ -238,6 +239,80 @@ struct DecodeShape {
   }
 };
 
+// What the CTAs share of the split's arithmetic.
+template <class C>
+struct DecodeShared {
+  long long scan[C::WARPS];
+  DecodeEnd ends[2];   // first and last unit
+};
+
+// Finds this CTA's units, by all its threads, and enters its first item; false
+// where it has no tile.
+template <class C>
+__device__ __forceinline__ bool decode_units(const PagedDecodeArgs& a, DecodeShared<C>& sh, DecodeWalk& walk) {
+  constexpr int threads = C::THREADS;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const DecodeShape<C> shape{a};
+  const int per = (a.B + threads - 1) / threads;
+  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    if (blockIdx.x == 0) {
+      const int n = a.lens[b];
+      if (n != shape.length(b)) atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+    }
+    mine += (long long)(shape.tiles(shape.length(b)) + C::ITEM_UNITS) * a.K;
+  }
+  long long inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long x = __shfl_up_sync(~0u, inc, d);
+    if (lane >= d) inc += x;
+  }
+  if (lane == 31) sh.scan[warp] = inc;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < threads / 32; ++w) {
+    if (w < warp) before += sh.scan[w];
+    total += sh.scan[w];
+  }
+  // CTA i: total / ctas units, and one more where i < total % ctas
+  const int ctas = (int)min((long long)gridDim.x, total), i = blockIdx.x;
+  if (i >= ctas) {
+    if (tid == 0 && !a.by_item && !a.unsplit) a.splits[i] = PagedDecodeSplit{0, -1, 0, 0};
+    return false;
+  }
+  const long long each = quotient(total, ctas), over = total - each * ctas;
+  const long long t0 = i * each + min((long long)i, over), t1 = t0 + each + (i < over ? 1 : 0);
+  const long long at = before + inc - mine;
+  if (t0 < at + mine && t1 - 1 >= at) {   // the requests that hold the first and the last unit
+    long long x = at;
+    for (int b = b0; b < b1; ++b) {
+      const int len = shape.length(b);
+      const long long next = x + (long long)(shape.tiles(len) + C::ITEM_UNITS) * a.K;
+      if (t0 >= x && t0 < next) sh.ends[0] = DecodeEnd{b, len, t0 - x};
+      if (t1 - 1 >= x && t1 - 1 < next) sh.ends[1] = DecodeEnd{b, len, t1 - 1 - x};
+      x = next;
+    }
+  }
+  __syncthreads();
+  const DecodePlace head = shape.place(sh.ends[0]), tail = shape.place(sh.ends[1]);
+  if (tid == 32 && !a.unsplit) {
+    // the item that the units end in, where it begins here and goes on in the
+    // next CTA: for the join, with its last CTA
+    const int tiles = shape.tiles(sh.ends[1].len);
+    const long long first = t1 - 1 - tail.rem + C::ITEM_UNITS;   // its first tile's unit
+    const bool split = tail.rem >= C::ITEM_UNITS && tail.rem + 1 < tiles + C::ITEM_UNITS && first >= t0;
+    if (split || !a.by_item) {
+      const long long unit = first + tiles - 1, cut = over * (each + 1);
+      const long long last = unit < cut ? quotient(unit, each + 1) : over + quotient(unit - cut, each);
+      const int item = tail.b * a.K + tail.k;
+      a.splits[a.by_item ? item : i] = PagedDecodeSplit{item, split ? i : -1, (int)last, 0};
+    }
+  }
+  return shape.begin(walk, head, tail);
+}
+
 // Whether any 16-bit (bf16) or 8-bit (e4m3) value of the `bytes` at `p` is not
 // finite; warp-wide.
 template <bool E4M3>
@@ -286,9 +361,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
   extern __shared__ __align__(1024) char smem[];
   __shared__ float sh_m[WARPS][16], sh_l[WARPS][16];
   __shared__ float4 sh_ml[TEAM ? WARPS : 1][32];
-  __shared__ long long sh_scan[8];
   __shared__ float sh_down[C::QTILES * 8];     // what undoes the scaling of a query row
-  __shared__ DecodeEnd sh_ends[2];      // first and last unit
+  __shared__ DecodeShared<C> sh;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
@@ -300,66 +374,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
 
   // ---- this CTA's units
   DecodeWalk walk;
-  {
-    const int per = (a.B + threads - 1) / threads;
-    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) {
-      if (blockIdx.x == 0) {
-        const int n = a.lens[b];
-        if (n != shape.length(b)) atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
-      }
-      mine += (long long)(shape.tiles(shape.length(b)) + C::ITEM_UNITS) * a.K;
-    }
-    long long inc = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const long long x = __shfl_up_sync(~0u, inc, d);
-      if (lane >= d) inc += x;
-    }
-    if (lane == 31) sh_scan[warp] = inc;
-    __syncthreads();
-    long long before = 0, total = 0;
-    for (int w = 0; w < threads / 32; ++w) {
-      if (w < warp) before += sh_scan[w];
-      total += sh_scan[w];
-    }
-    // CTA i: total / ctas units, and one more where i < total % ctas
-    const int ctas = (int)min((long long)gridDim.x, total), i = blockIdx.x;
-    if (i >= ctas) {
-      if (tid == 0 && !a.by_item && !a.unsplit) a.splits[i] = PagedDecodeSplit{0, -1, 0, 0};
-      return;
-    }
-    const long long each = quotient(total, ctas), over = total - each * ctas;
-    const long long t0 = i * each + min((long long)i, over), t1 = t0 + each + (i < over ? 1 : 0);
-    const long long at = before + inc - mine;
-    if (t0 < at + mine && t1 - 1 >= at) {   // the requests that hold the first and the last unit
-      long long x = at;
-      for (int b = b0; b < b1; ++b) {
-        const int len = shape.length(b);
-        const long long next = x + (long long)(shape.tiles(len) + C::ITEM_UNITS) * a.K;
-        if (t0 >= x && t0 < next) sh_ends[0] = DecodeEnd{b, len, t0 - x};
-        if (t1 - 1 >= x && t1 - 1 < next) sh_ends[1] = DecodeEnd{b, len, t1 - 1 - x};
-        x = next;
-      }
-    }
-    __syncthreads();
-    const DecodePlace head = shape.place(sh_ends[0]), tail = shape.place(sh_ends[1]);
-    if (tid == 32 && !a.unsplit) {
-      // the item that the units end in, where it begins here and goes on in the
-      // next CTA: for the join, with its last CTA
-      const int tiles = shape.tiles(sh_ends[1].len);
-      const long long first = t1 - 1 - tail.rem + C::ITEM_UNITS;   // its first tile's unit
-      const bool split = tail.rem >= C::ITEM_UNITS && tail.rem + 1 < tiles + C::ITEM_UNITS && first >= t0;
-      if (split || !a.by_item) {
-        const long long unit = first + tiles - 1, cut = over * (each + 1);
-        const long long last = unit < cut ? quotient(unit, each + 1) : over + quotient(unit - cut, each);
-        const int item = tail.b * a.K + tail.k;
-        a.splits[a.by_item ? item : i] = PagedDecodeSplit{item, split ? i : -1, (int)last, 0};
-      }
-    }
-    if (!shape.begin(walk, head, tail)) return;
-  }
+  if (!decode_units<C>(a, sh, walk)) return;
   DecodeWalk ahead = walk;   // where the copies are
   bool more = true;
 
@@ -429,7 +444,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       }
     }
     cp_async_commit();
-    if (more && ++ahead.tile == ahead.end) more = shape.next_item(ahead, sh_ends[1]);
+    if (more && ++ahead.tile == ahead.end) more = shape.next_item(ahead, sh.ends[1]);
     look_up();
   };
   look_up();
@@ -803,7 +818,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       }
     const bool whole = walk.begun == 0 && walk.end == walk.tiles;
     DecodeWalk then = walk;
-    const bool go_on = shape.next_item(then, sh_ends[1]);
+    const bool go_on = shape.next_item(then, sh.ends[1]);
     if (EARLY && go_on) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) load_q(then, nt, q_next[EARLY ? nt : 0]);
@@ -1059,76 +1074,6 @@ __global__ void __launch_bounds__(THREADS) paged_join_kernel(const __grid_consta
   if (share == 0 && r < R)
     put_result((char*)a.o + (int64_t)item * R * H * 2, a.lse + (int64_t)item * R, H, r, d, x, M, L,
                a.v_scale ? a.v_scale[item % a.K] : 1.0f);
-}
-
-// The most tiles that a request can have.
-template <class C>
-int64_t decode_most_tiles(const PagedDecodeArgs& a) {
-  int64_t keys = (int64_t)a.max_pages << a.lay.page_shift;
-  const int64_t seen = (int64_t)a.window + a.T - 1 + C::CK - 1;   // from a multiple of CK on
-  if (a.window > 0 && seen < keys) keys = seen;
-  return (keys + C::TK - 1) / C::TK;
-}
-// Requests of few tiles are not split, which saves the second launch: up to 4
-// tiles (64 requests x 8 kv heads x 256 keys: 20.0 us split, 17.5 whole; 8 x 8:
-// 8.2 and 7.8; 1 x 2 at H = 256: 8.1 and 8.9, and 2 us of the host), with items
-// for every CTA up to 8 (64 x 8 x 512 keys: 29.7 and 27.7 us; 1 x 2: 8.1 and 12.7).
-inline int64_t decode_whole_tiles(int64_t items, int ctas) { return items >= ctas ? 8 : 4; }
-
-template <class C>
-cudaError_t launch_decode(PagedDecodeArgs a, int grid, cudaStream_t st) {
-  constexpr size_t smem = C::RING + C::QBYTES;
-  static bool ready[64] = {};   // per device; setting it twice is harmless
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 64 || !ready[dev]) {
-    e = cudaFuncSetAttribute(paged_decode_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) ready[dev] = true;
-  }
-  a.unsplit = decode_most_tiles<C>(a) <= decode_whole_tiles((int64_t)a.B * a.K, grid);
-  paged_decode_kernel<C><<<grid, C::THREADS, smem, st>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || a.unsplit) return e;
-  cudaLaunchAttribute early{};
-  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.stream = st;
-  cfg.attrs = &early;
-  cfg.numAttrs = 1;
-  // Partials of an item: about grid / items, two more at most.  Up to 4: all in
-  // flight in one thread; up to 16: two shares of 8; more (one kv head of 131072
-  // keys: 304): 16 shares, 8 in flight each.
-  const int items = a.B * a.K, elements = a.G * a.T * (C::H / 4), partials = grid / items + 2;
-  const int shares = partials <= 4 ? 1 : partials <= 16 ? 2 : 16;
-  int per = shares == 16 ? 32 : 256 / shares;
-  while (per > 32 && per / 2 >= elements) per /= 2;
-  cfg.gridDim = dim3(a.by_item ? items : grid, (elements + per - 1) / per);
-  cfg.blockDim = dim3(shares * per);
-  switch (shares) {
-    case 1: return cudaLaunchKernelEx(&cfg, paged_join_kernel<C::H, 4, 256>, a, per);
-    case 2: return cudaLaunchKernelEx(&cfg, paged_join_kernel<C::H, 8, 256>, a, per);
-    default: return cudaLaunchKernelEx(&cfg, paged_join_kernel<C::H, 8, 512>, a, per);
-  }
-}
-
-// Up to 8, 16 and (H <= 128: registers) 32 rows: warps on their own; more: teams.
-template <int H, bool E4M3>
-cudaError_t launch_decode_rows(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
-  const int R = a.G * a.T;
-  if (R <= 8) return launch_decode<DecodeCfg<H, E4M3, 1, 1>>(a, grid, st);
-  if (R <= 16) return launch_decode<DecodeCfg<H, E4M3, 2, 1>>(a, grid, st);
-  if constexpr (H <= 128) {
-    if (R <= 32) return launch_decode<DecodeCfg<H, E4M3, 4, 1>>(a, grid, st);
-    if (R <= 64) return launch_decode<DecodeCfg<H, E4M3, 4, 2>>(a, grid, st);
-    return launch_decode<DecodeCfg<H, E4M3, 4, 4>>(a, grid, st);
-  } else {
-    if (R <= 32) return launch_decode<DecodeCfg<H, E4M3, 2, 2>>(a, grid, st);
-    if (R <= 64) return launch_decode<DecodeCfg<H, E4M3, 2, 4>>(a, grid, st);
-    return launch_decode<DecodeCfg<H, E4M3, 2, 8>>(a, grid, st);
-  }
 }
 
 }  // namespace fa

@@ -1,5 +1,5 @@
 // Paged decode at head dim 64, e4m3 caches (a file of its own: compiled in parallel).
-#include "paged_decode.cuh"
+#include "paged_decode_launch.cuh"
 
 namespace fa {
 cudaError_t launch_paged_decode_h64_e4m3(const PagedDecodeArgs& a, int grid, cudaStream_t st) {

@@ -1,0 +1,92 @@
+// Launches of the paged decode: the kernel for a call's rows, and the join.
+#pragma once
+#include "paged_decode.cuh"
+#include "paged_decode_tc.cuh"
+
+namespace fa {
+
+// The most tiles that a request can have.
+template <class C>
+int64_t decode_most_tiles(const PagedDecodeArgs& a) {
+  int64_t keys = (int64_t)a.max_pages << a.lay.page_shift;
+  const int64_t seen = (int64_t)a.window + a.T - 1 + C::CK - 1;   // from a multiple of CK on
+  if (a.window > 0 && seen < keys) keys = seen;
+  return (keys + C::TK - 1) / C::TK;
+}
+// Requests of few tiles are not split, which saves the second launch: up to 4
+// tiles (64 requests x 8 kv heads x 256 keys: 20.0 us split, 17.5 whole; 8 x 8:
+// 8.2 and 7.8; 1 x 2 at H = 256: 8.1 and 8.9, and 2 us of the host), with items
+// for every CTA up to 8 (64 x 8 x 512 keys: 29.7 and 27.7 us; 1 x 2: 8.1 and 12.7).
+inline int64_t decode_whole_tiles(int64_t items, int ctas) { return items >= ctas ? 8 : 4; }
+
+template <int H>
+cudaError_t launch_join(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  // Partials of an item: about grid / items, two more at most.  Up to 4: all in
+  // flight in one thread; up to 16: two shares of 8; more (one kv head of 131072
+  // keys: 304): 16 shares, 8 in flight each.
+  const int items = a.B * a.K, elements = a.G * a.T * (H / 4), partials = grid / items + 2;
+  const int shares = partials <= 4 ? 1 : partials <= 16 ? 2 : 16;
+  int per = shares == 16 ? 32 : 256 / shares;
+  while (per > 32 && per / 2 >= elements) per /= 2;
+  cfg.gridDim = dim3(a.by_item ? items : grid, (elements + per - 1) / per);
+  cfg.blockDim = dim3(shares * per);
+  switch (shares) {
+    case 1: return cudaLaunchKernelEx(&cfg, paged_join_kernel<H, 4, 256>, a, per);
+    case 2: return cudaLaunchKernelEx(&cfg, paged_join_kernel<H, 8, 256>, a, per);
+    default: return cudaLaunchKernelEx(&cfg, paged_join_kernel<H, 8, 512>, a, per);
+  }
+}
+
+// The first grid: KERNEL of a configuration C, then the join unless no item is split.
+template <class C, void (*KERNEL)(const PagedDecodeArgs)>
+cudaError_t launch_decode(PagedDecodeArgs a, int grid, cudaStream_t st) {
+  static bool ready[64] = {};   // per device; setting it twice is harmless
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !ready[dev]) {
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev] = true;
+  }
+  a.unsplit = decode_most_tiles<C>(a) <= decode_whole_tiles((int64_t)a.B * a.K, grid);
+  KERNEL<<<grid, C::THREADS, C::SMEM, st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.unsplit) return e;
+  return launch_join<C::H>(a, grid, st);
+}
+template <class C>
+cudaError_t launch_decode(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
+  return launch_decode<C, paged_decode_kernel<C>>(a, grid, st);
+}
+
+// Up to 8, 16 and (H <= 128: registers) 32 rows: warps on their own; more: tcgen05
+// for bf16 up to H = 128, else teams.
+template <int H, bool E4M3>
+cudaError_t launch_decode_rows(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
+  const int R = a.G * a.T;
+  if (R <= 8) return launch_decode<DecodeCfg<H, E4M3, 1, 1>>(a, grid, st);
+  if (R <= 16) return launch_decode<DecodeCfg<H, E4M3, 2, 1>>(a, grid, st);
+  if constexpr (H <= 128) {
+    if (R <= 32) return launch_decode<DecodeCfg<H, E4M3, 4, 1>>(a, grid, st);
+    if constexpr (!E4M3) {
+      return launch_decode<DecodeTcCfg<H>, paged_decode_tc_kernel<DecodeTcCfg<H>>>(a, grid, st);
+    } else {
+      if (R <= 64) return launch_decode<DecodeCfg<H, E4M3, 4, 2>>(a, grid, st);
+      return launch_decode<DecodeCfg<H, E4M3, 4, 4>>(a, grid, st);
+    }
+  } else {
+    if (R <= 32) return launch_decode<DecodeCfg<H, E4M3, 2, 2>>(a, grid, st);
+    if (R <= 64) return launch_decode<DecodeCfg<H, E4M3, 2, 4>>(a, grid, st);
+    return launch_decode<DecodeCfg<H, E4M3, 2, 8>>(a, grid, st);
+  }
+}
+
+}  // namespace fa
