@@ -727,7 +727,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
                 const float hx = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
                 const float hy = __uint_as_float(__float_as_uint(y) & 0xffff0000u);
                 p[kt][nt][h] = transpose8x8(__byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632));
-                pl[kt][nt][h] = transpose8x8(pack_bf16x2(fmaf(x, 0x1p-20f, x - hx), fmaf(y, 0x1p-20f, y - hy)));
+                pl[kt][nt][h] = transpose8x8(pack_bf16x2(fmaf(x, 1 + 0x1p-20f, -hx), fmaf(y, 1 + 0x1p-20f, -hy)));
               }
             }
         // Operand V^T of 16 keys and 16 dims (8-bit: 32 dims, two operands).

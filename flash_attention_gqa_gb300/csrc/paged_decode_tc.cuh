@@ -9,16 +9,19 @@
 // 3000 cycles in which an SM's share of the memory rate delivers its 64 KB, so
 // memory is the bound again.
 //
-// Roles (288 threads, one CTA an SM):
-//   warps 0-3  softmax and results: thread r owns row r, a lane of tensor memory
-//   warps 4-7  copies: each 32 keys of a tile, by cp.async (pages may end
-//              anywhere, and keys past the request have to arrive as zeros)
-//   warp  8    products (lane 0), tensor memory
+// Roles (352 threads, one CTA an SM):
+//   warps 0-7   softmax and results: warps w and w + 4 share 32 rows (a thread
+//               per row, a lane of tensor memory), each half of the keys of a
+//               tile and half of the head dims of o
+//   warps 8, 9  copies: each 64 keys of a tile, by cp.async (pages may end
+//               anywhere, and keys past the request have to arrive as zeros)
+//   warp  10    products (lane 0), tensor memory
 // Tensor memory: S of tiles n and n + 1 at columns 0 and 128, o at 256.  The
 // weights' two bf16 terms, 64 columns each, are the A operands of o += P V: one
-// over its S, one at 384 or 448.
-// Shared memory: the queries and a ring of K, V pairs, in chunks of [rows x
-// 128 B] with the 128-byte swizzle of the operand descriptors.
+// over its S (32 columns in each half of it), one at 384 or 448.
+// Shared memory: the queries and a ring of K and V tiles (K(0), V(0), K(1), ..),
+// in chunks of [rows x 128 B] with the 128-byte swizzle of the operand
+// descriptors.
 #pragma once
 #include "paged_decode.cuh"
 
@@ -29,13 +32,13 @@ struct DecodeTcCfg {
   static constexpr int H = H_, HC = H / 64;
   static constexpr int CK = 128, TEAMS = 1, TK = 128;   // a tile is 128 keys
   static constexpr int ITEM_UNITS = 2;
-  static constexpr int WARPS = 9, THREADS = WARPS * 32;
+  static constexpr int WARPS = 11, THREADS = WARPS * 32;
   static constexpr int CHUNK = 128 * 128;               // 128 rows of 64 dims
-  static constexpr int HALF = HC * CHUNK;               // a slot holds K, then V
-  static constexpr int SLOT = 2 * HALF;
-  static constexpr int STAGES = H == 64 ? 6 : 3;        // 192 KB
+  static constexpr int SLOT = HC * CHUNK;               // a tile of K or of V
+  static constexpr int STAGES = H == 64 ? 12 : 6;       // 192 KB
+  static constexpr int FLIGHT = STAGES / 2;             // tiles in flight behind the newest
   static constexpr int RING = STAGES * SLOT;
-  static constexpr int SMEM = HALF + RING + 1024;       // queries, ring, alignment
+  static constexpr int SMEM = SLOT + RING;              // queries, ring
   static constexpr int UPR = H / 8;                     // 16-byte units of a key
 };
 
@@ -55,16 +58,15 @@ template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __grid_constant__ PagedDecodeArgs a) {
   constexpr int H = C::H, HC = C::HC, S = C::STAGES;
   constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ DecodeShared<C> sh;
-  __shared__ __align__(8) uint64_t bars[2 * S + 9];
+  __shared__ __align__(8) uint64_t bars[2 * S + 13];
   __shared__ uint32_t sh_tmem;
   __shared__ int sh_abort, sh_keep;    // sh_keep: o holds something before an item's first product
-  __shared__ uint32_t sh_bad[2][4];    // keys of a tile (by its parity) whose value is not finite
+  __shared__ uint32_t sh_bad[2][8];    // keys of a tile (by its parity) whose value is not finite
+  __shared__ float sh_top[2][2][128];  // [parity][half] largest scores of the rows; sums at the end
 
-  const uint32_t raw = smem_u32(smem_raw);
-  uint8_t* const sm = smem_raw + (((raw + 1023) & ~1023u) - raw);
-  const uint32_t q_u = smem_u32(sm), ring_u = q_u + C::HALF;
+  const uint32_t q_u = smem_u32(sm), ring_u = q_u + C::SLOT;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int R = a.G * a.T;
   const DecodeShape<C> shape{a};
@@ -76,6 +78,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
   auto pv_done = [&](int n) { return smem_u32(bars + 2 * S + 4 + (n & 1)); };
   const uint32_t q_full = smem_u32(bars + 2 * S + 6), rows_met = smem_u32(bars + 2 * S + 7);
   const uint32_t teardown = smem_u32(bars + 2 * S + 8);
+  auto pair_met = [&](int w) { return smem_u32(bars + 2 * S + 9 + (w & 3)); };
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   DecodeWalk walk;
@@ -83,20 +86,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
   if (tid == 0) {
     sh_abort = 0;
     for (int s = 0; s < S; ++s) {
-      mbar_init(full(s), 128);
+      mbar_init(full(s), 64);
       mbar_init(empty(s), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full(i), 1);
-      mbar_init(p_full(i), 128);
+      mbar_init(p_full(i), 256);
       mbar_init(pv_done(i), 1);
     }
-    mbar_init(q_full, 128);
-    mbar_init(rows_met, 128);
+    mbar_init(q_full, 256);
+    mbar_init(rows_met, 256);
+    for (int w = 0; w < 4; ++w) mbar_init(pair_met(w), 64);
     mbar_init(teardown, 1);
     fence_barrier_init();
   }
-  if (warp == 8) {
+  if (warp == 10) {
     tmem_alloc(smem_u32(&sh_tmem), 512);
     tmem_relinquish();
   }
@@ -106,43 +110,47 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
   const uint32_t tmem = sh_tmem;
   constexpr uint32_t O_COL = 256, REST_COL = 384;
 
-  if (warp == 8) {
+  if (warp == 10) {
     // -------------------------------------------------------------- products
     if (lane == 0) {
       constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);   // S = Q K^T
       constexpr uint32_t id_o = idesc_bf16(128, H, false, true);      // o += P V
       const uint64_t dq = sdesc_sw128(q_u, 16, 1024), dk = sdesc_sw128(ring_u, 16, 1024);
-      const uint64_t dv = sdesc_sw128(ring_u + C::HALF, C::CHUNK, 1024);
+      const uint64_t dv = sdesc_sw128(ring_u, C::CHUNK, 1024);
       bool ok = true;
       int n = 0;   // tiles so far
       auto issue_pv = [&](int n, bool first) -> bool {
-        if (!mbar_wait(p_full(n), (n >> 1) & 1, ab)) return false;
+        const int unit = 2 * n + 1;   // V(n)
+        if (!mbar_wait(full(unit % S), (unit / S) & 1, ab) || !mbar_wait(p_full(n), (n >> 1) & 1, ab)) return false;
         tc_fence_after();
         const uint32_t p = tmem + 128 * (n & 1);
-        const uint64_t v = sdesc_add(dv, (n % S) * C::SLOT);
+        const uint64_t v = sdesc_add(dv, (unit % S) * C::SLOT);
         const bool keep = !first || *reinterpret_cast<volatile int*>(&sh_keep);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + O_COL, p + kk * 8, sdesc_add(v, kk * 2048), id_o, keep || kk > 0 ? 1u : 0u);
+          mma_ts(tmem + O_COL, p + kk / 4 * 64 + kk % 4 * 8, sdesc_add(v, kk * 2048), id_o,
+                 keep || kk > 0 ? 1u : 0u);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_ts(tmem + O_COL, tmem + REST_COL + 64 * (n & 1) + kk * 8, sdesc_add(v, kk * 2048), id_o, 1u);
-        mma_commit(empty(n % S));
+        mma_commit(empty(unit % S));
         mma_commit(pv_done(n));
         return true;
       };
       for (int item = 0; ok; ++item) {
         ok = mbar_wait(q_full, item & 1, ab);
         for (; ok && walk.tile < walk.end; ++walk.tile, ++n) {
-          if (!(ok = mbar_wait(full(n % S), (n / S) & 1, ab))) break;
+          const int unit = 2 * n;   // K(n)
+          if (!(ok = mbar_wait(full(unit % S), (unit / S) & 1, ab))) break;
           tc_fence_after();
-          const uint64_t k = sdesc_add(dk, (n % S) * C::SLOT);
+          const uint64_t k = sdesc_add(dk, (unit % S) * C::SLOT);
 #pragma unroll
           for (int c = 0; c < HC; ++c)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               mma_ss(tmem + 128 * (n & 1), sdesc_add(dq, c * C::CHUNK + kk * 32),
                      sdesc_add(k, c * C::CHUNK + kk * 32), id_s, c > 0 || kk > 0 ? 1u : 0u);
+          mma_commit(empty(unit % S));
           mma_commit(s_full(n));
           // o += P V of the tile before, while this one's softmax runs
           if (walk.tile > walk.begun) ok = issue_pv(n - 1, walk.tile - 1 == walk.begun);
@@ -156,88 +164,124 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
       }
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp >= 8) {
     // ---------------------------------------------------------------- copies
-    const int w = warp - 4;
-    constexpr int RPJ = 32 / C::UPR;   // rows a copy of the warp
+    const int w = warp - 8;
+    constexpr int RPJ = 32 / C::UPR, D = C::FLIGHT;   // rows a copy of the warp; tiles in flight
     const int64_t lane_src = (lane / C::UPR) * a.lay.token + (lane % C::UPR) * 16;
     const int64_t row_step = a.lay.token * RPJ;
     const int u = lane % C::UPR, lr = lane / C::UPR;   // unit and first row of this lane
-    const uint32_t lane_dst = (u >> 3) * C::CHUNK + (w * 32 + lr) * 128 + (((u & 7) ^ lr) << 4);
+    const uint32_t lane_dst = (u >> 3) * C::CHUNK + (w * 64 + lr) * 128 + (((u & 7) ^ lr) << 4);
     bool more = true, ok = true;
-    int n = 0;
-    while (more && ok) {
-      const int s = walk.first + walk.tile * C::TK + w * 32 + lane;   // this lane's key
-      const bool live = s >= shape.low(walk.len) && s < walk.len;
-      int64_t off = -1;
-      if (live) {
-        const int page = __ldg(a.block_table + (int64_t)walk.b * a.max_pages + (s >> a.lay.page_shift));
-        if (page >= 0 && page < a.lay.n_pages)
-          off = page * a.lay.page + walk.k * a.lay.head + (s & ((1 << a.lay.page_shift) - 1)) * a.lay.token;
-        else
-          atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+    int unit = 0;   // K(n): 2 n, V(n): 2 n + 1
+    // This lane's two keys of the next tile: looked up a tile early.
+    bool live[2];
+    int page[2], in[2], head = 0;
+    auto look_up = [&]() {
+      head = walk.k;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int s = walk.first + walk.tile * C::TK + w * 64 + h * 32 + lane;
+        live[h] = more && s >= shape.low(walk.len) && s < walk.len;
+        in[h] = s & ((1 << a.lay.page_shift) - 1);
+        page[h] = -1;
+        if (live[h])
+          page[h] = __ldg(a.block_table + (int64_t)walk.b * a.max_pages + (s >> a.lay.page_shift));
       }
-      if (n >= S && !(ok = tc_wait(empty(n % S), (n / S - 1) & 1, ab))) break;
-      const uint32_t dst = ring_u + (n % S) * C::SLOT + lane_dst;
-      if (a.lay.page_shift >= 4 && __all_sync(~0u, off >= 0)) {
+    };
+    look_up();
+    while (more && ok) {
+      int64_t off[2];
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {   // 16 keys or more a page: one offset per 16 keys, and steps
-          const int64_t at = __shfl_sync(~0u, off, kt * 16) + lane_src;
-          const char *pk = (const char*)a.k_cache + at, *pv = (const char*)a.v_cache + at;
+      for (int h = 0; h < 2; ++h) {
+        off[h] = -1;
+        if (live[h]) {
+          if (page[h] >= 0 && page[h] < a.lay.n_pages)
+            off[h] = page[h] * a.lay.page + head * a.lay.head + in[h] * a.lay.token;
+          else
+            atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+        }
+      }
+      if (++walk.tile == walk.end) more = shape.next_item(walk, sh.ends[1]);
+      look_up();
+      const bool steps = a.lay.page_shift >= 4 && __all_sync(~0u, off[0] >= 0 && off[1] >= 0);
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv, ++unit) {
+        const char* const base = (const char*)(kv ? a.v_cache : a.k_cache);
+        if (unit >= S && !(ok = tc_wait(empty(unit % S), (unit / S - 1) & 1, ab))) break;
+        const uint32_t dst = ring_u + (unit % S) * C::SLOT + lane_dst;
+        if (steps) {
 #pragma unroll
-          for (int j = kt * 16 / RPJ; j < (kt + 1) * 16 / RPJ; ++j) {
-            const uint32_t d = (dst ^ (((j * RPJ) & 7) << 4)) + j * RPJ * 128;
-            cp_async16(d, pk, 16);
-            cp_async16(d + C::HALF, pv, 16);
-            pk += row_step;
-            pv += row_step;
+          for (int kt = 0; kt < 4; ++kt) {   // 16 keys or more a page: one offset per 16 keys, and steps
+            const char* src = base + __shfl_sync(~0u, off[kt >> 1], (kt & 1) * 16) + lane_src;
+#pragma unroll
+            for (int j = kt * 16 / RPJ; j < (kt + 1) * 16 / RPJ; ++j) {
+              cp_async16((dst ^ (((j * RPJ) & 7) << 4)) + j * RPJ * 128, src, 16);
+              src += row_step;
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < 64 / RPJ; ++j) {
+            const int row = j * RPJ + lr;
+            const int64_t at0 = __shfl_sync(~0u, off[0], row & 31), at1 = __shfl_sync(~0u, off[1], row & 31);
+            const int64_t at = row < 32 ? at0 : at1;
+            // nothing is read, and zeros are written, where there is no key (q: an address that exists)
+            cp_async16((dst ^ (((j * RPJ) & 7) << 4)) + j * RPJ * 128,
+                       at >= 0 ? base + at + u * 16 : (const char*)a.q, at >= 0 ? 16 : 0);
           }
         }
-      } else {
-#pragma unroll 1
-        for (int j = 0; j < 32 / RPJ; ++j) {
-          const int64_t at = __shfl_sync(~0u, off, j * RPJ + lr);
-          const uint32_t bytes = at >= 0 ? 16 : 0, d = (dst ^ (((j * RPJ) & 7) << 4)) + j * RPJ * 128;
-          // nothing is read, and zeros are written, where bytes = 0 (q: an address that exists)
-          cp_async16(d, at >= 0 ? (const char*)a.k_cache + at + u * 16 : (const char*)a.q, bytes);
-          cp_async16(d + C::HALF, at >= 0 ? (const char*)a.v_cache + at + u * 16 : (const char*)a.q, bytes);
+        cp_async_commit();
+        if (unit >= D) {   // that tile has landed: for the tensor cores to read
+          cp_async_wait<D>();
+          fence_proxy_async_smem();
+          mbar_arrive(full((unit - D) % S));
         }
       }
-      cp_async_commit();
-      if (n > 0) {   // the tile before has landed: for the tensor cores to read
-        cp_async_wait<1>();
-        fence_proxy_async_smem();
-        mbar_arrive(full((n - 1) % S));
-      }
-      ++n;
-      if (++walk.tile == walk.end) more = shape.next_item(walk, sh.ends[1]);
     }
     cp_async_wait<0>();
     if (ok) {
       fence_proxy_async_smem();
-      mbar_arrive(full((n - 1) % S));
+      for (int i = max(0, unit - D); i < unit; ++i) mbar_arrive(full(i % S));
     }
   } else {
     // --------------------------------------------------------------- softmax
-    const int r = tid, t = r % a.T;
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    const int r = tid & 127, half = tid >> 7, t = r % a.T;
+    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) * 32 << 16);
+    constexpr int HD = H / 2;        // dims of o of a half
+    const int d0 = half * HD;
     bool ok = true;
-    int n = 0, meetings = 0;
-    // all four warps have got here (a barrier with a limit)
+    int n = 0, meetings = 0, pairs = 0;
+    // all eight warps have got here (a barrier with a limit)
     auto meet = [&]() -> bool {
       mbar_arrive(rows_met);
       return tc_wait(rows_met, meetings++ & 1, ab);
     };
-    while (true) {
-      const int64_t item = (int64_t)walk.b * a.K + walk.k;
-      const char* const src = (const char*)a.q + (item * R + r) * (H * 2);
+    // Place of unit u of a row's chunk: halves of one chunk (H = 64) keep to their
+    // four places, or all eight are turned.
+    auto turned = [&](int u) { return HC == 1 ? (u & 4) | ((u + r) & 3) : (u + r) & 7; };
+    // This thread's half of its query row; rows past the last are zeros.
+    auto load_q = [&](const DecodeWalk& w) {
+      const char* const src = (const char*)a.q + (((int64_t)w.b * a.K + w.k) * R + r) * (H * 2);
 #pragma unroll
-      for (int u = 0; u < H / 8; ++u) {
-        const uint4 x = r < R ? __ldg(reinterpret_cast<const uint4*>(src) + u) : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(sm + (u >> 3) * C::CHUNK + sw128_offset(r, u & 7)) = x;
+      for (int i = 0; i < HD / 8; ++i) {
+        const int u = half * (HD / 8) + i;
+        cp_async16(q_u + (u >> 3) * C::CHUNK + sw128_offset(r, u & 7),
+                   r < R ? src + u * 16 : (const char*)a.q, r < R ? 16 : 0);
       }
+      cp_async_commit();
+    };
+    auto q_loaded = [&]() {
+      cp_async_wait<0>();
       fence_proxy_async_smem();
       mbar_arrive(q_full);
+    };
+    load_q(walk);
+    q_loaded();
+    while (true) {
+      const int64_t item = (int64_t)walk.b * a.K + walk.k;
+      DecodeWalk then = walk;
+      const bool go_on = shape.next_item(then, sh.ends[1]);
       const int hi = walk.len - a.T + t + 1, lo = a.window > 0 ? hi - a.window : 0;   // keys of this row
       const int full_hi = walk.len - a.T + 1;                              // keys of every row
       const int full_lo = a.window > 0 ? max(0, walk.len - a.window) : 0;
@@ -245,11 +289,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
       for (; walk.tile < walk.end; ++walk.tile, ++n) {
         if (!(ok = tc_wait(s_full(n), (n >> 1) & 1, ab))) break;
         tc_fence_after();
+        // With the last scores computed, the queries' place is free for the next item's.
+        const bool last = walk.tile + 1 == walk.end;
+        if (last && go_on) load_q(then);
         const uint32_t s_col = lanes + 128 * (n & 1);
         const bool first = walk.tile == walk.begun;
         const int key0 = walk.first + walk.tile * C::TK;
         const bool masked = key0 < full_lo || key0 + C::TK > full_hi;
-        // 32 scores at a time, twice: for the maximum and for the weights
+        // 32 scores at a time, twice: for the maximum and for the weights; 64 a half
         auto load_s = [&](int i, uint32_t (&sv)[32]) {
           tmem_ld32(s_col + 32 * i, sv);
           tmem_wait_ld();
@@ -262,13 +309,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
         };
         float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
           uint32_t sv[32];
-          load_s(i, sv);
+          load_s(2 * half + i, sv);
 #pragma unroll
           for (int j = 0; j < 32; ++j) pm[j & 3] = fmaxf(pm[j & 3], __uint_as_float(sv[j]));
         }
-        const float top = LOG2E * fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+        float top = LOG2E * fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+        sh_top[n & 1][half][r] = top;
+        mbar_arrive(pair_met(warp));
+        if (!(ok = tc_wait(pair_met(warp), pairs++ & 1, ab))) break;
+        top = fmaxf(top, sh_top[n & 1][half ^ 1][r]);
         // The base is raised only where a score passes it by 8, as in paged_decode.cuh.
         float alpha = 1.0f;
         if (top > m + 8.0f || (first && top > m)) {
@@ -280,7 +331,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
           if (!(ok = tc_wait(pv_done(n - 1), ((n - 1) >> 1) & 1, ab))) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < H; c += 32) {
+          for (int c = d0; c < d0 + HD; c += 32) {
             uint32_t ov[32];
             tmem_ld32(lanes + O_COL + c, ov);
             tmem_wait_ld();
@@ -296,30 +347,34 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
           // Values that are not finite, of keys that some row does not keep: 0 x inf
           // would reach it.  Their products are done here, row by row, and they are
           // zeros to the tensor cores.
-          if (!(ok = tc_wait(full(n % S), (n / S) & 1, ab))) break;
-          uint8_t* const v_row = sm + C::HALF + (n % S) * C::SLOT + C::HALF + tid * 128;
-          bool bad = false;   // key `tid` of the tile
+          const int unit = 2 * n + 1;   // V(n)
+          if (!(ok = tc_wait(full(unit % S), (unit / S) & 1, ab))) break;
+          uint8_t* const v_tile = sm + C::SLOT + (unit % S) * C::SLOT;
+          uint8_t* const v_row = v_tile + r * 128;   // key r of the tile: half of its dims
+          bool bad = false;
 #pragma unroll
-          for (int c = 0; c < HC; ++c)
+          for (int i = 0; i < HC * 4; ++i) {
+            const int u = half * (HC * 4) + i;   // (places turned by the row, against bank conflicts)
+            const uint4 x = *reinterpret_cast<const uint4*>(v_row + (u >> 3) * C::CHUNK + turned(u) * 16);
+            const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint4 x = *reinterpret_cast<const uint4*>(v_row + c * C::CHUNK + i * 16);
-              const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                bad |= (y[j] & 0x7f80u) == 0x7f80u || (y[j] & 0x7f800000u) == 0x7f800000u;
-            }
+            for (int j = 0; j < 4; ++j)
+              bad |= (y[j] & 0x7f80u) == 0x7f80u || (y[j] & 0x7f800000u) == 0x7f800000u;
+          }
           const uint32_t ballot = __ballot_sync(~0u, bad);
           const uint32_t* const met = sh_bad[n & 1];
           if (lane == 0) sh_bad[n & 1][warp] = ballot;
           if (!(ok = meet())) break;
-          if (met[0] | met[1] | met[2] | met[3]) {
+          uint32_t any = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) any |= met[i];
+          if (any) {
             if (first) {
               uint32_t zero[32];
 #pragma unroll
               for (int i = 0; i < 32; ++i) zero[i] = 0;
 #pragma unroll 1
-              for (int c = 0; c < H; c += 32) tmem_st32(lanes + O_COL + c, zero);
+              for (int c = d0; c < d0 + HD; c += 32) tmem_st32(lanes + O_COL + c, zero);
               if (tid == 0) sh_keep = 1;
             } else {
               if (!(ok = tc_wait(pv_done(n - 1), ((n - 1) >> 1) & 1, ab))) break;
@@ -328,20 +383,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
             tmem_wait_st();
 #pragma unroll 1
             for (int key = 0; key < 128; ++key) {
-              if (!((met[key >> 5] >> (key & 31)) & 1u)) continue;
+              if (!(((met[key >> 5] | met[4 + (key >> 5)]) >> (key & 31)) & 1u)) continue;
               const bool kept = key0 + key >= lo && key0 + key < hi;
               const float x = tmem_ld1(s_col + key);
               tmem_wait_ld();
               const float p = fast_exp2(fmaf(x, LOG2E, -base));
-              const uint8_t* const v = sm + C::HALF + (n % S) * C::SLOT + C::HALF;
 #pragma unroll 1
-              for (int c = 0; c < H; c += 32) {
+              for (int c = d0; c < d0 + HD; c += 32) {
                 uint32_t ov[32];
                 tmem_ld32(lanes + O_COL + c, ov);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  const uint4 x8 = *reinterpret_cast<const uint4*>(v + (c >> 6) * C::CHUNK +
+                  const uint4 x8 = *reinterpret_cast<const uint4*>(v_tile + (c >> 6) * C::CHUNK +
                                                                    sw128_offset(key, (c & 63) / 8 + i));
                   const uint32_t y[4] = {x8.x, x8.y, x8.z, x8.w};
 #pragma unroll
@@ -359,23 +413,24 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
               }
             }
             if (!(ok = meet())) break;   // all rows have read them
-            if (bad) {
+            if (((met[warp & 3] | met[4 + (warp & 3)]) >> lane) & 1u) {
 #pragma unroll
-              for (int c = 0; c < HC; ++c)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  *reinterpret_cast<uint4*>(v_row + c * C::CHUNK + i * 16) = make_uint4(0, 0, 0, 0);
+              for (int i = 0; i < HC * 4; ++i) {
+                const int u = half * (HC * 4) + i;
+                *reinterpret_cast<uint4*>(v_row + (u >> 3) * C::CHUNK + turned(u) * 16) = make_uint4(0, 0, 0, 0);
+              }
             }
             __syncwarp();
             fence_proxy_async_smem();
           }
         }
 
-        // Weights as two bf16 terms (paged_decode.cuh): the cut over scores already
-        // read, the rest beside o.
+        // Weights as two bf16 terms (paged_decode.cuh): the cut over the scores that
+        // this half has read, the rest beside o.
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int h = 0; h < 2; ++h) {
+          const int i = 2 * half + h;
           uint32_t sv[32], cut[16], rest[16];
           load_s(i, sv);
 #pragma unroll
@@ -386,25 +441,30 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
             const float hx = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
             const float hy = __uint_as_float(__float_as_uint(y) & 0xffff0000u);
             cut[j] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-            rest[j] = pack_bf16x2(fmaf(x, 0x1p-20f, x - hx), fmaf(y, 0x1p-20f, y - hy));
+            rest[j] = pack_bf16x2(fmaf(x, 1 + 0x1p-20f, -hx), fmaf(y, 1 + 0x1p-20f, -hy));
           }
-          tmem_st16(s_col + 16 * i, cut);
+          tmem_st16(s_col + 64 * half + 16 * h, cut);
           tmem_st16(lanes + REST_COL + 64 * (n & 1) + 16 * i, rest);
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(p_full(n));
+        if (last && go_on) q_loaded();
       }
       // ---- end of the CTA's part of the item: o from tensor memory
       if (!ok || !(ok = tc_wait(pv_done(n - 1), ((n - 1) >> 1) & 1, ab))) break;
       tc_fence_after();
+      sh_top[n & 1][half][r] = l;
+      mbar_arrive(pair_met(warp));
+      if (!(ok = tc_wait(pair_met(warp), pairs++ & 1, ab))) break;
+      l += sh_top[n & 1][half ^ 1][r];
       const bool whole = walk.begun == 0 && walk.end == walk.tiles;
       const float f = l == 0.0f ? 0.0f : (a.v_scale ? __ldg(a.v_scale + walk.k) : 1.0f) / l;
       float* const mine =
           a.partials + ((int64_t)blockIdx.x * 2 + (walk.begun == 0 ? 1 : 0)) * paged_partial_floats(R, H);
 #pragma unroll 1
-      for (int c = 0; c < H; c += 32) {
+      for (int c = d0; c < d0 + HD; c += 32) {
         uint32_t ov[32];
         tmem_ld32(lanes + O_COL + c, ov);
         tmem_wait_ld();
@@ -425,7 +485,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
         }
         __syncwarp();
       }
-      if (r < R) {
+      if (r < R && half == 0) {
         if (whole) {
           a.lse[item * R + r] = (m + log2f(l)) * LN2;   // -inf with no key
         } else {
@@ -435,13 +495,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
       }
       if (whole && a.by_item && !a.unsplit && tid == 0) a.splits[item] = PagedDecodeSplit{(int)item, -1, 0, 0};
       tc_fence_before();
-      if (!shape.next_item(walk, sh.ends[1])) break;
+      if (!go_on) break;
+      walk = then;
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 10) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
