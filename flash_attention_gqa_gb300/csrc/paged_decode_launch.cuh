@@ -67,25 +67,22 @@ cudaError_t launch_decode(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
   return launch_decode<C, paged_decode_kernel<C>>(a, grid, st);
 }
 
-// Up to 8, 16 and (H <= 128: registers) 32 rows: warps on their own; more: tcgen05
-// for bf16 up to H = 128, else teams.
+// Up to 8, 16 and 32 rows: warps on their own (teams of two for 32 at H = 256:
+// registers).  More: tcgen05 for bf16, else teams.  Both sides of 32 for bf16, at
+// 16 requests x 4 kv heads x 8192 keys, mma.sync and tcgen05: at H = 128 32 rows
+// take 56 and 62 us, 64 rows 102 and 63; at H = 256 99 and 107, 202 and 110.
 template <int H, bool E4M3>
 cudaError_t launch_decode_rows(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
   const int R = a.G * a.T;
+  constexpr int NT = H == 256 ? 2 : 4, PER = NT * 8;   // rows a warp of a team
   if (R <= 8) return launch_decode<DecodeCfg<H, E4M3, 1, 1>>(a, grid, st);
   if (R <= 16) return launch_decode<DecodeCfg<H, E4M3, 2, 1>>(a, grid, st);
-  if constexpr (H <= 128) {
-    if (R <= 32) return launch_decode<DecodeCfg<H, E4M3, 4, 1>>(a, grid, st);
-    if constexpr (!E4M3) {
-      return launch_decode<DecodeTcCfg<H>, paged_decode_tc_kernel<DecodeTcCfg<H>>>(a, grid, st);
-    } else {
-      if (R <= 64) return launch_decode<DecodeCfg<H, E4M3, 4, 2>>(a, grid, st);
-      return launch_decode<DecodeCfg<H, E4M3, 4, 4>>(a, grid, st);
-    }
+  if (R <= 32) return launch_decode<DecodeCfg<H, E4M3, NT, 32 / PER>>(a, grid, st);
+  if constexpr (!E4M3) {
+    return launch_decode<DecodeTcCfg<H>, paged_decode_tc_kernel<DecodeTcCfg<H>>>(a, grid, st);
   } else {
-    if (R <= 32) return launch_decode<DecodeCfg<H, E4M3, 2, 2>>(a, grid, st);
-    if (R <= 64) return launch_decode<DecodeCfg<H, E4M3, 2, 4>>(a, grid, st);
-    return launch_decode<DecodeCfg<H, E4M3, 2, 8>>(a, grid, st);
+    if (R <= 64) return launch_decode<DecodeCfg<H, E4M3, NT, 64 / PER>>(a, grid, st);
+    return launch_decode<DecodeCfg<H, E4M3, NT, 128 / PER>>(a, grid, st);
   }
 }
 

@@ -1,5 +1,5 @@
-// Paged decode for 33 to 128 query rows per kv head, bf16 caches, H = 64 and 128:
-// tcgen05 products on tiles of 128 rows x 128 keys.
+// Paged decode for many query rows per kv head (up to 128), bf16 caches: tcgen05
+// products on tiles of 128 rows x 128 keys (64 at H = 256).
 //
 // The split over CTAs, the partials and the join are those of paged_decode.cuh;
 // only the work on a tile differs.  The query rows fill the 128-row operand
@@ -16,9 +16,9 @@
 //   warps 8, 9  copies: each 64 keys of a tile, by cp.async (pages may end
 //               anywhere, and keys past the request have to arrive as zeros)
 //   warp  10    products (lane 0), tensor memory
-// Tensor memory: S of tiles n and n + 1 at columns 0 and 128, o at 256.  The
-// weights' two bf16 terms, 64 columns each, are the A operands of o += P V: one
-// over its S (32 columns in each half of it), one at 384 or 448.
+// Tensor memory: S of tiles n and n + 1, o, and the weights' two bf16 terms, A
+// operands of o += P V: the one over its S (in each half of it), the other
+// beside o.
 // Shared memory: the queries and a ring of K and V tiles (K(0), V(0), K(1), ..),
 // in chunks of [rows x 128 B] with the 128-byte swizzle of the operand
 // descriptors.
@@ -30,15 +30,21 @@ namespace fa {
 template <int H_>
 struct DecodeTcCfg {
   static constexpr int H = H_, HC = H / 64;
-  static constexpr int CK = 128, TEAMS = 1, TK = 128;   // a tile is 128 keys
+  static constexpr int TN = H == 256 ? 64 : 128;        // keys of a tile
+  static constexpr int CK = TN, TEAMS = 1, TK = TN;
   static constexpr int ITEM_UNITS = 2;
   static constexpr int WARPS = 11, THREADS = WARPS * 32;
-  static constexpr int CHUNK = 128 * 128;               // 128 rows of 64 dims
+  static constexpr int QCHUNK = 128 * 128;              // 128 query rows of 64 dims
+  static constexpr int QBYTES = HC * QCHUNK;
+  static constexpr int CHUNK = TN * 128;                // TN keys of 64 dims
   static constexpr int SLOT = HC * CHUNK;               // a tile of K or of V
-  static constexpr int STAGES = H == 64 ? 12 : 6;       // 192 KB
+  static constexpr int STAGES = H == 64 ? 12 : H == 128 ? 6 : 5;   // 192, 192 and 160 KB
   static constexpr int FLIGHT = STAGES / 2;             // tiles in flight behind the newest
   static constexpr int RING = STAGES * SLOT;
-  static constexpr int SMEM = SLOT + RING;              // queries, ring
+  static constexpr int SMEM = QBYTES + RING;
+  // Tensor memory: S at 0 and TN, o at 256, the weights' second terms at REST_COL
+  // and TN / 2 behind it.
+  static constexpr uint32_t O_COL = 256, REST_COL = H == 256 ? 128 : 384;
   static constexpr int UPR = H / 8;                     // 16-byte units of a key
 };
 
@@ -56,7 +62,8 @@ __device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __grid_constant__ PagedDecodeArgs a) {
-  constexpr int H = C::H, HC = C::HC, S = C::STAGES;
+  constexpr int H = C::H, HC = C::HC, S = C::STAGES, TN = C::TN;
+  constexpr uint32_t O_COL = C::O_COL, REST_COL = C::REST_COL;
   constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
   extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ DecodeShared<C> sh;
@@ -66,7 +73,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
   __shared__ uint32_t sh_bad[2][8];    // keys of a tile (by its parity) whose value is not finite
   __shared__ float sh_top[2][2][128];  // [parity][half] largest scores of the rows; sums at the end
 
-  const uint32_t q_u = smem_u32(sm), ring_u = q_u + C::SLOT;
+  const uint32_t q_u = smem_u32(sm), ring_u = q_u + C::QBYTES;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int R = a.G * a.T;
   const DecodeShape<C> shape{a};
@@ -108,12 +115,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh_tmem;
-  constexpr uint32_t O_COL = 256, REST_COL = 384;
 
   if (warp == 10) {
     // -------------------------------------------------------------- products
     if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);   // S = Q K^T
+      constexpr uint32_t id_s = idesc_bf16(128, TN, false, false);   // S = Q K^T
       constexpr uint32_t id_o = idesc_bf16(128, H, false, true);      // o += P V
       const uint64_t dq = sdesc_sw128(q_u, 16, 1024), dk = sdesc_sw128(ring_u, 16, 1024);
       const uint64_t dv = sdesc_sw128(ring_u, C::CHUNK, 1024);
@@ -123,16 +129,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
         const int unit = 2 * n + 1;   // V(n)
         if (!mbar_wait(full(unit % S), (unit / S) & 1, ab) || !mbar_wait(p_full(n), (n >> 1) & 1, ab)) return false;
         tc_fence_after();
-        const uint32_t p = tmem + 128 * (n & 1);
+        const uint32_t p = tmem + TN * (n & 1);
         const uint64_t v = sdesc_add(dv, (unit % S) * C::SLOT);
         const bool keep = !first || *reinterpret_cast<volatile int*>(&sh_keep);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + O_COL, p + kk / 4 * 64 + kk % 4 * 8, sdesc_add(v, kk * 2048), id_o,
+        for (int kk = 0; kk < TN / 16; ++kk)
+          mma_ts(tmem + O_COL, p + kk / (TN / 32) * (TN / 2) + kk % (TN / 32) * 8, sdesc_add(v, kk * 2048), id_o,
                  keep || kk > 0 ? 1u : 0u);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + O_COL, tmem + REST_COL + 64 * (n & 1) + kk * 8, sdesc_add(v, kk * 2048), id_o, 1u);
+        for (int kk = 0; kk < TN / 16; ++kk)
+          mma_ts(tmem + O_COL, tmem + REST_COL + TN / 2 * (n & 1) + kk * 8, sdesc_add(v, kk * 2048), id_o, 1u);
         mma_commit(empty(unit % S));
         mma_commit(pv_done(n));
         return true;
@@ -148,7 +154,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
           for (int c = 0; c < HC; ++c)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_ss(tmem + 128 * (n & 1), sdesc_add(dq, c * C::CHUNK + kk * 32),
+              mma_ss(tmem + TN * (n & 1), sdesc_add(dq, c * C::QCHUNK + kk * 32),
                      sdesc_add(k, c * C::CHUNK + kk * 32), id_s, c > 0 || kk > 0 ? 1u : 0u);
           mma_commit(empty(unit % S));
           mma_commit(s_full(n));
@@ -171,17 +177,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
     const int64_t lane_src = (lane / C::UPR) * a.lay.token + (lane % C::UPR) * 16;
     const int64_t row_step = a.lay.token * RPJ;
     const int u = lane % C::UPR, lr = lane / C::UPR;   // unit and first row of this lane
-    const uint32_t lane_dst = (u >> 3) * C::CHUNK + (w * 64 + lr) * 128 + (((u & 7) ^ lr) << 4);
+    const uint32_t lane_dst = (u >> 3) * C::CHUNK + (w * (TN / 2) + lr) * 128 + (((u & 7) ^ lr) << 4);
     bool more = true, ok = true;
     int unit = 0;   // K(n): 2 n, V(n): 2 n + 1
-    // This lane's two keys of the next tile: looked up a tile early.
-    bool live[2];
-    int page[2], in[2], head = 0;
+    // This lane's keys of the next tile: looked up a tile early.
+    constexpr int NK = TN / 64;
+    bool live[NK];
+    int page[NK], in[NK], head = 0;
     auto look_up = [&]() {
       head = walk.k;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int s = walk.first + walk.tile * C::TK + w * 64 + h * 32 + lane;
+      for (int h = 0; h < NK; ++h) {
+        const int s = walk.first + walk.tile * TN + w * (TN / 2) + h * 32 + lane;
         live[h] = more && s >= shape.low(walk.len) && s < walk.len;
         in[h] = s & ((1 << a.lay.page_shift) - 1);
         page[h] = -1;
@@ -191,9 +198,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
     };
     look_up();
     while (more && ok) {
-      int64_t off[2];
+      int64_t off[NK];
+      bool all = true;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < NK; ++h) {
         off[h] = -1;
         if (live[h]) {
           if (page[h] >= 0 && page[h] < a.lay.n_pages)
@@ -201,10 +209,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
           else
             atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
         }
+        all &= off[h] >= 0;
       }
       if (++walk.tile == walk.end) more = shape.next_item(walk, sh.ends[1]);
       look_up();
-      const bool steps = a.lay.page_shift >= 4 && __all_sync(~0u, off[0] >= 0 && off[1] >= 0);
+      const bool steps = a.lay.page_shift >= 4 && __all_sync(~0u, all);
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++unit) {
         const char* const base = (const char*)(kv ? a.v_cache : a.k_cache);
@@ -212,7 +221,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
         const uint32_t dst = ring_u + (unit % S) * C::SLOT + lane_dst;
         if (steps) {
 #pragma unroll
-          for (int kt = 0; kt < 4; ++kt) {   // 16 keys or more a page: one offset per 16 keys, and steps
+          for (int kt = 0; kt < TN / 32; ++kt) {   // 16 keys or more a page: one offset per 16 keys, and steps
             const char* src = base + __shfl_sync(~0u, off[kt >> 1], (kt & 1) * 16) + lane_src;
 #pragma unroll
             for (int j = kt * 16 / RPJ; j < (kt + 1) * 16 / RPJ; ++j) {
@@ -222,9 +231,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
           }
         } else {
 #pragma unroll 1
-          for (int j = 0; j < 64 / RPJ; ++j) {
+          for (int j = 0; j < TN / 2 / RPJ; ++j) {
             const int row = j * RPJ + lr;
-            const int64_t at0 = __shfl_sync(~0u, off[0], row & 31), at1 = __shfl_sync(~0u, off[1], row & 31);
+            const int64_t at0 = __shfl_sync(~0u, off[0], row & 31), at1 = __shfl_sync(~0u, off[NK - 1], row & 31);
             const int64_t at = row < 32 ? at0 : at1;
             // nothing is read, and zeros are written, where there is no key (q: an address that exists)
             cp_async16((dst ^ (((j * RPJ) & 7) << 4)) + j * RPJ * 128,
@@ -257,16 +266,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
       mbar_arrive(rows_met);
       return tc_wait(rows_met, meetings++ & 1, ab);
     };
-    // Place of unit u of a row's chunk: halves of one chunk (H = 64) keep to their
-    // four places, or all eight are turned.
-    auto turned = [&](int u) { return HC == 1 ? (u & 4) | ((u + r) & 3) : (u + r) & 7; };
+    // For the search of V: this thread's key of a tile and its part of the key's
+    // 16-byte units, and the place in its chunk of a unit (turned by the key,
+    // against bank conflicts, within the part).
+    constexpr int PARTS = 256 / TN, UPP = HC * 8 / PARTS;
+    const int v_key = tid % TN, v_unit = tid / TN * UPP;
+    auto v_place = [&](int u) { return (u >> 3) * C::CHUNK + (UPP == 4 ? (u & 4) | ((u + v_key) & 3) : (u + v_key) & 7) * 16; };
     // This thread's half of its query row; rows past the last are zeros.
     auto load_q = [&](const DecodeWalk& w) {
       const char* const src = (const char*)a.q + (((int64_t)w.b * a.K + w.k) * R + r) * (H * 2);
 #pragma unroll
       for (int i = 0; i < HD / 8; ++i) {
         const int u = half * (HD / 8) + i;
-        cp_async16(q_u + (u >> 3) * C::CHUNK + sw128_offset(r, u & 7),
+        cp_async16(q_u + (u >> 3) * C::QCHUNK + sw128_offset(r, u & 7),
                    r < R ? src + u * 16 : (const char*)a.q, r < R ? 16 : 0);
       }
       cp_async_commit();
@@ -292,11 +304,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
         // With the last scores computed, the queries' place is free for the next item's.
         const bool last = walk.tile + 1 == walk.end;
         if (last && go_on) load_q(then);
-        const uint32_t s_col = lanes + 128 * (n & 1);
+        const uint32_t s_col = lanes + TN * (n & 1);
         const bool first = walk.tile == walk.begun;
-        const int key0 = walk.first + walk.tile * C::TK;
-        const bool masked = key0 < full_lo || key0 + C::TK > full_hi;
-        // 32 scores at a time, twice: for the maximum and for the weights; 64 a half
+        const int key0 = walk.first + walk.tile * TN;
+        const bool masked = key0 < full_lo || key0 + TN > full_hi;
+        // 32 scores at a time, twice: for the maximum and for the weights; TN / 2 a half
         auto load_s = [&](int i, uint32_t (&sv)[32]) {
           tmem_ld32(s_col + 32 * i, sv);
           tmem_wait_ld();
@@ -309,9 +321,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
         };
         float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < TN / 64; ++i) {
           uint32_t sv[32];
-          load_s(2 * half + i, sv);
+          load_s(TN / 64 * half + i, sv);
 #pragma unroll
           for (int j = 0; j < 32; ++j) pm[j & 3] = fmaxf(pm[j & 3], __uint_as_float(sv[j]));
         }
@@ -349,13 +361,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
           // zeros to the tensor cores.
           const int unit = 2 * n + 1;   // V(n)
           if (!(ok = tc_wait(full(unit % S), (unit / S) & 1, ab))) break;
-          uint8_t* const v_tile = sm + C::SLOT + (unit % S) * C::SLOT;
-          uint8_t* const v_row = v_tile + r * 128;   // key r of the tile: half of its dims
+          uint8_t* const v_tile = sm + C::QBYTES + (unit % S) * C::SLOT;
           bool bad = false;
 #pragma unroll
-          for (int i = 0; i < HC * 4; ++i) {
-            const int u = half * (HC * 4) + i;   // (places turned by the row, against bank conflicts)
-            const uint4 x = *reinterpret_cast<const uint4*>(v_row + (u >> 3) * C::CHUNK + turned(u) * 16);
+          for (int i = 0; i < UPP; ++i) {
+            const uint4 x = *reinterpret_cast<const uint4*>(v_tile + v_key * 128 + v_place(v_unit + i));
             const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -365,9 +375,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
           const uint32_t* const met = sh_bad[n & 1];
           if (lane == 0) sh_bad[n & 1][warp] = ballot;
           if (!(ok = meet())) break;
+          // keys 32 i .. 32 i + 31
+          auto bad_keys = [&](int i) {
+            uint32_t x = 0;
+#pragma unroll
+            for (int p = 0; p < PARTS; ++p) x |= met[p * (TN / 32) + i];
+            return x;
+          };
           uint32_t any = 0;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) any |= met[i];
+          for (int i = 0; i < TN / 32; ++i) any |= bad_keys(i);
           if (any) {
             if (first) {
               uint32_t zero[32];
@@ -382,8 +399,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
             }
             tmem_wait_st();
 #pragma unroll 1
-            for (int key = 0; key < 128; ++key) {
-              if (!(((met[key >> 5] | met[4 + (key >> 5)]) >> (key & 31)) & 1u)) continue;
+            for (int key = 0; key < TN; ++key) {
+              if (!((bad_keys(key >> 5) >> (key & 31)) & 1u)) continue;
               const bool kept = key0 + key >= lo && key0 + key < hi;
               const float x = tmem_ld1(s_col + key);
               tmem_wait_ld();
@@ -413,12 +430,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
               }
             }
             if (!(ok = meet())) break;   // all rows have read them
-            if (((met[warp & 3] | met[4 + (warp & 3)]) >> lane) & 1u) {
+            if ((bad_keys(v_key >> 5) >> lane) & 1u) {
 #pragma unroll
-              for (int i = 0; i < HC * 4; ++i) {
-                const int u = half * (HC * 4) + i;
-                *reinterpret_cast<uint4*>(v_row + (u >> 3) * C::CHUNK + turned(u) * 16) = make_uint4(0, 0, 0, 0);
-              }
+              for (int i = 0; i < UPP; ++i)
+                *reinterpret_cast<uint4*>(v_tile + v_key * 128 + v_place(v_unit + i)) = make_uint4(0, 0, 0, 0);
             }
             __syncwarp();
             fence_proxy_async_smem();
@@ -429,8 +444,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
         // this half has read, the rest beside o.
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int i = 2 * half + h;
+        for (int h = 0; h < TN / 64; ++h) {
+          const int i = TN / 64 * half + h;
           uint32_t sv[32], cut[16], rest[16];
           load_s(i, sv);
 #pragma unroll
@@ -443,8 +458,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
             cut[j] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
             rest[j] = pack_bf16x2(fmaf(x, 1 + 0x1p-20f, -hx), fmaf(y, 1 + 0x1p-20f, -hy));
           }
-          tmem_st16(s_col + 64 * half + 16 * h, cut);
-          tmem_st16(lanes + REST_COL + 64 * (n & 1) + 16 * i, rest);
+          tmem_st16(s_col + TN / 2 * half + 16 * h, cut);
+          tmem_st16(lanes + REST_COL + TN / 2 * (n & 1) + 16 * i, rest);
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_wait_st();
@@ -455,10 +470,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
       // ---- end of the CTA's part of the item: o from tensor memory
       if (!ok || !(ok = tc_wait(pv_done(n - 1), ((n - 1) >> 1) & 1, ab))) break;
       tc_fence_after();
-      sh_top[n & 1][half][r] = l;
+      // the last tile's place, which all have read; the next tile's may be written before it is read
+      float(&sums)[2][128] = sh_top[(n - 1) & 1];
+      sums[half][r] = l;
       mbar_arrive(pair_met(warp));
       if (!(ok = tc_wait(pair_met(warp), pairs++ & 1, ab))) break;
-      l += sh_top[n & 1][half ^ 1][r];
+      l += sums[half ^ 1][r];
       const bool whole = walk.begun == 0 && walk.end == walk.tiles;
       const float f = l == 0.0f ? 0.0f : (a.v_scale ? __ldg(a.v_scale + walk.k) : 1.0f) / l;
       float* const mine =
@@ -498,6 +515,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
       if (!go_on) break;
       walk = then;
     }
+    cp_async_wait<0>();   // queries of a next item, where a wait has run out
   }
 
   tc_fence_before();

@@ -294,6 +294,36 @@ def test_decode_ragged_batch(lib):
     _check(P.problem(4, B=300, K=2, G=4, T=1, H=64, lens=lens, page=16))
 
 
+@pytest.mark.parametrize("page", [1, 4, 8, 16, 128])
+@pytest.mark.parametrize("rows", [(40, 1), (12, 5)], ids=lambda r: "G%d_T%d" % r)
+def test_decode_many_rows_page_sizes_and_layouts(lib, rows, page):
+    G, T = rows
+    for H, layout, dtype in ((64, "head", BF16), (128, "token", BF16), (256, "token", BF16),
+                             (128, "token", E4M3)):
+        _check(P.problem(page, B=4, K=2, G=G, T=T, H=H, lens=[300, 3, 129, 64], page=page,
+                         layout=layout, dtype=dtype, pad=32))
+
+
+def test_decode_many_rows_ragged_batch(lib):
+    """Several requests a CTA: the next one's queries arrive during the last one's end."""
+    rng = np.random.default_rng(1)
+    lens = [int(x) for x in np.exp(rng.uniform(0, math.log(900), 220))]
+    for H, G, T in ((64, 33, 1), (128, 9, 4), (256, 40, 1)):
+        p = P.problem(H, B=220, K=2, G=G, T=T, H=H, lens=lens, page=16)
+        o, lse = _check(p)
+        again = _decode(p)
+        assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+def test_decode_many_rows_large_scores(lib):
+    """The base of the exponents moves, and o with it, along the keys."""
+    for H in (64, 128, 256):
+        p = P.problem(9, B=3, K=1, G=64, T=1, H=H, lens=[900, 64, 1], page=16)
+        q, kc, *_ = p
+        kc.mul_(torch.linspace(0.05, 3, kc.shape[0])[:, None, None, None].bfloat16())
+        _check(((q.float() * 40).bfloat16(), *p[1:]))
+
+
 @pytest.mark.parametrize("dtype", [BF16, E4M3], ids=["bf16", "e4m3"])
 @pytest.mark.parametrize("B", [3, 200])
 @pytest.mark.parametrize("longest", [64, 256, 272, 512, 528])
@@ -357,10 +387,11 @@ def test_decode_infinities_and_nan_of_masked_keys_stay_there(lib, G):
                        want, 64, dtype == E4M3, 40)
 
 
-def test_decode_infinities_of_kept_keys(lib):
+@pytest.mark.parametrize("G", [4, 36])
+def test_decode_infinities_of_kept_keys(lib, G):
     """An infinite value that a query keeps is in its result as such; scores of -inf have no weight,
     and one of +inf leaves no number."""
-    p = P.problem(21, B=3, K=1, G=4, T=1, H=64, lens=[300, 1, 40], page=16)
+    p = P.problem(21, B=3, K=1, G=G, T=1, H=64, lens=[300, 1, 40], page=16)
     q, kc, vc, table, lens, *_ = p
     q.abs_().clamp_(min=1e-3)
     at = lambda b, s: (int(table[b, s // 16]), 0, s % 16)
@@ -372,7 +403,7 @@ def test_decode_infinities_of_kept_keys(lib):
     inf, none = torch.isinf(o[..., 0, :]), torch.isnan(o[..., 0, :])
     assert (o[0, 0, :, 0, 2] == math.inf).all() and (o[0, 0, :, 0, 3] == -math.inf).all()
     assert (o[1, 0, :, 0, 4] == math.inf).all() and none[0, 0, :, 6].all()
-    assert inf.sum() == 12 and none.sum() == 4
+    assert inf.sum() == 3 * G and none.sum() == G
     # the key of -inf scores counts as absent
     n = 40
     keep = [s for s in range(n) if s != 7]
