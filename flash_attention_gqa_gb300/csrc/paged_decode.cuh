@@ -997,14 +997,16 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
 // Few registers and threads a CTA, so that the whole grid starts at once as the
 // first one ends (512 threads of 75 registers, one CTA an SM, took 4 us).
 template <int H, int U, int THREADS>
-__global__ void __launch_bounds__(THREADS) paged_join_kernel(const __grid_constant__ PagedDecodeArgs a, int per) {
+__global__ void __launch_bounds__(THREADS)
+paged_join_kernel(const __grid_constant__ PagedDecodeArgs a, int ctas, int per) {
   __shared__ float4 sx[THREADS];
   __shared__ float2 sml[THREADS];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // (L2 loads: this grid may have started before the first one wrote)
   const int4 split = __ldcg(reinterpret_cast<const int4*>(a.splits) + blockIdx.x);
   const int item = split.x, first = split.y, n = split.z - first + 1;   // n partials
-  if (first < 0) return;
+  // (an entry of a whole item holds anything where a wait of the first kernel ran out before it)
+  if (first < 0 || split.z < first || split.z >= ctas || (unsigned)item >= (unsigned)(a.B * a.K)) return;
   const int R = a.G * a.T, shares = blockDim.x / per;
   const int share = threadIdx.x / per, at = threadIdx.x % per;
   const int i = blockIdx.y * per + at;

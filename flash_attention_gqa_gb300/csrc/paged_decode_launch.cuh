@@ -38,9 +38,9 @@ cudaError_t launch_join(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
   cfg.gridDim = dim3(a.by_item ? items : grid, (elements + per - 1) / per);
   cfg.blockDim = dim3(shares * per);
   switch (shares) {
-    case 1: return cudaLaunchKernelEx(&cfg, paged_join_kernel<H, 4, 256>, a, per);
-    case 2: return cudaLaunchKernelEx(&cfg, paged_join_kernel<H, 8, 256>, a, per);
-    default: return cudaLaunchKernelEx(&cfg, paged_join_kernel<H, 8, 512>, a, per);
+    case 1: return cudaLaunchKernelEx(&cfg, paged_join_kernel<H, 4, 256>, a, grid, per);
+    case 2: return cudaLaunchKernelEx(&cfg, paged_join_kernel<H, 8, 256>, a, grid, per);
+    default: return cudaLaunchKernelEx(&cfg, paged_join_kernel<H, 8, 512>, a, grid, per);
   }
 }
 

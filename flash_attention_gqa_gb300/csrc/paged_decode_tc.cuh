@@ -164,9 +164,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
         if (ok) ok = issue_pv(n - 1, walk.end - 1 == walk.begun);
         if (!shape.next_item(walk, sh.ends[1])) break;
       }
-      if (!ok) {   // until the products issued are over (bounded): tensor memory is freed below
+      if (!ok) {   // until the products issued are over: tensor memory is freed below
         mma_commit(teardown);
-        mbar_wait_teardown(teardown, 0, a.wait_limit_ns);
+        mbar_wait_teardown(teardown, 0, max(a.wait_limit_ns, (uint64_t)1000000000));   // they take microseconds
       }
     }
     __syncwarp();
@@ -515,7 +515,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
       if (!go_on) break;
       walk = then;
     }
-    cp_async_wait<0>();   // queries of a next item, where a wait has run out
+    if (!ok) {   // a wait has run out: until what is in flight has landed
+      cp_async_wait<0>();
+      tmem_wait_st();
+    }
   }
 
   tc_fence_before();
