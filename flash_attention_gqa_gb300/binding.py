@@ -507,6 +507,17 @@ def attention_backward(q, k, v, o, lse, dO, *, causal=False, seg_q=None, seg_kv=
     return dq, dk, dv
 
 
+def _allocating_on(stream, device):
+    """Scope in which torch allocates from the memory of `stream` (None: the current one): memory of
+    another stream could be given out again before this one's work is over."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if stream
+                  else torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
+
+
 def paged_tables(cached_lens, new_lens, free_pages, free_used, block_table, *, n_pages, page_size,
                  max_tokens, stream=None):
     """Allocate a step's outputs with torch and run fa_paged_tables, which also writes the
@@ -514,8 +525,9 @@ def paged_tables(cached_lens, new_lens, free_pages, free_used, block_table, *, n
     free_used) tensors, the last for the next step."""
     new = lambda n, dtype=torch.int32: torch.empty(n, dtype=dtype, device=cached_lens.device)
     B = cached_lens.shape[0]
-    total, starts, used = new(B), new(B + 1), new(1)
-    slots, positions = new(max_tokens, torch.int64), new(max_tokens)
+    with _allocating_on(stream, cached_lens.device):
+        total, starts, used = new(B), new(B + 1), new(1)
+        slots, positions = new(max_tokens, torch.int64), new(max_tokens)
     fa_paged_tables(cached_lens, new_lens, free_pages, free_used, block_table, total, starts, slots,
                     positions, used, n_pages, page_size, stream)
     return total, starts, slots, positions, used
@@ -525,12 +537,12 @@ def paged_attention_decode(q, k_cache, v_cache, block_table, lens, *, k_scale=No
                            window=0, stream=None, workspace=None):
     """Allocate o / lse (and the workspace unless given) and run fa_paged_decode."""
     B, K, G, T, H = q.shape
-    o = torch.empty_like(q)
-    lse = torch.empty((B, K, G, T), dtype=torch.float32, device=q.device)
-    if workspace is None:
-        with torch.cuda.device(q.device):
+    with _allocating_on(stream, q.device):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, K, G, T), dtype=torch.float32, device=q.device)
+        if workspace is None:
             n = fa_paged_decode_workspace_size(B, K, G, T, H)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+            workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
     fa_paged_decode(q, k_cache, v_cache, block_table, lens, o, lse, workspace, k_scale, v_scale,
                     window, stream)
     return o, lse

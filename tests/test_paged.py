@@ -540,6 +540,32 @@ def test_decode_on_two_streams(lib):
     _ok()
 
 
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "address"])
+def test_helpers_allocate_on_the_stream_of_the_call(lib, raw, monkeypatch):
+    """What a call on a side stream allocates and lets go of is not given to the current one."""
+    p = P.problem(15, B=4, K=2, G=8, T=1, H=128, lens=[900, 3000, 17, 64], page=16)
+    want = _decode(p)
+    q, table, lens = (p[i].cuda() for i in (0, 3, 4))
+    caches = [P.to_device(x, "cuda") for x in p[1:3]]
+    torch.cuda.synchronize()
+    side, seen = torch.cuda.Stream(), []
+    plain = binding.fa_paged_decode
+    monkeypatch.setattr(binding, "fa_paged_decode",
+                        lambda *a: (seen.append((a[7].data_ptr(), a[7].nbytes)), plain(*a))[1])
+    got = binding.paged_attention_decode(q, *caches, table, lens,
+                                         stream=side.cuda_stream if raw else side)
+    (at, size), = seen
+    others = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    assert at not in [x.data_ptr() for x in others]
+    steps = binding.paged_tables(_i32([3, 0]), _i32([1, 2]), _i32([0, 1]), _i32([0]),
+                                 _i32([[2], [0]]), n_pages=3, page_size=4, max_tokens=4,
+                                 stream=side.cuda_stream if raw else side)
+    side.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert steps[2].tolist() == [11, 0, 1, -1]
+    _ok()
+
+
 def test_empty_row_of_queries(lib):
     for shape in ((0, 2, 4, 1, 64), (2, 0, 4, 1, 64), (2, 2, 4, 0, 64)):
         q = torch.zeros(shape, dtype=BF16, device="cuda")
