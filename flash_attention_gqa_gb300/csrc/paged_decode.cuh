@@ -71,6 +71,10 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(addr));
   return x;
 }
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 x) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -100,6 +104,17 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t
   asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
       "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
       : "=r"(lo), "=r"(hi) : "r"(x));
+}
+
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t x) { return __half22float2(*reinterpret_cast<__half2*>(&x)); }
+
+// For 8-bit caches a query row, `big` its largest value, is scaled to [2^10, 2^11)
+// (1 for rows of zeros or infinities) and rounded to f16: exact for bf16 values down
+// to 2^-27 of the largest.
+__device__ __forceinline__ void e4m3_query_scale(float big, float& up, float& down) {
+  const int e = big > 0.0f && big < INFINITY ? min(10 - ((int)(__float_as_uint(big) >> 23) - 127), 126) : 0;
+  up = __uint_as_float((uint32_t)(e + 127) << 23);
+  down = __uint_as_float((uint32_t)(127 - e) << 23);
 }
 
 // The base of a column that has met no score: finite, so that masked scores
@@ -473,8 +488,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       }
     }
   };
-  // For 8-bit caches rows are scaled to [2^10, 2^11) and rounded to f16: exact for
-  // bf16 values down to 2^-27 of the row's largest.  Returns what undoes it.
+  // The rows of an n-tile, scaled and rounded to f16 for 8-bit caches.  Returns what
+  // undoes it.
   auto scale_q = [&](uint2 (&x)[KS]) -> float {
     float big = 0.0f;
 #pragma unroll
@@ -484,16 +499,14 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     }
     big = fmaxf(big, __shfl_xor_sync(~0u, big, 1));
     big = fmaxf(big, __shfl_xor_sync(~0u, big, 2));
-    // 2^e with big * 2^e in [2^10, 2^11); 1 for rows of zeros or infinities
-    const int e = big > 0.0f && big < INFINITY
-                      ? min(10 - ((int)(__float_as_uint(big) >> 23) - 127), 126) : 0;
-    const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+    float up, down;
+    e4m3_query_scale(big, up, down);
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const float2 p = unpack_bf16x2(x[ks].x), q = unpack_bf16x2(x[ks].y);
       x[ks] = make_uint2(pack_f16x2(p.x * up, p.y * up), pack_f16x2(q.x * up, q.y * up));
     }
-    return __uint_as_float((uint32_t)(127 - e) << 23);
+    return down;
   };
   // The next item's queries are read while this one's results are written,
   // where registers allow it.

@@ -68,9 +68,10 @@ cudaError_t launch_decode(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
 }
 
 // Up to 8, 16 and 32 rows: warps on their own (teams of two for 32 at H = 256:
-// registers).  More: tcgen05 for bf16, else teams.  Both sides of 32 for bf16, at
-// 16 requests x 4 kv heads x 8192 keys, mma.sync and tcgen05: at H = 128 32 rows
-// take 56 and 62 us, 64 rows 102 and 63; at H = 256 99 and 107, 202 and 110.
+// registers).  More: tcgen05.  Both sides of 32 at 16 requests x 4 kv heads x 8192
+// keys, mma.sync and tcgen05: bf16 at H = 128 32 rows take 56 and 62 us, 64 rows
+// 102 and 63; at H = 256 99 and 107, 202 and 110.  8-bit at H = 128 64 rows 79 and
+// 65, 128 rows 139 and 69.
 template <int H, bool E4M3>
 cudaError_t launch_decode_rows(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
   const int R = a.G * a.T;
@@ -78,12 +79,8 @@ cudaError_t launch_decode_rows(const PagedDecodeArgs& a, int grid, cudaStream_t 
   if (R <= 8) return launch_decode<DecodeCfg<H, E4M3, 1, 1>>(a, grid, st);
   if (R <= 16) return launch_decode<DecodeCfg<H, E4M3, 2, 1>>(a, grid, st);
   if (R <= 32) return launch_decode<DecodeCfg<H, E4M3, NT, 32 / PER>>(a, grid, st);
-  if constexpr (!E4M3) {
-    return launch_decode<DecodeTcCfg<H>, paged_decode_tc_kernel<DecodeTcCfg<H>>>(a, grid, st);
-  } else {
-    if (R <= 64) return launch_decode<DecodeCfg<H, E4M3, NT, 64 / PER>>(a, grid, st);
-    return launch_decode<DecodeCfg<H, E4M3, NT, 128 / PER>>(a, grid, st);
-  }
+  using Tc = DecodeTcCfg<H, E4M3>;
+  return launch_decode<Tc, paged_decode_tc_kernel<Tc>>(a, grid, st);
 }
 
 }  // namespace fa

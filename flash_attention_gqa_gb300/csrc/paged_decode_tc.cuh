@@ -27,25 +27,31 @@
 
 namespace fa {
 
-template <int H_>
+template <int H_, bool E4M3_>
 struct DecodeTcCfg {
   static constexpr int H = H_, HC = H / 64;
+  static constexpr bool E4M3 = E4M3_;
   static constexpr int TN = H == 256 ? 64 : 128;        // keys of a tile
   static constexpr int CK = TN, TEAMS = 1, TK = TN;
   static constexpr int ITEM_UNITS = 2;
-  static constexpr int WARPS = 11, THREADS = WARPS * 32;
+  static constexpr int CW = E4M3 ? 4 : 2;               // copying warps
+  static constexpr int WARPS = 9 + CW, THREADS = WARPS * 32;
+  static constexpr int KPW = TN / CW;                   // keys of a tile a copying warp
   static constexpr int QCHUNK = 128 * 128;              // 128 query rows of 64 dims
   static constexpr int QBYTES = HC * QCHUNK;
   static constexpr int CHUNK = TN * 128;                // TN keys of 64 dims
   static constexpr int SLOT = HC * CHUNK;               // a tile of K or of V
-  static constexpr int STAGES = H == 64 ? 12 : H == 128 ? 6 : 5;   // 192, 192 and 160 KB
-  static constexpr int FLIGHT = STAGES / 2;             // tiles in flight behind the newest
+  // bf16: 192, 192 and 160 KB.  8-bit: 96, 128 and 96 KB of f16 tiles, and 80, 64 and
+  // 64 KB of bytes that wait for their conversion.
+  static constexpr int STAGES = E4M3 ? (H == 64 ? 6 : H == 128 ? 4 : 3) : H == 64 ? 12 : H == 128 ? 6 : 5;
+  static constexpr int RAW = E4M3 ? TN * H : 0, RAW_STAGES = H == 64 ? 10 : 4;
+  static constexpr int FLIGHT = E4M3 ? RAW_STAGES - 1 : STAGES / 2;   // tiles in flight behind the newest
   static constexpr int RING = STAGES * SLOT;
-  static constexpr int SMEM = QBYTES + RING;
+  static constexpr int SMEM = QBYTES + RING + RAW_STAGES * RAW;
   // Tensor memory: S at 0 and TN, o at 256, the weights' second terms at REST_COL
   // and TN / 2 behind it.
   static constexpr uint32_t O_COL = 256, REST_COL = H == 256 ? 128 : 384;
-  static constexpr int UPR = H / 8;                     // 16-byte units of a key
+  static constexpr int UPR = (E4M3 ? 1 : 2) * H / 16;   // 16-byte units of a key
 };
 
 // The bounded waits of this kernel's barriers, each by whole warps.
@@ -63,6 +69,7 @@ __device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __grid_constant__ PagedDecodeArgs a) {
   constexpr int H = C::H, HC = C::HC, S = C::STAGES, TN = C::TN;
+  constexpr bool E4M3 = C::E4M3;
   constexpr uint32_t O_COL = C::O_COL, REST_COL = C::REST_COL;
   constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -93,7 +100,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
   if (tid == 0) {
     sh_abort = 0;
     for (int s = 0; s < S; ++s) {
-      mbar_init(full(s), 64);
+      mbar_init(full(s), C::CW * 32);
       mbar_init(empty(s), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -107,7 +114,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
     mbar_init(teardown, 1);
     fence_barrier_init();
   }
-  if (warp == 10) {
+  if (warp == C::WARPS - 1) {
     tmem_alloc(smem_u32(&sh_tmem), 512);
     tmem_relinquish();
   }
@@ -116,11 +123,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
   tc_fence_after();
   const uint32_t tmem = sh_tmem;
 
-  if (warp == 10) {
+  if (warp == C::WARPS - 1) {
     // -------------------------------------------------------------- products
     if (lane == 0) {
-      constexpr uint32_t id_s = idesc_bf16(128, TN, false, false);   // S = Q K^T
-      constexpr uint32_t id_o = idesc_bf16(128, H, false, true);      // o += P V
+      constexpr auto idesc = E4M3 ? idesc_f16 : idesc_bf16;
+      constexpr uint32_t id_s = idesc(128, TN, false, false);   // S = Q K^T
+      constexpr uint32_t id_o = idesc(128, H, false, true);      // o += P V
       const uint64_t dq = sdesc_sw128(q_u, 16, 1024), dk = sdesc_sw128(ring_u, 16, 1024);
       const uint64_t dv = sdesc_sw128(ring_u, C::CHUNK, 1024);
       bool ok = true;
@@ -137,7 +145,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
           mma_ts(tmem + O_COL, p + kk / (TN / 32) * (TN / 2) + kk % (TN / 32) * 8, sdesc_add(v, kk * 2048), id_o,
                  keep || kk > 0 ? 1u : 0u);
 #pragma unroll
-        for (int kk = 0; kk < TN / 16; ++kk)
+        for (int kk = 0; !E4M3 && kk < TN / 16; ++kk)
           mma_ts(tmem + O_COL, tmem + REST_COL + TN / 2 * (n & 1) + kk * 8, sdesc_add(v, kk * 2048), id_o, 1u);
         mma_commit(empty(unit % S));
         mma_commit(pv_done(n));
@@ -173,22 +181,51 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- copies
     const int w = warp - 8;
-    constexpr int RPJ = 32 / C::UPR, D = C::FLIGHT;   // rows a copy of the warp; tiles in flight
+    constexpr int RPJ = 32 / C::UPR, NJ = C::KPW / RPJ, D = C::FLIGHT;   // rows a copy of the warp; copies
     const int64_t lane_src = (lane / C::UPR) * a.lay.token + (lane % C::UPR) * 16;
     const int64_t row_step = a.lay.token * RPJ;
     const int u = lane % C::UPR, lr = lane / C::UPR;   // unit and first row of this lane
-    const uint32_t lane_dst = (u >> 3) * C::CHUNK + (w * (TN / 2) + lr) * 128 + (((u & 7) ^ lr) << 4);
+    // 8-bit: this thread's units of a tile wait in places of its own, and are two units each as f16
+    const int u16 = E4M3 ? 2 * u : u;
+    const uint32_t lane_dst = (u16 >> 3) * C::CHUNK + (w * C::KPW + lr) * 128 + (((u16 & 7) ^ lr) << 4);
+    const uint32_t raw_u = ring_u + C::RING + w * (C::RAW / C::CW) + lane * 16;
+    auto place = [&](int unit, int j) -> uint32_t {   // of copy j
+      return E4M3 ? raw_u + unit % C::RAW_STAGES * C::RAW + j * 512
+                  : ring_u + unit % S * C::SLOT + (lane_dst ^ (((j * RPJ) & 7) << 4)) + j * RPJ * 128;
+    };
+    // Tile `unit` has landed: for the tensor cores to read, 8-bit values as f16 (exact).
+    auto hand_over = [&](int unit) -> bool {
+      if constexpr (E4M3) {
+        if (unit >= S && !tc_wait(empty(unit % S), (unit / S - 1) & 1, ab)) return false;
+        const uint32_t turn = (u >> 2 & 1) << 4;   // four lanes write the odd unit first: other banks
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const uint4 x = lds16(place(unit, j));
+          uint4 y[2];
+          e4m3x4_to_f16(x.x, y[0].x, y[0].y);
+          e4m3x4_to_f16(x.y, y[0].z, y[0].w);
+          e4m3x4_to_f16(x.z, y[1].x, y[1].y);
+          e4m3x4_to_f16(x.w, y[1].z, y[1].w);
+          const uint32_t dst = ring_u + unit % S * C::SLOT + (lane_dst ^ (((j * RPJ) & 7) << 4)) + j * RPJ * 128;
+          sts16(dst ^ turn, turn ? y[1] : y[0]);
+          sts16(dst ^ turn ^ 16, turn ? y[0] : y[1]);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(full(unit % S));
+      return true;
+    };
     bool more = true, ok = true;
     int unit = 0;   // K(n): 2 n, V(n): 2 n + 1
     // This lane's keys of the next tile: looked up a tile early.
-    constexpr int NK = TN / 64;
+    constexpr int NK = C::KPW < 32 ? 1 : C::KPW / 32;
     bool live[NK];
     int page[NK], in[NK], head = 0;
     auto look_up = [&]() {
       head = walk.k;
 #pragma unroll
       for (int h = 0; h < NK; ++h) {
-        const int s = walk.first + walk.tile * TN + w * (TN / 2) + h * 32 + lane;
+        const int s = walk.first + walk.tile * TN + w * C::KPW + h * 32 + lane % C::KPW;
         live[h] = more && s >= shape.low(walk.len) && s < walk.len;
         in[h] = s & ((1 << a.lay.page_shift) - 1);
         page[h] = -1;
@@ -217,42 +254,36 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++unit) {
         const char* const base = (const char*)(kv ? a.v_cache : a.k_cache);
-        if (unit >= S && !(ok = tc_wait(empty(unit % S), (unit / S - 1) & 1, ab))) break;
-        const uint32_t dst = ring_u + (unit % S) * C::SLOT + lane_dst;
+        if (!E4M3 && unit >= S && !(ok = tc_wait(empty(unit % S), (unit / S - 1) & 1, ab))) break;
         if (steps) {
 #pragma unroll
-          for (int kt = 0; kt < TN / 32; ++kt) {   // 16 keys or more a page: one offset per 16 keys, and steps
+          for (int kt = 0; kt < C::KPW / 16; ++kt) {   // 16 keys or more a page: one offset per 16 keys, and steps
             const char* src = base + __shfl_sync(~0u, off[kt >> 1], (kt & 1) * 16) + lane_src;
 #pragma unroll
             for (int j = kt * 16 / RPJ; j < (kt + 1) * 16 / RPJ; ++j) {
-              cp_async16((dst ^ (((j * RPJ) & 7) << 4)) + j * RPJ * 128, src, 16);
+              cp_async16(place(unit, j), src, 16);
               src += row_step;
             }
           }
         } else {
 #pragma unroll 1
-          for (int j = 0; j < TN / 2 / RPJ; ++j) {
+          for (int j = 0; j < NJ; ++j) {
             const int row = j * RPJ + lr;
             const int64_t at0 = __shfl_sync(~0u, off[0], row & 31), at1 = __shfl_sync(~0u, off[NK - 1], row & 31);
             const int64_t at = row < 32 ? at0 : at1;
             // nothing is read, and zeros are written, where there is no key (q: an address that exists)
-            cp_async16((dst ^ (((j * RPJ) & 7) << 4)) + j * RPJ * 128,
-                       at >= 0 ? base + at + u * 16 : (const char*)a.q, at >= 0 ? 16 : 0);
+            cp_async16(place(unit, j), at >= 0 ? base + at + u * 16 : (const char*)a.q, at >= 0 ? 16 : 0);
           }
         }
         cp_async_commit();
-        if (unit >= D) {   // that tile has landed: for the tensor cores to read
+        if (unit >= D) {
           cp_async_wait<D>();
-          fence_proxy_async_smem();
-          mbar_arrive(full((unit - D) % S));
+          if (!(ok = hand_over(unit - D))) break;
         }
       }
     }
     cp_async_wait<0>();
-    if (ok) {
-      fence_proxy_async_smem();
-      for (int i = max(0, unit - D); i < unit; ++i) mbar_arrive(full(i % S));
-    }
+    for (int i = max(0, unit - D); ok && i < unit; ++i) ok = hand_over(i);
   } else {
     // --------------------------------------------------------------- softmax
     const int r = tid & 127, half = tid >> 7, t = r % a.T;
@@ -283,15 +314,51 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
       }
       cp_async_commit();
     };
-    auto q_loaded = [&]() {
+    // What turns a product of the row into log2 units.  8-bit caches: queries as f16, their
+    // rows scaled to [2^10, 2^11) as in paged_decode.cuh (`met`: a place of sh_top that is free).
+    float sl2 = LOG2E, sl2_next = LOG2E;
+    auto q_loaded = [&](const DecodeWalk& w, float (&met)[2][128]) -> bool {
       cp_async_wait<0>();
+      if constexpr (E4M3) {
+        auto place = [&](int i) { return q_u + ((half * (HD / 8) + i) >> 3) * C::QCHUNK + sw128_offset(r, (half * (HD / 8) + i) & 7); };
+        float big = 0.0f;
+#pragma unroll 4
+        for (int i = 0; i < HD / 8; ++i) {
+          const uint4 x = lds16(place(i));
+          const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = unpack_bf16x2(y[j]);
+            big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+        }
+        met[half][r] = big;
+        mbar_arrive(pair_met(warp));
+        if (!tc_wait(pair_met(warp), pairs++ & 1, ab)) return false;
+        float up, down;
+        e4m3_query_scale(fmaxf(big, met[half ^ 1][r]), up, down);
+#pragma unroll 4
+        for (int i = 0; i < HD / 8; ++i) {
+          const uint4 x = lds16(place(i));
+          uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = unpack_bf16x2(y[j]);
+            y[j] = pack_f16x2(f.x * up, f.y * up);
+          }
+          sts16(place(i), make_uint4(y[0], y[1], y[2], y[3]));
+        }
+        sl2_next = down * (a.k_scale ? __ldg(a.k_scale + w.k) : 1.0f) * LOG2E;
+      }
       fence_proxy_async_smem();
       mbar_arrive(q_full);
+      return true;
     };
     load_q(walk);
-    q_loaded();
-    while (true) {
+    ok = q_loaded(walk, sh_top[1]);
+    while (ok) {
       const int64_t item = (int64_t)walk.b * a.K + walk.k;
+      sl2 = sl2_next;
       DecodeWalk then = walk;
       const bool go_on = shape.next_item(then, sh.ends[1]);
       const int hi = walk.len - a.T + t + 1, lo = a.window > 0 ? hi - a.window : 0;   // keys of this row
@@ -327,7 +394,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
 #pragma unroll
           for (int j = 0; j < 32; ++j) pm[j & 3] = fmaxf(pm[j & 3], __uint_as_float(sv[j]));
         }
-        float top = LOG2E * fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+        float top = sl2 * fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
         sh_top[n & 1][half][r] = top;
         mbar_arrive(pair_met(warp));
         if (!(ok = tc_wait(pair_met(warp), pairs++ & 1, ab))) break;
@@ -361,6 +428,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
           // zeros to the tensor cores.
           const int unit = 2 * n + 1;   // V(n)
           if (!(ok = tc_wait(full(unit % S), (unit / S) & 1, ab))) break;
+          constexpr uint32_t INF = E4M3 ? 0x7c00u : 0x7f80u;
           uint8_t* const v_tile = sm + C::QBYTES + (unit % S) * C::SLOT;
           bool bad = false;
 #pragma unroll
@@ -369,7 +437,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
             const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              bad |= (y[j] & 0x7f80u) == 0x7f80u || (y[j] & 0x7f800000u) == 0x7f800000u;
+              bad |= (y[j] & INF) == INF || (y[j] & INF << 16) == INF << 16;
           }
           const uint32_t ballot = __ballot_sync(~0u, bad);
           const uint32_t* const met = sh_bad[n & 1];
@@ -404,7 +472,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
               const bool kept = key0 + key >= lo && key0 + key < hi;
               const float x = tmem_ld1(s_col + key);
               tmem_wait_ld();
-              const float p = fast_exp2(fmaf(x, LOG2E, -base));
+              const float p = fast_exp2(fmaf(x, sl2, -base));
 #pragma unroll 1
               for (int c = d0; c < d0 + HD; c += 32) {
                 uint32_t ov[32];
@@ -417,7 +485,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
                   const uint32_t y[4] = {x8.x, x8.y, x8.z, x8.w};
 #pragma unroll
                   for (int j = 0; j < 4; ++j) {
-                    const float2 f = unpack_bf16x2(y[j]);
+                    const float2 f = E4M3 ? unpack_f16x2(y[j]) : unpack_bf16x2(y[j]);
                     const int d = 8 * i + 2 * j;
                     if (kept) {
                       ov[d] = __float_as_uint(__uint_as_float(ov[d]) + p * f.x);
@@ -441,7 +509,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
         }
 
         // Weights as two bf16 terms (paged_decode.cuh): the cut over the scores that
-        // this half has read, the rest beside o.
+        // this half has read, the rest beside o.  8-bit caches: one f16 term.
         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int h = 0; h < TN / 64; ++h) {
@@ -450,22 +518,26 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
           load_s(i, sv);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float x = fast_exp2(fmaf(__uint_as_float(sv[2 * j]), LOG2E, -base));
-            const float y = fast_exp2(fmaf(__uint_as_float(sv[2 * j + 1]), LOG2E, -base));
+            const float x = fast_exp2(fmaf(__uint_as_float(sv[2 * j]), sl2, -base));
+            const float y = fast_exp2(fmaf(__uint_as_float(sv[2 * j + 1]), sl2, -base));
             sum[j & 3] += x + y;
+            if (E4M3) {
+              cut[j] = pack_f16x2(x, y);
+              continue;
+            }
             const float hx = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
             const float hy = __uint_as_float(__float_as_uint(y) & 0xffff0000u);
             cut[j] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
             rest[j] = pack_bf16x2(fmaf(x, 1 + 0x1p-20f, -hx), fmaf(y, 1 + 0x1p-20f, -hy));
           }
           tmem_st16(s_col + TN / 2 * half + 16 * h, cut);
-          tmem_st16(lanes + REST_COL + TN / 2 * (n & 1) + 16 * i, rest);
+          if (!E4M3) tmem_st16(lanes + REST_COL + TN / 2 * (n & 1) + 16 * i, rest);
         }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(p_full(n));
-        if (last && go_on) q_loaded();
+        if (last && go_on && !(ok = q_loaded(then, sh_top[(n + 1) & 1]))) break;
       }
       // ---- end of the CTA's part of the item: o from tensor memory
       if (!ok || !(ok = tc_wait(pv_done(n - 1), ((n - 1) >> 1) & 1, ab))) break;
@@ -523,7 +595,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 10) {
+  if (warp == C::WARPS - 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -313,6 +313,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N, bool a
          ((b_mn ? 1u : 0u) << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
+// The same with f16 A/B (formats 0).
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t M, uint32_t N, bool a_mn, bool b_mn) {
+  return idesc_bf16(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+
 // Bits [lo, hi) of a 32-bit word, the bounds clamped to [0, 32].
 __device__ __forceinline__ uint32_t range_bits(int lo, int hi) {
   lo = lo < 0 ? 0 : lo;
