@@ -59,6 +59,13 @@ __device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, const Abo
   return __all_sync(~0u, mbar_wait(bar, parity, ab));
 }
 
+// True in one lane of the warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
 // 32 lanes x 1 column.
 __device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
   uint32_t r;
@@ -125,59 +132,69 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
 
   if (warp == C::WARPS - 1) {
     // -------------------------------------------------------------- products
-    if (lane == 0) {
-      constexpr auto idesc = E4M3 ? idesc_f16 : idesc_bf16;
-      constexpr uint32_t id_s = idesc(128, TN, false, false);   // S = Q K^T
-      constexpr uint32_t id_o = idesc(128, H, false, true);      // o += P V
-      const uint64_t dq = sdesc_sw128(q_u, 16, 1024), dk = sdesc_sw128(ring_u, 16, 1024);
-      const uint64_t dv = sdesc_sw128(ring_u, C::CHUNK, 1024);
-      bool ok = true;
-      int n = 0;   // tiles so far
-      auto issue_pv = [&](int n, bool first) -> bool {
-        const int unit = 2 * n + 1;   // V(n)
-        if (!mbar_wait(full(unit % S), (unit / S) & 1, ab) || !mbar_wait(p_full(n), (n >> 1) & 1, ab)) return false;
-        tc_fence_after();
-        const uint32_t p = tmem + TN * (n & 1);
-        const uint64_t v = sdesc_add(dv, (unit % S) * C::SLOT);
-        const bool keep = !first || *reinterpret_cast<volatile int*>(&sh_keep);
+    // The warp runs this as one, and one lane issues: what an instruction names is the
+    // same in all lanes, and said to be so (a shuffle).
+    const bool lead = elect_one();
+    constexpr auto idesc = E4M3 ? idesc_f16 : idesc_bf16;
+    constexpr uint32_t id_s = idesc(128, TN, false, false);   // S = Q K^T
+    constexpr uint32_t id_o = idesc(128, H, false, true);      // o += P V
+    const uint64_t dq = sdesc_sw128(q_u, 16, 1024), dk = sdesc_sw128(ring_u, 16, 1024);
+    const uint64_t dv = sdesc_sw128(ring_u, C::CHUNK, 1024);
+    auto same = [](uint32_t x) { return __shfl_sync(~0u, x, 0); };
+    const uint32_t tm = same(tmem);
+    bool ok = true;
+    int n = 0;   // tiles so far
+    auto issue_pv = [&](int n, bool first) -> bool {
+      const int unit = 2 * n + 1;   // V(n)
+      if (!tc_wait(full(unit % S), (unit / S) & 1, ab) || !tc_wait(p_full(n), (n >> 1) & 1, ab)) return false;
+      tc_fence_after();
+      const uint32_t odd = same(n & 1), slot = same(unit % S), p = tm + TN * odd, rest = tm + REST_COL + TN / 2 * odd;
+      const uint64_t v = sdesc_add(dv, slot * C::SLOT);
+      const uint32_t keep = same(!first || *reinterpret_cast<volatile int*>(&sh_keep));
+      if (lead) {
 #pragma unroll
         for (int kk = 0; kk < TN / 16; ++kk)
-          mma_ts(tmem + O_COL, p + kk / (TN / 32) * (TN / 2) + kk % (TN / 32) * 8, sdesc_add(v, kk * 2048), id_o,
-                 keep || kk > 0 ? 1u : 0u);
+          mma_ts(tm + O_COL, p + kk / (TN / 32) * (TN / 2) + kk % (TN / 32) * 8, sdesc_add(v, kk * 2048), id_o,
+                 kk > 0 ? 1u : keep);
 #pragma unroll
         for (int kk = 0; !E4M3 && kk < TN / 16; ++kk)
-          mma_ts(tmem + O_COL, tmem + REST_COL + TN / 2 * (n & 1) + kk * 8, sdesc_add(v, kk * 2048), id_o, 1u);
-        mma_commit(empty(unit % S));
-        mma_commit(pv_done(n));
-        return true;
-      };
-      for (int item = 0; ok; ++item) {
-        ok = mbar_wait(q_full, item & 1, ab);
-        for (; ok && walk.tile < walk.end; ++walk.tile, ++n) {
-          const int unit = 2 * n;   // K(n)
-          if (!(ok = mbar_wait(full(unit % S), (unit / S) & 1, ab))) break;
-          tc_fence_after();
-          const uint64_t k = sdesc_add(dk, (unit % S) * C::SLOT);
+          mma_ts(tm + O_COL, rest + kk * 8, sdesc_add(v, kk * 2048), id_o, 1u);
+        mma_commit(empty(slot));
+        mma_commit(pv_done(odd));
+      }
+      __syncwarp();
+      return true;
+    };
+    for (int item = 0; ok; ++item) {
+      ok = tc_wait(q_full, item & 1, ab);
+      for (; ok && walk.tile < walk.end; ++walk.tile, ++n) {
+        const int unit = 2 * n;   // K(n)
+        if (!(ok = tc_wait(full(unit % S), (unit / S) & 1, ab))) break;
+        tc_fence_after();
+        const uint32_t odd = same(n & 1), slot = same(unit % S), s = tm + TN * odd;
+        const uint64_t k = sdesc_add(dk, slot * C::SLOT);
+        if (lead) {
 #pragma unroll
           for (int c = 0; c < HC; ++c)
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_ss(tmem + TN * (n & 1), sdesc_add(dq, c * C::QCHUNK + kk * 32),
-                     sdesc_add(k, c * C::CHUNK + kk * 32), id_s, c > 0 || kk > 0 ? 1u : 0u);
-          mma_commit(empty(unit % S));
-          mma_commit(s_full(n));
-          // o += P V of the tile before, while this one's softmax runs
-          if (walk.tile > walk.begun) ok = issue_pv(n - 1, walk.tile - 1 == walk.begun);
+              mma_ss(s, sdesc_add(dq, c * C::QCHUNK + kk * 32), sdesc_add(k, c * C::CHUNK + kk * 32), id_s,
+                     c > 0 || kk > 0 ? 1u : 0u);
+          mma_commit(empty(slot));
+          mma_commit(s_full(odd));
         }
-        if (ok) ok = issue_pv(n - 1, walk.end - 1 == walk.begun);
-        if (!shape.next_item(walk, sh.ends[1])) break;
+        __syncwarp();
+        // o += P V of the tile before, while this one's softmax runs
+        if (walk.tile > walk.begun) ok = issue_pv(n - 1, walk.tile - 1 == walk.begun);
       }
-      if (!ok) {   // until the products issued are over: tensor memory is freed below
-        mma_commit(teardown);
-        mbar_wait_teardown(teardown, 0, max(a.wait_limit_ns, (uint64_t)1000000000));   // they take microseconds
-      }
+      if (ok) ok = issue_pv(n - 1, walk.end - 1 == walk.begun);
+      if (!shape.next_item(walk, sh.ends[1])) break;
     }
-    __syncwarp();
+    if (!ok) {   // until the products issued are over: tensor memory is freed below
+      if (lead) mma_commit(teardown);
+      mbar_wait_teardown(teardown, 0, max(a.wait_limit_ns, (uint64_t)1000000000));   // they take microseconds
+      __syncwarp();
+    }
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- copies
     const int w = warp - 8;

@@ -503,17 +503,19 @@ def test_decode_repeats_bitwise_whatever_the_workspace_holds(lib):
 
 @pytest.mark.parametrize("H", [64, 128, 256])
 def test_decode_wait_that_runs_out_ends_with_an_error(lib, H):
-    """Many query rows: the kernel's warps wait for one another, each time with a limit.  Whatever
-    the workspace holds then, the call ends, and the next one is right."""
+    """Many query rows: the kernel's warps wait for one another, each time with a limit (of no time
+    here).  Whatever the workspace holds where one runs out, the call ends, and the next is right."""
     p = P.problem(4, B=24, K=2, G=40, T=1, H=H, lens=[3000, 700, 40, 1] * 6, page=16)
-    _decode(p)
+    want = _decode(p)
     n = binding.fa_paged_decode_workspace_size(24, 2, 40, 1, H)
     for fill in (0, 1, 127, 255):
         ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
         assert binding.fa_set_wait_limit_ns(1) == binding.FA_OK
         try:
-            _decode(p, workspace=ws)
-            assert binding.fa_check_status() == binding.FA_ERR_DEVICE_TIMEOUT
+            o, lse = _decode(p, workspace=ws)
+            rc = binding.fa_check_status()
+            assert rc in (binding.FA_OK, binding.FA_ERR_DEVICE_TIMEOUT)   # OK: none has run out
+            assert rc or (torch.equal(o, want[0]) and torch.equal(lse, want[1]))
         finally:
             assert binding.fa_set_wait_limit_ns(2_000_000_000) == binding.FA_OK
     _check(p)
