@@ -45,7 +45,7 @@ struct DecodeTcCfg {
   // 64 KB of bytes that wait for their conversion.
   static constexpr int STAGES = E4M3 ? (H == 64 ? 6 : H == 128 ? 4 : 3) : H == 64 ? 12 : H == 128 ? 6 : 5;
   static constexpr int RAW = E4M3 ? TN * H : 0, RAW_STAGES = H == 64 ? 10 : 4;
-  static constexpr int FLIGHT = E4M3 ? RAW_STAGES - 1 : STAGES / 2;   // tiles in flight behind the newest
+  static constexpr int FLIGHT = RAW_STAGES - 1;         // 8-bit tiles in flight behind the newest
   static constexpr int RING = STAGES * SLOT;
   static constexpr int SMEM = QBYTES + RING + RAW_STAGES * RAW;
   // Tensor memory: S at 0 and TN, o at 256, the weights' second terms at REST_COL
@@ -57,6 +57,11 @@ struct DecodeTcCfg {
 // The bounded waits of this kernel's barriers, each by whole warps.
 __device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, const Abort& ab) {
   return __all_sync(~0u, mbar_wait(bar, parity, ab));
+}
+
+// One arrival on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // True in one lane of the warp.
@@ -147,6 +152,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
     auto issue_pv = [&](int n, bool first) -> bool {
       const int unit = 2 * n + 1;   // V(n)
       if (!tc_wait(full(unit % S), (unit / S) & 1, ab) || !tc_wait(p_full(n), (n >> 1) & 1, ab)) return false;
+      if (!E4M3) fence_proxy_async_smem();   // the copies were the generic proxy's
       tc_fence_after();
       const uint32_t odd = same(n & 1), slot = same(unit % S), p = tm + TN * odd, rest = tm + REST_COL + TN / 2 * odd;
       const uint64_t v = sdesc_add(dv, slot * C::SLOT);
@@ -170,6 +176,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
       for (; ok && walk.tile < walk.end; ++walk.tile, ++n) {
         const int unit = 2 * n;   // K(n)
         if (!(ok = tc_wait(full(unit % S), (unit / S) & 1, ab))) break;
+        if (!E4M3) fence_proxy_async_smem();   // the copies were the generic proxy's
         tc_fence_after();
         const uint32_t odd = same(n & 1), slot = same(unit % S), s = tm + TN * odd;
         const uint64_t k = sdesc_add(dk, slot * C::SLOT);
@@ -210,23 +217,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
       return E4M3 ? raw_u + unit % C::RAW_STAGES * C::RAW + j * 512
                   : ring_u + unit % S * C::SLOT + (lane_dst ^ (((j * RPJ) & 7) << 4)) + j * RPJ * 128;
     };
-    // Tile `unit` has landed: for the tensor cores to read, 8-bit values as f16 (exact).
+    // 8-bit tile `unit` has landed: to f16 (exact).
     auto hand_over = [&](int unit) -> bool {
-      if constexpr (E4M3) {
-        if (unit >= S && !tc_wait(empty(unit % S), (unit / S - 1) & 1, ab)) return false;
-        const uint32_t turn = (u >> 2 & 1) << 4;   // four lanes write the odd unit first: other banks
+      if (unit >= S && !tc_wait(empty(unit % S), (unit / S - 1) & 1, ab)) return false;
+      const uint32_t turn = (u >> 2 & 1) << 4;   // four lanes write the odd unit first: other banks
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          const uint4 x = lds16(place(unit, j));
-          uint4 y[2];
-          e4m3x4_to_f16(x.x, y[0].x, y[0].y);
-          e4m3x4_to_f16(x.y, y[0].z, y[0].w);
-          e4m3x4_to_f16(x.z, y[1].x, y[1].y);
-          e4m3x4_to_f16(x.w, y[1].z, y[1].w);
-          const uint32_t dst = ring_u + unit % S * C::SLOT + (lane_dst ^ (((j * RPJ) & 7) << 4)) + j * RPJ * 128;
-          sts16(dst ^ turn, turn ? y[1] : y[0]);
-          sts16(dst ^ turn ^ 16, turn ? y[0] : y[1]);
-        }
+      for (int j = 0; j < NJ; ++j) {
+        const uint4 x = lds16(place(unit, j));
+        uint4 y[2];
+        e4m3x4_to_f16(x.x, y[0].x, y[0].y);
+        e4m3x4_to_f16(x.y, y[0].z, y[0].w);
+        e4m3x4_to_f16(x.z, y[1].x, y[1].y);
+        e4m3x4_to_f16(x.w, y[1].z, y[1].w);
+        const uint32_t dst = ring_u + unit % S * C::SLOT + (lane_dst ^ (((j * RPJ) & 7) << 4)) + j * RPJ * 128;
+        sts16(dst ^ turn, turn ? y[1] : y[0]);
+        sts16(dst ^ turn ^ 16, turn ? y[0] : y[1]);
       }
       fence_proxy_async_smem();
       mbar_arrive(full(unit % S));
@@ -292,15 +297,20 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
             cp_async16(place(unit, j), at >= 0 ? base + at + u * 16 : (const char*)a.q, at >= 0 ? 16 : 0);
           }
         }
-        cp_async_commit();
-        if (unit >= D) {
-          cp_async_wait<D>();
-          if (!(ok = hand_over(unit - D))) break;
+        if constexpr (!E4M3) {
+          cp_async_arrive(full(unit % S));
+        } else {
+          cp_async_commit();
+          if (unit >= D) {
+            cp_async_wait<D>();
+            if (!(ok = hand_over(unit - D))) break;
+          }
         }
       }
     }
+    cp_async_commit();
     cp_async_wait<0>();
-    for (int i = max(0, unit - D); ok && i < unit; ++i) ok = hand_over(i);
+    for (int i = max(0, unit - D); E4M3 && ok && i < unit; ++i) ok = hand_over(i);
   } else {
     // --------------------------------------------------------------- softmax
     const int r = tid & 127, half = tid >> 7, t = r % a.T;
