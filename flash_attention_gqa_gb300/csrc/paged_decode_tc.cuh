@@ -34,9 +34,9 @@ struct DecodeTcCfg {
   static constexpr int TN = H == 256 ? 64 : 128;        // keys of a tile
   static constexpr int CK = TN, TEAMS = 1, TK = TN;
   static constexpr int ITEM_UNITS = 2;
-  static constexpr int CW = E4M3 ? 4 : 2;               // copying warps
+  static constexpr int CW = E4M3 ? 4 : 2;               // copying warps, two for a tile
   static constexpr int WARPS = 9 + CW, THREADS = WARPS * 32;
-  static constexpr int KPW = TN / CW;                   // keys of a tile a copying warp
+  static constexpr int KPW = TN / 2;                    // keys of a tile a copying warp
   static constexpr int QCHUNK = 128 * 128;              // 128 query rows of 64 dims
   static constexpr int QBYTES = HC * QCHUNK;
   static constexpr int CHUNK = TN * 128;                // TN keys of 64 dims
@@ -44,10 +44,11 @@ struct DecodeTcCfg {
   // bf16: 192, 192 and 160 KB.  8-bit: 96, 128 and 96 KB of f16 tiles, and 80, 64 and
   // 64 KB of bytes that wait for their conversion.
   static constexpr int STAGES = E4M3 ? (H == 64 ? 6 : H == 128 ? 4 : 3) : H == 64 ? 12 : H == 128 ? 6 : 5;
-  static constexpr int RAW = E4M3 ? TN * H : 0, RAW_STAGES = H == 64 ? 10 : 4;
+  static constexpr int KS = STAGES / 2, VS = STAGES - KS;   // for K and for V
+  static constexpr int RAW = E4M3 ? TN * H : 0, RAW_STAGES = H == 64 ? 5 : 2;   // of K, and of V
   static constexpr int FLIGHT = RAW_STAGES - 1;         // 8-bit tiles in flight behind the newest
   static constexpr int RING = STAGES * SLOT;
-  static constexpr int SMEM = QBYTES + RING + RAW_STAGES * RAW;
+  static constexpr int SMEM = QBYTES + RING + 2 * RAW_STAGES * RAW;
   // Tensor memory: S at 0 and TN, o at 256, the weights' second terms at REST_COL
   // and TN / 2 behind it.
   static constexpr uint32_t O_COL = 256, REST_COL = H == 256 ? 128 : 384;
@@ -97,6 +98,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
   const int R = a.G * a.T;
   const DecodeShape<C> shape{a};
   const Abort ab{&sh_abort, a.wait_limit_ns, a.err};
+  // Slots: K(n) takes turn n / KS of slot n % KS, V(n) the same behind them.
+  auto slot_of = [](int n, int kv) { return kv ? C::KS + n % C::VS : n % C::KS; };
+  auto turn_of = [](int n, int kv) { return kv ? n / C::VS : n / C::KS; };
   auto full = [&](int s) { return smem_u32(bars + s); };
   auto empty = [&](int s) { return smem_u32(bars + S + s); };
   auto s_full = [&](int n) { return smem_u32(bars + 2 * S + (n & 1)); };
@@ -112,7 +116,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
   if (tid == 0) {
     sh_abort = 0;
     for (int s = 0; s < S; ++s) {
-      mbar_init(full(s), C::CW * 32);
+      mbar_init(full(s), 64);
       mbar_init(empty(s), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -150,11 +154,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
     bool ok = true;
     int n = 0;   // tiles so far
     auto issue_pv = [&](int n, bool first) -> bool {
-      const int unit = 2 * n + 1;   // V(n)
-      if (!tc_wait(full(unit % S), (unit / S) & 1, ab) || !tc_wait(p_full(n), (n >> 1) & 1, ab)) return false;
+      if (!tc_wait(full(slot_of(n, 1)), turn_of(n, 1) & 1, ab) || !tc_wait(p_full(n), (n >> 1) & 1, ab)) return false;
       if (!E4M3) fence_proxy_async_smem();   // the copies were the generic proxy's
       tc_fence_after();
-      const uint32_t odd = same(n & 1), slot = same(unit % S), p = tm + TN * odd, rest = tm + REST_COL + TN / 2 * odd;
+      const uint32_t odd = same(n & 1), slot = same(slot_of(n, 1)), p = tm + TN * odd, rest = tm + REST_COL + TN / 2 * odd;
       const uint64_t v = sdesc_add(dv, slot * C::SLOT);
       const uint32_t keep = same(!first || *reinterpret_cast<volatile int*>(&sh_keep));
       if (lead) {
@@ -174,11 +177,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
     for (int item = 0; ok; ++item) {
       ok = tc_wait(q_full, item & 1, ab);
       for (; ok && walk.tile < walk.end; ++walk.tile, ++n) {
-        const int unit = 2 * n;   // K(n)
-        if (!(ok = tc_wait(full(unit % S), (unit / S) & 1, ab))) break;
+        if (!(ok = tc_wait(full(slot_of(n, 0)), turn_of(n, 0) & 1, ab))) break;
         if (!E4M3) fence_proxy_async_smem();   // the copies were the generic proxy's
         tc_fence_after();
-        const uint32_t odd = same(n & 1), slot = same(unit % S), s = tm + TN * odd;
+        const uint32_t odd = same(n & 1), slot = same(slot_of(n, 0)), s = tm + TN * odd;
         const uint64_t k = sdesc_add(dk, slot * C::SLOT);
         if (lead) {
 #pragma unroll
@@ -204,7 +206,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
     }
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- copies
-    const int w = warp - 8;
+    // bf16: two warps, each half of the keys of K(n) and then of V(n).  8-bit: two for K
+    // and two for V, which then wait for slots of their own kind only.
+    const int w = (warp - 8) & 1, kind = E4M3 ? (warp - 8) >> 1 : 0;
     constexpr int RPJ = 32 / C::UPR, NJ = C::KPW / RPJ, D = C::FLIGHT;   // rows a copy of the warp; copies
     const int64_t lane_src = (lane / C::UPR) * a.lay.token + (lane % C::UPR) * 16;
     const int64_t row_step = a.lay.token * RPJ;
@@ -212,33 +216,39 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
     // 8-bit: this thread's units of a tile wait in places of its own, and are two units each as f16
     const int u16 = E4M3 ? 2 * u : u;
     const uint32_t lane_dst = (u16 >> 3) * C::CHUNK + (w * C::KPW + lr) * 128 + (((u16 & 7) ^ lr) << 4);
-    const uint32_t raw_u = ring_u + C::RING + w * (C::RAW / C::CW) + lane * 16;
-    auto place = [&](int unit, int j) -> uint32_t {   // of copy j
-      return E4M3 ? raw_u + unit % C::RAW_STAGES * C::RAW + j * 512
-                  : ring_u + unit % S * C::SLOT + (lane_dst ^ (((j * RPJ) & 7) << 4)) + j * RPJ * 128;
+    const uint32_t raw_u = ring_u + C::RING + (kind * C::RAW_STAGES * 2 + w) * (C::RAW / 2) + lane * 16;
+    auto row_place = [&](int slot, int j) {   // of copy j
+      return ring_u + slot * C::SLOT + (lane_dst ^ (((j * RPJ) & 7) << 4)) + j * RPJ * 128;
     };
-    // 8-bit tile `unit` has landed: to f16 (exact).
-    auto hand_over = [&](int unit) -> bool {
-      if (unit >= S && !tc_wait(empty(unit % S), (unit / S - 1) & 1, ab)) return false;
+    auto place = [&](int n, int kv, int j) -> uint32_t {
+      return E4M3 ? raw_u + n % C::RAW_STAGES * C::RAW + j * 512 : row_place(slot_of(n, kv), j);
+    };
+    auto free_slot = [&](int n, int kv) -> bool {
+      return turn_of(n, kv) == 0 || tc_wait(empty(slot_of(n, kv)), (turn_of(n, kv) - 1) & 1, ab);
+    };
+    // 8-bit tile n has landed: to f16 (exact).
+    auto hand_over = [&](int n) -> bool {
+      if (!free_slot(n, kind)) return false;
+      const int slot = slot_of(n, kind);
       const uint32_t turn = (u >> 2 & 1) << 4;   // four lanes write the odd unit first: other banks
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
-        const uint4 x = lds16(place(unit, j));
+        const uint4 x = lds16(place(n, kind, j));
         uint4 y[2];
         e4m3x4_to_f16(x.x, y[0].x, y[0].y);
         e4m3x4_to_f16(x.y, y[0].z, y[0].w);
         e4m3x4_to_f16(x.z, y[1].x, y[1].y);
         e4m3x4_to_f16(x.w, y[1].z, y[1].w);
-        const uint32_t dst = ring_u + unit % S * C::SLOT + (lane_dst ^ (((j * RPJ) & 7) << 4)) + j * RPJ * 128;
+        const uint32_t dst = row_place(slot, j);
         sts16(dst ^ turn, turn ? y[1] : y[0]);
         sts16(dst ^ turn ^ 16, turn ? y[0] : y[1]);
       }
       fence_proxy_async_smem();
-      mbar_arrive(full(unit % S));
+      mbar_arrive(full(slot));
       return true;
     };
     bool more = true, ok = true;
-    int unit = 0;   // K(n): 2 n, V(n): 2 n + 1
+    int n = 0;
     // This lane's keys of the next tile: looked up a tile early.
     constexpr int NK = C::KPW < 32 ? 1 : C::KPW / 32;
     bool live[NK];
@@ -256,7 +266,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
       }
     };
     look_up();
-    while (more && ok) {
+    for (; more && ok; ++n) {
       int64_t off[NK];
       bool all = true;
 #pragma unroll
@@ -274,16 +284,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
       look_up();
       const bool steps = a.lay.page_shift >= 4 && __all_sync(~0u, all);
 #pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv, ++unit) {
+      for (int kv = kind; kv < (E4M3 ? kind + 1 : 2); ++kv) {
         const char* const base = (const char*)(kv ? a.v_cache : a.k_cache);
-        if (!E4M3 && unit >= S && !(ok = tc_wait(empty(unit % S), (unit / S - 1) & 1, ab))) break;
+        if (!E4M3 && !(ok = free_slot(n, kv))) break;
         if (steps) {
 #pragma unroll
           for (int kt = 0; kt < C::KPW / 16; ++kt) {   // 16 keys or more a page: one offset per 16 keys, and steps
             const char* src = base + __shfl_sync(~0u, off[kt >> 1], (kt & 1) * 16) + lane_src;
 #pragma unroll
             for (int j = kt * 16 / RPJ; j < (kt + 1) * 16 / RPJ; ++j) {
-              cp_async16(place(unit, j), src, 16);
+              cp_async16(place(n, kv, j), src, 16);
               src += row_step;
             }
           }
@@ -294,23 +304,23 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
             const int64_t at0 = __shfl_sync(~0u, off[0], row & 31), at1 = __shfl_sync(~0u, off[NK - 1], row & 31);
             const int64_t at = row < 32 ? at0 : at1;
             // nothing is read, and zeros are written, where there is no key (q: an address that exists)
-            cp_async16(place(unit, j), at >= 0 ? base + at + u * 16 : (const char*)a.q, at >= 0 ? 16 : 0);
+            cp_async16(place(n, kv, j), at >= 0 ? base + at + u * 16 : (const char*)a.q, at >= 0 ? 16 : 0);
           }
         }
         if constexpr (!E4M3) {
-          cp_async_arrive(full(unit % S));
+          cp_async_arrive(full(slot_of(n, kv)));
         } else {
           cp_async_commit();
-          if (unit >= D) {
+          if (n >= D) {
             cp_async_wait<D>();
-            if (!(ok = hand_over(unit - D))) break;
+            if (!(ok = hand_over(n - D))) break;
           }
         }
       }
     }
     cp_async_commit();
     cp_async_wait<0>();
-    for (int i = max(0, unit - D); E4M3 && ok && i < unit; ++i) ok = hand_over(i);
+    for (int i = max(0, n - D); E4M3 && ok && i < n; ++i) ok = hand_over(i);
   } else {
     // --------------------------------------------------------------- softmax
     const int r = tid & 127, half = tid >> 7, t = r % a.T;
@@ -453,10 +463,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
           // Values that are not finite, of keys that some row does not keep: 0 x inf
           // would reach it.  Their products are done here, row by row, and they are
           // zeros to the tensor cores.
-          const int unit = 2 * n + 1;   // V(n)
-          if (!(ok = tc_wait(full(unit % S), (unit / S) & 1, ab))) break;
+          if (!(ok = tc_wait(full(slot_of(n, 1)), turn_of(n, 1) & 1, ab))) break;
           constexpr uint32_t INF = E4M3 ? 0x7c00u : 0x7f80u;
-          uint8_t* const v_tile = sm + C::QBYTES + (unit % S) * C::SLOT;
+          uint8_t* const v_tile = sm + C::QBYTES + slot_of(n, 1) * C::SLOT;
           bool bad = false;
 #pragma unroll
           for (int i = 0; i < UPP; ++i) {
