@@ -73,8 +73,8 @@ struct PagedDecodeArgs {
 };
 
 // Workspace of a decode: the splits, then partials, on a GPU with sm_count SMs.
-// CTAs an SM: two of 4 warps up to H = 128 and 32 query rows, else one (of 4 warps
-// at H = 256 up to 16 rows, of 8 with more rows): what rings and registers allow.
+// CTAs an SM: two of 4 warps up to H = 128 and 32 query rows, else one: what rings
+// and registers allow.
 struct PagedDecodePlan {
   int ctas;
   size_t partials;   // offset

@@ -26,17 +26,16 @@
 // mostly padding and its operands would pass through tensor memory and
 // barriers.  The issue slots are 23% used at R = 8 in bf16 and 38% with 8-bit
 // caches, 41% at R = 32.  mma.sync runs at one m16n8k16 per 8 cycles and
-// sub-core here (640 TFLOP/s), so from R = 64 on it and the instructions around
-// it are the bound (102 us for 64 rows, 181 us for 128, where 32 take 56 us and
-// 8 take 47 us: 16 requests x 4 kv heads x 8192 keys).  The S^T accumulator
-// becomes the P^T operand by one 8x8 transpose (movmatrix), and maxima and sums
-// live in the lanes that own the columns.
+// sub-core here (640 TFLOP/s), so it and the instructions around it would be the
+// bound from R = 64 on (102 us for 64 rows where 32 take 56 us and 8 take 47 us: 16
+// requests x 4 kv heads x 8192 keys): paged_decode_tc.cuh takes those.  The S^T
+// accumulator becomes the P^T operand by one 8x8 transpose (movmatrix), and maxima
+// and sums live in the lanes that own the columns.
 //
-// Streams.  Up to 32 rows (16 at H = 256) each warp is on its own: it copies its
-// keys (16-byte cp.async, swizzled so that ldmatrix is conflict-free) into its
-// own ring, and waits for nobody until its CTA's part of the item ends; the
-// ring runs ahead across items.  With more rows, teams of 2 to 8 warps share a
-// ring and hold 32 rows (16) each.
+// Streams.  Each warp is on its own: it copies its keys (16-byte cp.async,
+// swizzled so that ldmatrix is conflict-free) into its own ring, and waits for
+// nobody until its CTA's part of the item ends; the ring runs ahead across items.
+// 17 to 32 rows at H = 256: teams of two warps share a ring and hold 16 rows each.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>

@@ -67,18 +67,22 @@ cudaError_t launch_decode(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
   return launch_decode<C, paged_decode_kernel<C>>(a, grid, st);
 }
 
-// Up to 8, 16 and 32 rows: warps on their own (teams of two for 32 at H = 256:
-// registers).  More: tcgen05.  Both sides of 32 at 16 requests x 4 kv heads x 8192
-// keys, mma.sync and tcgen05: bf16 at H = 128 32 rows take 56 and 62 us, 64 rows
-// 102 and 63; at H = 256 99 and 107, 202 and 110.  8-bit at H = 128 64 rows 79 and
-// 65, 128 rows 139 and 69.
+// Up to 8, 16 and 32 rows: mma.sync, warps on their own (teams of two for 8-bit
+// caches' 32 rows at H = 256: registers).  More, and over 16 rows of bf16 at H =
+// 256: tcgen05.  Both sides at 16 requests x 4 kv heads x 8192 keys, mma.sync and
+// tcgen05: bf16 at H = 64 32 rows take 35 and 46 us; at H = 128 32 rows 56 and 55
+// (8 x 4 rows, ragged: 30 and 34), 64 rows 102 and 56; at H = 256 16 rows 89 and
+// 89, 32 rows 99 and 93, 64 rows 202 and 98.  8-bit at H = 128 32 rows 44 and 58,
+// 64 rows 79 and 59, 128 rows 139 and 64; at H = 256 32 rows 77 and 101.
 template <int H, bool E4M3>
 cudaError_t launch_decode_rows(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
   const int R = a.G * a.T;
-  constexpr int NT = H == 256 ? 2 : 4, PER = NT * 8;   // rows a warp of a team
   if (R <= 8) return launch_decode<DecodeCfg<H, E4M3, 1, 1>>(a, grid, st);
   if (R <= 16) return launch_decode<DecodeCfg<H, E4M3, 2, 1>>(a, grid, st);
-  if (R <= 32) return launch_decode<DecodeCfg<H, E4M3, NT, 32 / PER>>(a, grid, st);
+  if constexpr (H <= 128 || E4M3) {
+    constexpr int NT = H == 256 ? 2 : 4;
+    if (R <= 32) return launch_decode<DecodeCfg<H, E4M3, NT, 4 / NT>>(a, grid, st);
+  }
   using Tc = DecodeTcCfg<H, E4M3>;
   return launch_decode<Tc, paged_decode_tc_kernel<Tc>>(a, grid, st);
 }

@@ -1,27 +1,33 @@
-// Paged decode for many query rows per kv head (up to 128), bf16 caches: tcgen05
-// products on tiles of 128 rows x 128 keys (64 at H = 256).
+// Paged decode for many query rows per kv head (up to 128): tcgen05 products on
+// tiles of 128 rows x 128 keys (64 at H = 256).
 //
 // The split over CTAs, the partials and the join are those of paged_decode.cuh;
-// only the work on a tile differs.  The query rows fill the 128-row operand
-// here, and with mma.sync the products and the instructions around them bound
-// the kernel from 64 rows on.  A tile of 128 keys takes 8 + 16 instructions of
-// 64 cycles each at H = 128 (the weights enter as two bf16 terms), half of the
-// 3000 cycles in which an SM's share of the memory rate delivers its 64 KB, so
-// memory is the bound again.
+// only the work on a tile differs.  The query rows fill the 128-row operand here,
+// and with mma.sync the products and the instructions around them bound the kernel.
+// A tile of 128 keys takes 8 + 16 instructions of 64 cycles each at H = 128 (bf16:
+// the weights enter as two terms), 1536 of the 3000 cycles in which an SM's share
+// of the memory rate delivers its 64 KB.
 //
-// Roles (352 threads, one CTA an SM):
+// Measured, 16 requests x 4 kv heads x 8192 keys: bf16, H = 128, 64 rows 56 us
+// (memory 40, and the fixed 10 of paged_decode.cuh): a tile every 2980 cycles, of
+// which the softmax warps work 2100 and the products take 1800; 128 rows 63 us.  H =
+// 256: 64 rows 98 us (memory 80).  H = 64: 46 us (memory 20): the softmax, 2300 cycles
+// a tile, is the bound, as it does not shrink with H.  8-bit caches: 59 us (H = 128;
+// memory 20), softmax and the conversions to f16 being the bound: both need the unit of
+// ex2 and of conversions.
+//
+// Roles (one CTA an SM):
 //   warps 0-7   softmax and results: warps w and w + 4 share 32 rows (a thread
 //               per row, a lane of tensor memory), each half of the keys of a
 //               tile and half of the head dims of o
-//   warps 8, 9  copies: each 64 keys of a tile, by cp.async (pages may end
-//               anywhere, and keys past the request have to arrive as zeros)
-//   warp  10    products (lane 0), tensor memory
-// Tensor memory: S of tiles n and n + 1, o, and the weights' two bf16 terms, A
-// operands of o += P V: the one over its S (in each half of it), the other
-// beside o.
-// Shared memory: the queries and a ring of K and V tiles (K(0), V(0), K(1), ..),
-// in chunks of [rows x 128 B] with the 128-byte swizzle of the operand
-// descriptors.
+//   warps 8, 9  copies: each half of the keys of a tile, by cp.async (pages may end
+//               anywhere, and keys past the request have to arrive as zeros); 8-bit
+//               caches: warps 8 and 9 for K, 10 and 11 for V, which they also convert
+//   last warp   products, tensor memory
+// Tensor memory: S of tiles n and n + 1, o, and the weights, A operands of o += P V:
+// one term over its S (in each half of it), the other of bf16's two beside o.
+// Shared memory: the queries and rings of K and V tiles, in chunks of [rows x 128 B]
+// with the 128-byte swizzle of the operand descriptors.
 #pragma once
 #include "paged_decode.cuh"
 
@@ -33,7 +39,10 @@ struct DecodeTcCfg {
   static constexpr bool E4M3 = E4M3_;
   static constexpr int TN = H == 256 ? 64 : 128;        // keys of a tile
   static constexpr int CK = TN, TEAMS = 1, TK = TN;
-  static constexpr int ITEM_UNITS = 2;
+  // An item's fixed cost in tiles.  64 requests of 1 to 8192 keys, 64 rows: 51.2 us with 2,
+  // 46.0 with 3, 44.8 with 4; at H = 256, 32 rows, to 4096 keys: 44.9, 40.4 and 40.8 us.
+  // H = 64, 40 rows: 31.7, 33.1 and 35.2; 8-bit, 64 rows: 40.2, 42.8 and 45.3.
+  static constexpr int ITEM_UNITS = H == 64 || E4M3 ? 2 : 3;
   static constexpr int CW = E4M3 ? 4 : 2;               // copying warps, two for a tile
   static constexpr int WARPS = 9 + CW, THREADS = WARPS * 32;
   static constexpr int KPW = TN / 2;                    // keys of a tile a copying warp
