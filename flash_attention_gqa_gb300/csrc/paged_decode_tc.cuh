@@ -241,16 +241,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
       const int slot = slot_of(n, kind);
       const uint32_t turn = (u >> 2 & 1) << 4;   // four lanes write the odd unit first: other banks
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const uint4 x = lds16(place(n, kind, j));
-        uint4 y[2];
-        e4m3x4_to_f16(x.x, y[0].x, y[0].y);
-        e4m3x4_to_f16(x.y, y[0].z, y[0].w);
-        e4m3x4_to_f16(x.z, y[1].x, y[1].y);
-        e4m3x4_to_f16(x.w, y[1].z, y[1].w);
-        const uint32_t dst = row_place(slot, j);
-        sts16(dst ^ turn, turn ? y[1] : y[0]);
-        sts16(dst ^ turn ^ 16, turn ? y[0] : y[1]);
+      for (int j0 = 0; j0 < NJ; j0 += 8) {   // eight reads in flight
+        uint4 x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = lds16(place(n, kind, j0 + j));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          uint4 y[2];
+          e4m3x4_to_f16(x[j].x, y[0].x, y[0].y);
+          e4m3x4_to_f16(x[j].y, y[0].z, y[0].w);
+          e4m3x4_to_f16(x[j].z, y[1].x, y[1].y);
+          e4m3x4_to_f16(x[j].w, y[1].z, y[1].w);
+          const uint32_t dst = row_place(slot, j0 + j);
+          sts16(dst ^ turn, turn ? y[1] : y[0]);
+          sts16(dst ^ turn ^ 16, turn ? y[0] : y[1]);
+        }
       }
       fence_proxy_async_smem();
       mbar_arrive(full(slot));
