@@ -12,9 +12,8 @@
 // (memory 40, and the fixed 10 of paged_decode.cuh): a tile every 2980 cycles, of
 // which the softmax warps work 2100 and the products take 1800; 128 rows 63 us.  H =
 // 256: 64 rows 98 us (memory 80).  H = 64: 46 us (memory 20): the softmax, 2300 cycles
-// a tile, is the bound, as it does not shrink with H.  8-bit caches: 59 us (H = 128;
-// memory 20), softmax and the conversions to f16 being the bound: both need the unit of
-// ex2 and of conversions.
+// a tile, is the bound, as it does not shrink with H.  8-bit caches: 52 us (H = 128,
+// 64 rows; memory 20), a tile every 2650 cycles, for the same reason.
 //
 // Roles (one CTA an SM):
 //   warps 0-7   softmax and results: warps w and w + 4 share 32 rows (a thread
