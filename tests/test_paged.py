@@ -465,12 +465,13 @@ def test_decode_without_columns(lib):
     assert (o == 0).all() and torch.isneginf(lse).all()
 
 
-def test_decode_offsets_past_32_bits(lib):
+@pytest.mark.parametrize("G", [2, 40])
+def test_decode_offsets_past_32_bits(lib, G):
     """A cache of over 4 GiB a tensor, and its last page."""
     K, H, page, n_pages = 4, 128, 64, 70000
     caches = [torch.zeros((n_pages, K, page, H), dtype=BF16, device="cuda") for _ in range(2)]
     assert caches[0].numel() * 2 > 1 << 32
-    p = P.problem(13, B=2, K=K, G=2, T=1, H=H, lens=[150, 70], page=page)
+    p = P.problem(13, B=2, K=K, G=G, T=1, H=H, lens=[150, 70], page=page)
     q, kc, vc, table, lens, *_ = p
     far = torch.arange(n_pages - kc.shape[0], n_pages)
     far[0] = 3
@@ -499,6 +500,65 @@ def test_decode_repeats_bitwise_whatever_the_workspace_holds(lib):
             first = first or got
             assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
     _ok()
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("H", [64, 128, 256])
+def test_decode_many_rows_repeats_bitwise(lib, H, dtype):
+    """Whatever the workspace holds, on two streams at once, and captured and replayed."""
+    p = P.problem(14, B=3, K=2, G=20, T=3, H=H, lens=[5000, 17, 900], page=16, dtype=dtype)
+    n = binding.fa_paged_decode_workspace_size(3, 2, 20, 3, H)
+    first = _check(p, 4000)
+    for fill in (0, 255, 127):
+        got = _decode(p, 4000, torch.full((n,), fill, dtype=torch.uint8, device="cuda"))
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+    q, table, lens, ks, vs = (x if x is None else x.cuda() for x in (p[0], *p[3:]))
+    caches = [P.to_device(x, "cuda") for x in p[1:3]]
+    call = lambda: binding.paged_attention_decode(q, *caches, table, lens, k_scale=ks, v_scale=vs, window=4000)
+    torch.cuda.synchronize()
+    streams, results = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(10):
+        for st in streams:
+            with torch.cuda.stream(st):
+                results.append(call())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        results.append(call())
+    for _ in range(3):
+        graph.replay()
+    _ok()
+    for o, lse in results:
+        assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3], ids=["bf16", "e4m3"])
+def test_decode_many_rows_bad_pages_count_as_zeros(lib, dtype):
+    for H in (64, 128, 256):
+        p = P.problem(12, B=4, K=2, G=36, T=1, H=H, lens=[50, 260, 20, 33], page=16, dtype=dtype)
+        q, kc, vc, table, lens, ks, vs = p
+        table[1, 2], table[1, 9] = kc.shape[0], kc.shape[0]
+        o, lse = _decode(p)
+        assert binding.fa_check_status() == binding.FA_ERR_DEVICE_VALUE
+        zero = torch.zeros_like(kc[:1].contiguous())
+        zk, zv = (torch.cat([c.contiguous().view(torch.uint8), zero.view(torch.uint8)]).view(dtype)
+                  for c in (kc, vc))
+        want = P.decode(q, zk, zv, table, lens, ks, vs)
+        P.check_decode(o.cpu(), lse.cpu(), want, H, dtype == E4M3, 260)
+
+
+def test_decode_many_rows_8bit_query_range(lib):
+    """Query rows far from 1, as above, with the rows' scaling shared by two threads each."""
+    for H in (64, 256):
+        p = list(P.problem(10, B=2, K=1, G=40, T=1, H=H, lens=[300, 33], page=16, dtype=E4M3))
+        size = torch.tensor([1e-30, 1e-8, 1.0, 3.0, 0.0, 1e-38, 1e-4, 20.0]).repeat(5)[:, None, None]
+        p[0] = (p[0].float() * size).bfloat16()
+        _check(tuple(p))
+        for d in (0, H - 1):                        # the large part in either half of the dims
+            large = [x if x is None else x.clone() for x in p]
+            large[0][..., d] = 1e5
+            large[1].view(torch.uint8)[..., d] = 0
+            _check(tuple(large))
 
 
 @pytest.mark.parametrize("H", [64, 128, 256])
