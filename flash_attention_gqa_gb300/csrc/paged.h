@@ -80,9 +80,12 @@ struct PagedDecodePlan {
   size_t partials;   // offset
   size_t total;
 };
-// Floats of one partial: o [R, H], m [R], l [R], rounded up to 16 bytes.
+// Rows of a partial: over 16 of them, whole groups of 8.
+__host__ __device__ inline int paged_partial_rows(int R) { return R > 16 ? (R + 7) & ~7 : R; }
+// Floats of one partial, with P rows: o [P, H] (the tcgen05 kernel: [H / 4, P, 4]), m [P],
+// l [P], rounded up to 16 bytes.
 __host__ __device__ inline int64_t paged_partial_floats(int R, int H) {
-  return ((int64_t)R * (H + 2) + 3) & ~(int64_t)3;
+  return ((int64_t)paged_partial_rows(R) * (H + 2) + 3) & ~(int64_t)3;
 }
 inline PagedDecodePlan paged_decode_plan(int R, int H, int sm_count) {
   PagedDecodePlan p;

@@ -126,7 +126,7 @@ constexpr float kNoScore = -3e38f;
 template <int H_, bool E4M3_, int NT_, int WR_>
 struct DecodeCfg {
   static constexpr int H = H_, NT = NT_, WR = WR_;
-  static constexpr bool E4M3 = E4M3_, TEAM = WR > 1;
+  static constexpr bool TC = false, E4M3 = E4M3_, TEAM = WR > 1;
   static constexpr int ROWB = E4M3 ? H : 2 * H;        // bytes of a key
   static constexpr int UPR = ROWB / 16;                // 16-byte units of a key
   static constexpr int CK = E4M3 || H == 64 ? 32 : 16; // keys of a ring slot
@@ -357,11 +357,11 @@ __device__ __forceinline__ void put_result(void* o, float* lse, int H, int r, in
   *reinterpret_cast<uint2*>((char*)o + ((int64_t)r * H + d) * 2) = y;
   if (d == 0) lse[r] = (M + log2f(L)) * 0.6931471805599453f;   // -inf with no key
 }
-__device__ __forceinline__ void put_partial(float* dst, int H, int R, int r, int d, float4 x, float M, float L) {
+__device__ __forceinline__ void put_partial(float* dst, int H, int P, int r, int d, float4 x, float M, float L) {
   *reinterpret_cast<float4*>(dst + (int64_t)r * H + d) = x;
   if (d == 0) {
-    dst[(int64_t)R * H + r] = M;
-    dst[(int64_t)R * (H + 1) + r] = L;
+    dst[(int64_t)P * H + r] = M;
+    dst[(int64_t)P * (H + 1) + r] = L;
   }
 }
 
@@ -380,7 +380,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
-  const int R = a.G * a.T;
+  const int R = a.G * a.T, P = paged_partial_rows(R);
   const DecodeShape<C> shape{a};
 
   // The join may be launched as soon as every CTA has got here; it waits.
@@ -842,7 +842,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     float* const mine = a.partials + ((int64_t)blockIdx.x * 2 + (walk.begun == 0 ? 1 : 0)) * paged_partial_floats(R, H);
     auto put = [&](int r, int d, float4 x, float M, float L) {   // four dims of row r
       if (whole) put_result((char*)a.o + out_row * H * 2, a.lse + out_row, H, r, d, x, M, L, vscale);
-      else put_partial(mine, H, R, r, d, x, M, L);
+      else put_partial(mine, H, P, r, d, x, M, L);
     };
     // O^T goes through shared memory: the slot just used, free until the next
     // copies are issued.  Four dims stay together; dims move by 8 with the column
@@ -964,8 +964,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
               if (g == 0) a.lse[out_row + r] = (M + log2f(L)) * LN2;
             } else {
               if (g == 0) {
-                mine[(int64_t)R * H + r] = M;
-                mine[(int64_t)R * (H + 1) + r] = L;
+                mine[(int64_t)P * H + r] = M;
+                mine[(int64_t)P * (H + 1) + r] = L;
               }
 #pragma unroll
               for (int ds = 0; ds < KS; ++ds) {
@@ -1005,10 +1005,11 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
 
 // Joins the partials of an item that several CTAs of the first kernel share: a
 // thread per four dims of a row and share of the partials, `per` such elements a
-// CTA, whose shares are then summed in order.  U: partials in flight a thread.
+// CTA, whose shares are then summed in order.  U: partials in flight a thread.  TC:
+// partials of the tcgen05 kernel, of which a warp takes 4 x 4 dims of 8 rows.
 // Few registers and threads a CTA, so that the whole grid starts at once as the
 // first one ends (512 threads of 75 registers, one CTA an SM, took 4 us).
-template <int H, int U, int THREADS>
+template <int H, bool TC, int U, int THREADS>
 __global__ void __launch_bounds__(THREADS)
 paged_join_kernel(const __grid_constant__ PagedDecodeArgs a, int ctas, int per) {
   __shared__ float4 sx[THREADS];
@@ -1019,10 +1020,13 @@ paged_join_kernel(const __grid_constant__ PagedDecodeArgs a, int ctas, int per) 
   const int item = split.x, first = split.y, n = split.z - first + 1;   // n partials
   // (an entry of a whole item holds anything where a wait of the first kernel ran out before it)
   if (first < 0 || split.z < first || split.z >= ctas || (unsigned)item >= (unsigned)(a.B * a.K)) return;
-  const int R = a.G * a.T, shares = blockDim.x / per;
+  const int R = a.G * a.T, P = paged_partial_rows(R), shares = blockDim.x / per;
   const int share = threadIdx.x / per, at = threadIdx.x % per;
   const int i = blockIdx.y * per + at;
-  const int r = i / (H / 4), d = i % (H / 4) * 4;
+  const int groups = P / 8, tile = i / 32;   // groups of 8 rows; the warp's tile
+  const int r = TC ? (tile / (H / 16) < groups ? tile % groups * 8 + i % 8 : R) : i / (H / 4);
+  const int d = TC ? (tile / groups * 4 + i % 32 / 8) * 4 : i % (H / 4) * 4;
+  const int64_t at4 = TC ? ((int64_t)(d / 4) * P + r) * 4 : (int64_t)r * H + d;
   const int64_t part = paged_partial_floats(R, H);
   // partial 0 in slot 1 of its CTA, the others in slot 0 of theirs
   const float* const base = a.partials + (int64_t)first * 2 * part;
@@ -1038,9 +1042,9 @@ paged_join_kernel(const __grid_constant__ PagedDecodeArgs a, int ctas, int per) 
         m[u] = -INFINITY;
         if (p < n) {
           const float* const src = base + (p ? p * 2 : 1) * part;
-          y[u] = __ldcg(reinterpret_cast<const float4*>(src + r * H + d));
-          m[u] = __ldcg(src + R * H + r);
-          l[u] = __ldcg(src + R * H + R + r);
+          y[u] = __ldcg(reinterpret_cast<const float4*>(src + at4));
+          m[u] = __ldcg(src + P * H + r);
+          l[u] = __ldcg(src + P * H + P + r);
         }
       }
       float mn = M;

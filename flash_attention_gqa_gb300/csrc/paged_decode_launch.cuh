@@ -19,7 +19,7 @@ int64_t decode_most_tiles(const PagedDecodeArgs& a) {
 // for every CTA up to 8 (64 x 8 x 512 keys: 29.7 and 27.7 us; 1 x 2: 8.1 and 12.7).
 inline int64_t decode_whole_tiles(int64_t items, int ctas) { return items >= ctas ? 8 : 4; }
 
-template <int H>
+template <int H, bool TC>
 cudaError_t launch_join(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -31,16 +31,16 @@ cudaError_t launch_join(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
   // Partials of an item: about grid / items, two more at most.  Up to 4: all in
   // flight in one thread; up to 16: two shares of 8; more (one kv head of 131072
   // keys: 304): 16 shares, 8 in flight each.
-  const int items = a.B * a.K, elements = a.G * a.T * (H / 4), partials = grid / items + 2;
+  const int items = a.B * a.K, elements = (TC ? paged_partial_rows(a.G * a.T) : a.G * a.T) * (H / 4), partials = grid / items + 2;
   const int shares = partials <= 4 ? 1 : partials <= 16 ? 2 : 16;
   int per = shares == 16 ? 32 : 256 / shares;
   while (per > 32 && per / 2 >= elements) per /= 2;
   cfg.gridDim = dim3(a.by_item ? items : grid, (elements + per - 1) / per);
   cfg.blockDim = dim3(shares * per);
   switch (shares) {
-    case 1: return cudaLaunchKernelEx(&cfg, paged_join_kernel<H, 4, 256>, a, grid, per);
-    case 2: return cudaLaunchKernelEx(&cfg, paged_join_kernel<H, 8, 256>, a, grid, per);
-    default: return cudaLaunchKernelEx(&cfg, paged_join_kernel<H, 8, 512>, a, grid, per);
+    case 1: return cudaLaunchKernelEx(&cfg, paged_join_kernel<H, TC, 4, 256>, a, grid, per);
+    case 2: return cudaLaunchKernelEx(&cfg, paged_join_kernel<H, TC, 8, 256>, a, grid, per);
+    default: return cudaLaunchKernelEx(&cfg, paged_join_kernel<H, TC, 8, 512>, a, grid, per);
   }
 }
 
@@ -60,7 +60,7 @@ cudaError_t launch_decode(PagedDecodeArgs a, int grid, cudaStream_t st) {
   KERNEL<<<grid, C::THREADS, C::SMEM, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.unsplit) return e;
-  return launch_join<C::H>(a, grid, st);
+  return launch_join<C::H, C::TC>(a, grid, st);
 }
 template <class C>
 cudaError_t launch_decode(const PagedDecodeArgs& a, int grid, cudaStream_t st) {

@@ -35,7 +35,7 @@ namespace fa {
 template <int H_, bool E4M3_>
 struct DecodeTcCfg {
   static constexpr int H = H_, HC = H / 64;
-  static constexpr bool E4M3 = E4M3_;
+  static constexpr bool TC = true, E4M3 = E4M3_;
   static constexpr int TN = H == 256 ? 64 : 128;        // keys of a tile
   static constexpr int CK = TN, TEAMS = 1, TK = TN;
   // An item's fixed cost in tiles.  64 requests of 1 to 8192 keys, 64 rows: 51.2 us with 2,
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
 
   const uint32_t q_u = smem_u32(sm), ring_u = q_u + C::QBYTES;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int R = a.G * a.T;
+  const int R = a.G * a.T, P = paged_partial_rows(R);
   const DecodeShape<C> shape{a};
   const Abort ab{&sh_abort, a.wait_limit_ns, a.err};
   // Slots: K(n) takes turn n / KS of slot n % KS, V(n) the same behind them.
@@ -617,9 +617,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
             dst[i] = make_uint4(y[0], y[1], y[2], y[3]);
           }
         } else if (r < R) {
-          uint4* const dst = reinterpret_cast<uint4*>(mine + (int64_t)r * H + c);
+          // lanes side by side: rows as they are would take eight times the store cycles
+          uint4* const dst = reinterpret_cast<uint4*>(mine) + (int64_t)(c / 4) * P + r;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
+          for (int i = 0; i < 8; ++i) dst[i * P] = make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3]);
         }
         __syncwarp();
       }
@@ -627,8 +628,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
         if (whole) {
           a.lse[item * R + r] = (m + log2f(l)) * LN2;   // -inf with no key
         } else {
-          mine[(int64_t)R * H + r] = m;
-          mine[(int64_t)R * (H + 1) + r] = l;
+          mine[(int64_t)P * H + r] = m;
+          mine[(int64_t)P * (H + 1) + r] = l;
         }
       }
       if (whole && a.by_item && !a.unsplit && tid == 0) a.splits[item] = PagedDecodeSplit{(int)item, -1, 0, 0};
