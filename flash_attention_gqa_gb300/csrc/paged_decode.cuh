@@ -48,8 +48,13 @@
 namespace fa {
 
 // ------------------------------------------------------------- primitives
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Zeros; nothing is read (`src`: an address that exists).  With the size in a register
+// every copy would cost several times as much.
+__device__ __forceinline__ void cp_zeros16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, 0;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -438,8 +443,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         for (int j = kt * NJ / KT; j < (kt + 1) * NJ / KT; ++j) {
           if (j % WR == wr) {
             const uint32_t d = (dst + lane_dst ^ swz_step(j)) + j * RPJ * C::ROWB;
-            cp_async16(d, pk, 16);
-            cp_async16(d + C::HALF, pv, 16);
+            cp_async16(d, pk);
+            cp_async16(d + C::HALF, pv);
           }
           pk += row_step;
           pv += row_step;
@@ -451,10 +456,14 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         if (j % WR != wr) continue;
         const int row = j * RPJ + lane / C::UPR, u = lane % C::UPR;
         const int64_t off = __shfl_sync(~0u, key_off, row);
-        const uint32_t n = off >= 0 ? 16 : 0, d = dst + swz<C::UPR>(row, u);
-        // nothing is read where n = 0 (q: an address that exists)
-        cp_async16(d, off >= 0 ? (const char*)a.k_cache + off + u * 16 : (const char*)a.q, n);
-        cp_async16(d + C::HALF, off >= 0 ? (const char*)a.v_cache + off + u * 16 : (const char*)a.q, n);
+        const uint32_t d = dst + swz<C::UPR>(row, u);
+        if (off >= 0) {
+          cp_async16(d, (const char*)a.k_cache + off + u * 16);
+          cp_async16(d + C::HALF, (const char*)a.v_cache + off + u * 16);
+        } else {
+          cp_zeros16(d, a.q);
+          cp_zeros16(d + C::HALF, a.q);
+        }
       }
     }
     cp_async_commit();

@@ -265,13 +265,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
     // This lane's keys of the next tile: looked up a tile early.
     constexpr int NK = C::KPW < 32 ? 1 : C::KPW / 32;
     bool live[NK];
-    int page[NK], in[NK], head = 0;
+    int page[NK], in[NK], head = 0, next_lo = 0, next_hi = 0;   // rows [lo, hi) are keys
     auto look_up = [&]() {
       head = walk.k;
+      const int row0 = walk.first + walk.tile * TN + w * C::KPW;
+      next_lo = shape.low(walk.len) - row0;
+      next_hi = walk.len - row0;
 #pragma unroll
       for (int h = 0; h < NK; ++h) {
-        const int s = walk.first + walk.tile * TN + w * C::KPW + h * 32 + lane % C::KPW;
-        live[h] = more && s >= shape.low(walk.len) && s < walk.len;
+        const int row = h * 32 + lane, s = row0 + row;
+        live[h] = more && row >= next_lo && row < next_hi;
         in[h] = s & ((1 << a.lay.page_shift) - 1);
         page[h] = -1;
         if (live[h])
@@ -281,6 +284,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
     look_up();
     for (; more && ok; ++n) {
       int64_t off[NK];
+      const int lo = next_lo, hi = next_hi;
       bool all = true;
 #pragma unroll
       for (int h = 0; h < NK; ++h) {
@@ -293,20 +297,37 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
         }
         all &= off[h] >= 0;
       }
+      const bool steps = a.lay.page_shift >= 4 && __all_sync(~0u, all);
       if (++walk.tile == walk.end) more = shape.next_item(walk, sh.ends[1]);
       look_up();
-      const bool steps = a.lay.page_shift >= 4 && __all_sync(~0u, all);
 #pragma unroll 1
       for (int kv = kind; kv < (E4M3 ? kind + 1 : 2); ++kv) {
         const char* const base = (const char*)(kv ? a.v_cache : a.k_cache);
         if (!E4M3 && !(ok = free_slot(n, kv))) break;
-        if (steps) {
+        if (steps) {   // 16 keys or more a page: one offset per 16 keys, and steps
 #pragma unroll
-          for (int kt = 0; kt < C::KPW / 16; ++kt) {   // 16 keys or more a page: one offset per 16 keys, and steps
+          for (int kt = 0; kt < C::KPW / 16; ++kt) {
             const char* src = base + __shfl_sync(~0u, off[kt >> 1], (kt & 1) * 16) + lane_src;
 #pragma unroll
             for (int j = kt * 16 / RPJ; j < (kt + 1) * 16 / RPJ; ++j) {
-              cp_async16(place(n, kv, j), src, 16);
+              cp_async16(place(n, kv, j), src);
+              src += row_step;
+            }
+          }
+        } else if (a.lay.page_shift >= 4) {   // the same, where some rows are no keys
+#pragma unroll 1
+          for (int kt = 0; kt < C::KPW / 16; ++kt) {
+            const int last = min(kt * 16 + 16, hi) - 1;   // the last key of the 16
+            const int64_t at = __shfl_sync(~0u, kt < 2 ? off[0] : off[NK - 1], last & 31);
+            const bool some = last >= max(kt * 16, lo) && at >= 0;
+            const char* src = base + at - (last - kt * 16) * a.lay.token + lane_src;
+#pragma unroll
+            for (int j0 = 0; j0 < 16 / RPJ; ++j0) {
+              const int j = kt * (16 / RPJ) + j0, row = j * RPJ + lr;
+              if (some && row >= lo && row < hi)
+                cp_async16(place(n, kv, j), src);
+              else
+                cp_zeros16(place(n, kv, j), a.q);
               src += row_step;
             }
           }
@@ -316,8 +337,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
             const int row = j * RPJ + lr;
             const int64_t at0 = __shfl_sync(~0u, off[0], row & 31), at1 = __shfl_sync(~0u, off[NK - 1], row & 31);
             const int64_t at = row < 32 ? at0 : at1;
-            // nothing is read, and zeros are written, where there is no key (q: an address that exists)
-            cp_async16(place(n, kv, j), at >= 0 ? base + at + u * 16 : (const char*)a.q, at >= 0 ? 16 : 0);
+            if (at >= 0)
+              cp_async16(place(n, kv, j), base + at + u * 16);
+            else
+              cp_zeros16(place(n, kv, j), a.q);
           }
         }
         if constexpr (!E4M3) {
@@ -359,8 +382,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
 #pragma unroll
       for (int i = 0; i < HD / 8; ++i) {
         const int u = half * (HD / 8) + i;
-        cp_async16(q_u + (u >> 3) * C::QCHUNK + sw128_offset(r, u & 7),
-                   r < R ? src + u * 16 : (const char*)a.q, r < R ? 16 : 0);
+        const uint32_t dst = q_u + (u >> 3) * C::QCHUNK + sw128_offset(r, u & 7);
+        if (r < R)
+          cp_async16(dst, src + u * 16);
+        else
+          cp_zeros16(dst, a.q);
       }
       cp_async_commit();
     };
