@@ -70,10 +70,10 @@ cudaError_t launch_decode(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
 // Up to 8, 16 and 32 rows: mma.sync, warps on their own (teams of two for 8-bit
 // caches' 32 rows at H = 256: registers).  More, and over 16 rows of bf16 at H =
 // 256: tcgen05.  Both sides at 16 requests x 4 kv heads x 8192 keys, mma.sync and
-// tcgen05: bf16 at H = 64 32 rows take 35 and 46 us; at H = 128 32 rows 56 and 55
-// (8 x 4 rows, ragged: 30 and 34), 64 rows 102 and 56; at H = 256 16 rows 89 and
-// 89, 32 rows 99 and 93, 64 rows 202 and 98.  8-bit at H = 128 32 rows 44 and 50,
-// 64 rows 79 and 52, 128 rows 139 and 58; at H = 256 32 rows 77 and 87.
+// tcgen05: bf16 at H = 64 32 rows take 35 and 46 us; at H = 128 17 rows 53 and 56,
+// 32 rows 56 and 56, 64 rows 102 and 57; at H = 256 16 rows 89 and 89, 32 rows 99
+// and 93, 64 rows 202 and 97.  8-bit at H = 128 32 rows 44 and 50, 64 rows 79 and
+// 52, 128 rows 139 and 54; at H = 256 32 rows 77 and 87.
 template <int H, bool E4M3>
 cudaError_t launch_decode_rows(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
   const int R = a.G * a.T;

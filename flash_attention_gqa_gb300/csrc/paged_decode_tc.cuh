@@ -8,10 +8,10 @@
 // the weights enter as two terms), 1536 of the 3000 cycles in which an SM's share
 // of the memory rate delivers its 64 KB.
 //
-// Measured, 16 requests x 4 kv heads x 8192 keys: bf16, H = 128, 64 rows 56 us
+// Measured, 16 requests x 4 kv heads x 8192 keys: bf16, H = 128, 64 rows 57 us
 // (memory 40, and the fixed 10 of paged_decode.cuh): a tile every 2980 cycles, of
-// which the softmax warps work 2100 and the products take 1800; 128 rows 63 us.  H =
-// 256: 64 rows 98 us (memory 80).  H = 64: 46 us (memory 20): the softmax, 2300 cycles
+// which the softmax warps work 2100 and the products take 1800; 128 rows 60 us.  H =
+// 256: 64 rows 97 us (memory 80).  H = 64: 46 us (memory 20): the softmax, 2300 cycles
 // a tile, is the bound, as it does not shrink with H.  8-bit caches: 52 us (H = 128,
 // 64 rows; memory 20), a tile every 2650 cycles, for the same reason.
 //
@@ -38,10 +38,10 @@ struct DecodeTcCfg {
   static constexpr bool TC = true, E4M3 = E4M3_;
   static constexpr int TN = H == 256 ? 64 : 128;        // keys of a tile
   static constexpr int CK = TN, TEAMS = 1, TK = TN;
-  // An item's fixed cost in tiles.  64 requests of 1 to 8192 keys, 64 rows: 51.2 us with 2,
-  // 46.0 with 3, 44.8 with 4; at H = 256, 32 rows, to 4096 keys: 44.9, 40.4 and 40.8 us.
-  // H = 64, 40 rows: 31.7, 33.1 and 35.2; 8-bit, 64 rows: 40.2, 42.8 and 45.3.
-  static constexpr int ITEM_UNITS = H == 64 || E4M3 ? 2 : 3;
+  // An item's fixed cost in tiles.  64 requests of 1 to 8192 keys, 64 rows: 46.4 us with 1,
+  // 38.6 with 2, 39.6 with 3; 8-bit 42.7, 37.1 and 38.1; at H = 256, 32 rows, to 4096 keys
+  // 38.4, 36.5 and 37.7; at H = 64, 40 rows 32.3, 30.9 and 33.1.
+  static constexpr int ITEM_UNITS = 2;
   static constexpr int CW = E4M3 ? 4 : 2;               // copying warps, two for a tile
   static constexpr int WARPS = 9 + CW, THREADS = WARPS * 32;
   static constexpr int KPW = TN / 2;                    // keys of a tile a copying warp
