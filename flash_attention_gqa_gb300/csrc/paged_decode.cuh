@@ -433,14 +433,15 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     }
     const uint32_t dst = ring_u + slot * C::SLOT;
     constexpr int NJ = CK * C::UPR / 32, RPJ = 32 / C::UPR;   // copies a lane, rows a copy
-    if (a.lay.page_shift >= 4 && __all_sync(~0u, key_off >= 0)) {
-      // whole slot, 16 keys or more a page: one offset per 16 keys, and steps
+    if (a.lay.page_shift >= 3 && __all_sync(~0u, key_off >= 0)) {
+      // whole slot, 8 keys or more a page: one offset per 8 keys, and steps
+      constexpr int K8 = CK / 8;
 #pragma unroll
-      for (int kt = 0; kt < KT; ++kt) {
-        const int64_t off = __shfl_sync(~0u, key_off, kt * 16) + lane_src;
+      for (int k8 = 0; k8 < K8; ++k8) {
+        const int64_t off = __shfl_sync(~0u, key_off, k8 * 8) + lane_src;
         const char *pk = (const char*)a.k_cache + off, *pv = (const char*)a.v_cache + off;
 #pragma unroll
-        for (int j = kt * NJ / KT; j < (kt + 1) * NJ / KT; ++j) {
+        for (int j = k8 * NJ / K8; j < (k8 + 1) * NJ / K8; ++j) {
           if (j % WR == wr) {
             const uint32_t d = (dst + lane_dst ^ swz_step(j)) + j * RPJ * C::ROWB;
             cp_async16(d, pk);

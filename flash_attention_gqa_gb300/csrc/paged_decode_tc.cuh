@@ -297,38 +297,38 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
         }
         all &= off[h] >= 0;
       }
-      const bool steps = a.lay.page_shift >= 4 && __all_sync(~0u, all);
+      const bool steps = a.lay.page_shift >= 3 && __all_sync(~0u, all);
       if (++walk.tile == walk.end) more = shape.next_item(walk, sh.ends[1]);
       look_up();
 #pragma unroll 1
       for (int kv = kind; kv < (E4M3 ? kind + 1 : 2); ++kv) {
         const char* const base = (const char*)(kv ? a.v_cache : a.k_cache);
         if (!E4M3 && !(ok = free_slot(n, kv))) break;
-        if (steps) {   // 16 keys or more a page: one offset per 16 keys, and steps
+        if (steps) {   // 8 keys or more a page: one offset per 8 keys, and steps
 #pragma unroll
-          for (int kt = 0; kt < C::KPW / 16; ++kt) {
-            const char* src = base + __shfl_sync(~0u, off[kt >> 1], (kt & 1) * 16) + lane_src;
+          for (int k8 = 0; k8 < C::KPW; k8 += 8) {
+            const char* src = base + __shfl_sync(~0u, off[k8 / 32], k8 % 32) + lane_src;
 #pragma unroll
-            for (int j = kt * 16 / RPJ; j < (kt + 1) * 16 / RPJ; ++j) {
+            for (int j = k8 / RPJ; j < (k8 + 8) / RPJ; ++j) {
               cp_async16(place(n, kv, j), src);
               src += row_step;
             }
           }
-        } else if (a.lay.page_shift >= 4) {   // the same, where some rows are no keys
+        } else if (a.lay.page_shift >= 3) {   // the same, where some rows are no keys
 #pragma unroll 1
-          for (int kt = 0; kt < C::KPW / 16; ++kt) {
-            const int last = min(kt * 16 + 16, hi) - 1;   // the last key of the 16
-            const int64_t at = __shfl_sync(~0u, kt < 2 ? off[0] : off[NK - 1], last & 31);
-            const bool some = last >= max(kt * 16, lo) && at >= 0;
-            const char* src = base + at - (last - kt * 16) * a.lay.token + lane_src;
+          for (int k8 = 0; k8 < C::KPW; k8 += 8) {
+            const int last = min(k8 + 8, hi) - 1;   // the last key of the 8
+            const int64_t at = __shfl_sync(~0u, k8 < 32 ? off[0] : off[NK - 1], last & 31);
+            const bool some = last >= max(k8, lo) && at >= 0;
+            const char* src = base + at - (last - k8) * a.lay.token + lane_src;
+            const int j = k8 / RPJ;
 #pragma unroll
-            for (int j0 = 0; j0 < 16 / RPJ; ++j0) {
-              const int j = kt * (16 / RPJ) + j0, row = j * RPJ + lr;
+            for (int i = 0; i < 8 / RPJ; ++i) {
+              const int row = (j + i) * RPJ + lr;
               if (some && row >= lo && row < hi)
-                cp_async16(place(n, kv, j), src);
+                cp_async16(place(n, kv, j + i), src + i * row_step);
               else
-                cp_zeros16(place(n, kv, j), a.q);
-              src += row_step;
+                cp_zeros16(place(n, kv, j + i), a.q);
             }
           }
         } else {

@@ -229,7 +229,7 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v,
 
 /* ------------------------------------------------------------------------
  * Paged key-value cache.  K and V live in pages of `page_size` tokens (a power
- * of two, 1..65536) that belong to no request until a block table says so:
+ * of two, 1..65536; decode is fastest from 8 on) that belong to no request until a block table says so:
  *   k_cache, v_cache : [n_pages, K, page_size, H], bf16 or e4m3, one set of
  *                      strides for both (page, head, token; in elements, each a
  *                      multiple of 16 bytes, innermost dim contiguous), so
