@@ -24,8 +24,8 @@
 // Products.  mma.sync with the keys as the 16-row operand: S^T = K Q^T and
 // O^T += V^T P^T waste nothing at R = 8, where tcgen05's 128-row tile would be
 // mostly padding and its operands would pass through tensor memory and
-// barriers.  The issue slots are 23% used at R = 8 in bf16 and 38% with 8-bit
-// caches, 41% at R = 32.  mma.sync runs at one m16n8k16 per 8 cycles and
+// barriers.  The issue slots are 21% used at R = 8 in bf16 and 36% with 8-bit
+// caches, 29% at R = 32.  mma.sync runs at one m16n8k16 per 8 cycles and
 // sub-core here (640 TFLOP/s), so it and the instructions around it would be the
 // bound from R = 64 on (102 us for 64 rows where 32 take 56 us and 8 take 47 us: 16
 // requests x 4 kv heads x 8192 keys): paged_decode_tc.cuh takes those.  The S^T
