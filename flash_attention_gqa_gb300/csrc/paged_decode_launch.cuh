@@ -16,8 +16,11 @@ int64_t decode_most_tiles(const PagedDecodeArgs& a) {
 // Requests of few tiles are not split, which saves the second launch: up to 4
 // tiles (64 requests x 8 kv heads x 256 keys: 20.0 us split, 17.5 whole; 8 x 8:
 // 8.2 and 7.8; 1 x 2 at H = 256: 8.1 and 8.9, and 2 us of the host), with items
-// for every CTA up to 8 (64 x 8 x 512 keys: 29.7 and 27.7 us; 1 x 2: 8.1 and 12.7).
-inline int64_t decode_whole_tiles(int64_t items, int ctas) { return items >= ctas ? 8 : 4; }
+// for every CTA up to 512 keys (64 x 8 x 512 keys: 29.7 and 27.7 us; 40 rows at H =
+// 256, 64 x 4 x 500 keys: 38.0 and 33.8; more keys: 64 rows, 40 x 4 x 900 28.5 and
+// 35.4; at H = 64 40 x 8 x 700 17.6 and 19.4, 64 x 8 x 1000 28.0 and 26.4).
+template <class C>
+int64_t decode_whole_tiles(int64_t items, int ctas) { return items >= ctas ? 512 / C::TK : 4; }
 
 template <int H, bool TC>
 cudaError_t launch_join(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
@@ -56,7 +59,7 @@ cudaError_t launch_decode(PagedDecodeArgs a, int grid, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if (dev < 64) ready[dev] = true;
   }
-  a.unsplit = decode_most_tiles<C>(a) <= decode_whole_tiles((int64_t)a.B * a.K, grid);
+  a.unsplit = decode_most_tiles<C>(a) <= decode_whole_tiles<C>((int64_t)a.B * a.K, grid);
   KERNEL<<<grid, C::THREADS, C::SMEM, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.unsplit) return e;
