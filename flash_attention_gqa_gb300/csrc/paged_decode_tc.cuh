@@ -207,11 +207,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
       if (ok) ok = issue_pv(n - 1, walk.end - 1 == walk.begun);
       if (!shape.next_item(walk, sh.ends[1])) break;
     }
-    if (!ok) {   // until the products issued are over: tensor memory is freed below
-      if (lead) mma_commit(teardown);
-      mbar_wait_teardown(teardown, 0, max(a.wait_limit_ns, (uint64_t)1000000000));   // they take microseconds
-      __syncwarp();
-    }
+    // Until the products issued are over, whichever wait may have run out: the softmax warps'
+    // wait for the last one may, after this warp has done all that it had to.  Tensor memory is
+    // freed below and shared memory is given back.  They take microseconds.
+    if (lead) mma_commit(teardown);
+    mbar_wait_teardown(teardown, 0, max(a.wait_limit_ns, (uint64_t)1000000000));
+    __syncwarp();
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- copies
     // bf16: two warps, each half of the keys of K(n) and then of V(n).  8-bit: two for K
