@@ -125,6 +125,18 @@ __device__ __forceinline__ void e4m3_query_scale(float big, float& up, float& do
 // (-inf) have no weight against it.
 constexpr float kNoScore = -3e38f;
 
+// The base m of the exponents, per query row, in log2 units: it is raised only where a score x
+// passes it by kRaise, and then to kBelow under the largest; weights are 2^(x - m), and m
+// cancels in o / l.  bf16 terms reach as far down as fp32, so any base would do.  f16 ends
+// at 2^16, is coarser below 2^-14 and zero below 2^-25: with the base 11 under the largest score
+// (up to 15 under a later one), all weights down to 2^-25 of the largest keep f16's 2^-11, and
+// smaller ones are off by up to 2^-36 of it.  (With the largest weight near 1, a first token of
+// no value that stands 16 nats above the others would cost the result 6%.)
+template <bool F16>
+constexpr float kRaise = F16 ? 15.0f : 8.0f;
+template <bool F16>
+constexpr float kBelow = F16 ? 11.0f : 0.0f;
+
 // ------------------------------------------------------------ configuration
 // NT: n-tiles of 8 query rows per warp.  WR: warps of a team, which share a ring
 // and the keys in it, NT * 8 rows each.
@@ -678,9 +690,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         }
 
         // Online softmax, per column.  The base m of the exponents is raised only
-        // where a score passes it by 8 (in log2 units: weights stay below 2^8), so
-        // that most slots need neither the maximum over the lanes nor a rescaling
-        // of o: exact, as m cancels in o / l.
+        // where a score passes it by far (kRaise), so that most slots need neither the
+        // maximum over the lanes nor a rescaling of o.
         bool high = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -689,7 +700,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
             float mx = fmaxf(s[0][nt][j], s[0][nt][j + 2]);
 #pragma unroll
             for (int kt = 1; kt < KT2; ++kt) mx = fmaxf(mx, fmaxf(s[kt][nt][j], s[kt][nt][j + 2]));
-            high |= fmaf(mx, sl2[nt][j], -m[nt][j]) > 8.0f;
+            high |= fmaf(mx, sl2[nt][j], -m[nt][j]) > kRaise<E4M3>;
           }
         if (__any_sync(~0u, high)) {
 #pragma unroll
@@ -703,7 +714,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
               mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 4));
               mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 8));
               mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 16));
-              const float mn = fmaxf(m[nt][j], mx * sl2[nt][j]);
+              const float mn = fmaxf(m[nt][j], mx * sl2[nt][j] - kBelow<E4M3>);
               alpha[j] = fast_exp2(m[nt][j] - mn);
               m[nt][j] = mn;
               l[nt][j] *= alpha[j];
@@ -734,7 +745,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
         // O^T += V^T P^T.  bf16 caches: the weights go in as two bf16 terms, cut
         // and rest (off by 2^-16 in all), so that o is rounded to bf16 once, at the
         // end.  The rest is kept above zero, or an infinite value would give
-        // 0 x inf.  8-bit caches: one f16 term, off by 2^-12, against values of 2^-4.
+        // 0 x inf.  8-bit caches: one f16 term, off by 2^-11 (kRaise), against values off by 2^-4.
         uint32_t p[KT2][NT][2], pl[KT2][NT][2];
 #pragma unroll
         for (int kt = 0; kt < KT2; ++kt)

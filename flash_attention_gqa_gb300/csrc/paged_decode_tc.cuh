@@ -476,11 +476,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
         mbar_arrive(pair_met(warp));
         if (!(ok = tc_wait(pair_met(warp), pairs++ & 1, ab))) break;
         top = fmaxf(top, sh_top[n & 1][half ^ 1][r]);
-        // The base is raised only where a score passes it by 8, as in paged_decode.cuh.
+        // The base is raised only where a score passes it by far, as in paged_decode.cuh.
         float alpha = 1.0f;
-        if (top > m + 8.0f || (first && top > m)) {
-          alpha = fast_exp2(m - top);   // 0 where there was none (top is no -inf here)
-          m = top;
+        if (top > m + kRaise<E4M3> || (first && top > m)) {
+          const float to = top - kBelow<E4M3>;
+          alpha = fast_exp2(m - to);   // 0 where there was none (top is no -inf here)
+          m = to;
         }
         const float base = m == -INFINITY ? 0.0f : m;
         if (!first && __any_sync(~0u, alpha != 1.0f)) {

@@ -29,3 +29,47 @@ def test_decode_waits_that_run_out_anywhere_leave_nothing_behind(lib, H, dtype):
         again = _decode(p)
         _ok()
         assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+def _sinks(rows, H, n, B, spread=0.3):
+    """An 8-bit cache whose requests have one key far above the others, with values of zero: kv
+    heads 0 to 3 at the first position, 4 to 7 in the middle, 12 to 17 nats above."""
+    G, T = rows
+    p = P.problem(H, B=B, K=8, G=G, T=T, H=H, lens=[n] * B, page=16, dtype=E4M3)
+    q, kc, vc, table, lens, ks, vs = p
+    gap = torch.tensor([12.0, 14.0, 16.0, 17.0] * 2)
+    q.mul_(spread)
+    q[..., 0] = gap[:, None, None].bfloat16()
+    kc.view(torch.uint8)[..., 0] = 0
+    for b in range(B):
+        for h in range(8):
+            s = 0 if h < 4 else n // 2
+            at = (int(table[b, s // 16]), h, s % 16)
+            kc.view(torch.uint8)[at] = 0
+            kc[at][0] = torch.tensor(32.0).to(E4M3)
+            vc.view(torch.uint8)[at] = 0
+    ks.fill_(1 / 32)
+    return p
+
+
+@pytest.mark.parametrize("H", [64, 128, 256])
+@pytest.mark.parametrize("rows", [(8, 1), (4, 3), (24, 1), (40, 1), (16, 5)], ids=lambda r: "G%d_T%d" % r)
+def test_decode_8bit_keys_far_below_the_largest(lib, rows, H):
+    """Every other key weighs 2^-17 to 2^-25 of the largest, and is all of the result: the weights'
+    f16 terms have to hold them as well as they hold large ones.  Requests done whole, by one CTA
+    each, and split."""
+    for B, n in ((40, 450), (24, 1500), (2, 6000)):
+        _check(_sinks(rows, H, n, B))
+
+
+@pytest.mark.parametrize("G", [8, 24, 64])
+def test_decode_8bit_large_scores(lib, G):
+    """Scores in the hundreds that grow along the keys: the base of the exponents moves."""
+    for H in (64, 128, 256):
+        p = P.problem(9, B=3, K=1, G=G, T=1, H=H, lens=[900, 64, 1], page=16, dtype=E4M3)
+        q, kc, vc, table, lens, ks, vs = p
+        grow = torch.ones(kc.shape[0])
+        for j, page in enumerate(table[0][table[0] >= 0].tolist()):
+            grow[page] = 0.05 + 0.05 * j
+        kc.copy_((kc.float() * grow[:, None, None, None]).to(E4M3))
+        _check(((q.float() * 40).bfloat16(), kc, vc, table, lens, ks, vs))
