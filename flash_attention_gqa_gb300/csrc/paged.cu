@@ -204,7 +204,8 @@ cudaError_t launch_paged_tables(const PagedTablesArgs& a, cudaStream_t st) {
   const bool in_place = a.total_lens == a.cached_lens || a.free_used_out == a.free_used;
   auto* const kernel = in_place ? paged_tables_kernel<true> : paged_tables_kernel<false>;
   const size_t smem = (3 * (size_t)a.B + 1) * sizeof(int);
-  if (smem > 48 * 1024) {
+  // (needed from 48 KB of dynamic and static memory together on; half a KB is static)
+  if (smem > 47 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }

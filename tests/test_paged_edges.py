@@ -1,5 +1,9 @@
 """The paged cache operators where they can go wrong: waits that run out, values at the ends of
 their types, sizes at the limits of a launch, errors of other calls."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -73,3 +77,27 @@ def test_decode_8bit_large_scores(lib, G):
             grow[page] = 0.05 + 0.05 * j
         kc.copy_((kc.float() * grow[:, None, None, None]).to(E4M3))
         _check(((q.float() * 40).bfloat16(), kc, vc, table, lens, ks, vs))
+
+
+_TABLES_SIZES = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import numpy as np
+import _paged as P
+import test_paged as T
+for B in {sizes}:
+    for in_place in (False, True):
+        case = T._tables_case(B, B, 16, 40, 2)
+        for g, w in zip(T._run_tables(case, in_place), P.tables(*case[:7])):
+            assert np.array_equal(g.ravel(), np.asarray(w).ravel()), B
+T._ok()
+"""
+
+
+@pytest.mark.parametrize("sizes", [(4053, 4054, 4095), (4080,), (4096, 4095)], ids=str)
+def test_tables_around_48_kb_of_shared_memory(lib, sizes):
+    """In a process of their own: a call with more requests raises the launch's limit for later ones."""
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = _TABLES_SIZES.format(root=os.path.dirname(tests), tests=tests, sizes=sizes)
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
