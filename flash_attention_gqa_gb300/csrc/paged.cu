@@ -204,9 +204,12 @@ cudaError_t launch_paged_tables(const PagedTablesArgs& a, cudaStream_t st) {
   const bool in_place = a.total_lens == a.cached_lens || a.free_used_out == a.free_used;
   auto* const kernel = in_place ? paged_tables_kernel<true> : paged_tables_kernel<false>;
   const size_t smem = (3 * (size_t)a.B + 1) * sizeof(int);
-  // (needed from 48 KB of dynamic and static memory together on; half a KB is static)
+  // (needed from 48 KB of dynamic and static memory together on; half a KB is static.
+  // Always to what the largest call needs: the limit is the function's, and a smaller one
+  // would be met by the launch of another thread, or by an instantiated graph.)
   if (smem > 47 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr int most = (3 * kMaxPagedBatch + 1) * sizeof(int);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
   }
   // Two tokens a thread: the searches and look-ups of a token are a chain of

@@ -1,8 +1,10 @@
 """The paged cache operators where they can go wrong: waits that run out, values at the ends of
 their types, sizes at the limits of a launch, errors of other calls."""
 import os
+import struct
 import subprocess
 import sys
+import threading
 
 import pytest
 import torch
@@ -101,3 +103,44 @@ def test_tables_around_48_kb_of_shared_memory(lib, sizes):
     code = _TABLES_SIZES.format(root=os.path.dirname(tests), tests=tests, sizes=sizes)
     run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert run.returncode == 0, run.stderr[-2000:]
+
+
+def _tables_state(B):
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    lens = i32([3] * B)
+    return (lens, i32([1] * B), i32(range(B)), i32([0]), i32([[b] for b in range(B)]), torch.empty_like(lens),
+            i32([0] * (B + 1)), torch.empty(B, dtype=torch.int64, device="cuda"), None, i32([0]), B, 16)
+
+
+def _tables_done(args):
+    B = args[0].numel()
+    want = torch.arange(B, device="cuda")
+    return torch.equal(args[7], want * 16 + 3) and (args[5] == 4).all() and torch.equal(args[6][:-1].long(), want)
+
+
+def test_tables_of_different_sizes_in_two_threads(lib):
+    """One thread's launch with fewer requests leaves the other's its shared memory (calls without
+    the checks of the binding between them, so that the two meet)."""
+    states = [_tables_state(8192), _tables_state(4096)]
+    torch.cuda.synchronize()
+    start, failed = threading.Barrier(2), []
+
+    def work(args):
+        stream = torch.cuda.Stream()
+        c, n, f, u, t, total, starts, slots, _, out, n_pages, page = args
+        B = n_pages
+        record = struct.pack("17q", *(x.data_ptr() for x in (c, n, f)), B, u.data_ptr(), t.data_ptr(), 1,
+                             *(x.data_ptr() for x in (total, starts, slots)), 0, B, out.data_ptr(), B, n_pages,
+                             page, stream.cuda_stream)
+        torch.cuda.set_device(0)
+        start.wait()
+        failed.append(sum(lib.fa_paged_tables_packed(record) for _ in range(40000)))
+
+    threads = [threading.Thread(target=work, args=(s,)) for s in states]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert failed == [0, 0]
+    _ok()
+    assert all(_tables_done(s) for s in states)
