@@ -238,14 +238,14 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t st) {
   int64_t tokens = (four ? 4 : 1) * kAppendThreads / units;
   if (tokens < 1) tokens = 1;
   const unsigned blocks = (unsigned)((a.N + tokens - 1) / tokens);
-  if (a.e4m3) {
-    if (four) paged_append_kernel<true, 4><<<blocks, kAppendThreads, 0, st>>>(a, (int)tokens);
-    else paged_append_kernel<true, 1><<<blocks, kAppendThreads, 0, st>>>(a, (int)tokens);
-  } else {
-    if (four) paged_append_kernel<false, 4><<<blocks, kAppendThreads, 0, st>>>(a, (int)tokens);
-    else paged_append_kernel<false, 1><<<blocks, kAppendThreads, 0, st>>>(a, (int)tokens);
-  }
-  return cudaGetLastError();
+  // (cudaLaunchKernelEx: its status is this launch's, whatever error an earlier call has left)
+  auto* const kernel = a.e4m3 ? (four ? paged_append_kernel<true, 4> : paged_append_kernel<true, 1>)
+                              : (four ? paged_append_kernel<false, 4> : paged_append_kernel<false, 1>);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kAppendThreads);
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, kernel, a, (int)tokens);
 }
 
 }  // namespace fa

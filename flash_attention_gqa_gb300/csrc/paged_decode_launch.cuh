@@ -60,8 +60,12 @@ cudaError_t launch_decode(PagedDecodeArgs a, int grid, cudaStream_t st) {
     if (dev < 64) ready[dev] = true;
   }
   a.unsplit = decode_most_tiles<C>(a) <= decode_whole_tiles<C>((int64_t)a.B * a.K, grid);
-  KERNEL<<<grid, C::THREADS, C::SMEM, st>>>(a);
-  e = cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  e = cudaLaunchKernelEx(&cfg, KERNEL, a);   // this launch's status, whatever an earlier call has left
   if (e != cudaSuccess || a.unsplit) return e;
   return launch_join<C::H, C::TC>(a, grid, st);
 }

@@ -144,3 +144,41 @@ def test_tables_of_different_sizes_in_two_threads(lib):
     assert failed == [0, 0]
     _ok()
     assert all(_tables_done(s) for s in states)
+
+
+def _three_calls(stream=None):
+    """The three operators as calls that return their status, and a check of what they did."""
+    tables = _tables_state(8)
+    gen = torch.Generator().manual_seed(0)
+    kv = torch.randn((2, 8, 2, 64), generator=gen).bfloat16().cuda()
+    caches = [torch.zeros((8, 2, 16, 64), dtype=BF16, device="cuda") for _ in range(2)]
+    slots = torch.arange(8, device="cuda") * 16
+    p = P.problem(3, B=3, K=2, G=4, T=1, H=64, lens=[700, 3, 40], page=16)
+    want = _check(p)
+    q, table, lens = (p[i].cuda() for i in (0, 3, 4))
+    pages = [P.to_device(c, "cuda") for c in p[1:3]]
+    o, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    ws = torch.empty(binding.fa_paged_decode_workspace_size(3, 2, 4, 1, 64), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+
+    def done():
+        _ok()
+        assert _tables_done(tables)
+        assert all(torch.equal(c[:, :, 0], x) for c, x in zip(caches, kv))
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+    return [lambda: binding.fa_paged_tables(*tables, stream=stream, check=False),
+            lambda: binding.fa_paged_append(*kv, slots, *caches, stream=stream, check=False),
+            lambda: binding.fa_paged_decode(q, *pages, table, lens, o, lse, ws, stream=stream, check=False)], done
+
+
+def test_errors_of_earlier_calls_are_not_theirs(lib):
+    """An error that another user of the runtime has left behind (here: a device that is none)."""
+    calls, done = _three_calls()
+    try:
+        for call in calls:
+            assert lib.cudaSetDevice(9999) != 0 and lib.cudaPeekAtLastError() != 0
+            assert call() == binding.FA_OK
+    finally:
+        lib.cudaGetLastError()
+    done()
