@@ -51,7 +51,13 @@ bool decode_shape_ok(int B, int K, int G, int T, int H) {
          (int64_t)B * K <= 65535;
 }
 
-int status(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+// The status of a launch.  A failed one leaves nothing behind that a later call, of this library or
+// of another user of the runtime, would take for its own.
+int status(cudaError_t e) {
+  if (e == cudaSuccess) return FA_OK;
+  cudaGetLastError();
+  return FA_ERR_CUDA;
+}
 
 }  // namespace
 

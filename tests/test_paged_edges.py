@@ -1,5 +1,6 @@
 """The paged cache operators where they can go wrong: waits that run out, values at the ends of
 their types, sizes at the limits of a launch, errors of other calls."""
+import ctypes
 import os
 import struct
 import subprocess
@@ -181,4 +182,23 @@ def test_errors_of_earlier_calls_are_not_theirs(lib):
             assert call() == binding.FA_OK
     finally:
         lib.cudaGetLastError()
+    done()
+
+
+def test_a_failed_call_leaves_no_error_behind(lib):
+    """Launches into a capture that something has spoiled (a synchronisation) are refused by the
+    runtime; the calls after it know nothing of that."""
+    stream = torch.cuda.Stream()
+    calls, done = _three_calls(stream)
+    at, graph = ctypes.c_void_p(stream.cuda_stream), ctypes.c_void_p()
+    for call in calls:
+        assert lib.cudaStreamBeginCapture(at, 2) == 0
+        assert lib.cudaStreamSynchronize(at) != 0
+        lib.cudaGetLastError()
+        rc, left = call(), lib.cudaPeekAtLastError()
+        assert lib.cudaStreamEndCapture(at, ctypes.byref(graph)) != 0
+        lib.cudaGetLastError()
+        assert rc == binding.FA_ERR_CUDA and left == 0
+    for call in calls:
+        assert call() == binding.FA_OK
     done()
