@@ -285,8 +285,11 @@ def fa_bwd_masked(q, k, v, o, lse, dO, seg_q, seg_kv, causal, mask, dq, dk, dv, 
 # few Python operations: all in one condition, sizes by numel of contiguous tensors, types
 # by identity.  Where it fails, _dense names the tensor that is wrong.
 
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream   # its address; a Stream object costs 2 us
+# What torch.cuda's functions call, 2 us cheaper without the objects around it.  A torch without
+# CUDA lacks both, and runs the host-only parts of this module all the same.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
 # The packed calls' records: ctypes takes 2 us for two dozen arguments, and a sixth of it here.
 _TABLES, _APPEND, _DECODE = (struct.Struct(f"{n}q").pack for n in (17, 21, 25))
 _BF16, _I32, _I64, _F32, _E4M3 = (torch.bfloat16, torch.int32, torch.int64, torch.float32,

@@ -1,7 +1,10 @@
 """The paged cache operators without a GPU: argument checks of the C ABI (fake pointers: every
 call is refused, or has nothing to do, before any launch) and of the binding."""
 import ctypes
+import os
 import struct
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -132,3 +135,29 @@ def test_packed_sizes_have_to_fit(clib, name, n):  # noqa: F811
 def test_argument_types_are_plain(clib):  # noqa: F811
     for name in ("fa_paged_tables", "fa_paged_append", "fa_paged_decode"):
         assert binding.SIGNATURES[name][0] is ctypes.c_int
+
+
+_WITHOUT_CUDA = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+from flash_attention_gqa_gb300 import binding
+assert binding.FA_OK == 0 and "fa_paged_decode" in binding.SIGNATURES
+lens = torch.zeros(2, dtype=torch.int32)
+try:
+    binding.fa_paged_tables(lens, lens, lens, lens[:1], lens[:, None], lens, lens, lens.long(), None,
+                            lens[:1], 2, 16)
+except ValueError as e:
+    assert "CUDA" in str(e)
+else:
+    raise AssertionError("tensors on the CPU were taken")
+"""
+
+
+def test_binding_imports_with_a_torch_without_cuda():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", _WITHOUT_CUDA.format(root=root)], capture_output=True, text=True)
+    assert run.returncode == 0, run.stderr
