@@ -120,6 +120,12 @@ __device__ __forceinline__ void e4m3_query_scale(float big, float& up, float& do
   up = __uint_as_float((uint32_t)(e + 127) << 23);
   down = __uint_as_float((uint32_t)(127 - e) << 23);
 }
+// What turns a product of such a row into log2 units.  Kept between the ends of fp32: masked
+// scores (-inf) times zero, and scores of zero times infinity, would be no numbers.
+__device__ __forceinline__ float e4m3_score_scale(float down, float kscale) {
+  const float x = down * kscale * 1.4426950408889634f, least = 0x1p-126f, most = 0x1.fffffep127f;
+  return x < least ? least : x > most ? most : x;   // (NaN stays)
+}
 
 // The base of a column that has met no score: finite, so that masked scores
 // (-inf) have no weight against it.
@@ -565,7 +571,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) sl2[nt][j] = sh_down[row0 + nt * 8 + 2 * c + j] * kscale * LOG2E;
+          for (int j = 0; j < 2; ++j) sl2[nt][j] = e4m3_score_scale(sh_down[row0 + nt * 8 + 2 * c + j], kscale);
       }
     } else {
       uint2 x[NT][KS];
@@ -584,7 +590,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
           const float down = scale_q(x[nt]);
 #pragma unroll
           for (int j = 0; j < 2; ++j)
-            sl2[nt][j] = __shfl_sync(~0u, down, (2 * c + j) * 4) * kscale * LOG2E;
+            sl2[nt][j] = e4m3_score_scale(__shfl_sync(~0u, down, (2 * c + j) * 4), kscale);
         }
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {

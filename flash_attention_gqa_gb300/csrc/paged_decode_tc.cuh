@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
           }
           sts16(place(i), make_uint4(y[0], y[1], y[2], y[3]));
         }
-        sl2_next = down * (a.k_scale ? __ldg(a.k_scale + w.k) : 1.0f) * LOG2E;
+        sl2_next = e4m3_score_scale(down, a.k_scale ? __ldg(a.k_scale + w.k) : 1.0f);
       }
       fence_proxy_async_smem();
       mbar_arrive(q_full);

@@ -202,3 +202,16 @@ def test_a_failed_call_leaves_no_error_behind(lib):
     for call in calls:
         assert call() == binding.FA_OK
     done()
+
+
+@pytest.mark.parametrize("G", [8, 12, 24, 40])
+def test_decode_8bit_scores_at_the_ends_of_fp32(lib, G):
+    """Queries and scales whose product, with what undoes the queries' scaling, leaves fp32: scores
+    of nothing (masked keys stay masked, the kept ones weigh the same), and keys of zeros."""
+    for H in (64, 128, 256):
+        p = list(P.problem(17, B=3, K=3, G=G, T=1, H=H, lens=[300, 21, 40], page=16, dtype=E4M3))
+        p[0][:, :2] = (p[0][:, :2].float() * 1e-30).bfloat16()
+        p[5] = torch.tensor([1e-20, 1e-38, 1e3])
+        p[0][:, 2] = 1e38
+        p[1].view(torch.uint8)[:, 2] = 0
+        _check(tuple(p))
