@@ -311,7 +311,10 @@ def _paged_cache(k_cache, v_cache, k_scale, v_scale, K: int, H: int, index: int)
     if len(shape) != 4 or shape[1] != K or shape[3] != H or v_cache.shape != shape:
         raise ValueError(f"k_cache and v_cache must be [n_pages, {K}, page_size, {H}], "
                          f"got {tuple(shape)} and {tuple(v_cache.shape)}")
-    if (stride[3] != 1 or v_cache.stride() != stride) and k_cache.numel():
+    # (of dims of one, no stride is used)
+    if (stride[3] != 1 or v_cache.stride() != stride) and k_cache.numel() and any(
+            n > 1 and (x != y or i == 3 and x != 1)
+            for i, (n, x, y) in enumerate(zip(shape, stride, v_cache.stride()))):
         raise ValueError("k_cache and v_cache must have the same strides, innermost 1")
     if k_cache.get_device() != index or v_cache.get_device() != index or index < 0:
         raise ValueError("k_cache and v_cache must be on the CUDA device of the other tensors")

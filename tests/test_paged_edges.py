@@ -215,3 +215,31 @@ def test_decode_8bit_scores_at_the_ends_of_fp32(lib, G):
         p[0][:, 2] = 1e38
         p[1].view(torch.uint8)[:, 2] = 0
         _check(tuple(p))
+
+
+@pytest.mark.parametrize("single", ["heads", "page size", "pages"])
+def test_strides_of_single_dims_may_differ(lib, single):
+    """A dimension of one has no stride that matters: a cache written as [pages, page size, K, H] is
+    one written as [pages, K, page size, H] where K or the page size is one."""
+    n_pages, K, page = dict(zip(("heads", "page size", "pages"), ((9, 1, 16), (60, 2, 1), (1, 2, 64))))[single]
+    gen = torch.Generator().manual_seed(2)
+    k, v = (torch.randn((n_pages, K, page, 64), generator=gen).bfloat16().cuda() for _ in range(2))
+    if single == "pages":
+        odd = v.as_strided(v.shape, (7, *v.stride()[1:]))
+    else:
+        odd = v.view(n_pages, page, K, 64).transpose(1, 2)
+        assert torch.equal(odd, v)
+    assert odd.stride() != k.stride()
+    table = torch.arange(n_pages, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([min(60, n_pages * page)], dtype=torch.int32, device="cuda")
+    q = torch.randn((1, K, 4, 1, 64), generator=gen).bfloat16().cuda() / 8
+    want = binding.paged_attention_decode(q, k, v, table, lens)
+    for caches in ((k, odd), (odd, v)):
+        if caches[0] is odd:
+            want = binding.paged_attention_decode(q, v, v, table, lens)
+        o, lse = binding.paged_attention_decode(q, *caches, table, lens)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    new = torch.randn((1, K, 64), generator=gen).bfloat16().cuda()
+    binding.fa_paged_append(new, new, torch.tensor([5], device="cuda"), k, odd)
+    assert torch.equal(k[5 // page, :, 5 % page], new[0]) and torch.equal(v[5 // page, :, 5 % page], new[0])
+    _ok()
