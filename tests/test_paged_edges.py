@@ -12,7 +12,7 @@ import torch
 
 from flash_attention_gqa_gb300 import binding
 import _paged as P
-from test_paged import BF16, E4M3, _check, _decode, _ok
+from test_paged import BF16, E4M3, _append_case, _check, _decode, _ok, _stored
 
 pytestmark = pytest.mark.gpu
 
@@ -243,3 +243,56 @@ def test_strides_of_single_dims_may_differ(lib, single):
     binding.fa_paged_append(new, new, torch.tensor([5], device="cuda"), k, odd)
     assert torch.equal(k[5 // page, :, 5 % page], new[0]) and torch.equal(v[5 // page, :, 5 % page], new[0])
     _ok()
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("shape", [(60001, 3, 64, 16, "token"), (8003, 5, 256, 32, "head"),
+                                   (9999, 8, 128, 64, "head")], ids=lambda s: "N%d_K%d_H%d" % s[:3])
+def test_append_of_many_tokens(lib, shape, dtype):
+    """Four pairs of loads a thread: heads that do not divide a CTA's units, a last CTA with few
+    tokens, padding and slots past the cache among the loads."""
+    N, K, H, page, layout = shape
+    k, v, slots, caches, scales = _append_case(N, N, K, H, page, dtype, layout, pad=32)
+    past = torch.rand(N, generator=torch.Generator().manual_seed(N)) < 0.01
+    n_slots = caches[0].shape[0] * page
+    slots[past] = n_slots + slots[past].clamp(min=0)
+    dev = [P.to_device(c, "cuda") for c in caches]
+    binding.fa_paged_append(*(P.to_device(x, "cuda") for x in (k, v)), slots.cuda(), *dev,
+                            *(x if x is None else x.cuda() for x in scales))
+    assert binding.fa_check_status() == binding.FA_ERR_DEVICE_VALUE
+    live = (slots >= 0) & (slots < n_slots)
+    at = slots[live]
+    bits = torch.int16 if dtype is BF16 else torch.uint8
+    for x, want, got, scale in zip((k, v), caches, dev, scales):
+        put = x if scale is None else _stored(x, scale)
+        want.view(bits)[at // page, :, at % page] = put.contiguous().view(bits)[live]
+        assert torch.equal(got.cpu().contiguous().view(bits), want.contiguous().view(bits))
+    _ok()
+
+
+@pytest.mark.parametrize("G", [8, 20, 40])
+def test_decode_8bit_without_scales(lib, G):
+    for H in (64, 128, 256):
+        p = list(P.problem(23, B=3, K=2, G=G, T=1, H=H, lens=[700, 1, 90], page=16, dtype=E4M3))
+        for c in p[1:3]:
+            c.copy_((c.float() / 32).to(E4M3))
+        for scales in ([None, None], [p[5] * 16, None], [None, p[6]]):
+            p[5:] = scales
+            _check(tuple(p))
+
+
+@pytest.mark.parametrize("G", [1, 40])
+@pytest.mark.parametrize("B,K", [(8191, 8), (257, 255)])
+def test_decode_of_many_heads(lib, B, K, G):
+    """Close to the limit of B * K; every 97th request is compared."""
+    rng = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 41, (B,), generator=rng)
+    lens[::97] = torch.arange(len(lens[::97])) % 60
+    lens[5] = 3000
+    p = P.problem(B, B=B, K=K, G=G, T=1, H=64, lens=lens.tolist(), page=16)
+    o, lse = (x.cpu() for x in _decode(p))
+    _ok()
+    some = torch.cat([torch.arange(0, B, 97), torch.tensor([5, B - 1])])[:40 if K > 8 else None]
+    q, kc, vc, table, n, *_ = p
+    want = P.decode(q[some], kc, vc, table[some], n[some])
+    P.check_decode(o[some], lse[some], want, 64, False, 3000)
