@@ -9,7 +9,6 @@ constexpr int kMaxPagedBatch = 8192;       // requests of one call: their offset
 constexpr int kMaxPageSize = 65536;        // tokens per page, a power of two
 constexpr int kMaxPagedLen = 1 << 30;      // keys of one request (max_pages * page_size)
 constexpr int kMaxPagedRows = 128;         // query rows per kv head, G * T
-constexpr float kE4m3Max = 448.0f;
 
 // Where key (page, kv head, offset in the page) of a cache starts, in bytes
 // from the cache's base: the strides are those of [pages, K, page_size, H].

@@ -26,16 +26,18 @@
 // mostly padding and its operands would pass through tensor memory and
 // barriers.  The issue slots are 21% used at R = 8 in bf16 and 36% with 8-bit
 // caches, 29% at R = 32.  mma.sync runs at one m16n8k16 per 8 cycles and
-// sub-core here (640 TFLOP/s), so it and the instructions around it would be the
-// bound from R = 64 on (102 us for 64 rows where 32 take 56 us and 8 take 47 us: 16
-// requests x 4 kv heads x 8192 keys): paged_decode_tc.cuh takes those.  The S^T
+// sub-core here (640 TFLOP/s), so it and the instructions around it are the bound
+// from some 32 rows on (8 rows 47 us, 32 rows 56, 64 rows 102: 16 requests x 4 kv
+// heads x 8192 keys): paged_decode_tc.cuh takes more than 32 rows, and at H = 256 more
+// than 16 of bf16 caches.  The S^T
 // accumulator becomes the P^T operand by one 8x8 transpose (movmatrix), and maxima
 // and sums live in the lanes that own the columns.
 //
 // Streams.  Each warp is on its own: it copies its keys (16-byte cp.async,
 // swizzled so that ldmatrix is conflict-free) into its own ring, and waits for
 // nobody until its CTA's part of the item ends; the ring runs ahead across items.
-// 17 to 32 rows at H = 256: teams of two warps share a ring and hold 16 rows each.
+// 17 to 32 rows of 8-bit caches at H = 256: teams of two warps share a ring and hold 16
+// rows each.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>

@@ -16,9 +16,10 @@ int64_t decode_most_tiles(const PagedDecodeArgs& a) {
 // Requests of few tiles are not split, which saves the second launch: up to 4
 // tiles (64 requests x 8 kv heads x 256 keys: 20.0 us split, 17.5 whole; 8 x 8:
 // 8.2 and 7.8; 1 x 2 at H = 256: 8.1 and 8.9, and 2 us of the host), with items
-// for every CTA up to 512 keys (64 x 8 x 512 keys: 29.7 and 27.7 us; 40 rows at H =
-// 256, 64 x 4 x 500 keys: 38.0 and 33.8; more keys: 64 rows, 40 x 4 x 900 28.5 and
-// 35.4; at H = 64 40 x 8 x 700 17.6 and 19.4, 64 x 8 x 1000 28.0 and 26.4).
+// for every CTA up to 512 keys (64 x 8 x 512 keys: 29.7 split and 27.7 us whole; 40 rows
+// at H = 256, 64 x 4 x 500 keys: 38.0 and 33.8).  With more keys it depends on how full the
+// last round of CTAs is, which the rule does not look at: 64 rows, 40 x 4 x 900 28.5 split and
+// 35.4 whole; at H = 64 40 x 8 x 700 17.6 and 19.4, but 64 x 8 x 1000 28.0 and 26.4.
 template <class C>
 int64_t decode_whole_tiles(int64_t items, int ctas) { return items >= ctas ? 512 / C::TK : 4; }
 

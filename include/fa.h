@@ -282,8 +282,8 @@ int fa_paged_tables(const int32_t* cached_lens, const int32_t* new_lens,
  *   cache[slot / page_size, k, slot % page_size, :] = x[n, k, :],  slot = slots[n]
  * k, v: bf16 [N, K, H] with token and head strides in elements (multiples of 8,
  * so views of a fused projection's output work), 16-byte aligned.  An e4m3
- * cache gets x / scale[k] rounded to nearest even and saturated at +-448 (NaN
- * stays NaN); k_scale, v_scale: float32 [K] in device memory, positive, or
+ * cache gets the float32 quotient x / scale[k] rounded to nearest even and saturated
+ * at +-448 (NaN stays NaN); k_scale, v_scale: float32 [K] in device memory, positive, or
  * NULL for 1 (NULL with a bf16 cache).  Tokens with slot < 0 are skipped
  * (padding); so is a slot past the cache, which sets FA_ERR_DEVICE_VALUE.
  * The slots of one call are distinct: of two tokens with one slot, either may
