@@ -31,6 +31,7 @@ FA_CACHE_E4M3 = 1
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _L = ctypes.c_int64
+_F = ctypes.c_float
 SIGNATURES = {
     "fa_fwd": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _P]),
     "fa_bwd_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I]),
@@ -59,6 +60,17 @@ SIGNATURES = {
     "fa_paged_tables_packed": (_I, [ctypes.c_char_p]),
     "fa_paged_append_packed": (_I, [ctypes.c_char_p]),
     "fa_paged_decode_packed": (_I, [ctypes.c_char_p]),
+    "fa_rotary": (_I, [_P, _L, _L, _L, _P, _L, _L, _L, _P, _L, _L, _L, _P, _L, _L, _L, _P, _L, _L, _L,
+                       _P, _P, _I, _I, _I, _I, _F, _I, _I, _I, _I, _I, _P]),
+    "fa_paged_rotary_append": (_I, [_P, _L, _L, _P, _L, _L, _L, _P, _L, _L, _P, _L, _L, _P, _L, _L, _P,
+                                    _P, _I, _I, _I, _F, _P, _P, _P, _I, _P, _P, _L, _L, _L, _I, _I, _I,
+                                    _I, _I, _I, _I, _P]),
+    "fa_paged_free": (_I, [_P, _P, _I, _P, _P, _I, _P, _P, _I, _P, _P, _P, _I, _I, _I, _P]),
+    "fa_paged_fork": (_I, [_P, _P, _P, _I, _P, _P, _I, _P, _P, _I, _P, _P, _P, _P, _I, _I, _I, _P]),
+    "fa_paged_compact": (_I, [_P, _P, _I, _P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
+    "fa_paged_copy": (_I, [_P, _I, _P, _P, _I, _L, _L, _L, _L, _I, _I, _I, _I, _I, _P]),
+    **{f"fa_{n}_packed": (_I, [ctypes.c_char_p]) for n in (
+        "rotary", "paged_rotary_append", "paged_free", "paged_fork", "paged_compact", "paged_copy")},
     "fa_check_status": (_I, [_P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_set_wait_limit_ns": (_I, [ctypes.c_uint64]),
@@ -292,6 +304,8 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda index: torch.cuda.current_stream(index).cuda_stream)
 # The packed calls' records: ctypes takes 2 us for two dozen arguments, and a sixth of it here.
 _TABLES, _APPEND, _DECODE = (struct.Struct(f"{n}q").pack for n in (17, 21, 25))
+_ROTARY, _ROTARY_APPEND, _FREE, _FORK, _COMPACT, _COPY = (
+    struct.Struct(f"{n}q").pack for n in (33, 39, 16, 18, 16, 15))
 _BF16, _I32, _I64, _F32, _E4M3 = (torch.bfloat16, torch.int32, torch.int64, torch.float32,
                                   torch.float8_e4m3fn)
 
@@ -452,6 +466,243 @@ def fa_paged_decode_workspace_size(B, K, G, T, H) -> int:
     return int(load().fa_paged_decode_workspace_size(B, K, G, T, H))
 
 
+# ------------------------------------------- rotary positions, pages: C names
+
+def _float_bits(x: float) -> int:
+    return struct.unpack("i", struct.pack("f", x))[0]
+
+
+def _turning(positions, inv_freq, axes, dims: int, dev: int):
+    """(positions' strides, number of axes, axes' address) of checked positions [n_axes, ...] or, of
+    one axis, [...], with `dims` dims behind the axis."""
+    if positions.dtype is not _I32 or positions.get_device() != dev:
+        raise ValueError(f"positions must be an int32 tensor on cuda:{dev}")
+    st = positions.stride()
+    if len(st) == dims:
+        n_axes, st = 1, (0, *st)
+    elif len(st) == dims + 1:
+        n_axes = positions.shape[0]
+    else:
+        raise ValueError(f"positions must have {dims} dims, or the axes before them, "
+                         f"got {tuple(positions.shape)}")
+    pairs = inv_freq.numel()
+    _dense(inv_freq, _F32, pairs, dev, "inv_freq")
+    return st, n_axes, pairs, 0 if axes is None else _dense(axes, _I32, pairs, dev, "axes")
+
+
+def _pair_rows(x, out, dev: int, name: str):
+    """Checks bfloat16 tensors of one shape on the device, innermost stride 1; returns their strides."""
+    sx, so = x.stride(), out.stride()
+    if (x.dtype is not _BF16 or out.dtype is not _BF16 or x.shape != out.shape or len(sx) != 4
+            or x.get_device() != dev or out.get_device() != dev
+            or ((sx[3] != 1 or so[3] != 1) and x.numel())):
+        raise ValueError(f"{name} and {name}_out must be bfloat16 tensors of one shape [B, T, heads, H] on "
+                         f"cuda:{dev}, innermost stride 1")
+    return sx, so
+
+
+def fa_rotary(q, q_out, k, k_out, positions, inv_freq, axes=None, *, q_scale=1.0, adjacent=False,
+              inverse=False, stream=None, check=True) -> int:
+    """Turn q [B, T, heads, H] and k (or None) by positions [n_axes, B, T] or [B, T] into q_out and
+    k_out, any strides (see fa.h).  q_out may be q, and k_out k."""
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor")
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return fa_rotary(q, q_out, k, k_out, positions, inv_freq, axes, q_scale=q_scale,
+                             adjacent=adjacent, inverse=inverse, stream=stream, check=check)
+    sq, sqo = _pair_rows(q, q_out, dev, "q")
+    B, T, heads, H = q.shape
+    if k is None:
+        kp = kop = kh = 0
+        sk = sko = (0, 0, 0)
+    else:
+        sk, sko = _pair_rows(k, k_out, dev, "k")
+        if k.shape[0] != B or k.shape[1] != T or k.shape[3] != H:
+            raise ValueError(f"k must be [{B}, {T}, heads, {H}], got {tuple(k.shape)}")
+        kp, kop, kh = k.data_ptr(), k_out.data_ptr(), k.shape[2]
+    sp, n_axes, pairs, ax = _turning(positions, inv_freq, axes, 2, dev)
+    if positions.shape[-2] != B or positions.shape[-1] != T:
+        raise ValueError(f"positions must be [n_axes, {B}, {T}], got {tuple(positions.shape)}")
+    rc = (_lib or load()).fa_rotary_packed(_ROTARY(
+        q.data_ptr(), sq[0], sq[1], sq[2], q_out.data_ptr(), sqo[0], sqo[1], sqo[2],
+        kp, sk[0], sk[1], sk[2], kop, sko[0], sko[1], sko[2],
+        positions.data_ptr(), sp[0], sp[1], sp[2], inv_freq.data_ptr(), ax, pairs, n_axes,
+        1 if adjacent else 0, 1 if inverse else 0, _float_bits(q_scale), B, T, heads, kh, H,
+        _current_stream(dev) if stream is None else _raw_stream(stream)))
+    if rc and check:
+        _check("fa_rotary", rc)
+    return rc
+
+
+def fa_paged_rotary_append(q, k, v, positions, inv_freq, slots, q_out, k_cache, v_cache, axes=None,
+                           k_scale=None, v_scale=None, *, q_scale=1.0, adjacent=False, stream=None,
+                           check=True) -> int:
+    """Turn q [N, heads, H] into q_out, [B, K, G, T, H] with B * T = N or [N, heads, H], and write the
+    turned k and v [N, K, H] into the pages of `slots`.  positions [n_axes, N] or [N]."""
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor")
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return fa_paged_rotary_append(q, k, v, positions, inv_freq, slots, q_out, k_cache, v_cache,
+                                          axes, k_scale, v_scale, q_scale=q_scale, adjacent=adjacent,
+                                          stream=stream, check=check)
+    N, heads, H = q.shape
+    K = k.shape[1]
+    sq, sk, sv, so = q.stride(), k.stride(), v.stride(), q_out.stride()
+    if (not _BF16 is q.dtype is k.dtype is v.dtype is q_out.dtype or k.shape != v.shape
+            or len(sk) != 3 or k.shape[0] != N or k.shape[2] != H
+            or not dev == k.get_device() == v.get_device() == q_out.get_device()
+            or ((sk[2] != 1 or sv[2] != 1) and k.numel())
+            or ((sq[2] != 1 or so[-1] != 1) and q.numel())):
+        raise ValueError("q, k and v must be bfloat16 tensors [N, heads, H] (k and v of one shape) and "
+                         "q_out one on their device, innermost stride 1")
+    if len(so) == 5:
+        B, Kq, G, T, Ho = q_out.shape
+        if B * T != N or Kq * G != heads or Ho != H or (Kq > 1 and G > 1 and so[1] != G * so[2]):
+            raise ValueError(f"q_out must be [B, K, G, T, {H}] with B * T = {N} and K * G = {heads}, one "
+                             f"stride for all heads, got {tuple(q_out.shape)}")
+        ob, ot, oh = so[0], so[3], so[2] if G > 1 else so[1]
+    else:
+        if q_out.shape != q.shape:
+            raise ValueError(f"q_out must be [B, K, G, T, {H}] or {tuple(q.shape)}, got {tuple(q_out.shape)}")
+        B, T, (ob, ot, oh) = 1, N, (0, so[0], so[1])
+    sp, n_axes, pairs, ax = _turning(positions, inv_freq, axes, 1, dev)
+    if positions.shape[-1] != N:
+        raise ValueError(f"positions must be [n_axes, {N}], got {tuple(positions.shape)}")
+    kind, cs, st, ks, vs = _paged_cache(k_cache, v_cache, k_scale, v_scale, K, H, dev)
+    rc = (_lib or load()).fa_paged_rotary_append_packed(_ROTARY_APPEND(
+        q.data_ptr(), sq[0], sq[1], q_out.data_ptr(), ob, ot, oh, k.data_ptr(), sk[0], sk[1],
+        v.data_ptr(), sv[0], sv[1], positions.data_ptr(), sp[0], sp[1], inv_freq.data_ptr(), ax, pairs,
+        n_axes, 1 if adjacent else 0, _float_bits(q_scale), _dense(slots, _I64, N, dev, "slots"),
+        k_cache.data_ptr(), v_cache.data_ptr(), kind, ks, vs, st[0], st[1], st[2], B, T, heads, K, H,
+        cs[0], cs[2], _current_stream(dev) if stream is None else _raw_stream(stream)))
+    if rc and check:
+        _check("fa_paged_rotary_append", rc)
+    return rc
+
+
+def _pool(lens, block_table, shares, free_pages, free_used, lens_out, free_used_out):
+    """(device, B, max_pages, n_pages, n_free) of the checked tensors of a pool."""
+    dev = lens.get_device()
+    if dev < 0:
+        raise ValueError("lens must be a CUDA tensor")
+    B, n_pages, n_free = lens.numel(), shares.numel(), free_pages.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must have {B} rows, got {tuple(block_table.shape)}")
+    max_pages = block_table.shape[1]
+    if not (_I32 is lens.dtype is block_table.dtype is shares.dtype is free_pages.dtype
+            is free_used.dtype is lens_out.dtype is free_used_out.dtype
+            and dev == block_table.get_device() == shares.get_device() == free_pages.get_device()
+            == free_used.get_device() == lens_out.get_device() == free_used_out.get_device()
+            and B == lens_out.numel() and 1 == free_used.numel() == free_used_out.numel()
+            and lens.is_contiguous() and block_table.is_contiguous() and shares.is_contiguous()
+            and free_pages.is_contiguous() and lens_out.is_contiguous()):
+        for t, n, name in ((lens, B, "lens"), (block_table, B * max_pages, "block_table"),
+                           (shares, n_pages, "shares"), (free_pages, n_free, "free_pages"),
+                           (free_used, 1, "free_used"), (lens_out, B, "lens_out"),
+                           (free_used_out, 1, "free_used_out")):
+            _dense(t, _I32, n, dev, name)
+    return dev, B, max_pages, n_pages, n_free
+
+
+def fa_paged_free(rows, lens, block_table, shares, free_pages, free_used, lens_out, free_used_out,
+                  page_size, keep=None, stream=None, check=True) -> int:
+    """Requests rows keep their first `keep` tokens (None: none) and give their other pages back
+    (see fa.h).  lens_out may be lens and free_used_out may be free_used."""
+    dev, B, max_pages, n_pages, n_free = _pool(lens, block_table, shares, free_pages, free_used, lens_out,
+                                               free_used_out)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return fa_paged_free(rows, lens, block_table, shares, free_pages, free_used, lens_out,
+                                 free_used_out, page_size, keep, stream, check)
+    N = rows.numel()
+    rc = (_lib or load()).fa_paged_free_packed(_FREE(
+        _dense(rows, _I32, N, dev, "rows"), 0 if keep is None else _dense(keep, _I32, N, dev, "keep"), N,
+        lens.data_ptr(), block_table.data_ptr(), max_pages, shares.data_ptr(), free_pages.data_ptr(),
+        n_free, free_used.data_ptr(), lens_out.data_ptr(), free_used_out.data_ptr(), B, n_pages, page_size,
+        _current_stream(dev) if stream is None else _raw_stream(stream)))
+    if rc and check:
+        _check("fa_paged_free", rc)
+    return rc
+
+
+def fa_paged_fork(parents, children, lens, block_table, shares, free_pages, free_used, lens_out, copies,
+                  free_used_out, page_size, fork_lens=None, stream=None, check=True) -> int:
+    """Requests children go on with the first fork_lens tokens (None: all) of parents, whose full pages
+    they share; copies [N, 3] is for fa_paged_copy (see fa.h)."""
+    dev, B, max_pages, n_pages, n_free = _pool(lens, block_table, shares, free_pages, free_used, lens_out,
+                                               free_used_out)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return fa_paged_fork(parents, children, lens, block_table, shares, free_pages, free_used,
+                                 lens_out, copies, free_used_out, page_size, fork_lens, stream, check)
+    N = parents.numel()
+    rc = (_lib or load()).fa_paged_fork_packed(_FORK(
+        _dense(parents, _I32, N, dev, "parents"), _dense(children, _I32, N, dev, "children"),
+        0 if fork_lens is None else _dense(fork_lens, _I32, N, dev, "fork_lens"), N, lens.data_ptr(),
+        block_table.data_ptr(), max_pages, shares.data_ptr(), free_pages.data_ptr(), n_free,
+        free_used.data_ptr(), lens_out.data_ptr(), _dense(copies, _I32, 3 * N, dev, "copies"),
+        free_used_out.data_ptr(), B, n_pages, page_size,
+        _current_stream(dev) if stream is None else _raw_stream(stream)))
+    if rc and check:
+        _check("fa_paged_fork", rc)
+    return rc
+
+
+def fa_paged_compact(lens, block_table, shares, free_pages, free_used, block_table_out, shares_out,
+                     free_pages_out, moves, page_size, stream=None, check=True) -> int:
+    """Tables, share counts and free list of the pool made dense by at most len(moves) moves, which
+    fa_paged_copy carries out (see fa.h).  The first three outputs may be their inputs."""
+    dev, B, max_pages, n_pages, n_free = _pool(lens, block_table, shares, free_pages, free_used, lens, free_used)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return fa_paged_compact(lens, block_table, shares, free_pages, free_used, block_table_out,
+                                    shares_out, free_pages_out, moves, page_size, stream, check)
+    n = moves.numel() // 3
+    rc = (_lib or load()).fa_paged_compact_packed(_COMPACT(
+        lens.data_ptr(), block_table.data_ptr(), max_pages, shares.data_ptr(), free_pages.data_ptr(),
+        n_free, free_used.data_ptr(), _dense(block_table_out, _I32, B * max_pages, dev, "block_table_out"),
+        _dense(shares_out, _I32, n_pages, dev, "shares_out"),
+        _dense(free_pages_out, _I32, n_free, dev, "free_pages_out"), _dense(moves, _I32, 3 * n, dev, "moves"),
+        n, B, n_pages, page_size, _current_stream(dev) if stream is None else _raw_stream(stream)))
+    if rc and check:
+        _check("fa_paged_compact", rc)
+    return rc
+
+
+def fa_paged_copy(moves, k_cache, v_cache, stream=None, check=True) -> int:
+    """Carry out moves [N, 3] (page, page, tokens) in caches [n_pages, K, page_size, H], or of several
+    layers [layers, n_pages, K, page_size, H]."""
+    dev = moves.get_device()
+    if dev < 0:
+        raise ValueError("moves must be a CUDA tensor")
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return fa_paged_copy(moves, k_cache, v_cache, stream, check)
+    layers, sl, kc, vc = 1, 0, k_cache, v_cache
+    if k_cache.dim() == 5:
+        layers, sl = k_cache.shape[0], k_cache.stride(0)
+        if v_cache.dim() != 5 or v_cache.shape[0] != layers or (layers > 1 and v_cache.stride(0) != sl):
+            raise ValueError("k_cache and v_cache must have the same layers, with the same stride")
+        if layers == 0:
+            return FA_OK
+        kc, vc = k_cache[0], v_cache[0]
+    if kc.dim() != 4:
+        raise ValueError(f"k_cache must have 4 or 5 dims, got {tuple(k_cache.shape)}")
+    N, K, H = moves.numel() // 3, kc.shape[1], kc.shape[3]
+    kind, cs, st, _, _ = _paged_cache(kc, vc, None, None, K, H, dev)
+    rc = (_lib or load()).fa_paged_copy_packed(_COPY(
+        _dense(moves, _I32, 3 * N, dev, "moves"), N, k_cache.data_ptr(), v_cache.data_ptr(), kind, sl, st[0],
+        st[1], st[2], layers, K, H, cs[0], cs[2],
+        _current_stream(dev) if stream is None else _raw_stream(stream)))
+    if rc and check:
+        _check("fa_paged_copy", rc)
+    return rc
+
+
 # ------------------------------------------------------- tensor helpers
 
 def block_mask_from_dense(mask, device=None):
@@ -552,3 +803,66 @@ def paged_attention_decode(q, k_cache, v_cache, block_table, lens, *, k_scale=No
     fa_paged_decode(q, k_cache, v_cache, block_table, lens, o, lse, workspace, k_scale, v_scale,
                     window, stream)
     return o, lse
+
+
+def _rotary_pair(q, k, positions, inv_freq, axes, adjacent, q_scale, inverse, stream):
+    """Shared by the two helpers below: outputs laid out the other way round."""
+    def laid(x):
+        B, T, heads, H = x.shape
+        if inverse:
+            return torch.empty((B, T, heads, H), dtype=x.dtype, device=x.device)
+        return torch.empty((B, heads, T, H), dtype=x.dtype, device=x.device).transpose(1, 2)
+
+    with _allocating_on(stream, q.device):
+        q_out, k_out = laid(q), None if k is None else laid(k)
+    fa_rotary(q, q_out, k, k_out, positions, inv_freq, axes, q_scale=q_scale, adjacent=adjacent,
+              inverse=inverse, stream=stream)
+    return q_out, k_out
+
+
+def rotary_forward(q, k, positions, inv_freq, axes=None, *, q_scale=None, adjacent=False, stream=None):
+    """Turn a projection's q [B, T, K * G, H] and k [B, T, K, H] and lay them out for the attention:
+    returns q [B, K, G, T, H], multiplied by q_scale (None: H**-0.5), and k [B, K, T, H]."""
+    B, T, heads, H = q.shape
+    K = k.shape[2]
+    if K == 0 or heads % K:
+        raise ValueError(f"q's heads must be a multiple of k's, got {heads} and {K}")
+    q, k = _rotary_pair(q, k, positions, inv_freq, axes, adjacent,
+                        H ** -0.5 if q_scale is None else q_scale, False, stream)
+    return q.transpose(1, 2).unflatten(1, (K, heads // K)), k.transpose(1, 2)
+
+
+def rotary_backward(dq, dk, positions, inv_freq, axes=None, *, q_scale=None, adjacent=False, stream=None):
+    """Gradients of rotary_forward's q [B, T, K * G, H] and k [B, T, K, H] from the attention's dq
+    [B, K, G, T, H] and dk [B, K, T, H] (contiguous, as attention_backward gives them)."""
+    _need(dq, torch.bfloat16, "dq"); _need(dk, torch.bfloat16, "dk")
+    H = dq.shape[-1]
+    return _rotary_pair(dq.flatten(1, 2).transpose(1, 2), dk.transpose(1, 2), positions, inv_freq, axes,
+                        adjacent, H ** -0.5 if q_scale is None else q_scale, True, stream)
+
+
+def paged_free(rows, lens, block_table, shares, free_pages, free_used, *, page_size, keep=None, stream=None):
+    """Run fa_paged_free in place: lens, shares, free_pages and free_used are updated."""
+    fa_paged_free(rows, lens, block_table, shares, free_pages, free_used, lens, free_used, page_size, keep,
+                  stream)
+
+
+def paged_fork(parents, children, lens, block_table, shares, free_pages, free_used, *, page_size,
+               fork_lens=None, stream=None):
+    """Run fa_paged_fork in place: lens, block_table, shares and free_used are updated.  Returns the
+    copies [N, 3] that fa_paged_copy has to carry out."""
+    with _allocating_on(stream, lens.device):
+        copies = torch.empty((parents.numel(), 3), dtype=torch.int32, device=lens.device)
+    fa_paged_fork(parents, children, lens, block_table, shares, free_pages, free_used, lens, copies, free_used,
+                  page_size, fork_lens, stream)
+    return copies
+
+
+def paged_compact(lens, block_table, shares, free_pages, free_used, *, page_size, max_moves, stream=None):
+    """Run fa_paged_compact in place: block_table, shares and free_pages are updated.  Returns the
+    moves [max_moves, 3] that fa_paged_copy has to carry out."""
+    with _allocating_on(stream, lens.device):
+        moves = torch.empty((max_moves, 3), dtype=torch.int32, device=lens.device)
+    fa_paged_compact(lens, block_table, shares, free_pages, free_used, block_table, shares, free_pages, moves,
+                     page_size, stream)
+    return moves

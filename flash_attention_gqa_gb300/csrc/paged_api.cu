@@ -8,55 +8,15 @@
 #include "../../include/fa.h"
 #include "kernels.h"
 #include "paged.h"
+#include "paged_checks.h"
+
+using namespace fa;
 
 namespace {
 
-bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-// A required pointer of `n`-byte aligned elements.
-bool usable(const void* p, unsigned n) { return p != nullptr && aligned(p, n); }
-
-int log2_exact(int n) {
-  if (n < 1 || (n & (n - 1)) != 0) return -1;
-  int s = 0;
-  while ((1 << s) < n) ++s;
-  return s;
-}
-
-bool head_dim_ok(int H) { return H == 64 || H == 128 || H == 256; }
-
-// Checks a cache's type, strides (in elements) and page geometry, and fills
-// `lay` with them in bytes.  Rows start on 16-byte boundaries.  The stride of a
-// dimension of one is never used, whatever it is.
-int make_layout(fa::PagedLayout* lay, int cache_type, int64_t page_stride, int64_t head_stride,
-                int64_t token_stride, int K, int n_pages, int page_size) {
-  if (cache_type != FA_CACHE_BF16 && cache_type != FA_CACHE_E4M3) return FA_ERR_INVALID_ARG;
-  if (n_pages <= 1) page_stride = 0;
-  if (K <= 1) head_stride = 0;
-  if (page_size == 1) token_stride = 0;
-  if (n_pages < 0 || page_size < 1 || page_stride < 0 || head_stride < 0 || token_stride < 0)
-    return FA_ERR_INVALID_ARG;
-  const int shift = log2_exact(page_size);
-  if (shift < 0 || page_size > fa::kMaxPageSize) return FA_ERR_UNSUPPORTED;
-  const int64_t es = cache_type == FA_CACHE_BF16 ? 2 : 1;
-  const int64_t most = int64_t{1} << 40;
-  if (page_stride > most || head_stride > most || token_stride > most) return FA_ERR_INVALID_ARG;
-  if (((page_stride | head_stride | token_stride) * es) & 15) return FA_ERR_INVALID_ARG;
-  *lay = fa::PagedLayout{page_stride * es, head_stride * es, token_stride * es, n_pages, shift};
-  return FA_OK;
-}
-
 bool decode_shape_ok(int B, int K, int G, int T, int H) {
-  return head_dim_ok(H) && (int64_t)G * T <= fa::kMaxPagedRows && B <= fa::kMaxPagedBatch &&
+  return head_dim_ok(H) && (int64_t)G * T <= kMaxPagedRows && B <= kMaxPagedBatch &&
          (int64_t)B * K <= 65535;
-}
-
-// The status of a launch.  A failed one leaves nothing behind that a later call, of this library or
-// of another user of the runtime, would take for its own.
-int status(cudaError_t e) {
-  if (e == cudaSuccess) return FA_OK;
-  cudaGetLastError();
-  return FA_ERR_CUDA;
 }
 
 }  // namespace
@@ -192,93 +152,10 @@ int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int
 
 }  // extern "C"
 
-namespace {
-
-// Reads a record of 8-byte arguments in order; `ok` falls where a size does not
-// fit an int.
-struct Record {
-  const int64_t* at;
-  bool ok = true;
-  template <class T>
-  T* ptr() { return reinterpret_cast<T*>(static_cast<uintptr_t>(*at++)); }
-  int64_t wide() { return *at++; }
-  int size() {
-    const int64_t x = *at++;
-    if (x < INT32_MIN || x > INT32_MAX) ok = false;
-    return static_cast<int>(x);
-  }
-};
-
-}  // namespace
-
 extern "C" {
 
-int fa_paged_tables_packed(const int64_t* args) {
-  if (!args) return FA_ERR_INVALID_ARG;
-  Record r{args};
-  const auto* cached = r.ptr<const int32_t>();
-  const auto* fresh = r.ptr<const int32_t>();
-  const auto* free_pages = r.ptr<const int32_t>();
-  const int n_free = r.size();
-  const auto* used = r.ptr<const int32_t>();
-  auto* table = r.ptr<int32_t>();
-  const int max_pages = r.size();
-  auto* total = r.ptr<int32_t>();
-  auto* starts = r.ptr<int32_t>();
-  auto* slots = r.ptr<int64_t>();
-  auto* positions = r.ptr<int32_t>();
-  const int max_tokens = r.size();
-  auto* used_out = r.ptr<int32_t>();
-  const int B = r.size(), n_pages = r.size(), page_size = r.size();
-  void* stream = r.ptr<void>();
-  if (!r.ok) return FA_ERR_INVALID_ARG;
-  return fa_paged_tables(cached, fresh, free_pages, n_free, used, table, max_pages, total, starts, slots,
-                         positions, max_tokens, used_out, B, n_pages, page_size, stream);
-}
-
-int fa_paged_append_packed(const int64_t* args) {
-  if (!args) return FA_ERR_INVALID_ARG;
-  Record r{args};
-  const void* k = r.ptr<const void>();
-  const void* v = r.ptr<const void>();
-  const int64_t kt = r.wide(), kh = r.wide(), vt = r.wide(), vh = r.wide();
-  const auto* slots = r.ptr<const int64_t>();
-  void* kc = r.ptr<void>();
-  void* vc = r.ptr<void>();
-  const int type = r.size();
-  const auto* ks = r.ptr<const float>();
-  const auto* vs = r.ptr<const float>();
-  const int64_t page = r.wide(), head = r.wide(), token = r.wide();
-  const int N = r.size(), K = r.size(), H = r.size(), n_pages = r.size(), page_size = r.size();
-  void* stream = r.ptr<void>();
-  if (!r.ok) return FA_ERR_INVALID_ARG;
-  return fa_paged_append(k, v, kt, kh, vt, vh, slots, kc, vc, type, ks, vs, page, head, token, N, K, H,
-                         n_pages, page_size, stream);
-}
-
-int fa_paged_decode_packed(const int64_t* args) {
-  if (!args) return FA_ERR_INVALID_ARG;
-  Record r{args};
-  const void* q = r.ptr<const void>();
-  const void* kc = r.ptr<const void>();
-  const void* vc = r.ptr<const void>();
-  const int type = r.size();
-  const auto* ks = r.ptr<const float>();
-  const auto* vs = r.ptr<const float>();
-  const int64_t page = r.wide(), head = r.wide(), token = r.wide();
-  const auto* table = r.ptr<const int32_t>();
-  const auto* lens = r.ptr<const int32_t>();
-  const int window = r.size();
-  void* o = r.ptr<void>();
-  auto* lse = r.ptr<float>();
-  void* workspace = r.ptr<void>();
-  const size_t bytes = static_cast<size_t>(r.wide());
-  const int B = r.size(), K = r.size(), G = r.size(), T = r.size(), H = r.size();
-  const int n_pages = r.size(), page_size = r.size(), max_pages = r.size();
-  void* stream = r.ptr<void>();
-  if (!r.ok) return FA_ERR_INVALID_ARG;
-  return fa_paged_decode(q, kc, vc, type, ks, vs, page, head, token, table, lens, window, o, lse, workspace,
-                         bytes, B, K, G, T, H, n_pages, page_size, max_pages, stream);
-}
+int fa_paged_tables_packed(const int64_t* args) { return call_packed(fa_paged_tables, args); }
+int fa_paged_append_packed(const int64_t* args) { return call_packed(fa_paged_append, args); }
+int fa_paged_decode_packed(const int64_t* args) { return call_packed(fa_paged_decode, args); }
 
 }  // extern "C"

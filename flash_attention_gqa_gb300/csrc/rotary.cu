@@ -1,0 +1,247 @@
+// Rotary positions: pairs (a, b) of a head's dims turned by position times frequency,
+//
+//   a' = (a cos - b sin) scale,   b' = (b cos + a sin) scale,
+//
+// for queries and keys in one launch, and in the serving form with keys and values going
+// straight into the cache's pages.  The gradient is the same with the angle's sign turned.
+//
+// Angles.  A position is a whole number, so only the fraction of frequency / 2 pi counts: as 64
+// fixed-point bits, of which position times bits mod 2^64 is the turn, exact to position * 2^-64
+// however far the position is (position * frequency in fp32 is off by 2^-24 of the angle: 0.03 at
+// 500000).  Its upper half becomes an angle of fp32 precision in (-pi, pi].
+//
+// Bound by memory: every value is read and written once.
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "ptx.cuh"
+#include "rotary.h"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 256;
+
+// The fraction of f / (2 pi) in 2^-64 turns, rounded down in size: f = m 2^(e - 150), times
+// floor(2^128 / (2 pi)).
+__device__ __forceinline__ uint64_t turns_per_step(float f) {
+  constexpr uint64_t HI = 0x28be60db9391054aull, LO = 0x7f09d5f47d4d3770ull;
+  const uint32_t bits = __float_as_uint(f);
+  const int e = max((int)(bits >> 23 & 255), 1);
+  const uint64_t m = (bits & 0x7fffff) | ((bits >> 23 & 255) ? 0x800000 : 0);
+  const uint64_t p0 = m * LO, h = m * HI;
+  const uint64_t p1 = __umul64hi(m, LO) + h, p2 = __umul64hi(m, HI) + (p1 < h ? 1 : 0);
+  const int s = 214 - e;   // the product's bits from here on; the 64 lowest of them
+  uint64_t r;
+  if (s >= 128) r = s >= 192 ? 0 : p2 >> (s - 128);
+  else if (s >= 64) r = s == 64 ? p1 : p1 >> (s - 64) | p2 << (128 - s);
+  else if (s > 0) r = p0 >> s | p1 << (64 - s);
+  else r = p0 << -s;
+  return bits >> 31 ? 0 - r : r;
+}
+
+__device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d) {
+  uint16_t lo, hi;   // nearest even, saturating at +-448; NaN stays NaN
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+  return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+__device__ __forceinline__ void widen(uint4 x, float (&f)[8]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = unpack_bf16x2(w[i]);
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+}
+
+// A unit is two 16-byte vectors of a head: dims that turn together, or two vectors side by side
+// in the lanes' order.  A CTA takes `tokens` tokens: it loads its first units, then works out
+// their angles once for all heads, in shared memory in the order in which lanes read them, while
+// the loads are on their way.
+template <int TO, int PER>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a, int tokens) {
+  extern __shared__ float4 turn[];   // [token][pairs / 2]: cos, sin of two pairs
+  const uint32_t upr = a.H / 16;                          // units of a head
+  const int shift = a.H == 64 ? 2 : a.H == 128 ? 3 : 4;   // log2 of it
+  const uint32_t heads = a.QH + a.KH * (TO == ROTARY_PLAIN ? 1 : 2);
+  const uint32_t N = (uint32_t)a.B * a.T, n0 = blockIdx.x * (uint32_t)tokens;
+  const uint32_t here = min((uint32_t)tokens, N - n0), all = here * heads * upr;
+  const uint32_t half = a.pairs / 8;   // vectors of one half of the turned dims
+
+  struct Unit {
+    uint4 x, y;       // the two vectors
+    uint32_t t, head, ux, uy;
+    bool live;
+  };
+  Unit w[PER];
+  auto load = [&](uint32_t i0) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const uint32_t i = i0 + j * kThreads;
+      Unit& c = w[j];
+      c.live = i < all;
+      if (!c.live) continue;
+      const uint32_t u = i & (upr - 1), rest = i >> shift;
+      c.t = rest / heads;
+      c.head = rest - c.t * heads;
+      // vectors u and u + half turn together; behind them those that stay as they are
+      const uint32_t gap = a.adjacent ? upr : u < half ? half : upr - half;
+      c.ux = a.adjacent || u < half ? u : u + half;
+      c.uy = c.ux + gap;
+      const uint32_t n = n0 + c.t, b = n / a.T, t = n - b * a.T;
+      const bool isq = c.head < a.QH, isk = !isq && c.head < a.QH + a.KH;
+      const RotaryRows& r = isq ? a.q : isk ? a.k : a.v;
+      const uint32_t h = isq ? c.head : isk ? c.head - a.QH : c.head - a.QH - a.KH;
+      const char* src = (const char*)r.at + b * r.batch + t * r.token + h * r.head;
+      // (plain loads, not those of constant memory: outputs may be in the inputs' place)
+      c.x = __ldcg(reinterpret_cast<const uint4*>(src + c.ux * 16));
+      c.y = __ldcg(reinterpret_cast<const uint4*>(src + c.uy * 16));
+    }
+  };
+  uint32_t i0 = threadIdx.x;
+  load(i0);
+
+  const uint32_t angles = here * a.pairs;
+  for (uint32_t i = threadIdx.x; i < angles; i += kThreads) {
+    const uint32_t t = i / a.pairs, p = i - t * a.pairs, n = n0 + t, b = n / a.T;
+    int axis = a.axes ? a.axes[p] : 0;
+    float f = a.inv_freq[p];
+    if ((unsigned)axis >= (unsigned)a.n_axes || !(fabsf(f) < INFINITY)) {
+      atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+      if ((unsigned)axis >= (unsigned)a.n_axes) axis = 0;
+      if (!(fabsf(f) < INFINITY)) f = 0.0f;
+    }
+    const int64_t pos = a.positions[axis * a.pos_axis + b * a.pos_batch + (n - b * a.T) * a.pos_token];
+    const uint64_t turned = (uint64_t)pos * turns_per_step(f);
+    float s, c;
+    sincospif((float)(int32_t)(turned >> 32) * 0x1p-31f, &s, &c);
+    if (a.inverse) s = -s;
+    const uint32_t group = a.adjacent ? p >> 2 : p >> 3, in = a.adjacent ? (p & 3) >> 1 : (p & 7) >> 1;
+    const uint32_t groups = a.adjacent ? a.pairs / 4 : half;
+    reinterpret_cast<float2*>(turn + t * (a.pairs / 2) + in * groups + group)[p & 1] = make_float2(c, s);
+  }
+  __syncthreads();
+
+  for (;;) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const Unit& c = w[j];
+      if (!c.live) continue;
+      const uint32_t n = n0 + c.t, b = n / a.T, t = n - b * a.T;
+      int64_t slot = 0;
+      if (TO != ROTARY_PLAIN) {
+        slot = a.slots[n];
+        if (slot < 0) continue;   // padding
+      }
+      const bool isq = c.head < a.QH, isv = TO != ROTARY_PLAIN && c.head >= a.QH + a.KH;
+      const uint32_t h = isq ? c.head : isv ? c.head - a.QH - a.KH : c.head - a.QH;
+      float x[8], y[8];
+      widen(c.x, x);
+      widen(c.y, y);
+      if (!isv) {
+        const float4* const at = turn + c.t * (a.pairs / 2);
+        if (a.adjacent) {
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            const uint32_t u = v ? c.uy : c.ux;
+            if (u >= 2 * half) continue;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float4 cs = at[i * (2 * half) + u];
+              float(&f)[8] = v ? y : x;
+              const float a0 = f[4 * i], b0 = f[4 * i + 1], a1 = f[4 * i + 2], b1 = f[4 * i + 3];
+              f[4 * i] = a0 * cs.x - b0 * cs.y;
+              f[4 * i + 1] = b0 * cs.x + a0 * cs.y;
+              f[4 * i + 2] = a1 * cs.z - b1 * cs.w;
+              f[4 * i + 3] = b1 * cs.z + a1 * cs.w;
+            }
+          }
+        } else if (c.ux < half) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 cs = at[i * half + c.ux];
+            const float a0 = x[2 * i], a1 = x[2 * i + 1];
+            x[2 * i] = a0 * cs.x - y[2 * i] * cs.y;
+            y[2 * i] = y[2 * i] * cs.x + a0 * cs.y;
+            x[2 * i + 1] = a1 * cs.z - y[2 * i + 1] * cs.w;
+            y[2 * i + 1] = y[2 * i + 1] * cs.z + a1 * cs.w;
+          }
+        }
+        if (isq) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[i] *= a.q_scale;
+            y[i] *= a.q_scale;
+          }
+        }
+      }
+      auto pack = [](const float (&f)[8]) {
+        return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                          pack_bf16x2(f[6], f[7]));
+      };
+      if (isq || TO == ROTARY_PLAIN) {
+        const RotaryRows& r = isq ? a.q_out : a.k_out;
+        char* const dst = (char*)r.at + b * r.batch + t * r.token + h * r.head;
+        *reinterpret_cast<uint4*>(dst + c.ux * 16) = pack(x);
+        *reinterpret_cast<uint4*>(dst + c.uy * 16) = pack(y);
+        continue;
+      }
+      const int64_t page = slot >> a.lay.page_shift, in = slot & ((1 << a.lay.page_shift) - 1);
+      if (page >= a.lay.n_pages) {
+        atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+        continue;
+      }
+      char* const dst = (char*)(isv ? a.v_cache : a.k_cache) + page * a.lay.page + h * a.lay.head + in * a.lay.token;
+      if (TO == ROTARY_BF16) {
+        *reinterpret_cast<uint4*>(dst + c.ux * 16) = isv ? c.x : pack(x);
+        *reinterpret_cast<uint4*>(dst + c.uy * 16) = isv ? c.y : pack(y);
+      } else {
+        // (rounded once, from fp32)
+        const float* const scales = isv ? a.v_scale : a.k_scale;
+        const float s = scales ? scales[h] : 1.0f;
+        auto squeeze = [s](const float (&f)[8]) {
+          return make_uint2(to_e4m3x4(f[0] / s, f[1] / s, f[2] / s, f[3] / s),
+                            to_e4m3x4(f[4] / s, f[5] / s, f[6] / s, f[7] / s));
+        };
+        *reinterpret_cast<uint2*>(dst + c.ux * 8) = squeeze(x);
+        *reinterpret_cast<uint2*>(dst + c.uy * 8) = squeeze(y);
+      }
+    }
+    i0 += PER * kThreads;
+    if (i0 >= all) break;
+    load(i0);
+  }
+}
+
+template <int TO>
+cudaError_t launch(const RotaryArgs& a, int sm_count, cudaStream_t st) {
+  const int64_t N = (int64_t)a.B * a.T;
+  const int64_t units = (int64_t)(a.QH + a.KH * (TO == ROTARY_PLAIN ? 1 : 2)) * (a.H / 16), all = N * units;
+  // Four units a thread once that fills the GPU (8 CTAs on each of its SMs), one below.
+  const bool four = all >= (int64_t)4 * kThreads * 8 * sm_count;
+  int64_t tokens = (four ? 4 : 1) * kThreads / units;
+  // (angles in 32 KB of shared memory at most: units >= pairs / 4, 1024 units)
+  if (tokens < 1) tokens = 1;
+  auto* const kernel = four ? rotary_kernel<TO, 4> : rotary_kernel<TO, 1>;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((N + tokens - 1) / tokens));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)tokens * a.pairs * sizeof(float2);
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, kernel, a, (int)tokens);
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(const RotaryArgs& a, RotaryTo to, int sm_count, cudaStream_t st) {
+  switch (to) {
+    case ROTARY_PLAIN: return launch<ROTARY_PLAIN>(a, sm_count, st);
+    case ROTARY_BF16: return launch<ROTARY_BF16>(a, sm_count, st);
+    default: return launch<ROTARY_E4M3>(a, sm_count, st);
+  }
+}
+
+}  // namespace fa

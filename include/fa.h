@@ -21,8 +21,8 @@
  * Errors: every call validates all arguments on the host before launching
  * anything and returns one of the FA_* codes below.  A bounded device-side
  * wait that runs out of time sets a device error word; fa_check_status()
- * reports it as FA_ERR_DEVICE_TIMEOUT (and clears it).  Lengths, page ids and
- * slots that the paged operators find out of range in device memory set the
+ * reports it as FA_ERR_DEVICE_TIMEOUT (and clears it).  Lengths, page ids, slots
+ * and the like that the operators find out of range in device memory set the
  * same word (FA_ERR_DEVICE_VALUE); nothing outside the caller's buffers is
  * touched for them.
  */
@@ -328,17 +328,163 @@ int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int
    unsupported sizes). */
 size_t fa_paged_decode_workspace_size(int B, int K, int G, int T, int H);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions.  Of each head's H dims the first 2 * n_pairs are turned in
+ * pairs, the others stay: pair i of a token at positions p[0 .. n_axes) by
+ *   angle = p[axes[i]] * inv_freq[i]          (axes NULL: axis 0)
+ *   a' = a cos(angle) - b sin(angle),   b' = b cos(angle) + a sin(angle)
+ * where (a, b) are dims (i, i + n_pairs), or (2i, 2i + 1) with `adjacent`.
+ * Queries are then multiplied by q_scale (H**-0.5 for the attention here).
+ * Several axes give image or video tokens their time, height and width; how
+ * pairs are dealt to axes is up to `axes`.  Angles are exact to 2^-23 or so at
+ * any int32 position; arithmetic is float32, the result rounded once.
+ * n_pairs: a multiple of 8 up to H / 2; H in {64, 128, 256}; n_axes <= 16;
+ * B * T <= 2^30; q_heads + 2 * k_heads <= 65535.
+ * positions: int32, of (axis, b, t) through its strides; inv_freq float32 [n_pairs],
+ * finite; axes int32 [n_pairs], in [0, n_axes).  All in device memory; an axis
+ * out of range counts as 0 and a frequency that is not finite as 0, and both
+ * set FA_ERR_DEVICE_VALUE.
+ */
+
 /*
- * The three calls above with their arguments in one record, for callers that
+ * q, q_out [B, T, q_heads, H] and k, k_out [B, T, k_heads, H], bf16, each through
+ * strides (batch, token, head) in elements, multiples of 8: views of a fused
+ * projection, and the attention's [B, K, G, T, H] and [B, K, S, H], are both
+ * such tensors.  Either may have no heads (pointers NULL then).  `inverse` turns
+ * the other way: the gradients of q and k from those of q_out and k_out (q_scale
+ * as in the forward call).  q_out may be q, and k_out k, with the same strides;
+ * no other overlap.
+ */
+int fa_rotary(const void* q, int64_t q_batch_stride, int64_t q_token_stride, int64_t q_head_stride,
+              void* q_out, int64_t q_out_batch_stride, int64_t q_out_token_stride,
+              int64_t q_out_head_stride, const void* k, int64_t k_batch_stride,
+              int64_t k_token_stride, int64_t k_head_stride, void* k_out,
+              int64_t k_out_batch_stride, int64_t k_out_token_stride, int64_t k_out_head_stride,
+              const int32_t* positions, int64_t pos_axis_stride, int64_t pos_batch_stride,
+              int64_t pos_token_stride, const float* inv_freq, const int32_t* axes, int n_pairs,
+              int n_axes, int adjacent, int inverse, float q_scale, int B, int T, int q_heads,
+              int k_heads, int H, void* stream);
+
+/*
+ * The serving form: queries turned and laid out for fa_paged_decode, keys turned
+ * and written with the values into the cache's pages, as fa_paged_append would.
+ * q [N, q_heads, H], k and v [N, k_heads, H], positions (axis, n) and slots [N], with
+ * N = B * T tokens, token n = b * T + t; q_out through strides (batch, token,
+ * head).  A key for an e4m3 cache is divided by its scale and rounded from
+ * float32, once.  Tokens with slot < 0 are skipped, their row of q_out too;
+ * slots, scales and the cache otherwise as in fa_paged_append.
+ */
+int fa_paged_rotary_append(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                           void* q_out, int64_t q_out_batch_stride, int64_t q_out_token_stride,
+                           int64_t q_out_head_stride, const void* k, int64_t k_token_stride,
+                           int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                           int64_t v_head_stride, const int32_t* positions,
+                           int64_t pos_axis_stride, int64_t pos_token_stride,
+                           const float* inv_freq, const int32_t* axes, int n_pairs, int n_axes,
+                           int adjacent, float q_scale, const int64_t* slots, void* k_cache,
+                           void* v_cache, int cache_type, const float* k_scale,
+                           const float* v_scale, int64_t page_stride, int64_t head_stride,
+                           int64_t token_stride, int B, int T, int q_heads, int k_heads, int H,
+                           int n_pages, int page_size, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Pages between steps.  Requests can hold pages in common: shares[p] (int32
+ * [n_pages], zeros at the start) counts the requests beside the first that hold
+ * page p.  fa_paged_tables leaves it alone: the pages that it opens have one
+ * holder.  The free list is fa_paged_tables's: free_pages[*free_used ..
+ * n_free) belong to no request.  pages(n) = ceil(n / page_size).
+ * All pointers are device memory; B <= 8192, N <= 8192, n_pages <= 2^21.  lens_out
+ * may be lens, free_used_out free_used (in place); no other overlap but those
+ * named.  A call that cannot be met changes nothing (outputs that are not
+ * in place become copies of the inputs) and sets FA_ERR_DEVICE_VALUE.
+ */
+
+/*
+ * Requests end, or give back their last tokens (drafted ones that were not
+ * taken).  Request rows[i] (< 0: none) keeps its first keep[i] tokens (keep NULL:
+ * 0): lens_out[row] = keep, and of each page in entries pages(keep) ..
+ * pages(len) - 1 the count falls by one, or, if this was its only holder, it
+ * goes back to the free list: *free_used_out = *free_used - n, and
+ * free_pages[*free_used_out .. *free_used) are the n pages in the order of their
+ * ids.  Tables stay as they are.
+ * Cannot be met: a row past B or named twice; a length out of range; keep outside
+ * [0, len]; a last page that is kept in part while others hold it too (it would
+ * get this request's next tokens); more pages than *free_used.  Page ids outside
+ * [0, n_pages) are skipped, and a page that is given back more often than it is
+ * held comes back once; both set FA_ERR_DEVICE_VALUE.
+ */
+int fa_paged_free(const int32_t* rows, const int32_t* keep, int N, const int32_t* lens,
+                  const int32_t* block_table, int max_pages, int32_t* shares,
+                  int32_t* free_pages, int n_free, const int32_t* free_used, int32_t* lens_out,
+                  int32_t* free_used_out, int B, int n_pages, int page_size, void* stream);
+
+/*
+ * Requests go on as several: children[i], a request without tokens, gets the
+ * first n tokens of parents[i] (< 0: no entry), n = fork_lens[i], or all of them with
+ * fork_lens NULL.  Full pages are shared; the tokens of a last one that is not
+ * full get a page from the free list (in entry order), and their copy is left to
+ * fa_paged_copy: copies[i] = (page of the parent, page of the child, tokens), or
+ * (-1, -1, 0).  lens_out[child] = n.
+ * Cannot be met: a parent past B, a child outside [0, B) or named twice or that has
+ * tokens, a parent that is a child of the call, n outside [0, lens[parent]], a
+ * length out of range, too few free pages.  A page id outside [0, n_pages) is
+ * passed on without a count or a copy, and sets FA_ERR_DEVICE_VALUE.
+ */
+int fa_paged_fork(const int32_t* parents, const int32_t* children, const int32_t* fork_lens, int N,
+                  const int32_t* lens, int32_t* block_table, int max_pages, int32_t* shares,
+                  const int32_t* free_pages, int n_free, const int32_t* free_used,
+                  int32_t* lens_out, int32_t* copies, int32_t* free_used_out, int B, int n_pages,
+                  int page_size, void* stream);
+
+/*
+ * Makes a pool dense: as long as a free page is lower than a held one (in a table,
+ * before its request's end), the lowest free page takes the place of the highest
+ * held one, up to max_moves times.  moves[j] = (old page, new page, page_size) for
+ * fa_paged_copy, which has to run before the pages are used again; (-1, -1, 0)
+ * behind the last.  block_table_out and shares_out follow, and free_pages_out
+ * [*free_used ..) are the pages then free, in the order of their ids (*free_used stays).
+ * Pages in neither a table nor the free list stay where they are.  The three
+ * outputs may be the inputs; otherwise they get all of them (free pages from
+ * *free_used on).
+ * Cannot be met: a length or a page id out of range, a free page that is in a
+ * table or twice in the list (moves are all (-1, -1, 0) then).
+ */
+int fa_paged_compact(const int32_t* lens, const int32_t* block_table, int max_pages,
+                     const int32_t* shares, const int32_t* free_pages, int n_free,
+                     const int32_t* free_used, int32_t* block_table_out, int32_t* shares_out,
+                     int32_t* free_pages_out, int32_t* moves, int max_moves, int B, int n_pages,
+                     int page_size, void* stream);
+
+/*
+ * Copies the first moves[i][2] tokens of page moves[i][0] to page moves[i][1], keys and
+ * values of all heads and layers; (-1, -1, .) is no move.  The caches are
+ * [layers, n_pages, K, page_size, H] through strides, as above (a layer's stride is a
+ * multiple of 16 bytes too); what is behind the tokens copied stays.  No page is the
+ * destination of one move and part of another.  A page or a count out of range
+ * skips the move and sets FA_ERR_DEVICE_VALUE.
+ */
+int fa_paged_copy(const int32_t* moves, int N, void* k_cache, void* v_cache, int cache_type,
+                  int64_t layer_stride, int64_t page_stride, int64_t head_stride,
+                  int64_t token_stride, int layers, int K, int H, int n_pages, int page_size,
+                  void* stream);
+
+/*
+ * The calls on paged caches, pages and rotary positions with their arguments in one record, for callers that
  * pay for each argument (foreign-function interfaces: two dozen of them cost
  * more than the rest of a small call).  The record holds the plain call's
  * arguments in order, 8 bytes each: addresses as integers, sizes as signed
- * integers.  A size that does not fit its plain argument's type is
- * FA_ERR_INVALID_ARG; all else is as in the plain call.
+ * integers, a float as its bits.  A size that does not fit its plain argument's type
+ * is FA_ERR_INVALID_ARG; all else is as in the plain call.
  */
 int fa_paged_tables_packed(const int64_t* args);   /* 17 */
 int fa_paged_append_packed(const int64_t* args);   /* 21 */
 int fa_paged_decode_packed(const int64_t* args);   /* 25 */
+int fa_rotary_packed(const int64_t* args);   /* 33 */
+int fa_paged_rotary_append_packed(const int64_t* args);   /* 39 */
+int fa_paged_free_packed(const int64_t* args);   /* 16 */
+int fa_paged_fork_packed(const int64_t* args);   /* 18 */
+int fa_paged_compact_packed(const int64_t* args);   /* 16 */
+int fa_paged_copy_packed(const int64_t* args);   /* 15 */
 
 /*
  * Synchronises `stream`, then reads and clears the device error word of the
