@@ -60,6 +60,9 @@ SIGNATURES = {
     "fa_paged_tables_packed": (_I, [ctypes.c_char_p]),
     "fa_paged_append_packed": (_I, [ctypes.c_char_p]),
     "fa_paged_decode_packed": (_I, [ctypes.c_char_p]),
+    "fa_paged_decode_shared": (_I, [_P, _P, _P, _I, _P, _P, _L, _L, _L, _P, _P, _P, _I, _P, _P, _I, _P,
+                                    _P, _P, ctypes.c_size_t, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
+    "fa_paged_decode_shared_workspace_size": (ctypes.c_size_t, [_I] * 7),
     "fa_rotary": (_I, [_P, _L, _L, _L, _P, _L, _L, _L, _P, _L, _L, _L, _P, _L, _L, _L, _P, _L, _L, _L,
                        _P, _P, _I, _I, _I, _I, _F, _I, _I, _I, _I, _I, _P]),
     "fa_paged_rotary_append": (_I, [_P, _L, _L, _P, _L, _L, _L, _P, _L, _L, _P, _L, _L, _P, _L, _L, _P,
@@ -70,7 +73,7 @@ SIGNATURES = {
     "fa_paged_compact": (_I, [_P, _P, _I, _P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
     "fa_paged_copy": (_I, [_P, _I, _P, _P, _I, _L, _L, _L, _L, _I, _I, _I, _I, _I, _P]),
     **{f"fa_{n}_packed": (_I, [ctypes.c_char_p]) for n in (
-        "rotary", "paged_rotary_append", "paged_free", "paged_fork", "paged_compact", "paged_copy")},
+        "paged_decode_shared", "rotary", "paged_rotary_append", "paged_free", "paged_fork", "paged_compact", "paged_copy")},
     "fa_check_status": (_I, [_P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
     "fa_set_wait_limit_ns": (_I, [ctypes.c_uint64]),
@@ -304,8 +307,8 @@ _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda index: torch.cuda.current_stream(index).cuda_stream)
 # The packed calls' records: ctypes takes 2 us for two dozen arguments, and a sixth of it here.
 _TABLES, _APPEND, _DECODE = (struct.Struct(f"{n}q").pack for n in (17, 21, 25))
-_ROTARY, _ROTARY_APPEND, _FREE, _FORK, _COMPACT, _COPY = (
-    struct.Struct(f"{n}q").pack for n in (33, 39, 16, 18, 16, 15))
+_ROTARY, _ROTARY_APPEND, _FREE, _FORK, _COMPACT, _COPY, _SHARED = (
+    struct.Struct(f"{n}q").pack for n in (33, 39, 16, 18, 16, 15, 29))
 _BF16, _I32, _I64, _F32, _E4M3 = (torch.bfloat16, torch.int32, torch.int64, torch.float32,
                                   torch.float8_e4m3fn)
 
@@ -464,6 +467,58 @@ def fa_paged_decode(q, k_cache, v_cache, block_table, lens, o, lse, workspace, k
 
 def fa_paged_decode_workspace_size(B, K, G, T, H) -> int:
     return int(load().fa_paged_decode_workspace_size(B, K, G, T, H))
+
+
+def fa_paged_decode_shared(q, k_cache, v_cache, block_table, lens, members, group_starts, prefix_lens, o,
+                           lse, workspace, k_scale=None, v_scale=None, stream=None, check=True) -> int:
+    """fa_paged_decode of requests that share prefixes: group g is the requests
+    members[group_starts[g]:group_starts[g + 1]], their first prefix_lens[g] tokens the same."""
+    dev = q.get_device()
+    if dev >= 0 and dev != _current_device():
+        with torch.cuda.device(dev):
+            return fa_paged_decode_shared(q, k_cache, v_cache, block_table, lens, members, group_starts,
+                                          prefix_lens, o, lse, workspace, k_scale, v_scale, stream, check)
+    B, K, G, T, H = q.shape
+    rows, n_groups, n_members = B * K * G * T, prefix_lens.numel(), members.numel()
+    kind, cs, st, ks, vs = _paged_cache(k_cache, v_cache, k_scale, v_scale, K, H, dev)
+    requests, max_pages = block_table.shape
+    if requests != B:
+        raise ValueError(f"block_table must have {B} rows, got {requests}")
+    ws = ws_bytes = 0
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    if not (_BF16 is q.dtype is o.dtype and lse.dtype is _F32
+            and _I32 is block_table.dtype is lens.dtype is members.dtype is group_starts.dtype
+            is prefix_lens.dtype
+            and dev == o.get_device() == lse.get_device() == block_table.get_device()
+            == lens.get_device() == members.get_device() == group_starts.get_device()
+            == prefix_lens.get_device()
+            and rows * H == o.numel() and rows == lse.numel() and B == lens.numel()
+            and n_groups + 1 == group_starts.numel()
+            and q.is_contiguous() and o.is_contiguous() and lse.is_contiguous()
+            and block_table.is_contiguous() and lens.is_contiguous() and members.is_contiguous()
+            and group_starts.is_contiguous() and prefix_lens.is_contiguous()):
+        for t, dtype, n, name in (
+                (q, _BF16, rows * H, "q"), (block_table, _I32, B * max_pages, "block_table"),
+                (lens, _I32, B, "lens"), (members, _I32, n_members, "members"),
+                (group_starts, _I32, n_groups + 1, "group_starts"),
+                (prefix_lens, _I32, n_groups, "prefix_lens"), (o, _BF16, rows * H, "o"),
+                (lse, _F32, rows, "lse")):
+            _dense(t, dtype, n, dev, name)
+    rc = (_lib or load()).fa_paged_decode_shared_packed(_SHARED(
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kind, ks, vs, st[0], st[1], st[2],
+        block_table.data_ptr(), lens.data_ptr(), members.data_ptr(), n_members, group_starts.data_ptr(),
+        prefix_lens.data_ptr(), n_groups, o.data_ptr(), lse.data_ptr(), ws, ws_bytes, B, K, G, T, H,
+        cs[0], cs[2], max_pages, _current_stream(dev) if stream is None else _raw_stream(stream)))
+    if rc and check:
+        _check("fa_paged_decode_shared", rc)
+    return rc
+
+
+def fa_paged_decode_shared_workspace_size(B, K, G, T, H, n_groups, n_members) -> int:
+    return int(load().fa_paged_decode_shared_workspace_size(B, K, G, T, H, n_groups, n_members))
 
 
 # ------------------------------------------- rotary positions, pages: C names
@@ -802,6 +857,22 @@ def paged_attention_decode(q, k_cache, v_cache, block_table, lens, *, k_scale=No
             workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
     fa_paged_decode(q, k_cache, v_cache, block_table, lens, o, lse, workspace, k_scale, v_scale,
                     window, stream)
+    return o, lse
+
+
+def paged_attention_decode_shared(q, k_cache, v_cache, block_table, lens, members, group_starts,
+                                  prefix_lens, *, k_scale=None, v_scale=None, stream=None,
+                                  workspace=None):
+    """Allocate o / lse (and the workspace unless given) and run fa_paged_decode_shared."""
+    B, K, G, T, H = q.shape
+    with _allocating_on(stream, q.device):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, K, G, T), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            n = fa_paged_decode_shared_workspace_size(B, K, G, T, H, prefix_lens.numel(), members.numel())
+            workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+    fa_paged_decode_shared(q, k_cache, v_cache, block_table, lens, members, group_starts, prefix_lens, o, lse,
+                           workspace, k_scale, v_scale, stream)
     return o, lse
 
 

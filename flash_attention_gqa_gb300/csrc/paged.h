@@ -52,6 +52,26 @@ struct PagedDecodeSplit {
   int item, first, last, pad;
 };
 
+// Attention of requests that share a prefix: its keys are attended to once for all rows of a group
+// (HEAD: tiles of 128 rows of one group, "chunks", take the requests' place), every request's own keys
+// behind it apart (TAIL), and both joined.
+enum DecodeMode { DECODE_ALL, DECODE_TAIL, DECODE_HEAD };
+
+// Rows [row, row + rows) of a group, counted over its members' G * T rows one member after the other.
+struct PagedChunk {
+  int len, leader;     // keys of the prefix, the request whose table row has their pages
+  int member, row;     // the group's first entry in members; the chunk's first row
+  int rows, base, pad0, pad1;   // base: rows, rounded up to 8 a chunk, of the chunks before
+};
+struct PagedSharedTables {
+  int32_t* begins;     // [B] first key that is not in the request's prefix
+  int32_t* places;     // [B] 128 * chunk + row of the request's first row, -1: no prefix
+  int32_t* members;    // [n_members] requests, -1: none
+  int32_t* n_chunks;
+  PagedChunk* chunks;
+  float* whole;        // partials of items that one CTA does: TAIL by item, HEAD by the chunks' bases
+};
+
 struct PagedDecodeArgs {
   const void* q;               // bf16 [B, K, G, T, H]
   const void *k_cache, *v_cache;
@@ -69,6 +89,7 @@ struct PagedDecodeArgs {
   bool by_item;                // entries of splits are items
   bool unsplit;                // no item is shared: no splits, no partials (set by the launch)
   uint32_t* err;
+  PagedSharedTables shared;    // TAIL and HEAD
 };
 
 // Workspace of a decode: the splits, then partials, on a GPU with sm_count SMs.
@@ -93,6 +114,59 @@ inline PagedDecodePlan paged_decode_plan(int R, int H, int sm_count) {
   p.total = p.partials + (((size_t)p.ctas * 2 * paged_partial_floats(R, H) * 4 + 255) & ~(size_t)255);
   return p;
 }
+
+// ---- attention of requests that share prefixes
+struct PagedSharedArgs {
+  PagedDecodeArgs tail;        // the requests' own keys: splits by item, partials
+  PagedDecodeSplit* head_splits;   // [chunks * K]
+  float* head_partials;        // [CTAs][2][128 rows]
+  float* head_whole;           // partials of whole items, by the chunks' bases
+  const int32_t *members, *group_starts, *prefix_lens;   // the caller's
+  int n_members, n_groups, max_chunks;
+  int head_ctas, tail_ctas;
+};
+
+// Its workspace: the tables that the first kernel writes, splits, partials.
+struct PagedSharedPlan {
+  int max_chunks, head_ctas, tail_ctas;
+  size_t begins, places, members, n_chunks, chunks, head_splits, tail_splits, head_partials, tail_partials,
+      head_whole, tail_whole, total;
+};
+inline PagedSharedPlan paged_shared_plan(int B, int K, int R, int H, int n_groups, int n_members, int sm_count) {
+  PagedSharedPlan p;
+  const int64_t rows = (int64_t)n_members * R;
+  p.max_chunks = (int)((rows + 127) / 128) + (n_groups < n_members ? n_groups : n_members);
+  p.head_ctas = sm_count;
+  p.tail_ctas = paged_decode_plan(R, H, sm_count).ctas;
+  size_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t here = at;
+    at += ((size_t)bytes + 255) & ~(size_t)255;
+    return here;
+  };
+  const int64_t split = sizeof(PagedDecodeSplit);
+  p.begins = take((int64_t)B * 4);
+  p.places = take((int64_t)B * 4);
+  p.members = take((int64_t)n_members * 4);
+  p.n_chunks = take(4);
+  p.chunks = take((int64_t)p.max_chunks * sizeof(PagedChunk));
+  p.head_splits = take((int64_t)p.max_chunks * K * split);
+  p.tail_splits = take((int64_t)B * K * split);
+  p.head_partials = take((int64_t)p.head_ctas * 2 * paged_partial_floats(128, H) * 4);
+  p.tail_partials = take((int64_t)p.tail_ctas * 2 * paged_partial_floats(R, H) * 4);
+  p.head_whole = take((rows + 8 * (int64_t)p.max_chunks) * K * (H + 2) * 4);
+  p.tail_whole = take((int64_t)B * K * paged_partial_floats(R, H) * 4);
+  p.total = at;
+  return p;
+}
+
+cudaError_t launch_paged_shared_setup(const PagedSharedArgs& a, cudaStream_t st);
+cudaError_t launch_paged_shared_h64_bf16(const PagedSharedArgs& a, cudaStream_t st);
+cudaError_t launch_paged_shared_h64_e4m3(const PagedSharedArgs& a, cudaStream_t st);
+cudaError_t launch_paged_shared_h128_bf16(const PagedSharedArgs& a, cudaStream_t st);
+cudaError_t launch_paged_shared_h128_e4m3(const PagedSharedArgs& a, cudaStream_t st);
+cudaError_t launch_paged_shared_h256_bf16(const PagedSharedArgs& a, cudaStream_t st);
+cudaError_t launch_paged_shared_h256_e4m3(const PagedSharedArgs& a, cudaStream_t st);
 
 cudaError_t launch_paged_tables(const PagedTablesArgs& a, cudaStream_t st);
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t st);

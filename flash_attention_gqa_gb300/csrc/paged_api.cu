@@ -150,12 +150,74 @@ int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int
   }
 }
 
-}  // extern "C"
+size_t fa_paged_decode_shared_workspace_size(int B, int K, int G, int T, int H, int n_groups, int n_members) {
+  if (B <= 0 || K <= 0 || G <= 0 || T <= 0 || !decode_shape_ok(B, K, G, T, H)) return 0;
+  if (n_groups < 0 || n_members < 0 || n_groups > kMaxPagedBatch || n_members > B) return 0;
+  return paged_shared_plan(B, K, G * T, H, n_groups, n_members, fa_device_sm_count()).total;
+}
 
-extern "C" {
+int fa_paged_decode_shared(const void* q, const void* k_cache, const void* v_cache, int cache_type,
+                           const float* k_scale, const float* v_scale, int64_t page_stride, int64_t head_stride,
+                           int64_t token_stride, const int32_t* block_table, const int32_t* lens,
+                           const int32_t* members, int n_members, const int32_t* group_starts,
+                           const int32_t* prefix_lens, int n_groups, void* o, float* lse, void* workspace,
+                           size_t workspace_bytes, int B, int K, int G, int T, int H, int n_pages, int page_size,
+                           int max_pages, void* stream) {
+  if (B < 0 || K < 0 || G < 0 || T < 0 || H < 0 || max_pages < 0 || n_members < 0 || n_groups < 0)
+    return FA_ERR_INVALID_ARG;
+  PagedSharedArgs s{};
+  PagedDecodeArgs& a = s.tail;
+  const int rc = make_layout(&a.lay, cache_type, page_stride, head_stride, token_stride, K, n_pages, page_size);
+  if (rc != FA_OK) return rc;
+  if (!decode_shape_ok(B, K, G, T, H) || (int64_t)max_pages * page_size > kMaxPagedLen || n_groups > kMaxPagedBatch)
+    return FA_ERR_UNSUPPORTED;
+  if (n_members > B) return FA_ERR_INVALID_ARG;
+  if (!aligned(k_scale, 4) || !aligned(v_scale, 4)) return FA_ERR_INVALID_ARG;
+  if (cache_type == FA_CACHE_BF16 && (k_scale || v_scale)) return FA_ERR_INVALID_ARG;
+  if ((int64_t)B * K * G * T == 0) return FA_OK;
+  if (!usable(q, 16) || !usable(o, 16) || !usable(lse, 4) || !usable(lens, 4)) return FA_ERR_INVALID_ARG;
+  if (max_pages > 0 && !usable(block_table, 4)) return FA_ERR_INVALID_ARG;
+  if (n_pages > 0 && (!usable(k_cache, 16) || !usable(v_cache, 16))) return FA_ERR_INVALID_ARG;
+  if (n_members > 0 && !usable(members, 4)) return FA_ERR_INVALID_ARG;
+  if (!usable(group_starts, 4) || (n_groups > 0 && !usable(prefix_lens, 4))) return FA_ERR_INVALID_ARG;
+  const PagedSharedPlan plan = paged_shared_plan(B, K, G * T, H, n_groups, n_members, fa_device_sm_count());
+  if (!usable(workspace, 256) || workspace_bytes < plan.total) return FA_ERR_INVALID_ARG;
+  char* const ws = static_cast<char*>(workspace);
+  a.q = q; a.k_cache = k_cache; a.v_cache = v_cache;
+  a.k_scale = k_scale; a.v_scale = v_scale;
+  a.block_table = block_table; a.lens = lens;
+  a.o = o; a.lse = lse;
+  a.B = B; a.K = K; a.G = G; a.T = T; a.H = H; a.max_pages = max_pages;
+  a.by_item = true;
+  a.splits = reinterpret_cast<PagedDecodeSplit*>(ws + plan.tail_splits);
+  a.partials = reinterpret_cast<float*>(ws + plan.tail_partials);
+  a.shared.begins = reinterpret_cast<int32_t*>(ws + plan.begins);
+  a.shared.places = reinterpret_cast<int32_t*>(ws + plan.places);
+  a.shared.members = reinterpret_cast<int32_t*>(ws + plan.members);
+  a.shared.n_chunks = reinterpret_cast<int32_t*>(ws + plan.n_chunks);
+  a.shared.chunks = reinterpret_cast<PagedChunk*>(ws + plan.chunks);
+  a.shared.whole = reinterpret_cast<float*>(ws + plan.tail_whole);
+  s.head_splits = reinterpret_cast<PagedDecodeSplit*>(ws + plan.head_splits);
+  s.head_partials = reinterpret_cast<float*>(ws + plan.head_partials);
+  s.head_whole = reinterpret_cast<float*>(ws + plan.head_whole);
+  s.members = members; s.group_starts = group_starts; s.prefix_lens = prefix_lens;
+  s.n_members = n_members; s.n_groups = n_groups; s.max_chunks = plan.max_chunks;
+  s.head_ctas = plan.head_ctas; s.tail_ctas = plan.tail_ctas;
+  a.wait_limit_ns = device_wait_limit_ns();
+  a.err = device_error_word();
+  if (!a.err || plan.tail_ctas == 0) return FA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool e4m3 = cache_type == FA_CACHE_E4M3;
+  switch (H) {
+    case 64: return status(e4m3 ? launch_paged_shared_h64_e4m3(s, st) : launch_paged_shared_h64_bf16(s, st));
+    case 128: return status(e4m3 ? launch_paged_shared_h128_e4m3(s, st) : launch_paged_shared_h128_bf16(s, st));
+    default: return status(e4m3 ? launch_paged_shared_h256_e4m3(s, st) : launch_paged_shared_h256_bf16(s, st));
+  }
+}
 
 int fa_paged_tables_packed(const int64_t* args) { return call_packed(fa_paged_tables, args); }
 int fa_paged_append_packed(const int64_t* args) { return call_packed(fa_paged_append, args); }
 int fa_paged_decode_packed(const int64_t* args) { return call_packed(fa_paged_decode, args); }
+int fa_paged_decode_shared_packed(const int64_t* args) { return call_packed(fa_paged_decode_shared, args); }
 
 }  // extern "C"

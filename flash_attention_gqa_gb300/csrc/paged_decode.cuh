@@ -71,6 +71,8 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
+// Until the grid before this one in a chain of early launches has ended.
+__device__ __forceinline__ void grid_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Not to be hoisted out of the loop that it stands in: that would take registers.
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   uint4 x;
@@ -148,8 +150,9 @@ constexpr float kBelow = F16 ? 11.0f : 0.0f;
 // ------------------------------------------------------------ configuration
 // NT: n-tiles of 8 query rows per warp.  WR: warps of a team, which share a ring
 // and the keys in it, NT * 8 rows each.
-template <int H_, bool E4M3_, int NT_, int WR_>
+template <int H_, bool E4M3_, int NT_, int WR_, DecodeMode MODE_ = DECODE_ALL>
 struct DecodeCfg {
+  static constexpr DecodeMode MODE = MODE_;
   static constexpr int H = H_, NT = NT_, WR = WR_;
   static constexpr bool TC = false, E4M3 = E4M3_, TEAM = WR > 1;
   static constexpr int ROWB = E4M3 ? H : 2 * H;        // bytes of a key
@@ -210,7 +213,8 @@ struct DecodeEnd {
 
 // The part of an item that a CTA does: tiles [begun, end) of its `tiles`.
 struct DecodeWalk {
-  int b, k, len, first, tiles;   // first: key of tile 0, a multiple of CK
+  int b, k, len, first, tiles;   // first: key of tile 0, a multiple of CK (TAIL: of 8)
+  int low;                       // TAIL: first key; HEAD: the table's row
   int tile, begun, end;
   int todo;                      // items that follow
 };
@@ -218,28 +222,44 @@ struct DecodeWalk {
 template <class C>
 struct DecodeShape {
   const PagedDecodeArgs& a;
+  // (TAIL and HEAD read tables that the call's first kernel has written, maybe while this grid was
+  // already there: L2 loads)
+  __device__ __forceinline__ int count() const {
+    return C::MODE == DECODE_HEAD ? __ldcg(a.shared.n_chunks) : a.B;
+  }
   __device__ __forceinline__ int length(int b) const {
+    if (C::MODE == DECODE_HEAD) return __ldcg(&a.shared.chunks[b].len);
     const int n = a.lens[b];
     return min(max(n, 0), a.max_pages << a.lay.page_shift);
   }
   // First key any of the T queries keeps.
-  __device__ __forceinline__ int low(int len) const {
+  __device__ __forceinline__ int low(int b, int len) const {
+    if (C::MODE == DECODE_HEAD) return 0;
+    if (C::MODE == DECODE_TAIL) return __ldcg(a.shared.begins + b);
     return a.window > 0 ? max(0, len - a.T + 1 - a.window) : 0;
   }
-  __device__ __forceinline__ int first(int len) const { return low(len) & ~(C::CK - 1); }
-  __device__ __forceinline__ int tiles(int len) const {
-    return max(1, (len - first(len) + C::TK - 1) / C::TK);   // an empty item writes its zeros
+  // The same, of the item that the walk is in.
+  __device__ __forceinline__ int low(const DecodeWalk& w) const {
+    return C::MODE == DECODE_TAIL ? w.low : low(w.b, w.len);
+  }
+  __device__ __forceinline__ int table_row(const DecodeWalk& w) const { return C::MODE == DECODE_HEAD ? w.low : w.b; }
+  __device__ __forceinline__ int first(int low) const { return low & ~((C::MODE == DECODE_TAIL ? 8 : C::CK) - 1); }
+  __device__ __forceinline__ int tiles(int b, int len) const {
+    return max(1, (len - first(low(b, len)) + C::TK - 1) / C::TK);   // an empty item writes its zeros
   }
   __device__ __forceinline__ DecodePlace place(const DecodeEnd& e) const {
-    const int per_item = tiles(e.len) + C::ITEM_UNITS, k = (int)quotient(e.t, per_item);
+    const int per_item = tiles(e.b, e.len) + C::ITEM_UNITS, k = (int)quotient(e.t, per_item);
     return DecodePlace{e.b, k, (int)(e.t - (long long)k * per_item)};
   }
   __device__ __forceinline__ void enter(DecodeWalk& w, int b, int k) const {
     w.b = b;
     w.k = k;
     w.len = length(b);
-    w.first = first(w.len);
-    w.tiles = tiles(w.len);
+    const int lo = low(b, w.len);
+    if (C::MODE == DECODE_TAIL) w.low = lo;
+    if (C::MODE == DECODE_HEAD) w.low = __ldcg(&a.shared.chunks[b].leader);
+    w.first = first(lo);
+    w.tiles = max(1, (w.len - w.first + C::TK - 1) / C::TK);
     w.tile = w.begun = 0;
     w.end = w.tiles;
   }
@@ -292,15 +312,16 @@ __device__ __forceinline__ bool decode_units(const PagedDecodeArgs& a, DecodeSha
   constexpr int threads = C::THREADS;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const DecodeShape<C> shape{a};
-  const int per = (a.B + threads - 1) / threads;
-  const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+  const int B = shape.count();
+  const int per = (B + threads - 1) / threads;
+  const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
   long long mine = 0;
   for (int b = b0; b < b1; ++b) {
-    if (blockIdx.x == 0) {
+    if (C::MODE != DECODE_HEAD && blockIdx.x == 0) {
       const int n = a.lens[b];
       if (n != shape.length(b)) atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
     }
-    mine += (long long)(shape.tiles(shape.length(b)) + C::ITEM_UNITS) * a.K;
+    mine += (long long)(shape.tiles(b, shape.length(b)) + C::ITEM_UNITS) * a.K;
   }
   long long inc = mine;
 #pragma unroll
@@ -328,7 +349,7 @@ __device__ __forceinline__ bool decode_units(const PagedDecodeArgs& a, DecodeSha
     long long x = at;
     for (int b = b0; b < b1; ++b) {
       const int len = shape.length(b);
-      const long long next = x + (long long)(shape.tiles(len) + C::ITEM_UNITS) * a.K;
+      const long long next = x + (long long)(shape.tiles(b, len) + C::ITEM_UNITS) * a.K;
       if (t0 >= x && t0 < next) sh.ends[0] = DecodeEnd{b, len, t0 - x};
       if (t1 - 1 >= x && t1 - 1 < next) sh.ends[1] = DecodeEnd{b, len, t1 - 1 - x};
       x = next;
@@ -339,7 +360,7 @@ __device__ __forceinline__ bool decode_units(const PagedDecodeArgs& a, DecodeSha
   if (tid == 32 && !a.unsplit) {
     // the item that the units end in, where it begins here and goes on in the
     // next CTA: for the join, with its last CTA
-    const int tiles = shape.tiles(sh.ends[1].len);
+    const int tiles = shape.tiles(sh.ends[1].b, sh.ends[1].len);
     const long long first = t1 - 1 - tail.rem + C::ITEM_UNITS;   // its first tile's unit
     const bool split = tail.rem >= C::ITEM_UNITS && tail.rem + 1 < tiles + C::ITEM_UNITS && first >= t0;
     if (split || !a.by_item) {
@@ -413,7 +434,10 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
 
   // ---- this CTA's units
   DecodeWalk walk;
-  if (!decode_units<C>(a, sh, walk)) return;
+  if (!decode_units<C>(a, sh, walk)) {
+    if (C::MODE == DECODE_TAIL) grid_before();
+    return;
+  }
   DecodeWalk ahead = walk;   // where the copies are
   bool more = true;
 
@@ -438,7 +462,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     key_live = false;
     if (!more) return;
     const int s = ahead.first + (ahead.tile * C::TEAMS + team) * CK + (lane & (CK - 1));
-    key_live = s >= shape.low(ahead.len) && s < ahead.len;
+    key_live = s >= shape.low(ahead) && s < ahead.len;
     key_in = s & ((1 << a.lay.page_shift) - 1);
     key_head = ahead.k;
     if (key_live) key_page = __ldg(a.block_table + (int64_t)ahead.b * a.max_pages + (s >> a.lay.page_shift));
@@ -608,7 +632,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       for (int j = 0; j < 2; ++j)
         col_hi[nt][j] = walk.len - a.T + 1 + (a.T == 1 ? 0 : (row0 + nt * 8 + 2 * c + j) % a.T);
     const int full_hi = walk.len - a.T + 1;                              // all columns keep keys
-    const int full_lo = a.window > 0 ? max(0, walk.len - a.window) : 0;   // in [full_lo, full_hi)
+    const int full_lo =   // in [full_lo, full_hi)
+        C::MODE == DECODE_TAIL ? walk.low : a.window > 0 ? max(0, walk.len - a.window) : 0;
 
     float o[KS][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -693,7 +718,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int key = key1 + kt * 16 + g + (i >> 1) * 8, hi = col_hi[nt][i & 1];
-                if (key >= hi || (a.window > 0 && key < hi - a.window)) s[kt][nt][i] = -INFINITY;
+                if (key >= hi || (C::MODE == DECODE_TAIL ? key < walk.low : a.window > 0 && key < hi - a.window))
+                  s[kt][nt][i] = -INFINITY;
               }
         }
 
@@ -868,9 +894,13 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     const int64_t out_row = item * R;
     // Partials: slot 1 of a CTA holds the item that starts in it, slot 0 one
     // that started before.
-    float* const mine = a.partials + ((int64_t)blockIdx.x * 2 + (walk.begun == 0 ? 1 : 0)) * paged_partial_floats(R, H);
+    // (TAIL: a whole item's place is by the item.)
+    float* const mine = C::MODE == DECODE_TAIL && whole
+                            ? a.shared.whole + item * paged_partial_floats(R, H)
+                            : a.partials + ((int64_t)blockIdx.x * 2 + (walk.begun == 0 ? 1 : 0)) * paged_partial_floats(R, H);
+    const bool finished = C::MODE == DECODE_ALL && whole;
     auto put = [&](int r, int d, float4 x, float M, float L) {   // four dims of row r
-      if (whole) put_result((char*)a.o + out_row * H * 2, a.lse + out_row, H, r, d, x, M, L, vscale);
+      if (finished) put_result((char*)a.o + out_row * H * 2, a.lse + out_row, H, r, d, x, M, L, vscale);
       else put_partial(mine, H, P, r, d, x, M, L);
     };
     // O^T goes through shared memory: the slot just used, free until the next
@@ -989,7 +1019,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
             const float L = l[nt][j], M = m[nt][j];
             f[j] = L == 0.0f ? 0.0f : vscale / L;
             if (r >= R) continue;
-            if (whole) {
+            if (finished) {
               if (g == 0) a.lse[out_row + r] = (M + log2f(L)) * LN2;
             } else {
               if (g == 0) {
@@ -1004,7 +1034,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
               }
             }
           }
-          if (whole) {   // transposed: row g, dims in pairs
+          if (finished) {   // transposed: row g, dims in pairs
             const int r = row0 + nt * 8 + g;
             char* const dst = (char*)a.o + (out_row + r) * (H * 2);
 #pragma unroll
@@ -1030,6 +1060,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     walk = then;
   }
   cp_async_wait<0>();
+  if (C::MODE == DECODE_TAIL) grid_before();   // so that this grid's end is the HEAD grid's, too
 }
 
 // Joins the partials of an item that several CTAs of the first kernel share: a
@@ -1043,7 +1074,7 @@ __global__ void __launch_bounds__(THREADS)
 paged_join_kernel(const __grid_constant__ PagedDecodeArgs a, int ctas, int per) {
   __shared__ float4 sx[THREADS];
   __shared__ float2 sml[THREADS];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_before();
   // (L2 loads: this grid may have started before the first one wrote)
   const int4 split = __ldcg(reinterpret_cast<const int4*>(a.splits) + blockIdx.x);
   const int item = split.x, first = split.y, n = split.z - first + 1;   // n partials

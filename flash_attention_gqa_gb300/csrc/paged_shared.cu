@@ -1,0 +1,160 @@
+// Attention of requests that share prefixes, its first kernel: who shares what.
+//
+// Checks the caller's groups and writes what the others go by (paged.h): the first key that each
+// request has for itself, where its rows are among its group's, and the groups' rows in chunks of
+// 128.  Whatever does not hold together is not shared, and reported: every request's keys are then
+// its own, and its result is the same.  A group of one shares nothing either.  Latency bounds it (one
+// CTA; the grids behind it are launched while it runs).
+#include <climits>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "paged.h"
+#include "ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 1024;
+
+// Entry of a sorted list of n + 1 with list[e] <= x < list[e + 1].
+__device__ __forceinline__ int entry_of(const int* list, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (list[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) paged_shared_setup_kernel(const __grid_constant__ PagedSharedArgs a) {
+  extern __shared__ int sm[];
+  const int n = a.n_groups, B = a.tail.B, T = a.tail.T, R = a.tail.G * T, tid = threadIdx.x;
+  int* const starts = sm;              // [n + 1]
+  int* const least = starts + n + 1;   // [n] longest prefix that all members' queries see; then the prefix
+  int* const lead = least + n;         // [n] lowest entry with a request
+  int* const live = lead + n;          // [n] entries with one
+  int* const first = live + n;         // [n + 1] chunks before the group
+  int* const base = first + n + 1;     // [n] padded rows before it
+  int* const claim = base + n;         // [B] lowest entry that names the request
+  __shared__ int sums[2][32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const PagedSharedTables& out = a.tail.shared;
+  const int most = a.tail.max_pages << a.tail.lay.page_shift;
+
+  for (int g = tid; g <= n; g += kThreads) starts[g] = a.group_starts[g];
+  for (int g = tid; g < n; g += kThreads) {
+    least[g] = lead[g] = INT_MAX;
+    live[g] = 0;
+  }
+  for (int b = tid; b < B; b += kThreads) {
+    claim[b] = INT_MAX;
+    out.begins[b] = 0;
+    out.places[b] = -1;
+  }
+  __syncthreads();
+  bool bad = false;
+  for (int g = tid; g < n; g += kThreads) bad |= starts[g] < 0 || starts[g + 1] < starts[g] || starts[g + 1] > a.n_members;
+  const bool none = __syncthreads_or(bad) || n == 0;   // no groups to go by
+  const int lo = none ? 0 : starts[0], hi = none ? 0 : starts[n];
+  for (int i = lo + tid; i < hi; i += kThreads) {
+    const int r = a.members[i];
+    if ((unsigned)r < (unsigned)B) atomicMin(&claim[r], i);
+    else bad = true;
+  }
+  __syncthreads();
+  for (int i = lo + tid; i < hi; i += kThreads) {
+    const int r = a.members[i];
+    if ((unsigned)r >= (unsigned)B) continue;
+    if (claim[r] != i) { bad = true; continue; }   // named twice
+    const int g = entry_of(starts, n, i), len = min(max(a.tail.lens[r], 0), most);
+    atomicMin(&least[g], max(0, len - T + 1));
+    atomicMin(&lead[g], i);
+    atomicAdd(&live[g], 1);
+  }
+  __syncthreads();
+
+  // chunks and padded rows of the groups before each
+  const int per = (n + kThreads - 1) / kThreads, g0 = min(tid * per, n), g1 = min(g0 + per, n);
+  auto chunks_of = [&](int g) { return live[g] > 1 && least[g] > 0 ? ((starts[g + 1] - starts[g]) * R + 127) >> 7 : 0; };
+  auto padded_of = [&](int g) { return chunks_of(g) ? ((starts[g + 1] - starts[g]) * R + 7) & ~7 : 0; };
+  int chunks = 0, padded = 0;
+  if (!none)
+    for (int g = g0; g < g1; ++g) {
+      const int want = a.prefix_lens[g];
+      if (live[g] > 0) {
+        bad |= want < 0 || want > least[g];
+        least[g] = min(max(want, 0), least[g]);
+      }
+      chunks += chunks_of(g);
+      padded += padded_of(g);
+    }
+  const int lane = tid & 31, warp = tid >> 5;
+  int ic = chunks, ip = padded;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(~0u, ic, d), y = __shfl_up_sync(~0u, ip, d);
+    if (lane >= d) { ic += x; ip += y; }
+  }
+  if (lane == 31) { sums[0][warp] = ic; sums[1][warp] = ip; }
+  __syncthreads();
+  int before = ic - chunks, base_at = ip - padded, all = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) { before += sums[0][w]; base_at += sums[1][w]; }
+    all += sums[0][w];
+  }
+  if (!none)
+    for (int g = g0; g < g1; ++g) {
+      first[g] = before;
+      base[g] = base_at;
+      before += chunks_of(g);
+      base_at += padded_of(g);
+    }
+  if (tid == 0) {
+    first[n] = all;
+    *out.n_chunks = all;
+  }
+  __syncthreads();
+  for (int i = tid; i < a.n_members; i += kThreads) {
+    int r = -1;
+    if (i >= lo && i < hi) {
+      r = a.members[i];
+      if ((unsigned)r >= (unsigned)B || claim[r] != i) r = -1;
+    }
+    out.members[i] = r;
+    if (r < 0) continue;
+    const int g = entry_of(starts, n, i);
+    if (chunks_of(g) == 0) continue;
+    out.begins[r] = least[g];
+    out.places[r] = first[g] * 128 + (i - starts[g]) * R;
+  }
+  for (int c = tid; c < all; c += kThreads) {
+    int g = entry_of(first, n, c);
+    const int row = (c - first[g]) * 128, rows = min(128, (starts[g + 1] - starts[g]) * R - row);
+    int4* const at = reinterpret_cast<int4*>(out.chunks + c);
+    at[0] = make_int4(least[g], a.members[lead[g]], starts[g], row);
+    at[1] = make_int4(rows, base[g] + row, 0, 0);
+  }
+  if (bad) atomicOr(a.tail.err, (uint32_t)DEV_BAD_VALUE);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_shared_setup(const PagedSharedArgs& a, cudaStream_t st) {
+  const size_t smem = ((size_t)6 * a.n_groups + 2 + a.tail.B) * sizeof(int);
+  // (always to what the largest call needs, as for the tables)
+  if (smem > 47 * 1024) {
+    constexpr int most = (7 * kMaxPagedBatch + 2) * sizeof(int);
+    const cudaError_t e =
+        cudaFuncSetAttribute(paged_shared_setup_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, paged_shared_setup_kernel, a);
+}
+
+}  // namespace fa

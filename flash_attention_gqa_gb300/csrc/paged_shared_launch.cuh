@@ -1,0 +1,211 @@
+// Attention of requests that share prefixes: the grids behind the first kernel (paged_shared.cu).
+//
+//   x = q . k over the prefix's keys, once for all rows of a group (HEAD), and over the request's own
+//   keys (TAIL); each leaves sums o, weights' sum l and base m, and the join adds them up:
+//   o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
+//
+// HEAD is the tcgen05 kernel of paged_decode_tc.cuh over chunks of 128 rows of a group in place of
+// requests, TAIL the decode kernels over keys from a request's first own one on; both leave partials
+// of whole items, too.  The four grids are launched early, one behind the other: TAIL's CTAs start as
+// HEAD's end.  HEAD waits for the tables before it lets TAIL start, TAIL ends only after HEAD has, and
+// the join waits for TAIL.
+#pragma once
+#include "paged_decode.cuh"
+#include "paged_decode_tc.cuh"
+
+namespace fa {
+
+// A thread per 4 dims of a row of item (b, k), a warp 8 rows of 16 dims; `per` such a CTA, times
+// shares of the partials, summed in order behind it.  U partials of a thread in flight.
+template <int H, bool TC, int U, int THREADS>
+__global__ void __launch_bounds__(THREADS)
+paged_shared_join_kernel(const __grid_constant__ PagedSharedArgs s, int per) {
+  __shared__ float4 sx[THREADS];
+  __shared__ float2 sml[THREADS];
+  grid_before();
+  const PagedDecodeArgs& a = s.tail;
+  const int item = blockIdx.x, b = item / a.K, k = item - b * a.K, R = a.G * a.T, P = paged_partial_rows(R);
+  const int shares = blockDim.x / per, share = threadIdx.x / per, at = threadIdx.x % per;
+  const int i = blockIdx.y * per + at, groups = (R + 7) / 8, tile = i / 32;
+  const int r = tile / groups < H / 16 ? tile % groups * 8 + i % 8 : R, d = tile / groups * 4 + i % 32 / 8;   // d: of 4
+  // (written by the grids before, maybe while this one was already there: L2 loads)
+  const int4 tail = __ldcg(reinterpret_cast<const int4*>(a.splits) + item);
+  const int place = r < R ? __ldcg(a.shared.places + b) : -1;
+  // (an entry may hold anything where a wait ran out before it was written)
+  const bool tail_split = tail.y >= 0 && tail.z >= tail.y && tail.z < s.tail_ctas;
+  const int n_tail = tail_split ? tail.z - tail.y + 1 : 1;
+  const int64_t part = paged_partial_floats(R, H), part_head = paged_partial_floats(128, H);
+  const float* const tail_at = tail_split ? a.partials + (int64_t)tail.y * 2 * part : a.shared.whole + item * part;
+  int n_head = 0, P_head = 128, r_head = 0;
+  const float* head_at = nullptr;
+  bool head_split = false;
+  if (place >= 0) {
+    const int row = place + r, chunk = row >> 7;
+    r_head = row & 127;
+    const int4 head = __ldcg(reinterpret_cast<const int4*>(s.head_splits) + (int64_t)chunk * a.K + k);
+    const int4 c = __ldcg(reinterpret_cast<const int4*>(a.shared.chunks + chunk) + 1);
+    head_split = head.y >= 0 && head.z >= head.y && head.z < s.head_ctas;
+    n_head = head_split ? head.z - head.y + 1 : 1;
+    if (!head_split) P_head = (c.x + 7) & ~7;
+    head_at = head_split ? s.head_partials + (int64_t)head.y * 2 * part_head
+                         : s.head_whole + ((int64_t)c.y * a.K + (int64_t)k * P_head) * (H + 2);
+  }
+  float M = -INFINITY, L = 0.0f;
+  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (r < R) {
+    const int n = n_head + n_tail;
+    for (int p0 = share; p0 < n; p0 += U * shares) {
+      float4 y[U];
+      float m[U], l[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int p = p0 + u * shares;
+        m[u] = -INFINITY;
+        if (p < n) {
+          // partial 0 of a split item is in slot 1 of its CTA, the others in slot 0 of theirs
+          const bool h = p < n_head;
+          const int q = h ? p : p - n_head;
+          const float* const src = h ? head_at + (head_split ? (q ? q * 2 : 1) * part_head : 0)
+                                     : tail_at + (tail_split ? (q ? q * 2 : 1) * part : 0);
+          const int rows = h ? P_head : P, row = h ? r_head : r;
+          const int64_t at4 = h || TC ? ((int64_t)d * rows + row) * 4 : (int64_t)row * H + d * 4;
+          y[u] = __ldcg(reinterpret_cast<const float4*>(src + at4));
+          m[u] = __ldcg(src + (int64_t)rows * H + row);
+          l[u] = __ldcg(src + (int64_t)rows * (H + 1) + row);
+        }
+      }
+      float mn = M;
+#pragma unroll
+      for (int u = 0; u < U; ++u) mn = fmaxf(mn, m[u]);
+      const float low = mn == -INFINITY ? 0.0f : mn, f0 = fast_exp2(M - low);
+      M = mn;
+      L *= f0;
+      x.x *= f0; x.y *= f0; x.z *= f0; x.w *= f0;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (p0 + u * shares < n && m[u] != -INFINITY) {   // (one with no key adds nothing)
+          const float f = fast_exp2(m[u] - low);
+          L += l[u] * f;
+          x.x += y[u].x * f;
+          x.y += y[u].y * f;
+          x.z += y[u].z * f;
+          x.w += y[u].w * f;
+        }
+      }
+    }
+  }
+  if (shares > 1) {
+    sx[threadIdx.x] = x;
+    sml[threadIdx.x] = make_float2(M, L);
+    __syncthreads();
+    if (share == 0) {
+      for (int w = 1; w < shares; ++w) M = fmaxf(M, sml[w * per + at].x);
+      const float low = M == -INFINITY ? 0.0f : M;
+      L = 0.0f;
+      x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int w = 0; w < shares; ++w) {
+        const float2 ml = sml[w * per + at];
+        const float4 y = sx[w * per + at];
+        const float f = fast_exp2(ml.x - low);
+        L += ml.y * f;
+        x.x += y.x * f;
+        x.y += y.y * f;
+        x.z += y.z * f;
+        x.w += y.w * f;
+      }
+    }
+  }
+  if (share == 0 && r < R)
+    put_result((char*)a.o + (int64_t)item * R * H * 2, a.lse + (int64_t)item * R, H, r, d * 4, x, M, L,
+               a.v_scale ? a.v_scale[k] : 1.0f);
+}
+
+// A grid that may start while the one before it in the stream still runs.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t st, const A&... args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <class C, void (*KERNEL)(const PagedDecodeArgs)>
+cudaError_t launch_shared_part(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
+  static bool ready[64] = {};   // per device; setting it twice is harmless
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !ready[dev]) {
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) ready[dev] = true;
+  }
+  return launch_early(KERNEL, dim3(grid), C::THREADS, C::SMEM, st, a);
+}
+
+template <int H, bool TC>
+cudaError_t launch_shared_join(const PagedSharedArgs& s, cudaStream_t st) {
+  const int R = s.tail.G * s.tail.T, items = s.tail.B * s.tail.K, elements = (R + 7) / 8 * 8 * (H / 4);
+  // Partials of a row: about CTAs / items, two more at most, of its own keys and of the prefix's, whose
+  // items are at least the rows in chunks times the heads.
+  const int chunks = max(1, max(min(s.n_groups, s.n_members / 2), (int)((int64_t)s.n_members * R / 128)));
+  const int partials = s.tail_ctas / items + 2 + s.head_ctas / (chunks * s.tail.K) + 2;
+  const int shares = partials <= 8 ? 1 : partials <= 16 ? 2 : 16;
+  int per = shares == 16 ? 32 : 256 / shares;
+  while (per > 32 && per / 2 >= elements) per /= 2;
+  const dim3 grid(items, (elements + per - 1) / per);
+  switch (shares) {
+    case 1: return launch_early(paged_shared_join_kernel<H, TC, 4, 256>, grid, per, 0, st, s, per);
+    case 2: return launch_early(paged_shared_join_kernel<H, TC, 8, 256>, grid, 2 * per, 0, st, s, per);
+    default: return launch_early(paged_shared_join_kernel<H, TC, 8, 512>, grid, 16 * per, 0, st, s, per);
+  }
+}
+
+template <int H, class C, void (*TAIL)(const PagedDecodeArgs)>
+cudaError_t launch_shared_grids(const PagedSharedArgs& s, const PagedDecodeArgs& head, cudaStream_t st,
+                                cudaError_t (*launch_head)(const PagedDecodeArgs&, int, cudaStream_t)) {
+  cudaError_t e = launch_paged_shared_setup(s, st);
+  if (e != cudaSuccess) return e;
+  e = launch_head(head, s.head_ctas, st);
+  if (e != cudaSuccess) return e;
+  e = launch_shared_part<C, TAIL>(s.tail, s.tail_ctas, st);
+  if (e != cudaSuccess) return e;
+  return launch_shared_join<H, C::TC>(s, st);
+}
+
+// The kernel for a request's own keys goes by its rows, as in launch_decode_rows.
+template <int H, bool E4M3>
+cudaError_t launch_shared(const PagedSharedArgs& s, cudaStream_t st) {
+  const int R = s.tail.G * s.tail.T;
+  PagedDecodeArgs head = s.tail;
+  head.splits = s.head_splits;
+  head.partials = s.head_partials;
+  head.shared.whole = s.head_whole;
+  using Head = DecodeTcCfg<H, E4M3, DECODE_HEAD>;
+  auto* const launch_head = launch_shared_part<Head, paged_decode_tc_kernel<Head>>;
+  if (R <= 8) {
+    using C = DecodeCfg<H, E4M3, 1, 1, DECODE_TAIL>;
+    return launch_shared_grids<H, C, paged_decode_kernel<C>>(s, head, st, launch_head);
+  }
+  if (R <= 16) {
+    using C = DecodeCfg<H, E4M3, 2, 1, DECODE_TAIL>;
+    return launch_shared_grids<H, C, paged_decode_kernel<C>>(s, head, st, launch_head);
+  }
+  if constexpr (H <= 128 || E4M3) {
+    constexpr int NT = H == 256 ? 2 : 4;
+    using C = DecodeCfg<H, E4M3, NT, 4 / NT, DECODE_TAIL>;
+    if (R <= 32) return launch_shared_grids<H, C, paged_decode_kernel<C>>(s, head, st, launch_head);
+  }
+  using C = DecodeTcCfg<H, E4M3, DECODE_TAIL>;
+  return launch_shared_grids<H, C, paged_decode_tc_kernel<C>>(s, head, st, launch_head);
+}
+
+}  // namespace fa

@@ -328,6 +328,37 @@ int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int
    unsupported sizes). */
 size_t fa_paged_decode_workspace_size(int B, int K, int G, int T, int H);
 
+/*
+ * fa_paged_decode for requests of which some share a prefix, whose keys and
+ * values are read once for all of a group.  Group g is the requests
+ * members[group_starts[g] .. group_starts[g + 1]), whose first prefix_lens[g]
+ * tokens are the same ones: in the same pages, as fa_paged_fork leaves them,
+ * or in equal ones; only one member's are read.  group_starts: int32
+ * [n_groups + 1], members [n_members], prefix_lens [n_groups], in device memory;
+ * n_groups <= 8192, n_members <= B.  Requests that no group names have no prefix.
+ * Results are those of fa_paged_decode without a window, to rounding; lengths
+ * and page ids out of range are dealt with as there.
+ * A group's prefix ends at the latest where all queries of all its members see it:
+ * after lens[b] - T + 1 tokens; a longer or negative one is cut to that, a member
+ * outside [0, B) left out, a request named again left to the first that names it,
+ * and where group_starts falls or leaves [0, n_members] nothing is shared.  All
+ * of these set FA_ERR_DEVICE_VALUE; results stay right.
+ * `workspace`: as in fa_paged_decode, of fa_paged_decode_shared_workspace_size bytes.
+ */
+int fa_paged_decode_shared(const void* q, const void* k_cache, const void* v_cache, int cache_type,
+                           const float* k_scale, const float* v_scale, int64_t page_stride,
+                           int64_t head_stride, int64_t token_stride, const int32_t* block_table,
+                           const int32_t* lens, const int32_t* members, int n_members,
+                           const int32_t* group_starts, const int32_t* prefix_lens, int n_groups,
+                           void* o, float* lse, void* workspace, size_t workspace_bytes, int B,
+                           int K, int G, int T, int H, int n_pages, int page_size, int max_pages,
+                           void* stream);
+
+/* Workspace bytes of fa_paged_decode_shared on the current device (0 for empty or
+   unsupported sizes). */
+size_t fa_paged_decode_shared_workspace_size(int B, int K, int G, int T, int H, int n_groups,
+                                             int n_members);
+
 /* ------------------------------------------------------------------------
  * Rotary positions.  Of each head's H dims the first 2 * n_pairs are turned in
  * pairs, the others stay: pair i of a token at positions p[0 .. n_axes) by
@@ -479,6 +510,7 @@ int fa_paged_copy(const int32_t* moves, int N, void* k_cache, void* v_cache, int
 int fa_paged_tables_packed(const int64_t* args);   /* 17 */
 int fa_paged_append_packed(const int64_t* args);   /* 21 */
 int fa_paged_decode_packed(const int64_t* args);   /* 25 */
+int fa_paged_decode_shared_packed(const int64_t* args);   /* 29 */
 int fa_rotary_packed(const int64_t* args);   /* 33 */
 int fa_paged_rotary_append_packed(const int64_t* args);   /* 39 */
 int fa_paged_free_packed(const int64_t* args);   /* 16 */
