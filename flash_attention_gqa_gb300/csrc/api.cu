@@ -13,6 +13,7 @@
 
 #include "../../include/fa.h"
 #include "kernels.h"
+#include "paged.h"
 #include "ptx.cuh"
 
 namespace fa {
@@ -58,6 +59,9 @@ uint64_t wait_limit() {
   return v;
 }
 
+}  // namespace
+
+namespace fa {
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -71,6 +75,30 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   });
   return fn;
 }
+
+bool make_cache_map(CUtensorMap* m, const void* cache, const PagedLayout& lay, int K, int H, bool e4m3, int rows) {
+  auto enc = encode_fn();
+  const int es = e4m3 ? 1 : 2, page = 1 << lay.page_shift;
+  // (of a dimension of one the layout has no stride, and none is used)
+  const cuuint64_t any = (cuuint64_t)H * es;
+  if (!enc || lay.n_pages < 1 || (page > 1 && lay.token == 0) || (K > 1 && lay.head == 0) ||
+      (lay.n_pages > 1 && lay.page == 0))
+    return false;
+  cuuint64_t dims[4] = {(cuuint64_t)H, (cuuint64_t)page, (cuuint64_t)K, (cuuint64_t)lay.n_pages};
+  cuuint64_t strides[3] = {page > 1 ? (cuuint64_t)lay.token : any, K > 1 ? (cuuint64_t)lay.head : any,
+                           lay.n_pages > 1 ? (cuuint64_t)lay.page : any};
+  cuuint32_t box[4] = {e4m3 ? (cuuint32_t)H : 64u, (cuuint32_t)rows, 1, 1};
+  cuuint32_t one[4] = {1, 1, 1, 1};
+  return enc(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(cache),
+             dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace fa
+
+namespace {
+using fa::encode_fn;
+
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool pow2_le128(int g) { return g >= 1 && g <= 128 && (g & (g - 1)) == 0; }

@@ -1,6 +1,7 @@
 // Internal interface of the paged key-value cache operators (paged.cu).
 #pragma once
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 namespace fa {
@@ -116,6 +117,16 @@ inline PagedDecodePlan paged_decode_plan(int R, int H, int sm_count) {
 }
 
 // ---- attention of requests that share prefixes
+// The HEAD grid's: the decode's, with chunks as its requests, and maps of the caches with boxes of
+// `rows` tokens of a page (64 dims of bf16, whole rows of e4m3); none where rows is 0.
+struct PagedHeadArgs {
+  CUtensorMap k_map, v_map;
+  PagedDecodeArgs a;
+  int rows;
+};
+// A map of a cache, for boxes of `rows` tokens; false where its strides cannot be mapped.
+bool make_cache_map(CUtensorMap* m, const void* cache, const PagedLayout& lay, int K, int H, bool e4m3, int rows);
+
 struct PagedSharedArgs {
   PagedDecodeArgs tail;        // the requests' own keys: splits by item, partials
   PagedDecodeSplit* head_splits;   // [chunks * K]

@@ -104,8 +104,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
 
   const uint32_t q_u = smem_u32(sm), ring_u = q_u + C::QBYTES;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr bool HEAD = C::MODE == DECODE_HEAD;   // 128 rows an item, that all see all its keys
-  const int R0 = a.G * a.T, T = HEAD ? 1 : a.T;
+  const int R = a.G * a.T, P = paged_partial_rows(R);
   const DecodeShape<C> shape{a};
   const Abort ab{&sh_abort, a.wait_limit_ns, a.err};
   // Slots: K(n) takes turn n / KS of slot n % KS, V(n) the same behind them.
@@ -120,8 +119,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
   const uint32_t teardown = smem_u32(bars + 2 * S + 8);
   auto pair_met = [&](int w) { return smem_u32(bars + 2 * S + 9 + (w & 3)); };
 
-  // (HEAD: what comes after it reads tables of the grid before, too, and starts knowing them written)
-  if (HEAD) grid_before();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   DecodeWalk walk;
   if (!decode_units<C>(a, sh, walk)) {
@@ -286,7 +283,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
         in[h] = s & ((1 << a.lay.page_shift) - 1);
         page[h] = -1;
         if (live[h])
-          page[h] = __ldg(a.block_table + (int64_t)shape.table_row(walk) * a.max_pages + (s >> a.lay.page_shift));
+          page[h] = __ldg(a.block_table + (int64_t)walk.b * a.max_pages + (s >> a.lay.page_shift));
       }
     };
     look_up();
@@ -367,7 +364,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
     for (int i = max(0, n - D); E4M3 && ok && i < n; ++i) ok = hand_over(i);
   } else {
     // --------------------------------------------------------------- softmax
-    const int r = tid & 127, half = tid >> 7, t = r % T;
+    const int r = tid & 127, half = tid >> 7, t = r % a.T;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) * 32 << 16);
     constexpr int HD = H / 2;        // dims of o of a half
     const int d0 = half * HD;
@@ -384,26 +381,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
     constexpr int PARTS = 256 / TN, UPP = HC * 8 / PARTS;
     const int v_key = tid % TN, v_unit = tid / TN * UPP;
     auto v_place = [&](int u) { return (u >> 3) * C::CHUNK + (UPP == 4 ? (u & 4) | ((u + v_key) & 3) : (u + v_key) & 7) * 16; };
-    // Rows of the item whose queries were loaded last, and of the one before it.
-    int R = R0, R_next = R0;
     // This thread's half of its query row; rows past the last are zeros.
     auto load_q = [&](const DecodeWalk& w) {
-      int64_t row = ((int64_t)w.b * a.K + w.k) * R0 + r;
-      if (HEAD) {   // row `in` of member `member`'s
-        const int4 c = __ldcg(reinterpret_cast<const int4*>(a.shared.chunks + w.b));
-        R_next = __ldcg(&a.shared.chunks[w.b].rows);
-        const int at = c.w + r, m = at / R0;
-        const int member = r < R_next ? __ldcg(a.shared.members + c.z + m) : -1;
-        if (member < 0) row = -1;
-        else row = ((int64_t)member * a.K + w.k) * R0 + at - m * R0;
-      }
-      const bool some = HEAD ? row >= 0 : r < R0;
-      const char* const src = (const char*)a.q + (HEAD && row < 0 ? 0 : row) * (H * 2);
+      const char* const src = (const char*)a.q + (((int64_t)w.b * a.K + w.k) * R + r) * (H * 2);
 #pragma unroll
       for (int i = 0; i < HD / 8; ++i) {
         const int u = half * (HD / 8) + i;
         const uint32_t dst = q_u + (u >> 3) * C::QCHUNK + sw128_offset(r, u & 7);
-        if (some)
+        if (r < R)
           cp_async16(dst, src + u * 16);
         else
           cp_zeros16(dst, a.q);
@@ -455,14 +440,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
     while (ok) {
       const int64_t item = (int64_t)walk.b * a.K + walk.k;
       sl2 = sl2_next;
-      R = R_next;
       DecodeWalk then = walk;
       const bool go_on = shape.next_item(then, sh.ends[1]);
       constexpr bool TAIL = C::MODE == DECODE_TAIL;
-      const int hi = walk.len - T + t + 1;   // keys of this row
-      const int lo = TAIL ? walk.low : !HEAD && a.window > 0 ? hi - a.window : 0;
-      const int full_hi = walk.len - T + 1;                              // keys of every row
-      const int full_lo = TAIL ? walk.low : !HEAD && a.window > 0 ? max(0, walk.len - a.window) : 0;
+      const int hi = walk.len - a.T + t + 1, lo = TAIL ? walk.low : a.window > 0 ? hi - a.window : 0;   // keys of this row
+      const int full_hi = walk.len - a.T + 1;                              // keys of every row
+      const int full_lo = TAIL ? walk.low : a.window > 0 ? max(0, walk.len - a.window) : 0;
       float m = -INFINITY, l = 0.0f;   // base of the exponents (log2 units), sum of the weights
       for (; walk.tile < walk.end; ++walk.tile, ++n) {
         if (!(ok = tc_wait(s_full(n), (n >> 1) & 1, ab))) break;
@@ -522,7 +505,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
         l *= alpha;
 
         if (first && tid == 0) sh_keep = 0;
-        if (masked && T > 1) {
+        if (masked && a.T > 1) {
           // Values that are not finite, of keys that some row does not keep: 0 x inf
           // would reach it.  Their products are done here, row by row, and they are
           // zeros to the tensor cores.
@@ -650,14 +633,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
       const bool whole = walk.begun == 0 && walk.end == walk.tiles;
       const float f = l == 0.0f ? 0.0f : (a.v_scale ? __ldg(a.v_scale + walk.k) : 1.0f) / l;
       const bool finished = C::MODE == DECODE_ALL && whole;
-      int P = HEAD ? 128 : paged_partial_rows(R);   // rows of the partial
-      float* mine = a.partials + ((int64_t)blockIdx.x * 2 + (walk.begun == 0 ? 1 : 0)) *
-                                     paged_partial_floats(HEAD ? 128 : R, H);
-      if (TAIL && whole) mine = a.shared.whole + item * paged_partial_floats(R, H);
-      if (HEAD && whole) {
-        P = (R + 7) & ~7;
-        mine = a.shared.whole + ((int64_t)__ldcg(&a.shared.chunks[walk.b].base) * a.K + (int64_t)walk.k * P) * (H + 2);
-      }
+      float* const mine =   // (TAIL: a whole item's place is by the item)
+          TAIL && whole
+              ? a.shared.whole + item * paged_partial_floats(R, H)
+              : a.partials + ((int64_t)blockIdx.x * 2 + (walk.begun == 0 ? 1 : 0)) * paged_partial_floats(R, H);
 #pragma unroll 1
       for (int c = d0; c < d0 + HD; c += 32) {
         uint32_t ov[32];
@@ -706,7 +685,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_decode_tc_kernel(const __
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (C::MODE == DECODE_TAIL) grid_before();
+  if (C::MODE == DECODE_TAIL) grid_before();   // as in paged_decode.cuh
 }
 
 }  // namespace fa

@@ -4,14 +4,14 @@
 //   keys (TAIL); each leaves sums o, weights' sum l and base m, and the join adds them up:
 //   o = sum_p 2^(m_p - M) o_p / sum_p 2^(m_p - M) l_p.
 //
-// HEAD is the tcgen05 kernel of paged_decode_tc.cuh over chunks of 128 rows of a group in place of
-// requests, TAIL the decode kernels over keys from a request's first own one on; both leave partials
-// of whole items, too.  The four grids are launched early, one behind the other: TAIL's CTAs start as
+// HEAD is paged_shared_head.cuh, TAIL the decode kernels over keys from a request's first own one on; both
+// leave partials of whole items, too.  The four grids are launched early, one behind the other: TAIL's CTAs start as
 // HEAD's end.  HEAD waits for the tables before it lets TAIL start, TAIL ends only after HEAD has, and
 // the join waits for TAIL.
 #pragma once
 #include "paged_decode.cuh"
 #include "paged_decode_tc.cuh"
+#include "paged_shared_head.cuh"
 
 namespace fa {
 
@@ -137,8 +137,8 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, int smem,
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <class C, void (*KERNEL)(const PagedDecodeArgs)>
-cudaError_t launch_shared_part(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
+template <class C, class Args, void (*KERNEL)(const Args)>
+cudaError_t launch_shared_part(const Args& a, int grid, cudaStream_t st) {
   static bool ready[64] = {};   // per device; setting it twice is harmless
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -170,13 +170,13 @@ cudaError_t launch_shared_join(const PagedSharedArgs& s, cudaStream_t st) {
 }
 
 template <int H, class C, void (*TAIL)(const PagedDecodeArgs)>
-cudaError_t launch_shared_grids(const PagedSharedArgs& s, const PagedDecodeArgs& head, cudaStream_t st,
-                                cudaError_t (*launch_head)(const PagedDecodeArgs&, int, cudaStream_t)) {
+cudaError_t launch_shared_grids(const PagedSharedArgs& s, const PagedHeadArgs& head, cudaStream_t st,
+                                cudaError_t (*launch_head)(const PagedHeadArgs&, int, cudaStream_t)) {
   cudaError_t e = launch_paged_shared_setup(s, st);
   if (e != cudaSuccess) return e;
   e = launch_head(head, s.head_ctas, st);
   if (e != cudaSuccess) return e;
-  e = launch_shared_part<C, TAIL>(s.tail, s.tail_ctas, st);
+  e = launch_shared_part<C, PagedDecodeArgs, TAIL>(s.tail, s.tail_ctas, st);
   if (e != cudaSuccess) return e;
   return launch_shared_join<H, C::TC>(s, st);
 }
@@ -185,12 +185,19 @@ cudaError_t launch_shared_grids(const PagedSharedArgs& s, const PagedDecodeArgs&
 template <int H, bool E4M3>
 cudaError_t launch_shared(const PagedSharedArgs& s, cudaStream_t st) {
   const int R = s.tail.G * s.tail.T;
-  PagedDecodeArgs head = s.tail;
-  head.splits = s.head_splits;
-  head.partials = s.head_partials;
-  head.shared.whole = s.head_whole;
-  using Head = DecodeTcCfg<H, E4M3, DECODE_HEAD>;
-  auto* const launch_head = launch_shared_part<Head, paged_decode_tc_kernel<Head>>;
+  using Head = HeadCfg<H, E4M3>;
+  PagedHeadArgs head;
+  head.a = s.tail;
+  head.a.splits = s.head_splits;
+  head.a.partials = s.head_partials;
+  head.a.shared.whole = s.head_whole;
+  // (boxes of less than 8 rows: more of them than lanes, and not on the swizzle's boundaries)
+  const int page = 1 << s.tail.lay.page_shift;
+  head.rows = page < 8 ? 0 : page < Head::KPW ? page : Head::KPW;
+  if (head.rows && !(make_cache_map(&head.k_map, s.tail.k_cache, s.tail.lay, s.tail.K, H, E4M3, head.rows) &&
+                     make_cache_map(&head.v_map, s.tail.v_cache, s.tail.lay, s.tail.K, H, E4M3, head.rows)))
+    head.rows = 0;
+  auto* const launch_head = launch_shared_part<Head, PagedHeadArgs, paged_head_kernel<Head>>;
   if (R <= 8) {
     using C = DecodeCfg<H, E4M3, 1, 1, DECODE_TAIL>;
     return launch_shared_grids<H, C, paged_decode_kernel<C>>(s, head, st, launch_head);
