@@ -7,6 +7,7 @@
 namespace fa {
 
 constexpr int kMaxPagedBatch = 8192;       // requests of one call: their offsets stay in shared memory
+constexpr int kMaxPagedGroups = 4096;      // groups that share a prefix, of one call
 constexpr int kMaxPageSize = 65536;        // tokens per page, a power of two
 constexpr int kMaxPagedLen = 1 << 30;      // keys of one request (max_pages * page_size)
 constexpr int kMaxPagedRows = 128;         // query rows per kv head, G * T

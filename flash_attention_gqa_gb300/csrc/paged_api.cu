@@ -3,6 +3,7 @@
 // allocates device memory or synchronises.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "../../include/fa.h"
@@ -13,6 +14,9 @@
 using namespace fa;
 
 namespace {
+
+// Bytes of keys and values up to which a call with shared prefixes does not make use of them.
+constexpr double kSharedLeast = 24e6;
 
 bool decode_shape_ok(int B, int K, int G, int T, int H) {
   return head_dim_ok(H) && (int64_t)G * T <= kMaxPagedRows && B <= kMaxPagedBatch &&
@@ -152,8 +156,9 @@ int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int
 
 size_t fa_paged_decode_shared_workspace_size(int B, int K, int G, int T, int H, int n_groups, int n_members) {
   if (B <= 0 || K <= 0 || G <= 0 || T <= 0 || !decode_shape_ok(B, K, G, T, H)) return 0;
-  if (n_groups < 0 || n_members < 0 || n_groups > kMaxPagedBatch || n_members > B) return 0;
-  return paged_shared_plan(B, K, G * T, H, n_groups, n_members, fa_device_sm_count()).total;
+  if (n_groups < 0 || n_members < 0 || n_groups > kMaxPagedGroups || n_members > B) return 0;
+  const size_t shared = paged_shared_plan(B, K, G * T, H, n_groups, n_members, fa_device_sm_count()).total;
+  return std::max(shared, fa_paged_decode_workspace_size(B, K, G, T, H));   // (small calls are decodes)
 }
 
 int fa_paged_decode_shared(const void* q, const void* k_cache, const void* v_cache, int cache_type,
@@ -169,7 +174,7 @@ int fa_paged_decode_shared(const void* q, const void* k_cache, const void* v_cac
   PagedDecodeArgs& a = s.tail;
   const int rc = make_layout(&a.lay, cache_type, page_stride, head_stride, token_stride, K, n_pages, page_size);
   if (rc != FA_OK) return rc;
-  if (!decode_shape_ok(B, K, G, T, H) || (int64_t)max_pages * page_size > kMaxPagedLen || n_groups > kMaxPagedBatch)
+  if (!decode_shape_ok(B, K, G, T, H) || (int64_t)max_pages * page_size > kMaxPagedLen || n_groups > kMaxPagedGroups)
     return FA_ERR_UNSUPPORTED;
   if (n_members > B) return FA_ERR_INVALID_ARG;
   if (!aligned(k_scale, 4) || !aligned(v_scale, 4)) return FA_ERR_INVALID_ARG;
@@ -181,7 +186,16 @@ int fa_paged_decode_shared(const void* q, const void* k_cache, const void* v_cac
   if (n_members > 0 && !usable(members, 4)) return FA_ERR_INVALID_ARG;
   if (!usable(group_starts, 4) || (n_groups > 0 && !usable(prefix_lens, 4))) return FA_ERR_INVALID_ARG;
   const PagedSharedPlan plan = paged_shared_plan(B, K, G * T, H, n_groups, n_members, fa_device_sm_count());
-  if (!usable(workspace, 256) || workspace_bytes < plan.total) return FA_ERR_INVALID_ARG;
+  if (!usable(workspace, 256) || workspace_bytes < std::max(plan.total, paged_decode_plan(G * T, H, fa_device_sm_count()).total))
+    return FA_ERR_INVALID_ARG;
+  // The prefixes' grid and what it takes to bring its results together cost some 8 us.  Where all keys, as
+  // far as the tables reach, are read faster than that even once for each request, they are.  (4 requests x 2
+  // kv heads x 552 keys at H = 256: 17.6 us and 10; see kSharedLeast.)
+  const double keys = (double)n_members * max_pages * page_size * K * H * (cache_type == FA_CACHE_BF16 ? 4 : 2);
+  if (n_groups == 0 || keys <= kSharedLeast)
+    return fa_paged_decode(q, k_cache, v_cache, cache_type, k_scale, v_scale, page_stride, head_stride,
+                           token_stride, block_table, lens, 0, o, lse, workspace, workspace_bytes, B, K, G, T, H,
+                           n_pages, page_size, max_pages, stream);
   char* const ws = static_cast<char*>(workspace);
   a.q = q; a.k_cache = k_cache; a.v_cache = v_cache;
   a.k_scale = k_scale; a.v_scale = v_scale;

@@ -29,10 +29,11 @@ __device__ __forceinline__ int entry_of(const int* list, int n, int x) {
 
 __global__ void __launch_bounds__(kThreads, 1) paged_shared_setup_kernel(const __grid_constant__ PagedSharedArgs a) {
   extern __shared__ int sm[];
-  const int n = a.n_groups, B = a.tail.B, T = a.tail.T, R = a.tail.G * T, tid = threadIdx.x;
+  const int n = a.n_groups, N = a.n_members, B = a.tail.B, T = a.tail.T, R = a.tail.G * T, tid = threadIdx.x;
   int* const starts = sm;              // [n + 1]
-  int* const least = starts + n + 1;   // [n] longest prefix that all members' queries see; then the prefix
-  int* const lead = least + n;         // [n] lowest entry with a request
+  int* const prefix = starts + n + 1;  // [n] the caller's, then what is shared
+  int* const least = prefix + n;       // [n] longest prefix that all members' queries see
+  int* const lead = least + n;         // [n] lowest entry with a request, then that request
   int* const live = lead + n;          // [n] entries with one
   int* const first = live + n;         // [n + 1] chunks before the group
   int* const base = first + n + 1;     // [n] padded rows before it
@@ -41,34 +42,44 @@ __global__ void __launch_bounds__(kThreads, 1) paged_shared_setup_kernel(const _
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const PagedSharedTables& out = a.tail.shared;
   const int most = a.tail.max_pages << a.tail.lay.page_shift;
-
+  // Two trips to memory, where the members are no more than the threads: members and groups, lengths.
+  int member = -1, len = 0;   // of entry tid
+  if (tid < N) member = a.members[tid];
+  int lo = a.group_starts[0], hi = a.group_starts[n];
   for (int g = tid; g <= n; g += kThreads) starts[g] = a.group_starts[g];
   for (int g = tid; g < n; g += kThreads) {
+    prefix[g] = a.prefix_lens[g];
     least[g] = lead[g] = INT_MAX;
     live[g] = 0;
   }
-  for (int b = tid; b < B; b += kThreads) {
-    claim[b] = INT_MAX;
-    out.begins[b] = 0;
-    out.places[b] = -1;
-  }
+  for (int b = tid; b < B; b += kThreads) claim[b] = INT_MAX;
+  if ((unsigned)member < (unsigned)B) len = a.tail.lens[member];
+  auto member_of = [&](int i) { return i == tid ? member : a.members[i]; };
+  auto length_of = [&](int i, int r) { return min(max(i == tid ? len : a.tail.lens[r], 0), most); };
   __syncthreads();
   bool bad = false;
-  for (int g = tid; g < n; g += kThreads) bad |= starts[g] < 0 || starts[g + 1] < starts[g] || starts[g + 1] > a.n_members;
+  for (int g = tid; g < n; g += kThreads) bad |= starts[g] < 0 || starts[g + 1] < starts[g] || starts[g + 1] > N;
   const bool none = __syncthreads_or(bad) || n == 0;   // no groups to go by
-  const int lo = none ? 0 : starts[0], hi = none ? 0 : starts[n];
-  for (int i = lo + tid; i < hi; i += kThreads) {
-    const int r = a.members[i];
+  if (none) lo = hi = 0;
+  for (int i = tid; i < hi; i += kThreads) {
+    if (i < lo) continue;
+    const int r = member_of(i);
     if ((unsigned)r < (unsigned)B) atomicMin(&claim[r], i);
     else bad = true;
   }
   __syncthreads();
-  for (int i = lo + tid; i < hi; i += kThreads) {
-    const int r = a.members[i];
-    if ((unsigned)r >= (unsigned)B) continue;
-    if (claim[r] != i) { bad = true; continue; }   // named twice
-    const int g = entry_of(starts, n, i), len = min(max(a.tail.lens[r], 0), most);
-    atomicMin(&least[g], max(0, len - T + 1));
+  // the entry's request, -1: none, or named before
+  auto request_of = [&](int i) {
+    if (i < lo || i >= hi) return -1;
+    const int r = member_of(i);
+    return (unsigned)r < (unsigned)B && claim[r] == i ? r : -1;
+  };
+  for (int i = tid; i < hi; i += kThreads) {
+    if (i < lo) continue;
+    const int r = request_of(i);
+    if (r < 0) { bad = true; continue; }
+    const int g = entry_of(starts, n, i);
+    atomicMin(&least[g], max(0, length_of(i, r) - T + 1));
     atomicMin(&lead[g], i);
     atomicAdd(&live[g], 1);
   }
@@ -76,18 +87,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_shared_setup_kernel(const _
 
   // chunks and padded rows of the groups before each
   const int per = (n + kThreads - 1) / kThreads, g0 = min(tid * per, n), g1 = min(g0 + per, n);
-  auto chunks_of = [&](int g) { return live[g] > 1 && least[g] > 0 ? ((starts[g + 1] - starts[g]) * R + 127) >> 7 : 0; };
-  auto padded_of = [&](int g) { return chunks_of(g) ? ((starts[g + 1] - starts[g]) * R + 7) & ~7 : 0; };
+  auto rows_of = [&](int g) { return live[g] > 1 && prefix[g] > 0 ? (starts[g + 1] - starts[g]) * R : 0; };
   int chunks = 0, padded = 0;
   if (!none)
     for (int g = g0; g < g1; ++g) {
-      const int want = a.prefix_lens[g];
+      const int want = prefix[g];
       if (live[g] > 0) {
         bad |= want < 0 || want > least[g];
-        least[g] = min(max(want, 0), least[g]);
+        prefix[g] = min(max(want, 0), least[g]);
+        lead[g] = a.members[lead[g]];
       }
-      chunks += chunks_of(g);
-      padded += padded_of(g);
+      chunks += (rows_of(g) + 127) >> 7;
+      padded += (rows_of(g) + 7) & ~7;
     }
   const int lane = tid & 31, warp = tid >> 5;
   int ic = chunks, ip = padded;
@@ -99,6 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_shared_setup_kernel(const _
   if (lane == 31) { sums[0][warp] = ic; sums[1][warp] = ip; }
   __syncthreads();
   int before = ic - chunks, base_at = ip - padded, all = 0;
+#pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) { before += sums[0][w]; base_at += sums[1][w]; }
     all += sums[0][w];
@@ -107,33 +119,33 @@ __global__ void __launch_bounds__(kThreads, 1) paged_shared_setup_kernel(const _
     for (int g = g0; g < g1; ++g) {
       first[g] = before;
       base[g] = base_at;
-      before += chunks_of(g);
-      base_at += padded_of(g);
+      before += (rows_of(g) + 127) >> 7;
+      base_at += (rows_of(g) + 7) & ~7;
     }
   if (tid == 0) {
     first[n] = all;
     *out.n_chunks = all;
   }
   __syncthreads();
-  for (int i = tid; i < a.n_members; i += kThreads) {
-    int r = -1;
-    if (i >= lo && i < hi) {
-      r = a.members[i];
-      if ((unsigned)r >= (unsigned)B || claim[r] != i) r = -1;
-    }
+  for (int i = tid; i < N; i += kThreads) {
+    const int r = request_of(i);
     out.members[i] = r;
     if (r < 0) continue;
     const int g = entry_of(starts, n, i);
-    if (chunks_of(g) == 0) continue;
-    out.begins[r] = least[g];
-    out.places[r] = first[g] * 128 + (i - starts[g]) * R;
+    const bool shares = rows_of(g) > 0;
+    out.begins[r] = shares ? prefix[g] : 0;
+    out.places[r] = shares ? first[g] * 128 + (i - starts[g]) * R : -1;
   }
+  for (int b = tid; b < B; b += kThreads)
+    if (claim[b] == INT_MAX) {
+      out.begins[b] = 0;
+      out.places[b] = -1;
+    }
   for (int c = tid; c < all; c += kThreads) {
-    int g = entry_of(first, n, c);
-    const int row = (c - first[g]) * 128, rows = min(128, (starts[g + 1] - starts[g]) * R - row);
+    const int g = entry_of(first, n, c), row = (c - first[g]) * 128;
     int4* const at = reinterpret_cast<int4*>(out.chunks + c);
-    at[0] = make_int4(least[g], a.members[lead[g]], starts[g], row);
-    at[1] = make_int4(rows, base[g] + row, 0, 0);
+    at[0] = make_int4(prefix[g], lead[g], starts[g], row);
+    at[1] = make_int4(min(128, rows_of(g) - row), base[g] + row, 0, 0);
   }
   if (bad) atomicOr(a.tail.err, (uint32_t)DEV_BAD_VALUE);
 }
@@ -141,10 +153,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_shared_setup_kernel(const _
 }  // namespace
 
 cudaError_t launch_paged_shared_setup(const PagedSharedArgs& a, cudaStream_t st) {
-  const size_t smem = ((size_t)6 * a.n_groups + 2 + a.tail.B) * sizeof(int);
+  const size_t smem = ((size_t)7 * a.n_groups + 2 + a.tail.B) * sizeof(int);
   // (always to what the largest call needs, as for the tables)
   if (smem > 47 * 1024) {
-    constexpr int most = (7 * kMaxPagedBatch + 2) * sizeof(int);
+    constexpr int most = (7 * kMaxPagedGroups + 2 + kMaxPagedBatch) * sizeof(int);
     const cudaError_t e =
         cudaFuncSetAttribute(paged_shared_setup_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;

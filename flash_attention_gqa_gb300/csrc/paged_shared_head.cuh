@@ -28,57 +28,129 @@ struct HeadCfg : DecodeTcCfg<H_, E4M3_, DECODE_HEAD> {
   static constexpr int NS = 3;   // S buffers
   static constexpr uint32_t O_COL = H_ == 256 ? 256 : 384;
   static_assert(NS * TN <= (int)O_COL && O_COL + H_ <= 512, "");
-  // Copying warps: one each for K and V; 8-bit caches, which they also convert: two each.
-  static constexpr int PER_TILE = E4M3_ ? 2 : 1, KPW = TN / PER_TILE;   // keys of a tile a warp
-  static constexpr int WARPS = 10 + 2 * PER_TILE, THREADS = WARPS * 32;
+  // Copying warps: one each for K and V; 8-bit caches: two each that make f16 of the bytes, and one for
+  // the bytes of both.
+  static constexpr int CONVERT = E4M3_ ? 4 : 0, KPW = TN / 2;   // keys of a tile a converting warp
+  static constexpr int WARPS = E4M3_ ? 15 : 12, THREADS = WARPS * 32;
   // Slots: scores are computed ahead of the weights, so K needs more of them.
   static constexpr int VS = STAGES / 2, KS = STAGES - VS;
   __device__ static __forceinline__ int slot_of(int n, int kv) { return kv ? KS + n % VS : n % KS; }
   __device__ static __forceinline__ int turn_of(int n, int kv) { return kv ? n / VS : n / KS; }
-  static constexpr int RAW_STAGES = Base::RAW_STAGES, RAW_BARS = E4M3_ ? 4 * RAW_STAGES : 0;
+  static constexpr int RAW_STAGES = Base::RAW_STAGES, RAW_BARS = E4M3_ ? 4 * RAW_STAGES : 0;   // full, empty, of K and V
 };
 
-// A copying warp's work: rows [w * KPW, (w + 1) * KPW) of every tile of K or of V (`kind`), into the slots
-// as they become free; the barriers of slot s are at full0 + 8 s and empty0 + 8 s.  By TMA, a lane a box of
-// one page's rows, in one instruction: cp.async by 16 bytes a lane keeps the load and store pipe busy for
-// 2600 cycles a tile, more than all the rest of it takes.  Rows past the prefix have to be zeros, which a box
-// can give for whole pages only (out of the map's range): a tile that ends inside a page goes by cp.async, as
-// does everything where there is no map.  8-bit rows land beside the slots (raw0: their barriers) and become
-// f16 on their way.
-template <class C>
+// a * b + c and a + b of two floats at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// A copying warp's work: every tile of K or of V (`kind`; 8-bit caches: first the one, then the other), into
+// its place at ring_u as that becomes free.  By TMA, a lane a box of one page's rows, in one instruction:
+// cp.async by 16 bytes a lane keeps the load and store pipe busy for 2600 cycles a tile, more than all the
+// rest of it takes.  Rows past the prefix have to be zeros, which a box can give for whole pages only (out
+// of the map's range): a tile that ends inside a page goes by cp.async, as does everything where there is
+// no map.  `place(n, kind)` waits until tile n's is free and gives its address and barrier (0: a wait ran out).
+template <class C, class Place, class Landed>
 __device__ __forceinline__ void head_copies(const PagedHeadArgs& s, const DecodeShape<C>& shape, DecodeWalk walk,
-                                            const DecodeEnd& last, uint32_t ring_u, uint32_t full0, uint32_t empty0,
-                                            uint32_t raw0, int w, int kind, const Abort& ab) {
-  constexpr int TN = C::TN, HC = C::HC, KPW = C::KPW, UPR = C::UPR, RS = C::RAW_STAGES;
+                                            const DecodeEnd& last, int kind0, int kinds, const Abort& ab, Place place,
+                                            Landed landed) {
+  constexpr int TN = C::TN, UPR = C::UPR;
   constexpr bool E4M3 = C::E4M3;
-  constexpr int CHUNKS = E4M3 ? 1 : HC;   // boxes of a page's rows
+  constexpr int CHUNKS = E4M3 ? 1 : C::HC;   // boxes of a page's rows
   const PagedDecodeArgs& a = s.a;
   const int lane = threadIdx.x & 31;
-  const CUtensorMap* const map = kind ? &s.v_map : &s.k_map;
-  const char* const base = (const char*)(kind ? a.v_cache : a.k_cache);
   const int shift = a.lay.page_shift, rows = s.rows;
-  const int boxes = rows ? KPW / rows * CHUNKS : 0;   // (<= 32: pages of 8 tokens at least)
+  const int boxes = rows ? TN / rows * CHUNKS : 0;   // (<= 32: pages of 8 tokens at least)
   const int box_row = rows ? lane / CHUNKS * rows : 0, box_chunk = lane % CHUNKS;
-  const uint32_t raw_u = ring_u + C::RING + (kind * RS * 2 + w) * (C::RAW / 2);
-  auto raw_full = [&](int n) { return raw0 + 8 * ((kind * 2 + w) * RS + n % RS); };
-  // A row past the prefix or without a page: -1.
-  auto page_of = [&](int row0, int row, int len, int table_row) -> int {
-    const int key = row0 + row;
+  // A row past the prefix: -1.
+  auto page_of = [&](int key, int len, int table_row) -> int {
     return key < len ? __ldg(a.block_table + (int64_t)table_row * a.max_pages + (key >> shift)) : -1;
   };
   auto known = [&](int page) { return page >= 0 && page < a.lay.n_pages; };
-  // 8-bit rows of tile n have landed: to f16 (exact).
-  auto hand_over = [&](int n) -> bool {
-    if (!tc_wait(raw_full(n), n / RS & 1, ab)) return false;
-    if (C::turn_of(n, kind) != 0 &&
-        !tc_wait(empty0 + 8 * C::slot_of(n, kind), (C::turn_of(n, kind) - 1) & 1, ab))
-      return false;
-    const int slot = C::slot_of(n, kind), u = lane % UPR, lr = lane / UPR;
-    const uint32_t odd = (u >> 2 & 1) << 4;   // four lanes write the odd unit first: other banks
-    constexpr int RPJ = 32 / UPR, NJ = KPW / RPJ;
-    const uint32_t from = raw_u + n % RS * C::RAW + lane * 16;
-    const uint32_t to = ring_u + slot * C::SLOT + (2 * u >> 3) * C::CHUNK + (w * KPW + lr) * 128;
-#pragma unroll
+  bool more = true, ok = true;
+  int n = 0;
+  // the page of this lane's box in the next tile, looked up a tile early
+  int page = page_of(walk.tile * TN + box_row, walk.len, shape.table_row(walk));
+  for (; more && ok; ++n) {
+    const int row0 = walk.tile * TN, len = walk.len, head = walk.k, table_row = shape.table_row(walk);
+    const int left = len - row0, mine = page;
+    if (++walk.tile == walk.end) more = shape.next_item(walk, last);
+    if (more) page = page_of(walk.tile * TN + box_row, walk.len, shape.table_row(walk));
+#pragma unroll 1
+    for (int kind = kind0; kind < kind0 + kinds; ++kind) {
+      uint32_t dst, bar;
+      if (!(ok = place(n, kind, dst, bar))) break;
+      if (rows && (left >= TN || (left & ((1 << shift) - 1)) == 0)) {
+        if (lane == 0) mbar_arrive_expect_tx(bar, TN * CHUNKS * (E4M3 ? C::H : 128));
+        __syncwarp();
+        if (lane < boxes) {
+          const bool key = box_row < left;
+          if (key && !known(mine)) atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+          tma_load_4d(dst + (E4M3 ? box_row * C::H : box_chunk * C::CHUNK + box_row * 128),
+                      kind ? &s.v_map : &s.k_map, bar, E4M3 ? 0 : box_chunk * 64,
+                      (row0 + box_row) & ((1 << shift) - 1), head, key && known(mine) ? mine : a.lay.n_pages);
+        }
+        if (lane != 0) mbar_arrive(bar);
+      } else {
+        const char* const base = (const char*)(kind ? a.v_cache : a.k_cache);
+#pragma unroll 1
+        for (int r0 = 0; r0 < TN; r0 += 32) {   // a lane a row's page, then all lanes 16-byte units
+          const int key = row0 + r0 + lane, at_page = page_of(key, len, table_row);
+          int64_t off = -1;
+          if (known(at_page))
+            off = at_page * a.lay.page + head * a.lay.head + (key & ((1 << shift) - 1)) * a.lay.token;
+          else if (key < len)
+            atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+#pragma unroll 1
+          for (int i = lane; i < 32 * UPR; i += 32) {
+            const int row = i / UPR, u = i % UPR;
+            const int64_t at = __shfl_sync(~0u, off, row);
+            const uint32_t to =
+                dst + (E4M3 ? (r0 + row) * C::H + u * 16 : (u >> 3) * C::CHUNK + sw128_offset(r0 + row, u & 7));
+            if (at >= 0)
+              cp_async16(to, base + at + u * 16);
+            else
+              cp_zeros16(to, a.q);
+          }
+        }
+        cp_async_arrive(bar);
+      }
+    }
+  }
+  // Where a wait has run out, here or elsewhere, what is in flight lands before the CTA ends.
+  cp_async_wait<0>();
+  if (!ok || *ab.flag) landed(n);
+}
+
+// A converting warp's work, 8-bit caches: rows [w * KPW, (w + 1) * KPW) of every tile of K or of V from bytes
+// to f16 (exact), from raw_u into the slots.
+template <class C, class Full, class Empty, class RawFull, class RawEmpty>
+__device__ __forceinline__ void head_converts(const DecodeShape<C>& shape, DecodeWalk walk, const DecodeEnd& last,
+                                              uint32_t ring_u, uint32_t raw_u, int w, int kind, const Abort& ab,
+                                              Full full, Empty empty, RawFull raw_full, RawEmpty raw_empty) {
+  constexpr int UPR = C::UPR, RPJ = 32 / UPR, NJ = C::KPW / RPJ, RS = C::RAW_STAGES;
+  const int lane = threadIdx.x & 31, u = lane % UPR, lr = lane / UPR;
+  const uint32_t odd = (u >> 2 & 1) << 4;   // four lanes write the odd unit first: other banks
+  bool more = true;
+  for (int n = 0; more; ++n) {
+    if (++walk.tile == walk.end) more = shape.next_item(walk, last);
+    const int slot = C::slot_of(n, kind);
+    if (!tc_wait(raw_full(n, kind), n / RS & 1, ab)) return;
+    if (C::turn_of(n, kind) != 0 && !tc_wait(empty(slot), (C::turn_of(n, kind) - 1) & 1, ab)) return;
+    const uint32_t from = raw_u + (kind * RS + n % RS) * C::RAW + w * (C::RAW / 2) + lane * 16;
+    const uint32_t to = ring_u + slot * C::SLOT + (2 * u >> 3) * C::CHUNK + (w * C::KPW + lr) * 128;
+#pragma unroll 1
     for (int j0 = 0; j0 < NJ; j0 += 8) {   // eight reads in flight
       uint4 x[8];
 #pragma unroll
@@ -97,73 +169,9 @@ __device__ __forceinline__ void head_copies(const PagedHeadArgs& s, const Decode
       }
     }
     fence_proxy_async_smem();
-    mbar_arrive(full0 + 8 * slot);
-    return true;
-  };
-  bool more = true, ok = true;
-  int n = 0;
-  // the page of this lane's box in the next tile, looked up a tile early
-  int page = page_of(walk.tile * TN + w * KPW, box_row, walk.len, shape.table_row(walk));
-  for (; more && ok; ++n) {
-    const int row0 = walk.tile * TN + w * KPW, len = walk.len, head = walk.k, table_row = shape.table_row(walk);
-    const int left = len - row0, mine = page;
-    if (++walk.tile == walk.end) more = shape.next_item(walk, last);
-    if (more) page = page_of(walk.tile * TN + w * KPW, box_row, walk.len, shape.table_row(walk));
-    uint32_t bar, dst;
-    if (E4M3) {
-      bar = raw_full(n);
-      dst = raw_u + n % RS * C::RAW;
-    } else {
-      const int slot = C::slot_of(n, kind);
-      if (C::turn_of(n, kind) != 0 && !(ok = tc_wait(empty0 + 8 * slot, (C::turn_of(n, kind) - 1) & 1, ab))) break;
-      bar = full0 + 8 * slot;
-      dst = ring_u + slot * C::SLOT;
-    }
-    if (rows && (left >= KPW || left <= 0 || (left & ((1 << shift) - 1)) == 0)) {
-      if (E4M3) fence_proxy_async_smem();   // the rows that were here have been read
-      if (lane == 0) mbar_arrive_expect_tx(bar, KPW * CHUNKS * (E4M3 ? C::H : 128));
-      __syncwarp();
-      if (lane < boxes) {
-        const bool key = box_row < left;
-        if (key && !known(mine)) atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
-        tma_load_4d(dst + (E4M3 ? box_row * C::H : box_chunk * C::CHUNK + box_row * 128), map, bar,
-                    E4M3 ? 0 : box_chunk * 64, (row0 + box_row) & ((1 << shift) - 1), head,
-                    key && known(mine) ? mine : a.lay.n_pages);
-      }
-      if (lane != 0) mbar_arrive(bar);
-    } else {
-#pragma unroll 1
-      for (int r0 = 0; r0 < KPW; r0 += 32) {   // a lane a row's page, then all lanes 16-byte units
-        const int at_page = page_of(row0, r0 + lane, len, table_row);
-        int64_t off = -1;
-        if (known(at_page))
-          off = at_page * a.lay.page + head * a.lay.head + ((row0 + r0 + lane) & ((1 << shift) - 1)) * a.lay.token;
-        else if (r0 + lane < left)
-          atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
-#pragma unroll 4
-        for (int i = lane; i < 32 * UPR; i += 32) {
-          const int row = i / UPR, u = i % UPR;
-          const int64_t at = __shfl_sync(~0u, off, row);
-          const uint32_t to = dst + (E4M3 ? (r0 + row) * C::H + u * 16 : (u >> 3) * C::CHUNK + sw128_offset(r0 + row, u & 7));
-          if (at >= 0)
-            cp_async16(to, base + at + u * 16);
-          else
-            cp_zeros16(to, a.q);
-        }
-      }
-      cp_async_arrive(bar);
-    }
-    if (E4M3 && n >= RS - 1 && !(ok = hand_over(n - RS + 1))) break;
+    mbar_arrive(full(slot));
+    mbar_arrive(raw_empty(n, kind));
   }
-  for (int i = max(0, n - RS + 1); E4M3 && ok && i < n; ++i) ok = hand_over(i);
-  // What is in flight lands, whichever wait may have run out.
-  const uint64_t limit = max(a.wait_limit_ns, (uint64_t)1000000000);
-  constexpr int IN_FLIGHT = E4M3 ? RS : C::KS > C::VS ? C::KS : C::VS;
-  cp_async_wait<0>();
-  if (!ok)
-    for (int i = max(0, n - IN_FLIGHT); i < n; ++i)
-      mbar_wait_teardown(E4M3 ? raw_full(i) : full0 + 8 * C::slot_of(i, kind),
-                         (E4M3 ? i / RS : C::turn_of(i, kind)) & 1, limit);
 }
 
 template <class C>
@@ -199,6 +207,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_head_kernel(const __grid_
   auto base_known = [&](int odd, int w) { return smem_u32(bars + 2 * S + 3 * NS + 3 + odd * 4 + (w & 3)); };
   auto pair_met = [&](int w) { return smem_u32(bars + 2 * S + 3 * NS + 11 + (w & 3)); };
 
+  auto raw_full = [&](int n, int kind) { return smem_u32(bars + 2 * S + 3 * NS + 15 + kind * C::RAW_STAGES + n % C::RAW_STAGES); };
+  auto raw_empty = [&](int n, int kind) { return raw_full(n, kind) + 16 * C::RAW_STAGES; };
+
   // The tables are written; what comes after this grid reads them, too, and starts knowing that.
   grid_before();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -207,7 +218,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_head_kernel(const __grid_
   if (tid == 0) {
     sh_abort = 0;
     for (int s = 0; s < S; ++s) {
-      mbar_init(full(s), C::PER_TILE * 32);
+      mbar_init(full(s), E4M3 ? 64 : 32);
       mbar_init(empty(s), 1);
     }
     for (int i = 0; i < NS; ++i) {
@@ -218,7 +229,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_head_kernel(const __grid_
     mbar_init(q_full, 256);
     mbar_init(o_free, 256);
     mbar_init(teardown, 2);
-    for (int i = 0; i < C::RAW_BARS; ++i) mbar_init(smem_u32(bars + 2 * S + 3 * NS + 15 + i), 32);
+    for (int i = 0; i < C::RAW_BARS / 4; ++i)
+      for (int kind = 0; kind < 2; ++kind) {
+        mbar_init(raw_full(i, kind), 32);
+        mbar_init(raw_empty(i, kind), 64);
+      }
     for (int w = 0; w < 4; ++w) {
       mbar_init(base_known(0, w), 32);
       mbar_init(base_known(1, w), 32);
@@ -309,8 +324,40 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_head_kernel(const __grid_
     __syncwarp();
   } else if (warp >= 8) {
     // ---------------------------------------------------------------- copies
-    head_copies<C>(args, shape, walk, sh.ends[1], ring_u, full(0), empty(0), smem_u32(bars + 2 * S + 3 * NS + 15),
-                   (warp - 8) % C::PER_TILE, (warp - 8) / C::PER_TILE, ab);
+    constexpr int RS = C::RAW_STAGES;
+    const uint64_t limit = max(a.wait_limit_ns, (uint64_t)1000000000);
+    if constexpr (E4M3) {
+      if (warp < 8 + C::CONVERT) {
+        head_converts<C>(shape, walk, sh.ends[1], ring_u, ring_u + C::RING, (warp - 8) & 1, (warp - 8) >> 1, ab, full,
+                         empty, raw_full, raw_empty);
+      } else {
+        head_copies<C>(
+            args, shape, walk, sh.ends[1], 0, 2, ab,
+            [&](int n, int kind, uint32_t& dst, uint32_t& bar) {
+              dst = ring_u + C::RING + (kind * RS + n % RS) * C::RAW;
+              bar = raw_full(n, kind);
+              return n < RS || tc_wait(raw_empty(n, kind), (n / RS - 1) & 1, ab);
+            },
+            [&](int n) {
+              for (int i = max(0, n - RS); i < n; ++i)
+                for (int kind = 0; kind < 2; ++kind) mbar_wait_teardown(raw_full(i, kind), i / RS & 1, limit);
+            });
+      }
+    } else {
+      const int mine = warp - 8;
+      head_copies<C>(
+          args, shape, walk, sh.ends[1], mine, 1, ab,
+          [&](int n, int kind, uint32_t& dst, uint32_t& bar) {
+            const int slot = C::slot_of(n, kind), turns = C::turn_of(n, kind);
+            dst = ring_u + slot * C::SLOT;
+            bar = full(slot);
+            return turns == 0 || tc_wait(empty(slot), (turns - 1) & 1, ab);
+          },
+          [&](int n) {
+            for (int i = max(0, n - (mine ? C::VS : C::KS)); i < n; ++i)
+              mbar_wait_teardown(full(C::slot_of(i, mine)), C::turn_of(i, mine) & 1, limit);
+          });
+    }
   } else {
     // --------------------------------------------------------------- softmax
     const int r = tid & 127, odd = tid >> 7;   // row; which tiles, and which half of queries and results
@@ -326,7 +373,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_head_kernel(const __grid_
       const int at = c.w + r, m = at / GT;
       const int member = r < rows_next ? __ldcg(a.shared.members + c.z + m) : -1;
       const char* const src = (const char*)a.q + (((int64_t)max(member, 0) * a.K + w.k) * GT + at - m * GT) * (H * 2);
-#pragma unroll
+#pragma unroll 4
       for (int i = 0; i < HD / 8; ++i) {
         const int u = odd * (HD / 8) + i;
         const uint32_t dst = q_u + (u >> 3) * C::QCHUNK + sw128_offset(r, u & 7);
@@ -382,6 +429,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_head_kernel(const __grid_
     for (int item = 0; ok; ++item) {
       sl2 = sl2_next;
       const int rows = rows_next;
+      const bool idle = (warp & 3) * 32 >= rows;
       DecodeWalk then = walk;
       const bool go_on = shape.next_item(then, sh.ends[1]);
       float m = -INFINITY, l = 0.0f;   // base of the exponents (log2 units), sum of these tiles' weights
@@ -392,6 +440,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_head_kernel(const __grid_
         // With the last scores computed, the queries' place is free for the next item's.
         const bool first = walk.tile == walk.begun, last = walk.tile + 1 == walk.end;
         if (last && go_on) load_q(then);
+        // (Rows of a warp past the chunk's: whatever their weights are, nobody reads their results.)
+        if (idle) {
+          if (n > 0 && !(ok = tc_wait(base_known(odd ^ 1, warp), (n - 1) >> 1 & 1, ab))) break;
+          mbar_arrive(base_known(odd, warp));
+          mbar_arrive(p_full(n));
+          if (last && go_on && !(ok = q_loaded(then))) break;
+          continue;
+        }
         const uint32_t s_col = lanes + TN * (n % NS);
         const int left = walk.len - walk.first - walk.tile * TN;   // keys from the tile's first on
         const bool masked = left < TN;
@@ -405,8 +461,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_head_kernel(const __grid_
           }
         };
         float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < TN / 32; i += 2) {
+#pragma unroll 1
+        for (int i = 0; i < TN / 32; i += 2) {   // (not unrolled: the first pass over the code costs its reading)
           uint32_t lo[32], hi[32];
           tmem_ld32(s_col + 32 * i, lo);
           tmem_ld32(s_col + 32 * i + 32, hi);
@@ -446,8 +502,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_head_kernel(const __grid_
           }
         }
         // Weights as two bf16 terms, cut and rest (paged_decode.cuh); 8-bit caches: one f16 term.
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        const float2 scale = make_float2(sl2, sl2), shift = make_float2(-base, -base);
+        const float2 more = make_float2(1 + 0x1p-20f, 1 + 0x1p-20f);
+#pragma unroll 1
         for (int i = 0; i < TN / 32; ++i) {
           uint32_t sv[32], cut[16], rest[16];
           tmem_ld32(s_col + 32 * i, sv);
@@ -455,22 +513,23 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_head_kernel(const __grid_
           mask(i, sv);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float x = fast_exp2(fmaf(__uint_as_float(sv[2 * j]), sl2, -base));
-            const float y = fast_exp2(fmaf(__uint_as_float(sv[2 * j + 1]), sl2, -base));
-            sum[j & 3] += x + y;
+            float2 x = fma2(make_float2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])), scale, shift);
+            x = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            sum[j & 1] = add2(sum[j & 1], x);
             if (E4M3) {
-              cut[j] = pack_f16x2(x, y);
+              cut[j] = pack_f16x2(x.x, x.y);
               continue;
             }
-            const float hx = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
-            const float hy = __uint_as_float(__float_as_uint(y) & 0xffff0000u);
-            cut[j] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
-            rest[j] = pack_bf16x2(fmaf(x, 1 + 0x1p-20f, -hx), fmaf(y, 1 + 0x1p-20f, -hy));
+            const float2 less = make_float2(-__uint_as_float(__float_as_uint(x.x) & 0xffff0000u),
+                                            -__uint_as_float(__float_as_uint(x.y) & 0xffff0000u));
+            cut[j] = __byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x7632);
+            const float2 y = fma2(x, more, less);
+            rest[j] = pack_bf16x2(y.x, y.y);
           }
           tmem_st16(s_col + 32 * i, cut);
           if (!E4M3) tmem_st16(s_col + 32 * i + 16, rest);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(p_full(n));
@@ -501,7 +560,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_head_kernel(const __grid_
           whole ? a.shared.whole + ((int64_t)__ldcg(&a.shared.chunks[walk.b].base) * a.K + (int64_t)walk.k * P) * (H + 2)
                 : a.partials + ((int64_t)blockIdx.x * 2 + (walk.begun == 0 ? 1 : 0)) * paged_partial_floats(128, H);
 #pragma unroll 1
-      for (int c = d0; c < d0 + HD; c += 32) {
+      for (int c = d0; c < d0 + HD && !idle; c += 32) {
         uint32_t ov[32];
         tmem_ld32(lanes + O_COL + c, ov);
         tmem_wait_ld();

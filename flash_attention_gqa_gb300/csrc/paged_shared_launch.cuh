@@ -193,7 +193,7 @@ cudaError_t launch_shared(const PagedSharedArgs& s, cudaStream_t st) {
   head.a.shared.whole = s.head_whole;
   // (boxes of less than 8 rows: more of them than lanes, and not on the swizzle's boundaries)
   const int page = 1 << s.tail.lay.page_shift;
-  head.rows = page < 8 ? 0 : page < Head::KPW ? page : Head::KPW;
+  head.rows = page < 8 ? 0 : page < Head::TN ? page : Head::TN;
   if (head.rows && !(make_cache_map(&head.k_map, s.tail.k_cache, s.tail.lay, s.tail.K, H, E4M3, head.rows) &&
                      make_cache_map(&head.v_map, s.tail.v_cache, s.tail.lay, s.tail.K, H, E4M3, head.rows)))
     head.rows = 0;

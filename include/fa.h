@@ -335,14 +335,15 @@ size_t fa_paged_decode_workspace_size(int B, int K, int G, int T, int H);
  * tokens are the same ones: in the same pages, as fa_paged_fork leaves them,
  * or in equal ones; only one member's are read.  group_starts: int32
  * [n_groups + 1], members [n_members], prefix_lens [n_groups], in device memory;
- * n_groups <= 8192, n_members <= B.  Requests that no group names have no prefix.
+ * n_groups <= 4096, n_members <= B.  Requests that no group names have no prefix.
  * Results are those of fa_paged_decode without a window, to rounding; lengths
  * and page ids out of range are dealt with as there.
  * A group's prefix ends at the latest where all queries of all its members see it:
  * after lens[b] - T + 1 tokens; a longer or negative one is cut to that, a member
  * outside [0, B) left out, a request named again left to the first that names it,
  * and where group_starts falls or leaves [0, n_members] nothing is shared.  All
- * of these set FA_ERR_DEVICE_VALUE; results stay right.
+ * of these set FA_ERR_DEVICE_VALUE; results stay right.  (A small call may read every
+ * request's keys on their own; it does not look at the groups then.)
  * `workspace`: as in fa_paged_decode, of fa_paged_decode_shared_workspace_size bytes.
  */
 int fa_paged_decode_shared(const void* q, const void* k_cache, const void* v_cache, int cache_type,
