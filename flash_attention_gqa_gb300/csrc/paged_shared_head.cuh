@@ -28,10 +28,9 @@ struct HeadCfg : DecodeTcCfg<H_, E4M3_, DECODE_HEAD> {
   static constexpr int NS = 3;   // S buffers
   static constexpr uint32_t O_COL = H_ == 256 ? 256 : 384;
   static_assert(NS * TN <= (int)O_COL && O_COL + H_ <= 512, "");
-  // Copying warps: one each for K and V; 8-bit caches: two each that make f16 of the bytes, and one for
-  // the bytes of both.
+  // Copying warps: one each for K and V; 8-bit caches: two more each, that make f16 of the bytes.
   static constexpr int CONVERT = E4M3_ ? 4 : 0, KPW = TN / 2;   // keys of a tile a converting warp
-  static constexpr int WARPS = E4M3_ ? 15 : 12, THREADS = WARPS * 32;
+  static constexpr int WARPS = 12 + CONVERT, THREADS = WARPS * 32;
   // Slots: scores are computed ahead of the weights, so K needs more of them.
   static constexpr int VS = STAGES / 2, KS = STAGES - VS;
   __device__ static __forceinline__ int slot_of(int n, int kv) { return kv ? KS + n % VS : n % KS; }
@@ -55,15 +54,15 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-// A copying warp's work: every tile of K or of V (`kind`; 8-bit caches: first the one, then the other), into
-// its place at ring_u as that becomes free.  By TMA, a lane a box of one page's rows, in one instruction:
+// A copying warp's work: every tile of K or of V (`kind`), into its place as that becomes free.  By TMA, a lane a box of one page's rows, in one instruction:
 // cp.async by 16 bytes a lane keeps the load and store pipe busy for 2600 cycles a tile, more than all the
 // rest of it takes.  Rows past the prefix have to be zeros, which a box can give for whole pages only (out
 // of the map's range): a tile that ends inside a page goes by cp.async, as does everything where there is
-// no map.  `place(n, kind)` waits until tile n's is free and gives its address and barrier (0: a wait ran out).
+// no map.  `place(n, ..)` waits until tile n's is free and gives its address and barrier, `landed(n)` until
+// the tiles before n that may be on their way have come.
 template <class C, class Place, class Landed>
 __device__ __forceinline__ void head_copies(const PagedHeadArgs& s, const DecodeShape<C>& shape, DecodeWalk walk,
-                                            const DecodeEnd& last, int kind0, int kinds, const Abort& ab, Place place,
+                                            const DecodeEnd& last, int kind, const Abort& ab, Place place,
                                             Landed landed) {
   constexpr int TN = C::TN, UPR = C::UPR;
   constexpr bool E4M3 = C::E4M3;
@@ -87,45 +86,42 @@ __device__ __forceinline__ void head_copies(const PagedHeadArgs& s, const Decode
     const int left = len - row0, mine = page;
     if (++walk.tile == walk.end) more = shape.next_item(walk, last);
     if (more) page = page_of(walk.tile * TN + box_row, walk.len, shape.table_row(walk));
-#pragma unroll 1
-    for (int kind = kind0; kind < kind0 + kinds; ++kind) {
-      uint32_t dst, bar;
-      if (!(ok = place(n, kind, dst, bar))) break;
-      if (rows && (left >= TN || (left & ((1 << shift) - 1)) == 0)) {
-        if (lane == 0) mbar_arrive_expect_tx(bar, TN * CHUNKS * (E4M3 ? C::H : 128));
-        __syncwarp();
-        if (lane < boxes) {
-          const bool key = box_row < left;
-          if (key && !known(mine)) atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
-          tma_load_4d(dst + (E4M3 ? box_row * C::H : box_chunk * C::CHUNK + box_row * 128),
-                      kind ? &s.v_map : &s.k_map, bar, E4M3 ? 0 : box_chunk * 64,
-                      (row0 + box_row) & ((1 << shift) - 1), head, key && known(mine) ? mine : a.lay.n_pages);
-        }
-        if (lane != 0) mbar_arrive(bar);
-      } else {
-        const char* const base = (const char*)(kind ? a.v_cache : a.k_cache);
-#pragma unroll 1
-        for (int r0 = 0; r0 < TN; r0 += 32) {   // a lane a row's page, then all lanes 16-byte units
-          const int key = row0 + r0 + lane, at_page = page_of(key, len, table_row);
-          int64_t off = -1;
-          if (known(at_page))
-            off = at_page * a.lay.page + head * a.lay.head + (key & ((1 << shift) - 1)) * a.lay.token;
-          else if (key < len)
-            atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
-#pragma unroll 1
-          for (int i = lane; i < 32 * UPR; i += 32) {
-            const int row = i / UPR, u = i % UPR;
-            const int64_t at = __shfl_sync(~0u, off, row);
-            const uint32_t to =
-                dst + (E4M3 ? (r0 + row) * C::H + u * 16 : (u >> 3) * C::CHUNK + sw128_offset(r0 + row, u & 7));
-            if (at >= 0)
-              cp_async16(to, base + at + u * 16);
-            else
-              cp_zeros16(to, a.q);
-          }
-        }
-        cp_async_arrive(bar);
+    uint32_t dst, bar;
+    if (!(ok = place(n, dst, bar))) break;
+    if (rows && (left >= TN || (left & ((1 << shift) - 1)) == 0)) {
+      if (lane == 0) mbar_arrive_expect_tx(bar, TN * CHUNKS * (E4M3 ? C::H : 128));
+      __syncwarp();
+      if (lane < boxes) {
+        const bool key = box_row < left;
+        if (key && !known(mine)) atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+        tma_load_4d(dst + (E4M3 ? box_row * C::H : box_chunk * C::CHUNK + box_row * 128),
+                    kind ? &s.v_map : &s.k_map, bar, E4M3 ? 0 : box_chunk * 64,
+                    (row0 + box_row) & ((1 << shift) - 1), head, key && known(mine) ? mine : a.lay.n_pages);
       }
+      if (lane != 0) mbar_arrive(bar);
+    } else {
+      const char* const base = (const char*)(kind ? a.v_cache : a.k_cache);
+#pragma unroll 1
+      for (int r0 = 0; r0 < TN; r0 += 32) {   // a lane a row's page, then all lanes 16-byte units
+        const int key = row0 + r0 + lane, at_page = page_of(key, len, table_row);
+        int64_t off = -1;
+        if (known(at_page))
+          off = at_page * a.lay.page + head * a.lay.head + (key & ((1 << shift) - 1)) * a.lay.token;
+        else if (key < len)
+          atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+#pragma unroll 1
+        for (int i = lane; i < 32 * UPR; i += 32) {
+          const int row = i / UPR, u = i % UPR;
+          const int64_t at = __shfl_sync(~0u, off, row);
+          const uint32_t to =
+              dst + (E4M3 ? (r0 + row) * C::H + u * 16 : (u >> 3) * C::CHUNK + sw128_offset(r0 + row, u & 7));
+          if (at >= 0)
+            cp_async16(to, base + at + u * 16);
+          else
+            cp_zeros16(to, a.q);
+        }
+      }
+      cp_async_arrive(bar);
     }
   }
   // Where a wait has run out, here or elsewhere, what is in flight lands before the CTA ends.
@@ -191,7 +187,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_head_kernel(const __grid_
   __shared__ float sh_big[2][128];      // largest values of the halves of a query row
 
   const uint32_t q_u = smem_u32(sm), ring_u = q_u + C::QBYTES;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = tid >> 5;
   const int GT = a.G * a.T;
   const DecodeShape<C> shape{a};
   const Abort ab{&sh_abort, a.wait_limit_ns, a.err};
@@ -331,24 +327,24 @@ __global__ void __launch_bounds__(C::THREADS, 1) paged_head_kernel(const __grid_
         head_converts<C>(shape, walk, sh.ends[1], ring_u, ring_u + C::RING, (warp - 8) & 1, (warp - 8) >> 1, ab, full,
                          empty, raw_full, raw_empty);
       } else {
+        const int mine = warp - 8 - C::CONVERT;
         head_copies<C>(
-            args, shape, walk, sh.ends[1], 0, 2, ab,
-            [&](int n, int kind, uint32_t& dst, uint32_t& bar) {
-              dst = ring_u + C::RING + (kind * RS + n % RS) * C::RAW;
-              bar = raw_full(n, kind);
-              return n < RS || tc_wait(raw_empty(n, kind), (n / RS - 1) & 1, ab);
+            args, shape, walk, sh.ends[1], mine, ab,
+            [&](int n, uint32_t& dst, uint32_t& bar) {
+              dst = ring_u + C::RING + (mine * RS + n % RS) * C::RAW;
+              bar = raw_full(n, mine);
+              return n < RS || tc_wait(raw_empty(n, mine), (n / RS - 1) & 1, ab);
             },
             [&](int n) {
-              for (int i = max(0, n - RS); i < n; ++i)
-                for (int kind = 0; kind < 2; ++kind) mbar_wait_teardown(raw_full(i, kind), i / RS & 1, limit);
+              for (int i = max(0, n - RS); i < n; ++i) mbar_wait_teardown(raw_full(i, mine), i / RS & 1, limit);
             });
       }
     } else {
       const int mine = warp - 8;
       head_copies<C>(
-          args, shape, walk, sh.ends[1], mine, 1, ab,
-          [&](int n, int kind, uint32_t& dst, uint32_t& bar) {
-            const int slot = C::slot_of(n, kind), turns = C::turn_of(n, kind);
+          args, shape, walk, sh.ends[1], mine, ab,
+          [&](int n, uint32_t& dst, uint32_t& bar) {
+            const int slot = C::slot_of(n, mine), turns = C::turn_of(n, mine);
             dst = ring_u + slot * C::SLOT;
             bar = full(slot);
             return turns == 0 || tc_wait(empty(slot), (turns - 1) & 1, ab);
