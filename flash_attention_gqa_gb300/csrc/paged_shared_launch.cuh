@@ -15,19 +15,20 @@
 
 namespace fa {
 
-// A thread per 4 dims of a row of item (b, k), a warp 8 rows of 16 dims; `per` such a CTA, times
-// shares of the partials, summed in order behind it.  U partials of a thread in flight.
+// A thread per 4 dims of a row of item (b, k), a warp up to 8 rows (2^rows_shift) side by side; `per` such
+// a CTA, times shares of the partials, summed in order behind it.  U partials of a thread in flight.
 template <int H, bool TC, int U, int THREADS>
 __global__ void __launch_bounds__(THREADS)
-paged_shared_join_kernel(const __grid_constant__ PagedSharedArgs s, int per) {
+paged_shared_join_kernel(const __grid_constant__ PagedSharedArgs s, int per, int rows_shift) {
   __shared__ float4 sx[THREADS];
   __shared__ float2 sml[THREADS];
   grid_before();
   const PagedDecodeArgs& a = s.tail;
   const int item = blockIdx.x, b = item / a.K, k = item - b * a.K, R = a.G * a.T, P = paged_partial_rows(R);
   const int shares = blockDim.x / per, share = threadIdx.x / per, at = threadIdx.x % per;
-  const int i = blockIdx.y * per + at, groups = (R + 7) / 8, tile = i / 32;
-  const int r = tile / groups < H / 16 ? tile % groups * 8 + i % 8 : R, d = tile / groups * 4 + i % 32 / 8;   // d: of 4
+  const int i = blockIdx.y * per + at, tile = i / 32, side = 1 << rows_shift, groups = (R + side - 1) >> rows_shift;
+  const int d = tile / groups * (32 >> rows_shift) + (i % 32 >> rows_shift);   // of 4
+  const int r = d < H / 4 ? tile % groups * side + (i & (side - 1)) : R;
   // (written by the grids before, maybe while this one was already there: L2 loads)
   const int4 tail = __ldcg(reinterpret_cast<const int4*>(a.splits) + item);
   const int place = r < R ? __ldcg(a.shared.places + b) : -1;
@@ -153,19 +154,25 @@ cudaError_t launch_shared_part(const Args& a, int grid, cudaStream_t st) {
 
 template <int H, bool TC>
 cudaError_t launch_shared_join(const PagedSharedArgs& s, cudaStream_t st) {
-  const int R = s.tail.G * s.tail.T, items = s.tail.B * s.tail.K, elements = (R + 7) / 8 * 8 * (H / 4);
+  const int R = s.tail.G * s.tail.T, items = s.tail.B * s.tail.K;
+  int rows_shift = H == 64 ? 1 : 0;   // (a warp's dims are no more than a row's)
+  while (rows_shift < 3 && (1 << rows_shift) < R) ++rows_shift;
+  const int side = 1 << rows_shift, elements = (R + side - 1) / side * side * (H / 4);
   // Partials of a row: about CTAs / items, two more at most, of its own keys and of the prefix's, whose
-  // items are at least the rows in chunks times the heads.
+  // items are at least the rows in chunks times the heads.  Several shares of them where they are many,
+  // as far as all threads are there at once (156 items of 20 partials: 25 us with 16 shares, 1248 CTAs of 512).
   const int chunks = max(1, max(min(s.n_groups, s.n_members / 2), (int)((int64_t)s.n_members * R / 128)));
   const int partials = s.tail_ctas / items + 2 + s.head_ctas / (chunks * s.tail.K) + 2;
-  const int shares = partials <= 8 ? 1 : partials <= 16 ? 2 : 16;
-  int per = shares == 16 ? 32 : 256 / shares;
+  const int64_t room = (int64_t)s.head_ctas * 1024 / ((int64_t)items * elements);
+  const int shares = partials <= 8 || room < 2 ? 1 : partials <= 16 || room < 4 ? 2 : room < 16 ? 4 : 16;
+  int per = shares == 16 ? 32 : shares == 4 ? 64 : 256 / shares;
   while (per > 32 && per / 2 >= elements) per /= 2;
   const dim3 grid(items, (elements + per - 1) / per);
   switch (shares) {
-    case 1: return launch_early(paged_shared_join_kernel<H, TC, 4, 256>, grid, per, 0, st, s, per);
-    case 2: return launch_early(paged_shared_join_kernel<H, TC, 8, 256>, grid, 2 * per, 0, st, s, per);
-    default: return launch_early(paged_shared_join_kernel<H, TC, 8, 512>, grid, 16 * per, 0, st, s, per);
+    case 1: return launch_early(paged_shared_join_kernel<H, TC, 4, 256>, grid, per, 0, st, s, per, rows_shift);
+    case 2:
+    case 4: return launch_early(paged_shared_join_kernel<H, TC, 8, 256>, grid, shares * per, 0, st, s, per, rows_shift);
+    default: return launch_early(paged_shared_join_kernel<H, TC, 8, 512>, grid, 16 * per, 0, st, s, per, rows_shift);
   }
 }
 
