@@ -32,8 +32,8 @@ def angles(pos, freq, axes):
     step = [int(Fraction(float(f)) * PER_TURN * 2 ** 120) for f in freq.tolist()]
     out = np.zeros((pos.shape[1], len(step)))
     for i, s in enumerate(step):
-        row = pos[int(axes[i]) if axes is not None else 0]
-        out[:, i] = [(int(p) * s) % 2 ** 120 / 2 ** 120 for p in row.tolist()]
+        row = pos[int(axes[i]) if axes is not None else 0].numpy().astype(object)
+        out[:, i] = ((row * s) % 2 ** 120 / 2 ** 120).astype(np.float64)
     return torch.from_numpy(out) * (2 * math.pi)
 
 
@@ -73,7 +73,8 @@ CASES = [  # B, T, q heads, k heads, H, pairs, axes, mixed, adjacent, far, strid
     (2, 129, 4, 4, 128, 40, 4, True, False, 2 ** 31 - 1, True), (1, 50, 3, 0, 256, 64, 3, True, True, 2 ** 30, True),
     (4, 11, 12, 3, 256, 8, 1, False, False, 0, True), (2, 500, 32, 8, 128, 64, 1, False, True, 0, False),
     (1, 3000, 1, 1, 64, 24, 2, False, False, 99999, False), (70, 1, 7, 7, 64, 32, 16, True, False, 0, True),
-    (1, 9000, 40, 8, 128, 64, 3, False, False, 0, True)]
+    (1, 9000, 40, 8, 128, 64, 3, False, False, 0, True), (1, 40000, 1, 0, 256, 128, 1, False, False, 0, False),
+    (3, 20001, 1, 1, 64, 32, 2, True, True, 0, True)]
 each_case = pytest.mark.parametrize("case", CASES, ids=lambda c: "B%d_T%d_h%d+%d_H%d_p%d_ax%d%s%s_%d%s" % (
     *c[:7], "m" if c[7] else "", "_adj" if c[8] else "", c[9], "_str" if c[10] else ""))
 
