@@ -68,20 +68,42 @@ struct PageSet {
 __host__ __device__ inline int set_words(int n_pages) { return ((n_pages + 31) / 32 + kCtas - 1) / kCtas; }
 
 // The warps of the cluster over the columns [first, last) of rows 0 .. n - 1: `S` warps a row, the
-// row's columns dealt to their lanes.  `f(row, column, live)` by whole warps, `range(row, first,
-// last)` says false for rows to be left out.
-template <class Range, class F>
-__device__ __forceinline__ void over_entries(int rank, int n, Range range, F f) {
+// row's columns dealt to their lanes, four of a lane at a time: `load(row, column)` of all four, then
+// `use(row, column, what it gave)`.  `range(row, first, last)` says false for rows to be left out.
+// `barrier()` is called once by all threads, before the first use.
+template <class Range, class Load, class Use, class Barrier>
+__device__ __forceinline__ void over_entries(int rank, int n, Range range, Load load, Use use, Barrier barrier) {
   const int lane = threadIdx.x & 31, warp = rank * kWarps + (threadIdx.x >> 5);
   constexpr int all = kCtas * kWarps;
   const int S = n >= all ? 1 : all / max(n, 1);   // warps a row
-  for (int i = warp / S; i < n; i += all / S) {
+  bool passed = false;
+  for (int i = warp / S; i < n; i += all) {   // (several rows a warp: only with one warp a row)
     int first, last;
     if (!range(i, first, last)) continue;
-    for (int j = first + warp % S * 32; j < last; j += S * 32) f(i, j + lane, j + lane < last);
-    if (n < all) break;   // (the warps left over by the division have no row)
+    for (int j = first + warp % S * 32; j < last; j += 4 * S * 32) {
+      int x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int column = j + k * S * 32 + lane;
+        if (column < last) x[k] = load(i, column);
+      }
+      if (!passed) barrier();
+      passed = true;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int column = j + k * S * 32 + lane;
+        if (column < last) use(i, column, x[k]);
+      }
+    }
   }
+  __syncwarp();
+  if (!passed) barrier();
 }
+// Rows of a call that stay in shared memory; more of them are looked up again.
+constexpr int kRowsKept = 1024;
+struct KeptRow {
+  int row, first, last;
+};
 
 // ------------------------------------------------------------------- free
 
@@ -90,6 +112,7 @@ __device__ __forceinline__ void over_entries(int rank, int n, Range range, F f) 
 __global__ void __launch_bounds__(kThreads, 1) pages_free_kernel(const __grid_constant__ PagesFreeArgs a) {
   extern __shared__ uint32_t bits[];
   __shared__ uint32_t seen[kMaxPagedBatch / 32];   // rows of the call
+  __shared__ KeptRow kept[kRowsKept];
   __shared__ int warp_sums[32], total;
   const cg::cluster_group cluster = cg::this_cluster();
   const PagesPool& p = a.p;
@@ -103,11 +126,13 @@ __global__ void __launch_bounds__(kThreads, 1) pages_free_kernel(const __grid_co
 
   bool bad = used < 0 || used > p.n_free, odd = false;
   for (int i = tid; i < a.N; i += kThreads) {
-    const int row = a.rows[i];
+    const int row = a.rows[i], keep = a.keep ? a.keep[i] : 0;
+    if (i < kRowsKept) kept[i] = KeptRow{row, 0, 0};
     if (row < 0) continue;
     if (row >= p.B) { bad = true; continue; }
+    const int len = p.lens[row];
     bad |= (atomicOr(&seen[row >> 5], 1u << (row & 31)) >> (row & 31) & 1) != 0;
-    const int len = p.lens[row], keep = a.keep ? a.keep[i] : 0;
+    if (i < kRowsKept) kept[i] = KeptRow{row, pages_of(keep, p.page_shift), pages_of(len, p.page_shift)};
     if (len < 0 || len > most || keep < 0 || keep > len) { bad = true; continue; }
     // the last page kept gets new tokens, which other requests would see
     if (keep < len && (keep & ((1 << p.page_shift) - 1)) != 0) {
@@ -117,22 +142,27 @@ __global__ void __launch_bounds__(kThreads, 1) pages_free_kernel(const __grid_co
   }
   // All CTAs have looked at everything, and agree.
   const bool fail = __syncthreads_or(bad);
-  cluster.sync();   // the sets are empty, the counts have been looked at
+  auto row_of = [&](int i) { return i < kRowsKept ? kept[i].row : a.rows[i]; };
   auto range = [&](int i, int& first, int& last) {
+    if (i < kRowsKept) {
+      first = kept[i].first;
+      last = kept[i].last;
+      return true;
+    }
     const int row = a.rows[i];
     if (row < 0) return false;
     first = pages_of(a.keep ? a.keep[i] : 0, p.page_shift);
     last = pages_of(p.lens[row], p.page_shift);
     return true;
   };
-  if (!fail)
-    over_entries(rank, a.N, range, [&](int i, int j, bool live) {
-      if (!live) return;
-      const int page = p.block_table[(int64_t)a.rows[i] * p.max_pages + j];
-      if (page < 0 || page >= p.n_pages) { odd = true; return; }
-      const int others = atomicSub(&p.shares[page], 1);
-      if (others <= 0) odd |= set.put(page) || others < 0;   // (below zero: given back before)
-    });
+  auto entry = [&](int i, int j) { return p.block_table[(int64_t)row_of(i) * p.max_pages + j]; };
+  auto known = [&](int page) { return page >= 0 && page < p.n_pages; };
+  // (behind the barrier: the sets are empty, the counts have been looked at)
+  over_entries(rank, fail ? 0 : a.N, range, entry, [&](int, int, int page) {
+    if (!known(page)) { odd = true; return; }
+    const int others = atomicSub(&p.shares[page], 1);
+    if (others <= 0) odd |= set.put(page) || others < 0;   // (below zero: given back before)
+  }, [&] { cluster.sync(); });
   cluster.sync();
   int count = 0;
   const int per = (set.words + kThreads - 1) / kThreads;
@@ -149,10 +179,9 @@ __global__ void __launch_bounds__(kThreads, 1) pages_free_kernel(const __grid_co
   }
   const bool over = !fail && all > used;   // more pages than the list has given out
   if (over) {
-    over_entries(rank, a.N, range, [&](int i, int j, bool live) {
-      const int page = live ? p.block_table[(int64_t)a.rows[i] * p.max_pages + j] : -1;
-      if (page >= 0 && page < p.n_pages) atomicAdd(&p.shares[page], 1);
-    });
+    over_entries(rank, a.N, range, entry, [&](int, int, int page) {
+      if (known(page)) atomicAdd(&p.shares[page], 1);
+    }, [] {});
   } else if (!fail) {
     // a warp a word, a lane a page
     int at = used - all + before;
@@ -244,23 +273,26 @@ __global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const __grid_co
       last = max(last, 1);   // (one at least: it writes the entry's copy)
       return true;
     };
-    over_entries(rank, a.N, range, [&](int i, int j, bool live) {
-      if (!live) return;
+    auto entry = [&](int i, int j) {
+      const int parent = a.parents[i];
+      return parent < 0 || j >= p.max_pages ? -1 : p.block_table[(int64_t)parent * p.max_pages + j];
+    };
+    auto known = [&](int page) { return page >= 0 && page < p.n_pages; };
+    over_entries(rank, a.N, range, entry, [&](int i, int j, int page) {
       const int parent = a.parents[i];
       const int n = parent < 0 ? 0 : length(i, parent), full = n >> p.page_shift, part = n & (P - 1);
       int32_t* const copy = a.copies + (int64_t)i * 3;
       if (j == full && part) {
-        const int from = p.block_table[(int64_t)parent * p.max_pages + j], to = p.free_pages[used + fresh[i]];
-        const bool known = from >= 0 && from < p.n_pages && to >= 0 && to < p.n_pages;
+        const int to = p.free_pages[used + fresh[i]];
+        const bool both = known(page) && known(to);
         a.table[(int64_t)a.children[i] * p.max_pages + j] = to;
-        copy[0] = known ? from : -1;
-        copy[1] = known ? to : -1;
-        copy[2] = known ? part : 0;
-        if (!known) atomicOr(p.err, (uint32_t)DEV_BAD_VALUE);
+        copy[0] = both ? page : -1;
+        copy[1] = both ? to : -1;
+        copy[2] = both ? part : 0;
+        if (!both) atomicOr(p.err, (uint32_t)DEV_BAD_VALUE);
       } else if (j < full) {
-        const int page = p.block_table[(int64_t)parent * p.max_pages + j];
         a.table[(int64_t)a.children[i] * p.max_pages + j] = page;
-        if (page >= 0 && page < p.n_pages)
+        if (known(page))
           atomicAdd(&p.shares[page], 1);
         else
           atomicOr(p.err, (uint32_t)DEV_BAD_VALUE);
@@ -269,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const __grid_co
         copy[0] = copy[1] = -1;
         copy[2] = 0;
       }
-    });
+    }, [] {});
   }
   cluster.sync();   // all lengths have been read
   if (rank == 0) {
@@ -313,21 +345,20 @@ __global__ void __launch_bounds__(kThreads, 1) pages_compact_kernel(const __grid
   for (int b = tid; b < p.B; b += kThreads) bad |= p.lens[b] < 0 || p.lens[b] > most_len;
   const bool wrong = __syncthreads_or(bad);   // the same in all CTAs
   for (int64_t i = g; i < (int64_t)a.max_moves * 3; i += grid) a.moves[i] = i % 3 == 2 ? 0 : -1;
-  cluster.sync();
 
   auto row = [&](int b, int& first, int& last) {
     first = 0;
     last = pages_of(p.lens[b], p.page_shift);
     return true;
   };
+  auto entry = [&](int b, int j) { return p.block_table[(int64_t)b * p.max_pages + j]; };
+  const PageSet in_use{cluster, held, words}, unused{cluster, spare, words};
+  bad = false;
+  over_entries(rank, wrong ? 0 : p.B, row, entry, [&](int, int, int page) {
+    if (page < 0 || page >= p.n_pages) bad = true;
+    else in_use.put(page);
+  }, [&] { cluster.sync(); });   // (the sets are empty)
   if (!wrong) {
-    const PageSet in_use{cluster, held, words}, unused{cluster, spare, words};
-    bad = false;
-    over_entries(rank, p.B, row, [&](int b, int j, bool live) {
-      const int page = live ? p.block_table[(int64_t)b * p.max_pages + j] : 0;
-      if (page < 0 || page >= p.n_pages) bad = true;
-      else if (live) in_use.put(page);
-    });
     for (int i = used + g; i < p.n_free; i += grid) {
       const int page = p.free_pages[i];
       bad |= page < 0 || page >= p.n_pages || unused.put(page);   // (twice in the list)
@@ -417,18 +448,15 @@ __global__ void __launch_bounds__(kThreads, 1) pages_compact_kernel(const __grid
       if (!in_place) last = p.max_pages;   // what is behind a request's pages, too
       return true;
     };
-    over_entries(rank, p.B, whole, [&](int b, int j, bool live) {
-      if (!live) return;
-      const int64_t at = (int64_t)b * p.max_pages + j;
-      const int page = p.block_table[at];
+    over_entries(rank, p.B, whole, entry, [&](int b, int j, int page) {
       int to = page;
       if (j < pages_of(p.lens[b], p.page_shift)) {
         const int above = all_held - held_below(page) - 1;
         if (above < a.max_moves && __ldcg(a.moves + (int64_t)above * 3) == page)
           to = __ldcg(a.moves + (int64_t)above * 3 + 1);
       }
-      if (!in_place || to != page) a.table_out[at] = to;
-    });
+      if (!in_place || to != page) a.table_out[(int64_t)b * p.max_pages + j] = to;
+    }, [] {});
     int at = used;
     for (int c = 0; c < rank; ++c) at += cluster.map_shared_rank(counts, c)[2];
     for (int w = warp; w < words; w += kWarps) {
