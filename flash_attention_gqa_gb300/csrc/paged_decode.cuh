@@ -205,9 +205,15 @@ struct DecodePlace {
   int b, k, rem;
 };
 
+// A request's keys: `low` the first that any query keeps, `row` its row of the table.
+struct DecodeSpan {
+  int len, low, row;
+};
+
 // Unit t of request b's.
 struct DecodeEnd {
-  int b, len;
+  int b;
+  DecodeSpan keys;
   long long t;
 };
 
@@ -227,47 +233,48 @@ struct DecodeShape {
   __device__ __forceinline__ int count() const {
     return C::MODE == DECODE_HEAD ? __ldcg(a.shared.n_chunks) : a.B;
   }
-  __device__ __forceinline__ int length(int b) const {
-    if (C::MODE == DECODE_HEAD) return __ldcg(&a.shared.chunks[b].len);
-    const int n = a.lens[b];
-    return min(max(n, 0), a.max_pages << a.lay.page_shift);
+  __device__ __forceinline__ DecodeSpan span(int b) const {
+    if (C::MODE == DECODE_HEAD) {
+      const int4 c = __ldcg(reinterpret_cast<const int4*>(a.shared.chunks + b));
+      return DecodeSpan{c.x, 0, c.y};
+    }
+    const int n = a.lens[b], len = min(max(n, 0), a.max_pages << a.lay.page_shift);
+    if (C::MODE == DECODE_TAIL) return DecodeSpan{len, __ldcg(a.shared.begins + b), b};
+    return DecodeSpan{len, low(len), b};
   }
   // First key any of the T queries keeps.
-  __device__ __forceinline__ int low(int b, int len) const {
-    if (C::MODE == DECODE_HEAD) return 0;
-    if (C::MODE == DECODE_TAIL) return __ldcg(a.shared.begins + b);
+  __device__ __forceinline__ int low(int len) const {
     return a.window > 0 ? max(0, len - a.T + 1 - a.window) : 0;
   }
   // The same, of the item that the walk is in.
   __device__ __forceinline__ int low(const DecodeWalk& w) const {
-    return C::MODE == DECODE_TAIL ? w.low : low(w.b, w.len);
+    return C::MODE == DECODE_TAIL ? w.low : C::MODE == DECODE_HEAD ? 0 : low(w.len);
   }
   __device__ __forceinline__ int table_row(const DecodeWalk& w) const { return C::MODE == DECODE_HEAD ? w.low : w.b; }
   __device__ __forceinline__ int first(int low) const { return low & ~((C::MODE == DECODE_TAIL ? 8 : C::CK) - 1); }
-  __device__ __forceinline__ int tiles(int b, int len) const {
-    return max(1, (len - first(low(b, len)) + C::TK - 1) / C::TK);   // an empty item writes its zeros
+  __device__ __forceinline__ int tiles(const DecodeSpan& s) const {
+    return max(1, (s.len - first(s.low) + C::TK - 1) / C::TK);   // an empty item writes its zeros
   }
   __device__ __forceinline__ DecodePlace place(const DecodeEnd& e) const {
-    const int per_item = tiles(e.b, e.len) + C::ITEM_UNITS, k = (int)quotient(e.t, per_item);
+    const int per_item = tiles(e.keys) + C::ITEM_UNITS, k = (int)quotient(e.t, per_item);
     return DecodePlace{e.b, k, (int)(e.t - (long long)k * per_item)};
   }
-  __device__ __forceinline__ void enter(DecodeWalk& w, int b, int k) const {
+  __device__ __forceinline__ void enter(DecodeWalk& w, int b, int k, const DecodeSpan& s) const {
     w.b = b;
     w.k = k;
-    w.len = length(b);
-    const int lo = low(b, w.len);
-    if (C::MODE == DECODE_TAIL) w.low = lo;
-    if (C::MODE == DECODE_HEAD) w.low = __ldcg(&a.shared.chunks[b].leader);
-    w.first = first(lo);
-    w.tiles = max(1, (w.len - w.first + C::TK - 1) / C::TK);
+    w.len = s.len;
+    if (C::MODE != DECODE_ALL) w.low = C::MODE == DECODE_TAIL ? s.low : s.row;
+    w.first = first(s.low);
+    w.tiles = tiles(s);
     w.tile = w.begun = 0;
     w.end = w.tiles;
   }
   // From the item that the CTA's units begin in to the one that they end in.
   // False where they hold no tile at all.
-  __device__ __forceinline__ bool begin(DecodeWalk& w, const DecodePlace& h, const DecodePlace& e) const {
+  __device__ __forceinline__ bool begin(DecodeWalk& w, const DecodePlace& h, const DecodeSpan& keys,
+                                        const DecodePlace& e) const {
     const int between = (e.b - h.b) * a.K + e.k - h.k;   // items
-    enter(w, h.b, h.k);
+    enter(w, h.b, h.k, keys);
     if (a.unsplit) {   // an item is done whole by the CTA that its first unit is in
       w.todo = between;
       return h.rem == 0 || next_item(w, DecodeEnd{});
@@ -284,7 +291,7 @@ struct DecodeShape {
     if (w.todo <= 0) return false;
     --w.todo;
     if (w.k + 1 == a.K) {
-      enter(w, w.b + 1, 0);
+      enter(w, w.b + 1, 0, span(w.b + 1));
     } else {
       ++w.k;
       w.tile = w.begun = 0;
@@ -316,12 +323,11 @@ __device__ __forceinline__ bool decode_units(const PagedDecodeArgs& a, DecodeSha
   const int per = (B + threads - 1) / threads;
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
   long long mine = 0;
+  DecodeSpan keys{0, 0, 0};   // of the last of this thread's requests
   for (int b = b0; b < b1; ++b) {
-    if (C::MODE != DECODE_HEAD && blockIdx.x == 0) {
-      const int n = a.lens[b];
-      if (n != shape.length(b)) atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
-    }
-    mine += (long long)(shape.tiles(b, shape.length(b)) + C::ITEM_UNITS) * a.K;
+    keys = shape.span(b);
+    if (C::MODE != DECODE_HEAD && blockIdx.x == 0 && a.lens[b] != keys.len) atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+    mine += (long long)(shape.tiles(keys) + C::ITEM_UNITS) * a.K;
   }
   long long inc = mine;
 #pragma unroll
@@ -348,10 +354,10 @@ __device__ __forceinline__ bool decode_units(const PagedDecodeArgs& a, DecodeSha
   if (t0 < at + mine && t1 - 1 >= at) {   // the requests that hold the first and the last unit
     long long x = at;
     for (int b = b0; b < b1; ++b) {
-      const int len = shape.length(b);
-      const long long next = x + (long long)(shape.tiles(b, len) + C::ITEM_UNITS) * a.K;
-      if (t0 >= x && t0 < next) sh.ends[0] = DecodeEnd{b, len, t0 - x};
-      if (t1 - 1 >= x && t1 - 1 < next) sh.ends[1] = DecodeEnd{b, len, t1 - 1 - x};
+      if (per > 1) keys = shape.span(b);
+      const long long next = x + (long long)(shape.tiles(keys) + C::ITEM_UNITS) * a.K;
+      if (t0 >= x && t0 < next) sh.ends[0] = DecodeEnd{b, keys, t0 - x};
+      if (t1 - 1 >= x && t1 - 1 < next) sh.ends[1] = DecodeEnd{b, keys, t1 - 1 - x};
       x = next;
     }
   }
@@ -360,7 +366,7 @@ __device__ __forceinline__ bool decode_units(const PagedDecodeArgs& a, DecodeSha
   if (tid == 32 && !a.unsplit) {
     // the item that the units end in, where it begins here and goes on in the
     // next CTA: for the join, with its last CTA
-    const int tiles = shape.tiles(sh.ends[1].b, sh.ends[1].len);
+    const int tiles = shape.tiles(sh.ends[1].keys);
     const long long first = t1 - 1 - tail.rem + C::ITEM_UNITS;   // its first tile's unit
     const bool split = tail.rem >= C::ITEM_UNITS && tail.rem + 1 < tiles + C::ITEM_UNITS && first >= t0;
     if (split || !a.by_item) {
@@ -370,7 +376,7 @@ __device__ __forceinline__ bool decode_units(const PagedDecodeArgs& a, DecodeSha
       a.splits[a.by_item ? item : i] = PagedDecodeSplit{item, split ? i : -1, (int)last, 0};
     }
   }
-  return shape.begin(walk, head, tail);
+  return shape.begin(walk, head, sh.ends[0].keys, tail);
 }
 
 // Whether any 16-bit (bf16) or 8-bit (e4m3) value of the `bytes` at `p` is not
