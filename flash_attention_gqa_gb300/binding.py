@@ -527,19 +527,18 @@ def _float_bits(x: float) -> int:
     return struct.unpack("i", struct.pack("f", x))[0]
 
 
-def _turning(positions, inv_freq, axes, dims: int, dev: int):
-    """(positions' strides, number of axes, axes' address) of checked positions [n_axes, ...] or, of
-    one axis, [...], with `dims` dims behind the axis."""
-    if positions.dtype is not _I32 or positions.get_device() != dev:
-        raise ValueError(f"positions must be an int32 tensor on cuda:{dev}")
-    st = positions.stride()
-    if len(st) == dims:
-        n_axes, st = 1, (0, *st)
-    elif len(st) == dims + 1:
-        n_axes = positions.shape[0]
-    else:
-        raise ValueError(f"positions must have {dims} dims, or the axes before them, "
-                         f"got {tuple(positions.shape)}")
+def _turning(positions, inv_freq, axes, tokens: tuple, dev: int):
+    """(positions' strides, number of axes, pairs, axes' address) of checked positions [n_axes, *tokens]
+    or, of one axis, [*tokens]."""
+    shape, st = positions.shape, positions.stride()
+    n_axes = 1
+    if len(shape) == len(tokens):
+        st = (0, *st)
+    elif len(shape) == len(tokens) + 1:
+        n_axes, shape = shape[0], shape[1:]
+    if shape != tokens or positions.dtype is not _I32 or positions.get_device() != dev:
+        raise ValueError(f"positions must be an int32 tensor {list(tokens)}, or the axes before them, on "
+                         f"cuda:{dev}, got {positions.dtype} {tuple(positions.shape)}")
     pairs = inv_freq.numel()
     _dense(inv_freq, _F32, pairs, dev, "inv_freq")
     return st, n_axes, pairs, 0 if axes is None else _dense(axes, _I32, pairs, dev, "axes")
@@ -577,9 +576,7 @@ def fa_rotary(q, q_out, k, k_out, positions, inv_freq, axes=None, *, q_scale=1.0
         if k.shape[0] != B or k.shape[1] != T or k.shape[3] != H:
             raise ValueError(f"k must be [{B}, {T}, heads, {H}], got {tuple(k.shape)}")
         kp, kop, kh = k.data_ptr(), k_out.data_ptr(), k.shape[2]
-    sp, n_axes, pairs, ax = _turning(positions, inv_freq, axes, 2, dev)
-    if positions.shape[-2] != B or positions.shape[-1] != T:
-        raise ValueError(f"positions must be [n_axes, {B}, {T}], got {tuple(positions.shape)}")
+    sp, n_axes, pairs, ax = _turning(positions, inv_freq, axes, (B, T), dev)
     rc = (_lib or load()).fa_rotary_packed(_ROTARY(
         q.data_ptr(), sq[0], sq[1], sq[2], q_out.data_ptr(), sqo[0], sqo[1], sqo[2],
         kp, sk[0], sk[1], sk[2], kop, sko[0], sko[1], sko[2],
@@ -604,29 +601,28 @@ def fa_paged_rotary_append(q, k, v, positions, inv_freq, slots, q_out, k_cache, 
             return fa_paged_rotary_append(q, k, v, positions, inv_freq, slots, q_out, k_cache, v_cache,
                                           axes, k_scale, v_scale, q_scale=q_scale, adjacent=adjacent,
                                           stream=stream, check=check)
-    N, heads, H = q.shape
-    K = k.shape[1]
+    N, heads, H = shape = q.shape
+    kv, out = k.shape, q_out.shape
     sq, sk, sv, so = q.stride(), k.stride(), v.stride(), q_out.stride()
-    if (not _BF16 is q.dtype is k.dtype is v.dtype is q_out.dtype or k.shape != v.shape
-            or len(sk) != 3 or k.shape[0] != N or k.shape[2] != H
+    if (not _BF16 is q.dtype is k.dtype is v.dtype is q_out.dtype or kv != v.shape
+            or len(kv) != 3 or kv[0] != N or kv[2] != H
             or not dev == k.get_device() == v.get_device() == q_out.get_device()
-            or ((sk[2] != 1 or sv[2] != 1) and k.numel())
-            or ((sq[2] != 1 or so[-1] != 1) and q.numel())):
+            or (sk[2] != 1 or sv[2] != 1) and k.numel()
+            or (sq[2] != 1 or so[-1] != 1) and q.numel()):
         raise ValueError("q, k and v must be bfloat16 tensors [N, heads, H] (k and v of one shape) and "
                          "q_out one on their device, innermost stride 1")
-    if len(so) == 5:
-        B, Kq, G, T, Ho = q_out.shape
+    K = kv[1]
+    if len(out) == 5:
+        B, Kq, G, T, Ho = out
         if B * T != N or Kq * G != heads or Ho != H or (Kq > 1 and G > 1 and so[1] != G * so[2]):
             raise ValueError(f"q_out must be [B, K, G, T, {H}] with B * T = {N} and K * G = {heads}, one "
-                             f"stride for all heads, got {tuple(q_out.shape)}")
+                             f"stride for all heads, got {tuple(out)}")
         ob, ot, oh = so[0], so[3], so[2] if G > 1 else so[1]
     else:
-        if q_out.shape != q.shape:
-            raise ValueError(f"q_out must be [B, K, G, T, {H}] or {tuple(q.shape)}, got {tuple(q_out.shape)}")
+        if out != shape:
+            raise ValueError(f"q_out must be [B, K, G, T, {H}] or {tuple(shape)}, got {tuple(out)}")
         B, T, (ob, ot, oh) = 1, N, (0, so[0], so[1])
-    sp, n_axes, pairs, ax = _turning(positions, inv_freq, axes, 1, dev)
-    if positions.shape[-1] != N:
-        raise ValueError(f"positions must be [n_axes, {N}], got {tuple(positions.shape)}")
+    sp, n_axes, pairs, ax = _turning(positions, inv_freq, axes, (N,), dev)
     kind, cs, st, ks, vs = _paged_cache(k_cache, v_cache, k_scale, v_scale, K, H, dev)
     rc = (_lib or load()).fa_paged_rotary_append_packed(_ROTARY_APPEND(
         q.data_ptr(), sq[0], sq[1], q_out.data_ptr(), ob, ot, oh, k.data_ptr(), sk[0], sk[1],
@@ -645,16 +641,19 @@ def _pool(lens, block_table, shares, free_pages, free_used, lens_out, free_used_
     if dev < 0:
         raise ValueError("lens must be a CUDA tensor")
     B, n_pages, n_free = lens.numel(), shares.numel(), free_pages.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table must have {B} rows, got {tuple(block_table.shape)}")
-    max_pages = block_table.shape[1]
-    if not (_I32 is lens.dtype is block_table.dtype is shares.dtype is free_pages.dtype
-            is free_used.dtype is lens_out.dtype is free_used_out.dtype
+    table = block_table.shape
+    if len(table) != 2 or table[0] != B:
+        raise ValueError(f"block_table must have {B} rows, got {tuple(table)}")
+    max_pages = table[1]
+    if not (_I32 is lens.dtype is block_table.dtype is shares.dtype is free_pages.dtype is free_used.dtype
             and dev == block_table.get_device() == shares.get_device() == free_pages.get_device()
-            == free_used.get_device() == lens_out.get_device() == free_used_out.get_device()
-            and B == lens_out.numel() and 1 == free_used.numel() == free_used_out.numel()
+            == free_used.get_device() and 1 == free_used.numel()
             and lens.is_contiguous() and block_table.is_contiguous() and shares.is_contiguous()
-            and free_pages.is_contiguous() and lens_out.is_contiguous()):
+            and free_pages.is_contiguous()
+            and (lens_out is lens or _I32 is lens_out.dtype and dev == lens_out.get_device()
+                 and B == lens_out.numel() and lens_out.is_contiguous())
+            and (free_used_out is free_used or _I32 is free_used_out.dtype
+                 and dev == free_used_out.get_device() and 1 == free_used_out.numel())):
         for t, n, name in ((lens, B, "lens"), (block_table, B * max_pages, "block_table"),
                            (shares, n_pages, "shares"), (free_pages, n_free, "free_pages"),
                            (free_used, 1, "free_used"), (lens_out, B, "lens_out"),
@@ -737,22 +736,27 @@ def fa_paged_copy(moves, k_cache, v_cache, stream=None, check=True) -> int:
     if dev != _current_device():
         with torch.cuda.device(dev):
             return fa_paged_copy(moves, k_cache, v_cache, stream, check)
-    layers, sl, kc, vc = 1, 0, k_cache, v_cache
-    if k_cache.dim() == 5:
-        layers, sl = k_cache.shape[0], k_cache.stride(0)
-        if v_cache.dim() != 5 or v_cache.shape[0] != layers or (layers > 1 and v_cache.stride(0) != sl):
-            raise ValueError("k_cache and v_cache must have the same layers, with the same stride")
-        if layers == 0:
-            return FA_OK
-        kc, vc = k_cache[0], v_cache[0]
-    if kc.dim() != 4:
+    shape, st, dtype = k_cache.shape, k_cache.stride(), k_cache.dtype
+    if len(shape) == 4:
+        shape, st = (1, *shape), (0, *st)
+    elif len(shape) != 5:
         raise ValueError(f"k_cache must have 4 or 5 dims, got {tuple(k_cache.shape)}")
-    N, K, H = moves.numel() // 3, kc.shape[1], kc.shape[3]
-    kind, cs, st, _, _ = _paged_cache(kc, vc, None, None, K, H, dev)
+    if (v_cache.shape != k_cache.shape or v_cache.dtype is not dtype or k_cache.get_device() != dev
+            or v_cache.get_device() != dev):
+        raise ValueError("k_cache and v_cache must have one type and shape, on the moves' device")
+    sv = v_cache.stride()
+    # (of dims of one, no stride is used)
+    if (st[4] != 1 or sv != st[-len(sv):]) and k_cache.numel() and any(
+            n > 1 and (x != y or i == 4 and x != 1)
+            for i, (n, x, y) in enumerate(zip(shape, st, (0, *sv)[-5:]))):
+        raise ValueError("k_cache and v_cache must have the same strides, innermost 1")
+    if dtype is not _BF16 and dtype is not _E4M3:
+        raise ValueError(f"the cache must be bfloat16 or float8_e4m3fn, got {dtype}")
+    N = moves.numel() // 3
     rc = (_lib or load()).fa_paged_copy_packed(_COPY(
-        _dense(moves, _I32, 3 * N, dev, "moves"), N, k_cache.data_ptr(), v_cache.data_ptr(), kind, sl, st[0],
-        st[1], st[2], layers, K, H, cs[0], cs[2],
-        _current_stream(dev) if stream is None else _raw_stream(stream)))
+        _dense(moves, _I32, 3 * N, dev, "moves"), N, k_cache.data_ptr(), v_cache.data_ptr(),
+        FA_CACHE_BF16 if dtype is _BF16 else FA_CACHE_E4M3, st[0], st[1], st[2], st[3], shape[0], shape[2],
+        shape[4], shape[1], shape[3], _current_stream(dev) if stream is None else _raw_stream(stream)))
     if rc and check:
         _check("fa_paged_copy", rc)
     return rc

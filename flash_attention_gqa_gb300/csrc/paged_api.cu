@@ -15,8 +15,12 @@ using namespace fa;
 
 namespace {
 
-// Bytes of keys and values up to which a call with shared prefixes does not make use of them.
-constexpr double kSharedLeast = 24e6;
+// Bytes of keys and values, each request's counted, up to which a call with shared prefixes does not make use
+// of them: the three grids that it takes more cost 10 to 15 us, and what several requests read comes from
+// L2.  Shared and not, at H = 128: 16 requests x 8 kv heads x 576 keys (38 MB) 21.8 and 10.8 us, x 2112 (138
+// MB) 22.6 and 18.6, x 8256 (541 MB) 25.9 and 51; 64 x 8 x 576 (151 MB) 26 to 30 and 22, x 2112 (554 MB) 32
+// and 53; in e4m3 64 x 8 x 2112 (277 MB) 33 and 38.
+constexpr double kSharedLeast = 200e6;
 
 bool decode_shape_ok(int B, int K, int G, int T, int H) {
   return head_dim_ok(H) && (int64_t)G * T <= kMaxPagedRows && B <= kMaxPagedBatch &&
@@ -188,11 +192,9 @@ int fa_paged_decode_shared(const void* q, const void* k_cache, const void* v_cac
   const PagedSharedPlan plan = paged_shared_plan(B, K, G * T, H, n_groups, n_members, fa_device_sm_count());
   if (!usable(workspace, 256) || workspace_bytes < std::max(plan.total, paged_decode_plan(G * T, H, fa_device_sm_count()).total))
     return FA_ERR_INVALID_ARG;
-  // The prefixes' grid and what it takes to bring its results together cost some 8 us.  Where all keys, as
-  // far as the tables reach, are read faster than that even once for each request, they are.  (4 requests x 2
-  // kv heads x 552 keys at H = 256: 17.6 us and 10; see kSharedLeast.)
+  // (as far as the tables reach: the lengths are on the device.  With a group for every member nothing is shared.)
   const double keys = (double)n_members * max_pages * page_size * K * H * (cache_type == FA_CACHE_BF16 ? 4 : 2);
-  if (n_groups == 0 || keys <= kSharedLeast)
+  if (n_groups >= n_members || keys <= kSharedLeast)
     return fa_paged_decode(q, k_cache, v_cache, cache_type, k_scale, v_scale, page_stride, head_stride,
                            token_stride, block_table, lens, 0, o, lse, workspace, workspace_bytes, B, K, G, T, H,
                            n_pages, page_size, max_pages, stream);

@@ -124,9 +124,9 @@ __device__ __forceinline__ void head_copies(const PagedHeadArgs& s, const Decode
       cp_async_arrive(bar);
     }
   }
-  // Where a wait has run out, here or elsewhere, what is in flight lands before the CTA ends.
+  // What is in flight lands before the CTA ends, whichever wait may run out, here or elsewhere, now or later.
   cp_async_wait<0>();
-  if (!ok || *ab.flag) landed(n);
+  landed(n);
 }
 
 // A converting warp's work, 8-bit caches: rows [w * KPW, (w + 1) * KPW) of every tile of K or of V from bytes

@@ -38,7 +38,7 @@ class Problem:
         need = sum(P.up(p + t, page) for p, t, _ in sizes)
         perm = torch.randperm(need + 3, generator=gen).tolist()
         # wide: a table that reaches far enough for the groups to be looked at (small calls do not)
-        width = max([P.up(p + t, page) for p, t, _ in sizes] + [0, 65536 // page if wide else 0]) + 2
+        width = max([P.up(p + t, page) for p, t, _ in sizes] + [0, (1 << 20) // page if wide else 0]) + 2
         table, lens = torch.full((B, width), -1, dtype=torch.int32), [0] * B
         owned = torch.zeros(need + 3, page, dtype=torch.bool)
         at, first, copies = 0, {}, []

@@ -19,7 +19,7 @@ def _i32(x):
 
 @pytest.mark.parametrize("dtype", [BF16, E4M3], ids=["bf16", "e4m3"])
 def test_serving(lib, dtype):
-    B, K, G, H, page, n_pages, cols = 10, 2, 4, 128, 16, 2000, 1024     # (wide tables: the groups are used)
+    B, K, G, H, page, n_pages, cols = 10, 2, 4, 128, 16, 2000, 8192     # (wide tables: the groups are used)
     gen = torch.Generator(device="cuda").manual_seed(5)
     rng = np.random.default_rng(5)
     caches = [torch.full((n_pages, K, page, H), float("nan"), device="cuda").to(dtype) for _ in range(2)]
