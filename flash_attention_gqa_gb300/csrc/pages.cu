@@ -38,7 +38,7 @@ __device__ __forceinline__ int scan_before(int x, int* warp_sums, int& total) {
   __syncthreads();   // (of an earlier call's sums)
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
-  int sums = warp_sums[lane];
+  int sums = lane < kWarps ? warp_sums[lane] : 0;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int y = __shfl_up_sync(~0u, sums, d);
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_free_kernel(const __grid_co
   extern __shared__ uint32_t bits[];
   __shared__ uint32_t seen[kMaxPagedBatch / 32];   // rows of the call
   __shared__ KeptRow kept[kRowsKept];
-  __shared__ int warp_sums[32], total;
+  __shared__ int warp_sums[32], totals[kCtas];
   const cg::cluster_group cluster = cg::this_cluster();
   const PagesPool& p = a.p;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = cluster.block_rank();
@@ -169,13 +169,12 @@ __global__ void __launch_bounds__(kThreads, 1) pages_free_kernel(const __grid_co
   for (int w = tid * per; w < min((tid + 1) * per, set.words); ++w) count += __popc(bits[w]);
   int here;
   scan_before(count, warp_sums, here);
-  if (tid == 0) total = here;
-  cluster.sync();
+  if (tid < kCtas) cluster.map_shared_rank(totals, tid)[rank] = here;
+  cluster.sync();   // (behind it, each CTA reads what is its own)
   int all = 0, before = 0;
   for (int c = 0; c < kCtas; ++c) {
-    const int x = *cluster.map_shared_rank(&total, c);
-    if (c < rank) before += x;
-    all += x;
+    if (c < rank) before += totals[c];
+    all += totals[c];
   }
   const bool over = !fail && all > used;   // more pages than the list has given out
   if (over) {
@@ -215,22 +214,30 @@ __global__ void __launch_bounds__(kThreads, 1) pages_free_kernel(const __grid_co
         if (row >= 0) a.lens_out[row] = a.keep ? a.keep[i] : 0;
       }
   }
-  cluster.sync();   // nobody's shared memory goes before all have read it
 }
 
 // ------------------------------------------------------------------- fork
 
 // A child takes its parent's full pages, whose share counts rise, and a fresh page for the tokens of
-// a last one that is not full: those are to be copied, and the list says so.
+// a last one that is not full: those are to be copied, and the list says so.  Children of one parent that
+// take the same of it raise a page's count together, by one of them: scattered atomics go 32 cycles a
+// warp (128 children of 512 pages: 65536 of them or 512).
 __global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const __grid_constant__ PagesForkArgs a) {
   extern __shared__ int fresh[];   // [N] free pages taken before the entry
-  __shared__ uint32_t seen[kMaxPagedBatch / 32];
+  int* const lead = fresh + a.N;   // [B] first entry of a parent
+  int* const count = lead + a.p.B; // [B] its entries
+  __shared__ uint32_t seen[kMaxPagedBatch / 32];    // children
+  __shared__ uint32_t mixed[kMaxPagedBatch / 32];   // parents whose children take different lengths
   __shared__ int warp_sums[32];
   const cg::cluster_group cluster = cg::this_cluster();
   const PagesPool& p = a.p;
   const int tid = threadIdx.x, rank = cluster.block_rank();
   const int P = 1 << p.page_shift;
-  for (int i = tid; i < kMaxPagedBatch / 32; i += kThreads) seen[i] = 0;
+  for (int i = tid; i < kMaxPagedBatch / 32; i += kThreads) seen[i] = mixed[i] = 0;
+  for (int b = tid; b < p.B; b += kThreads) {
+    lead[b] = a.N;
+    count[b] = 0;
+  }
   __syncthreads();
   const int used = *p.free_used;
   const long long most = (long long)p.max_pages << p.page_shift;
@@ -248,12 +255,18 @@ __global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const __grid_co
     const int held = p.lens[parent], n = length(i, parent);
     bad |= p.lens[child] != 0 || held < 0 || held > most || n < 0 || n > held;
     need += (n & (P - 1)) != 0;
+    atomicMin(&lead[parent], i);
+    atomicAdd(&count[parent], 1);
   }
   int all;
   int k = scan_before(need, warp_sums, all);
   for (int i = i0; i < i1; ++i) {   // (the scan's barriers: all children are in `seen`)
     const int parent = a.parents[i];
-    bad |= parent >= 0 && parent < p.B && (seen[parent >> 5] >> (parent & 31) & 1) != 0;
+    if (parent < 0 || parent >= p.B) continue;
+    bad |= (seen[parent >> 5] >> (parent & 31) & 1) != 0;
+    const int first = lead[parent];
+    if (a.fork_lens && first < a.N && a.fork_lens[i] != a.fork_lens[first])
+      atomicOr(&mixed[parent >> 5], 1u << (parent & 31));
   }
   const bool fail = __syncthreads_or(bad || all > p.n_free - used);
   if (!fail)
@@ -292,10 +305,12 @@ __global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const __grid_co
         if (!both) atomicOr(p.err, (uint32_t)DEV_BAD_VALUE);
       } else if (j < full) {
         a.table[(int64_t)a.children[i] * p.max_pages + j] = page;
-        if (known(page))
-          atomicAdd(&p.shares[page], 1);
-        else
+        if (!known(page))
           atomicOr(p.err, (uint32_t)DEV_BAD_VALUE);
+        else if (mixed[parent >> 5] >> (parent & 31) & 1)
+          atomicAdd(&p.shares[page], 1);
+        else if (lead[parent] == i)
+          atomicAdd(&p.shares[page], count[parent]);
       }
       if (j == 0 && !part) {
         copy[0] = copy[1] = -1;
@@ -540,7 +555,7 @@ cudaError_t launch_pages_free(const PagesFreeArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_pages_fork(const PagesForkArgs& a, cudaStream_t st) {
-  return launch_cluster(pages_fork_kernel, a, (size_t)a.N * 4, kMaxPagedBatch * 4, st);
+  return launch_cluster(pages_fork_kernel, a, ((size_t)a.N + 2 * (size_t)a.p.B) * 4, kMaxPagedBatch * 12, st);
 }
 
 cudaError_t launch_pages_compact(const PagesCompactArgs& a, cudaStream_t st) {
