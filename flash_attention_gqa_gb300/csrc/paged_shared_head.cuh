@@ -54,12 +54,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-// A copying warp's work: every tile of K or of V (`kind`), into its place as that becomes free.  By TMA, a lane a box of one page's rows, in one instruction:
-// cp.async by 16 bytes a lane keeps the load and store pipe busy for 2600 cycles a tile, more than all the
-// rest of it takes.  Rows past the prefix have to be zeros, which a box can give for whole pages only (out
-// of the map's range): a tile that ends inside a page goes by cp.async, as does everything where there is
-// no map.  `place(n, ..)` waits until tile n's is free and gives its address and barrier, `landed(n)` until
-// the tiles before n that may be on their way have come.
+// A copying warp's work: every tile of K or of V (`kind`), into its place as that becomes free.  By TMA,
+// a lane a box of one page's rows, in one instruction: cp.async by 16 bytes a lane keeps the load and store
+// pipe busy for 2600 cycles a tile, more than all the rest of it takes.  Rows past the prefix have to be
+// zeros, which a box can give for whole pages only (out of the map's range): a tile that ends inside a page
+// goes by cp.async, as does everything where there is no map.  `place(n, ..)` waits until tile n's is free
+// and gives its address and barrier, `landed(n)` until the tiles before n that may be on their way have come.
 template <class C, class Place, class Landed>
 __device__ __forceinline__ void head_copies(const PagedHeadArgs& s, const DecodeShape<C>& shape, DecodeWalk walk,
                                             const DecodeEnd& last, int kind, const Abort& ab, Place place,

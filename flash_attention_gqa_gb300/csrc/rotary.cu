@@ -207,12 +207,15 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
         *reinterpret_cast<uint4*>(dst + uy * 16) = isv ? c.y : pack(y);
       } else {
         // From fp32, by the scale's reciprocal: 1.5 * 2^-24 off before the rounding to e4m3's 2^-4 (a
-        // division per value takes twice the time of everything else).
+        // division per value takes twice the time of everything else).  `up` keeps the reciprocal a normal
+        // number: 0 / 1e-39 is 0, and 0 times an infinite reciprocal is none.
         const float* const scales = isv ? a.v_scale : a.k_scale;
-        const float s = scales ? 1.0f / scales[h] : 1.0f;
-        auto squeeze = [s](const float (&f)[8]) {
-          return make_uint2(to_e4m3x4(f[0] * s, f[1] * s, f[2] * s, f[3] * s),
-                            to_e4m3x4(f[4] * s, f[5] * s, f[6] * s, f[7] * s));
+        const float scale = scales ? scales[h] : 1.0f;
+        const float up = fabsf(scale) < 0x1p-64f ? 0x1p64f : fabsf(scale) > 0x1p64f ? 0x1p-64f : 1.0f;
+        const float s = 1.0f / (scale * up);
+        auto squeeze = [s, up](const float (&f)[8]) {
+          return make_uint2(to_e4m3x4(f[0] * s * up, f[1] * s * up, f[2] * s * up, f[3] * s * up),
+                            to_e4m3x4(f[4] * s * up, f[5] * s * up, f[6] * s * up, f[7] * s * up));
         };
         *reinterpret_cast<uint2*>(dst + ux * 8) = squeeze(x);
         *reinterpret_cast<uint2*>(dst + uy * 8) = squeeze(y);

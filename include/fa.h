@@ -402,9 +402,11 @@ int fa_rotary(const void* q, int64_t q_batch_stride, int64_t q_token_stride, int
  * and written with the values into the cache's pages, as fa_paged_append would.
  * q [N, q_heads, H], k and v [N, k_heads, H], positions (axis, n) and slots [N], with
  * N = B * T tokens, token n = b * T + t; q_out through strides (batch, token,
- * head).  A key for an e4m3 cache is divided by its scale and rounded from
- * float32, once.  Tokens with slot < 0 are skipped, their row of q_out too;
- * slots, scales and the cache otherwise as in fa_paged_append.
+ * head).  An e4m3 cache gets float32 values times the float32 reciprocal of
+ * their scale, rounded once (values within 2^-23 of the middle between two of
+ * e4m3 may go the other way than fa_paged_append's quotients).  Tokens with
+ * slot < 0 are skipped, their row of q_out too; slots, scales and the cache
+ * otherwise as in fa_paged_append.
  */
 int fa_paged_rotary_append(const void* q, int64_t q_token_stride, int64_t q_head_stride,
                            void* q_out, int64_t q_out_batch_stride, int64_t q_out_token_stride,

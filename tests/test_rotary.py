@@ -292,6 +292,30 @@ def test_rotary_append(lib, case, adjacent, dtype):
     _ok()
 
 
+@pytest.mark.parametrize("scale", [1e-39, 2e-38, 1e38, 3e38])
+def test_rotary_append_scales_at_the_ends_of_their_range(lib, scale):
+    # positions of zero: keys stay as they are, and only the scale and e4m3 are left
+    case = (1, 40, 0, 2, 1, 64, 32, 1, 8, "head", 0)
+    data = list(_append(case, E4M3))
+    k, v = data[1].contiguous(), data[2].contiguous()
+    big = scale * 20 if scale < 1 else 3e38
+    for x in (k, v):
+        x.copy_((x.float() * big / 4).clamp(-3e38, 3e38))
+        x[::3, :, ::2] = 0
+    scales = torch.full((2,), scale)
+    dev = [P.to_device(c, "cuda") for c in data[7]]
+    binding.fa_paged_rotary_append(data[0].cuda(), k.cuda(), v.cuda(), torch.zeros_like(data[3]).cuda(),
+                                   data[4].cuda(), data[6].cuda(), data[9].cuda(), *dev, None, scales.cuda(),
+                                   scales.cuda())
+    _ok()
+    at = data[6]
+    for x, c in zip((k, v), dev):
+        rows = c.cpu().contiguous().view(torch.uint8)[at // 8, :, at % 8].view(E4M3).double()
+        ref = (x.double() / scales.double()[0]).clamp(-448, 448)
+        tol = torch.maximum(2.0 ** -4 * ref.abs(), torch.tensor(2.0 ** -10).double())
+        assert ((rows - ref).abs() <= tol * (1 + 2.0 ** -20)).all()
+
+
 def test_rotary_append_slots_past_the_cache(lib):
     case = (1, 20, 0, 2, 2, 64, 32, 1, 8, "head", 0)
     data = list(_append(case, BF16))
