@@ -135,12 +135,18 @@ struct PagedSharedArgs {
   float* head_whole;           // partials of whole items, by the chunks' bases
   const int32_t *members, *group_starts, *prefix_lens;   // the caller's
   int n_members, n_groups, max_chunks;
-  int head_ctas, tail_ctas;
+  int head_ctas, tail_ctas, tail_parts;   // (parts: that the requests' own keys are dealt to)
 };
+
+// Whether the requests' own keys go to single warps (DecodeCfg::SOLO; not where a CTA's warps share the
+// queries' fragments): with two items for each CTA.
+inline bool paged_tail_solo(int64_t items, int R, int H, int ctas) {
+  return items >= 2 * ctas && (R <= 8 || (R <= 16 && H <= 128) || (R <= 32 && H == 64));
+}
 
 // Its workspace: the tables that the first kernel writes, splits, partials.
 struct PagedSharedPlan {
-  int max_chunks, head_ctas, tail_ctas;
+  int max_chunks, head_ctas, tail_ctas, tail_parts;
   size_t begins, places, members, n_chunks, chunks, head_splits, tail_splits, head_partials, tail_partials,
       head_whole, tail_whole, total;
 };
@@ -150,6 +156,7 @@ inline PagedSharedPlan paged_shared_plan(int B, int K, int R, int H, int n_group
   p.max_chunks = (int)((rows + 127) / 128) + (n_groups < n_members ? n_groups : n_members);
   p.head_ctas = sm_count;
   p.tail_ctas = paged_decode_plan(R, H, sm_count).ctas;
+  p.tail_parts = p.tail_ctas * (paged_tail_solo((int64_t)B * K, R, H, p.tail_ctas) ? 4 : 1);
   size_t at = 0;
   auto take = [&](int64_t bytes) {
     const size_t here = at;
@@ -165,7 +172,7 @@ inline PagedSharedPlan paged_shared_plan(int B, int K, int R, int H, int n_group
   p.head_splits = take((int64_t)p.max_chunks * K * split);
   p.tail_splits = take((int64_t)B * K * split);
   p.head_partials = take((int64_t)p.head_ctas * 2 * paged_partial_floats(128, H) * 4);
-  p.tail_partials = take((int64_t)p.tail_ctas * 2 * paged_partial_floats(R, H) * 4);
+  p.tail_partials = take((int64_t)p.tail_parts * 2 * paged_partial_floats(R, H) * 4);
   p.head_whole = take((rows + 8 * (int64_t)p.max_chunks) * K * (H + 2) * 4);
   p.tail_whole = take((int64_t)B * K * paged_partial_floats(R, H) * 4);
   p.total = at;

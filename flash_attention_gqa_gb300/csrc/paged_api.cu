@@ -218,7 +218,7 @@ int fa_paged_decode_shared(const void* q, const void* k_cache, const void* v_cac
   s.head_whole = reinterpret_cast<float*>(ws + plan.head_whole);
   s.members = members; s.group_starts = group_starts; s.prefix_lens = prefix_lens;
   s.n_members = n_members; s.n_groups = n_groups; s.max_chunks = plan.max_chunks;
-  s.head_ctas = plan.head_ctas; s.tail_ctas = plan.tail_ctas;
+  s.head_ctas = plan.head_ctas; s.tail_ctas = plan.tail_ctas; s.tail_parts = plan.tail_parts;
   a.wait_limit_ns = device_wait_limit_ns();
   a.err = device_error_word();
   if (!a.err || plan.tail_ctas == 0) return FA_ERR_CUDA;

@@ -150,9 +150,12 @@ constexpr float kBelow = F16 ? 11.0f : 0.0f;
 // ------------------------------------------------------------ configuration
 // NT: n-tiles of 8 query rows per warp.  WR: warps of a team, which share a ring
 // and the keys in it, NT * 8 rows each.
-template <int H_, bool E4M3_, int NT_, int WR_, DecodeMode MODE_ = DECODE_ALL>
+// SOLO (TAIL): the units are dealt to the warps, each of which does what else a CTA does: many short
+// items (paged_tail_solo) lose most of their time where a CTA's warps meet.
+template <int H_, bool E4M3_, int NT_, int WR_, DecodeMode MODE_ = DECODE_ALL, bool SOLO_ = false>
 struct DecodeCfg {
   static constexpr DecodeMode MODE = MODE_;
+  static constexpr bool SOLO = SOLO_;
   static constexpr int H = H_, NT = NT_, WR = WR_;
   static constexpr bool TC = false, E4M3 = E4M3_, TEAM = WR > 1;
   static constexpr int ROWB = E4M3 ? H : 2 * H;        // bytes of a key
@@ -162,17 +165,19 @@ struct DecodeCfg {
   static constexpr int SLOT = 2 * HALF;
   static constexpr int WARPS = TEAM ? 8 : 4;
   static constexpr int THREADS = WARPS * 32;
-  static constexpr int TEAMS = WARPS / WR;
+  static constexpr int RINGS = WARPS / WR;
+  static constexpr int TEAMS = SOLO ? 1 : RINGS;       // that share an item
   static constexpr int TK = TEAMS * CK;                // keys of a tile
-  static constexpr int ITEM_UNITS = 8 / TEAMS;         // an item's fixed cost, in tiles (below)
+  static constexpr int ITEM_UNITS = SOLO ? 4 : 8 / TEAMS;   // an item's fixed cost, in tiles (below)
   static constexpr bool QSMEM = TEAM || H * NT > 256;  // query fragments in shared memory
   static constexpr int QTILES = WR * NT;
   static constexpr int QBYTES = QSMEM ? H / 16 * QTILES * 32 * 8 : 0;
   // Streams of one warp: 24 KB of ring a warp up to H = 128 (two CTAs an SM,
   // up to 128 KB of copies in flight on it), 48 KB at H = 256 (one CTA).  Teams:
   // what the queries leave of 212 KB.
-  static constexpr int STAGES = TEAM ? (212 * 1024 - QBYTES) / (TEAMS * SLOT) : (H == 256 ? 48 : 24) * 1024 / SLOT;
-  static constexpr int RING = TEAMS * STAGES * SLOT;
+  static constexpr int STAGES = TEAM ? (212 * 1024 - QBYTES) / (RINGS * SLOT) : (H == 256 ? 48 : 24) * 1024 / SLOT;
+  static constexpr int RING = RINGS * STAGES * SLOT;
+  static_assert(!SOLO || (MODE == DECODE_TAIL && !TEAM && !QSMEM), "");
   static constexpr int SMEM = RING + QBYTES;
   static constexpr int MIN_CTAS = !TEAM && H <= 128 ? 2 : 1;
   static_assert(TEAM || (NT < 2 ? NT : 2) * 8 * H * 4 <= SLOT, "16 rows of a warp's O^T fit in a ring slot");
@@ -309,11 +314,11 @@ struct DecodeShape {
 template <class C>
 struct DecodeShared {
   long long scan[C::WARPS];
-  DecodeEnd ends[2];   // first and last unit
+  DecodeEnd ends[C::SOLO ? 2 * C::WARPS : 2];   // first and last unit (SOLO: of each warp)
 };
 
-// Finds this CTA's units, by all its threads, and enters its first item; false
-// where it has no tile.
+// Finds this CTA's units (SOLO: this warp's), by all its threads, and enters the first item; false
+// where there is no tile.
 template <class C>
 __device__ __forceinline__ bool decode_units(const PagedDecodeArgs& a, DecodeShared<C>& sh, DecodeWalk& walk) {
   constexpr int threads = C::THREADS;
@@ -324,11 +329,23 @@ __device__ __forceinline__ bool decode_units(const PagedDecodeArgs& a, DecodeSha
   const int b0 = min(tid * per, B), b1 = min(b0 + per, B);
   long long mine = 0;
   DecodeSpan keys{0, 0, 0};   // of the last of this thread's requests
-  for (int b = b0; b < b1; ++b) {
-    keys = shape.span(b);
-    if (C::MODE != DECODE_HEAD && blockIdx.x == 0 && a.lens[b] != keys.len) atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
-    mine += (long long)(shape.tiles(keys) + C::ITEM_UNITS) * a.K;
-  }
+  // Four requests' loads in flight, `use` in their order.
+  auto requests = [&](auto use) {
+#pragma unroll 1
+    for (int b = b0; b < b1; b += 4) {
+      DecodeSpan s[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[j] = shape.span(min(b + j, b1 - 1));
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (b + j < b1) use(b + j, s[j]);
+    }
+  };
+  requests([&](int b, const DecodeSpan& s) {
+    if (C::MODE != DECODE_HEAD && blockIdx.x == 0 && a.lens[b] != s.len) atomicOr(a.err, (uint32_t)DEV_BAD_VALUE);
+    keys = s;
+    mine += (long long)(shape.tiles(s) + C::ITEM_UNITS) * a.K;
+  });
   long long inc = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -343,30 +360,41 @@ __device__ __forceinline__ bool decode_units(const PagedDecodeArgs& a, DecodeSha
     total += sh.scan[w];
   }
   // CTA i: total / ctas units, and one more where i < total % ctas
-  const int ctas = (int)min((long long)gridDim.x, total), i = blockIdx.x;
-  if (i >= ctas) {
+  constexpr int mine_of = C::SOLO ? C::WARPS : 1;   // that this CTA deals out
+  const int all = gridDim.x * mine_of, ctas = (int)min((long long)all, total);
+  const int at_warp = C::SOLO ? __shfl_sync(~0u, warp, 0) : 0, i = blockIdx.x * mine_of + at_warp;
+  if (!C::SOLO && i >= ctas) {
     if (tid == 0 && !a.by_item && !a.unsplit) a.splits[i] = PagedDecodeSplit{0, -1, 0, 0};
     return false;
   }
   const long long each = quotient(total, ctas), over = total - each * ctas;
-  const long long t0 = i * each + min((long long)i, over), t1 = t0 + each + (i < over ? 1 : 0);
+  auto first_unit = [&](int i) { return i * each + min((long long)i, over); };
   const long long at = before + inc - mine;
-  if (t0 < at + mine && t1 - 1 >= at) {   // the requests that hold the first and the last unit
-    long long x = at;
-    for (int b = b0; b < b1; ++b) {
-      if (per > 1) keys = shape.span(b);
-      const long long next = x + (long long)(shape.tiles(keys) + C::ITEM_UNITS) * a.K;
-      if (t0 >= x && t0 < next) sh.ends[0] = DecodeEnd{b, keys, t0 - x};
-      if (t1 - 1 >= x && t1 - 1 < next) sh.ends[1] = DecodeEnd{b, keys, t1 - 1 - x};
-      x = next;
+#pragma unroll
+  for (int w = 0; w < mine_of; ++w) {
+    const long long t0 = first_unit(blockIdx.x * mine_of + w), t1 = first_unit(blockIdx.x * mine_of + w + 1);
+    if (t0 < at + mine && t1 - 1 >= at) {   // the requests that hold the first and the last unit
+      long long x = at;
+      auto find = [&](int b, const DecodeSpan& s) {
+        const long long next = x + (long long)(shape.tiles(s) + C::ITEM_UNITS) * a.K;
+        if (t0 >= x && t0 < next) sh.ends[2 * w] = DecodeEnd{b, s, t0 - x};
+        if (t1 - 1 >= x && t1 - 1 < next) sh.ends[2 * w + 1] = DecodeEnd{b, s, t1 - 1 - x};
+        x = next;
+      };
+      if (per == 1) find(b0, keys);   // (it has a unit, so it has a request)
+      else requests(find);
     }
   }
   __syncthreads();
-  const DecodePlace head = shape.place(sh.ends[0]), tail = shape.place(sh.ends[1]);
-  if (tid == 32 && !a.unsplit) {
+  if (C::SOLO && i >= ctas) return false;
+  const long long t0 = first_unit(i), t1 = first_unit(i + 1);
+  const DecodeEnd& begins = sh.ends[2 * at_warp];
+  const DecodeEnd& ends = sh.ends[2 * at_warp + 1];
+  const DecodePlace head = shape.place(begins), tail = shape.place(ends);
+  if ((C::SOLO ? lane == 0 : tid == 32) && !a.unsplit) {
     // the item that the units end in, where it begins here and goes on in the
     // next CTA: for the join, with its last CTA
-    const int tiles = shape.tiles(sh.ends[1].keys);
+    const int tiles = shape.tiles(ends.keys);
     const long long first = t1 - 1 - tail.rem + C::ITEM_UNITS;   // its first tile's unit
     const bool split = tail.rem >= C::ITEM_UNITS && tail.rem + 1 < tiles + C::ITEM_UNITS && first >= t0;
     if (split || !a.by_item) {
@@ -376,7 +404,7 @@ __device__ __forceinline__ bool decode_units(const PagedDecodeArgs& a, DecodeSha
       a.splits[a.by_item ? item : i] = PagedDecodeSplit{item, split ? i : -1, (int)last, 0};
     }
   }
-  return shape.begin(walk, head, sh.ends[0].keys, tail);
+  return shape.begin(walk, head, begins.keys, tail);
 }
 
 // Whether any 16-bit (bf16) or 8-bit (e4m3) value of the `bytes` at `p` is not
@@ -449,8 +477,9 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
 
   // ---- copies: lane r looks up key r of the next slot one slot early, then all
   // lanes copy 16-byte units of it
-  const int team = warp / WR, wr = warp % WR;
-  char* const ring = smem + team * S * C::SLOT;
+  const int team = C::SOLO ? 0 : warp / WR, wr = warp % WR;
+  const DecodeEnd& last = sh.ends[C::SOLO ? 2 * warp + 1 : 1];
+  char* const ring = smem + warp / WR * S * C::SLOT;
   const uint32_t ring_u = smem_u32(ring);
   int64_t key_off = -1;   // lane r: byte offset of key r of the slot to come, -1: zeros
   int key_page = -1, key_in = 0, key_head = 0;
@@ -518,7 +547,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       }
     }
     cp_async_commit();
-    if (more && ++ahead.tile == ahead.end) more = shape.next_item(ahead, sh.ends[1]);
+    if (more && ++ahead.tile == ahead.end) more = shape.next_item(ahead, last);
     look_up();
   };
   look_up();
@@ -891,7 +920,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       }
     const bool whole = walk.begun == 0 && walk.end == walk.tiles;
     DecodeWalk then = walk;
-    const bool go_on = shape.next_item(then, sh.ends[1]);
+    const bool go_on = shape.next_item(then, last);
     if (EARLY && go_on) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) load_q(then, nt, q_next[EARLY ? nt : 0]);
@@ -903,7 +932,8 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
     // (TAIL: a whole item's place is by the item.)
     float* const mine = C::MODE == DECODE_TAIL && whole
                             ? a.shared.whole + item * paged_partial_floats(R, H)
-                            : a.partials + ((int64_t)blockIdx.x * 2 + (walk.begun == 0 ? 1 : 0)) * paged_partial_floats(R, H);
+                            : a.partials + ((C::SOLO ? (int64_t)blockIdx.x * WARPS + warp : (int64_t)blockIdx.x) * 2 +
+                                             (walk.begun == 0 ? 1 : 0)) * paged_partial_floats(R, H);
     const bool finished = C::MODE == DECODE_ALL && whole;
     auto put = [&](int r, int d, float4 x, float M, float L) {   // four dims of row r
       if (finished) put_result((char*)a.o + out_row * H * 2, a.lse + out_row, H, r, d, x, M, L, vscale);
@@ -943,23 +973,25 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
               sh_l[warp][nt * 8 + 2 * c + j] = l[n0 + nt][j];
             }
         }
-        __syncthreads();
+        if (C::SOLO) __syncwarp(); else __syncthreads();
         const int rows = min(NR * 8, R - n0 * 8);
-        for (int i = tid; i < rows * (H / 4); i += threads) {
+        for (int i = C::SOLO ? lane : tid; i < rows * (H / 4); i += C::SOLO ? 32 : threads) {
           const int r = i / (H / 4), d = i % (H / 4) * 4;
-          float M = sh_m[0][r], L = 0.0f;
+          constexpr int parts = C::SOLO ? 1 : WARPS;   // of this CTA's: the other warps' items are others
+          const int w0 = C::SOLO ? warp : 0;
+          float M = sh_m[w0][r], L = 0.0f;
 #pragma unroll
-          for (int w = 1; w < WARPS; ++w) M = fmaxf(M, sh_m[w][r]);
+          for (int w = 1; w < parts; ++w) M = fmaxf(M, sh_m[w][r]);
           const float base = M == -INFINITY ? 0.0f : M;
           float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           // every warp's ring has the same slot at the same place
-          const float* at = reinterpret_cast<const float*>(smem + ((const char*)so - ring)) + r * H +
+          const float* at = reinterpret_cast<const float*>(C::SOLO ? (const char*)so : smem + ((const char*)so - ring)) + r * H +
                             (d ^ (((r >> 1) & 3) << 3));
 #pragma unroll
-          for (int w = 0; w < WARPS; ++w) {
-            const float f = fast_exp2(sh_m[w][r] - base);
+          for (int w = 0; w < parts; ++w) {
+            const float f = fast_exp2(sh_m[w0 + w][r] - base);
             const float4 y = *reinterpret_cast<const float4*>(at + w * (S * C::SLOT / 4));
-            L += sh_l[w][r] * f;
+            L += sh_l[w0 + w][r] * f;
             x.x += y.x * f;
             x.y += y.y * f;
             x.z += y.z * f;
@@ -967,7 +999,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
           }
           put(n0 * 8 + r, d, x, M, L);
         }
-        __syncthreads();
+        if (C::SOLO) __syncwarp(); else __syncthreads();
       }
     } else {
       // Teams are joined in pairs, an n-tile at a time: a lane of the one adds
@@ -1061,7 +1093,7 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       }
     }
 
-    if (whole && a.by_item && !a.unsplit && tid == 0) a.splits[item] = PagedDecodeSplit{(int)item, -1, 0, 0};
+    if (whole && a.by_item && !a.unsplit && (C::SOLO ? lane == 0 : tid == 0)) a.splits[item] = PagedDecodeSplit{(int)item, -1, 0, 0};
     if (!go_on) break;
     walk = then;
   }

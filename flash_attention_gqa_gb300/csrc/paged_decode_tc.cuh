@@ -36,7 +36,7 @@ template <int H_, bool E4M3_, DecodeMode MODE_ = DECODE_ALL>
 struct DecodeTcCfg {
   static constexpr DecodeMode MODE = MODE_;
   static constexpr int H = H_, HC = H / 64;
-  static constexpr bool TC = true, E4M3 = E4M3_;
+  static constexpr bool TC = true, E4M3 = E4M3_, SOLO = false;
   static constexpr int TN = H == 256 ? 64 : 128;        // keys of a tile
   static constexpr int CK = TN, TEAMS = 1, TK = TN;
   // An item's fixed cost in tiles.  64 requests of 1 to 8192 keys, 64 rows: 46.4 us with 1,

@@ -33,7 +33,7 @@ paged_shared_join_kernel(const __grid_constant__ PagedSharedArgs s, int per, int
   const int4 tail = __ldcg(reinterpret_cast<const int4*>(a.splits) + item);
   const int place = r < R ? __ldcg(a.shared.places + b) : -1;
   // (an entry may hold anything where a wait ran out before it was written)
-  const bool tail_split = tail.y >= 0 && tail.z >= tail.y && tail.z < s.tail_ctas;
+  const bool tail_split = tail.y >= 0 && tail.z >= tail.y && tail.z < s.tail_parts;
   const int n_tail = tail_split ? tail.z - tail.y + 1 : 1;
   const int64_t part = paged_partial_floats(R, H), part_head = paged_partial_floats(128, H);
   const float* const tail_at = tail_split ? a.partials + (int64_t)tail.y * 2 * part : a.shared.whole + item * part;
@@ -162,7 +162,7 @@ cudaError_t launch_shared_join(const PagedSharedArgs& s, cudaStream_t st) {
   // items are at least the rows in chunks times the heads.  Several shares of them where they are many,
   // as far as all threads are there at once (156 items of 20 partials: 25 us with 16 shares, 1248 CTAs of 512).
   const int chunks = max(1, max(min(s.n_groups, s.n_members / 2), (int)((int64_t)s.n_members * R / 128)));
-  const int partials = s.tail_ctas / items + 2 + s.head_ctas / (chunks * s.tail.K) + 2;
+  const int partials = s.tail_parts / items + 2 + s.head_ctas / (chunks * s.tail.K) + 2;
   const int64_t room = (int64_t)s.head_ctas * 1024 / ((int64_t)items * elements);
   const int shares = partials <= 8 || room < 2 ? 1 : partials <= 16 || room < 4 ? 2 : room < 16 ? 4 : 16;
   int per = shares == 16 ? 32 : shares == 4 ? 64 : 256 / shares;
@@ -188,6 +188,22 @@ cudaError_t launch_shared_grids(const PagedSharedArgs& s, const PagedHeadArgs& h
   return launch_shared_join<H, C::TC>(s, st);
 }
 
+// Up to NT * 8 rows.
+template <int H, bool E4M3, int NT>
+cudaError_t launch_shared_rows(const PagedSharedArgs& s, const PagedHeadArgs& head, cudaStream_t st,
+                               cudaError_t (*launch_head)(const PagedHeadArgs&, int, cudaStream_t)) {
+  constexpr int tiles = H == 256 && NT == 4 ? 2 : NT;
+  if constexpr (H * NT <= 256) {
+    if (s.tail_parts > s.tail_ctas) {
+      using C = DecodeCfg<H, E4M3, NT, 1, DECODE_TAIL, true>;
+      static_assert(C::WARPS == 4, "as in paged_shared_plan");
+      return launch_shared_grids<H, C, paged_decode_kernel<C>>(s, head, st, launch_head);
+    }
+  }
+  using C = DecodeCfg<H, E4M3, tiles, NT / tiles, DECODE_TAIL>;
+  return launch_shared_grids<H, C, paged_decode_kernel<C>>(s, head, st, launch_head);
+}
+
 // The kernel for a request's own keys goes by its rows, as in launch_decode_rows.
 template <int H, bool E4M3>
 cudaError_t launch_shared(const PagedSharedArgs& s, cudaStream_t st) {
@@ -205,18 +221,10 @@ cudaError_t launch_shared(const PagedSharedArgs& s, cudaStream_t st) {
                      make_cache_map(&head.v_map, s.tail.v_cache, s.tail.lay, s.tail.K, H, E4M3, head.rows)))
     head.rows = 0;
   auto* const launch_head = launch_shared_part<Head, PagedHeadArgs, paged_head_kernel<Head>>;
-  if (R <= 8) {
-    using C = DecodeCfg<H, E4M3, 1, 1, DECODE_TAIL>;
-    return launch_shared_grids<H, C, paged_decode_kernel<C>>(s, head, st, launch_head);
-  }
-  if (R <= 16) {
-    using C = DecodeCfg<H, E4M3, 2, 1, DECODE_TAIL>;
-    return launch_shared_grids<H, C, paged_decode_kernel<C>>(s, head, st, launch_head);
-  }
+  if (R <= 8) return launch_shared_rows<H, E4M3, 1>(s, head, st, launch_head);
+  if (R <= 16) return launch_shared_rows<H, E4M3, 2>(s, head, st, launch_head);
   if constexpr (H <= 128 || E4M3) {
-    constexpr int NT = H == 256 ? 2 : 4;
-    using C = DecodeCfg<H, E4M3, NT, 4 / NT, DECODE_TAIL>;
-    if (R <= 32) return launch_shared_grids<H, C, paged_decode_kernel<C>>(s, head, st, launch_head);
+    if (R <= 32) return launch_shared_rows<H, E4M3, 4>(s, head, st, launch_head);
   }
   using C = DecodeTcCfg<H, E4M3, DECODE_TAIL>;
   return launch_shared_grids<H, C, paged_decode_tc_kernel<C>>(s, head, st, launch_head);
