@@ -168,7 +168,7 @@ struct DecodeCfg {
   static constexpr int RINGS = WARPS / WR;
   static constexpr int TEAMS = SOLO ? 1 : RINGS;       // that share an item
   static constexpr int TK = TEAMS * CK;                // keys of a tile
-  static constexpr int ITEM_UNITS = SOLO ? 4 : 8 / TEAMS;   // an item's fixed cost, in tiles (below)
+  static constexpr int ITEM_UNITS = SOLO ? 2 : 8 / TEAMS;   // an item's fixed cost, in tiles (below)
   static constexpr bool QSMEM = TEAM || H * NT > 256;  // query fragments in shared memory
   static constexpr int QTILES = WR * NT;
   static constexpr int QBYTES = QSMEM ? H / 16 * QTILES * 32 * 8 : 0;
@@ -203,7 +203,8 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 // The list that is dealt to the CTAs: per item (b, k) ITEM_UNITS units that
 // stand for its start and end (about the time of two tiles of four warps), then
 // one unit per tile.  64 requests of 1 to 16384 tokens: 108 us without those
-// units, 75.0, 74.4, 75.3 and 76.8 us with 1, 2, 3 and 6.
+// units, 75.0, 74.4, 75.3 and 76.8 us with 1, 2, 3 and 6.  SOLO: 1024 items of up to 1024 keys of
+// 8-bit caches 54.9, 53.7, 53.9 and 56.6 us with 1, 2, 4 and 8.
 
 // A place in the list: unit `rem` of item (b, k).
 struct DecodePlace {
