@@ -245,6 +245,36 @@ def test_more_requests_than_a_wave(lib):
     _ok()
 
 
+# With two items or more for each CTA the requests' own keys go to single warps.
+def _tails(n, most, least=1):
+    return [least + (i * 37 + i * i) % most for i in range(n)]
+
+
+WARPS = {
+    "h128_rows8": ([(100, _tails(16, 90))] * 20, [0, 1, 33], dict(K=2, G=8, T=1, H=128, page=16)),
+    "h128_rows16": ([(64, _tails(16, 60, 4))] * 20, [0, 1, 3, 40], dict(K=2, G=4, T=4, H=128, page=32)),
+    "h256_rows8": ([(33, _tails(16, 70, 2))] * 10, [0, 1, 50], dict(K=2, G=4, T=2, H=256, page=16)),
+    "h64_rows32": ([(40, _tails(20, 50, 4))] * 16, [0, 2, 70], dict(K=2, G=8, T=4, H=64, page=8)),
+    "h64_rows16": ([(40, _tails(20, 50, 8))] * 16, [0, 7, 70], dict(K=2, G=2, T=8, H=64, page=4)),
+    "one_head": ([(16, _tails(14, 40))] * 48, [5] * 30, dict(K=1, G=3, T=1, H=64, page=256)),
+    "long_and_short": ([(32, [900] + [1] * 40)] * 8, [700, 1], dict(K=2, G=4, T=1, H=128, page=64)),
+    "one_long": ([(32, [2000] + [1] * 319)], [], dict(K=2, G=1, T=1, H=64, page=64, layout="token")),
+}
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("name", WARPS)
+def test_own_keys_by_warps(lib, name, dtype):
+    groups, alone, kw = WARPS[name]
+    p = Problem(len(name), groups, alone, dtype=dtype, **kw).on_device()
+    assert len(p.lens) * kw["K"] >= 2 * 152 * (1 if kw["H"] == 256 else 2)
+    o, lse = p.run()
+    p.check(o, lse)
+    o2, lse2 = p.run()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    _ok()
+
+
 def test_agrees_with_the_decode_on_a_large_case(lib):
     """64 samples of an 8000-token prompt, 8 kv heads: against the decode without sharing, both rounded
     to bf16 once."""
