@@ -69,10 +69,12 @@ __host__ __device__ inline int set_words(int n_pages) { return ((n_pages + 31) /
 
 // The warps of the cluster over the columns [first, last) of rows 0 .. n - 1: `S` warps a row, the
 // row's columns dealt to their lanes, four of a lane at a time: `load(row, column)` of all four, then
-// `use(row, column, what it gave)`.  `range(row, first, last)` says false for rows to be left out.
-// `barrier()` is called once by all threads, before the first use.
-template <class Range, class Load, class Use, class Barrier>
-__device__ __forceinline__ void over_entries(int rank, int n, Range range, Load load, Use use, Barrier barrier) {
+// `take(what it gave)` of all four, then `use(row, column, what the one and the other gave)`.
+// `range(row, first, last)` says false for rows to be left out.  `barrier()` is called once by all
+// threads, before the first take.
+template <class Range, class Load, class Take, class Use, class Barrier>
+__device__ __forceinline__ void over_entries(int rank, int n, Range range, Load load, Take take, Use use,
+                                             Barrier barrier) {
   const int lane = threadIdx.x & 31, warp = rank * kWarps + (threadIdx.x >> 5);
   constexpr int all = kCtas * kWarps;
   const int S = n >= all ? 1 : all / max(n, 1);   // warps a row
@@ -89,16 +91,23 @@ __device__ __forceinline__ void over_entries(int rank, int n, Range range, Load 
       }
       if (!passed) barrier();
       passed = true;
+      int y[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j + k * S * 32 + lane < last) y[k] = take(x[k]);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int column = j + k * S * 32 + lane;
-        if (column < last) use(i, column, x[k]);
+        if (column < last) use(i, column, x[k], y[k]);
       }
     }
   }
   __syncwarp();
   if (!passed) barrier();
 }
+struct Nothing {
+  __device__ int operator()(int) const { return 0; }
+};
 // Rows of a call that stay in shared memory; more of them are looked up again.
 constexpr int kRowsKept = 1024;
 struct KeptRow {
@@ -158,9 +167,10 @@ __global__ void __launch_bounds__(kThreads, 1) pages_free_kernel(const __grid_co
   auto entry = [&](int i, int j) { return p.block_table[(int64_t)row_of(i) * p.max_pages + j]; };
   auto known = [&](int page) { return page >= 0 && page < p.n_pages; };
   // (behind the barrier: the sets are empty, the counts have been looked at)
-  over_entries(rank, fail ? 0 : a.N, range, entry, [&](int, int, int page) {
+  over_entries(rank, fail ? 0 : a.N, range, entry, [&](int page) {
+    return known(page) ? atomicSub(&p.shares[page], 1) : 0;
+  }, [&](int, int, int page, int others) {
     if (!known(page)) { odd = true; return; }
-    const int others = atomicSub(&p.shares[page], 1);
     if (others <= 0) odd |= set.put(page) || others < 0;   // (below zero: given back before)
   }, [&] { cluster.sync(); });
   cluster.sync();
@@ -178,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_free_kernel(const __grid_co
   }
   const bool over = !fail && all > used;   // more pages than the list has given out
   if (over) {
-    over_entries(rank, a.N, range, entry, [&](int, int, int page) {
+    over_entries(rank, a.N, range, entry, Nothing{}, [&](int, int, int page, int) {
       if (known(page)) atomicAdd(&p.shares[page], 1);
     }, [] {});
   } else if (!fail) {
@@ -291,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_fork_kernel(const __grid_co
       return parent < 0 || j >= p.max_pages ? -1 : p.block_table[(int64_t)parent * p.max_pages + j];
     };
     auto known = [&](int page) { return page >= 0 && page < p.n_pages; };
-    over_entries(rank, a.N, range, entry, [&](int i, int j, int page) {
+    over_entries(rank, a.N, range, entry, Nothing{}, [&](int i, int j, int page, int) {
       const int parent = a.parents[i];
       const int n = parent < 0 ? 0 : length(i, parent), full = n >> p.page_shift, part = n & (P - 1);
       int32_t* const copy = a.copies + (int64_t)i * 3;
@@ -369,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_compact_kernel(const __grid
   auto entry = [&](int b, int j) { return p.block_table[(int64_t)b * p.max_pages + j]; };
   const PageSet in_use{cluster, held, words}, unused{cluster, spare, words};
   bad = false;
-  over_entries(rank, wrong ? 0 : p.B, row, entry, [&](int, int, int page) {
+  over_entries(rank, wrong ? 0 : p.B, row, entry, Nothing{}, [&](int, int, int page, int) {
     if (page < 0 || page >= p.n_pages) bad = true;
     else in_use.put(page);
   }, [&] { cluster.sync(); });   // (the sets are empty)
@@ -463,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_compact_kernel(const __grid
       if (!in_place) last = p.max_pages;   // what is behind a request's pages, too
       return true;
     };
-    over_entries(rank, p.B, whole, entry, [&](int b, int j, int page) {
+    over_entries(rank, p.B, whole, entry, Nothing{}, [&](int b, int j, int page, int) {
       int to = page;
       if (j < pages_of(p.lens[b], p.page_shift)) {
         const int above = all_held - held_below(page) - 1;
