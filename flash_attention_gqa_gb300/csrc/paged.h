@@ -90,6 +90,7 @@ struct PagedDecodeArgs {
   PagedDecodeSplit* splits;    // workspace: [CTAs]
   bool by_item;                // entries of splits are items
   bool unsplit;                // no item is shared: no splits, no partials (set by the launch)
+  bool by_warps;               // many short items may go to single warps (DecodeCfg::SOLO)
   uint32_t* err;
   PagedSharedTables shared;    // TAIL and HEAD
 };

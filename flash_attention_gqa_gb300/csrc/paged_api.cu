@@ -109,12 +109,13 @@ size_t fa_paged_decode_workspace_size(int B, int K, int G, int T, int H) {
   return fa::paged_decode_plan(G * T, H, fa_device_sm_count()).total;
 }
 
-int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int cache_type,
-                    const float* k_scale, const float* v_scale, int64_t page_stride,
-                    int64_t head_stride, int64_t token_stride, const int32_t* block_table,
-                    const int32_t* lens, int window, void* o, float* lse, void* workspace,
-                    size_t workspace_bytes, int B, int K, int G, int T, int H, int n_pages,
-                    int page_size, int max_pages, void* stream) {
+// `by_warps`: as in PagedDecodeArgs.  (fa_paged_decode leaves short items to CTAs, whose sums come in another
+// order: its results stay what they were.)
+static int decode(bool by_warps, const void* q, const void* k_cache, const void* v_cache, int cache_type,
+                  const float* k_scale, const float* v_scale, int64_t page_stride, int64_t head_stride,
+                  int64_t token_stride, const int32_t* block_table, const int32_t* lens, int window, void* o,
+                  float* lse, void* workspace, size_t workspace_bytes, int B, int K, int G, int T, int H,
+                  int n_pages, int page_size, int max_pages, void* stream) {
   if (B < 0 || K < 0 || G < 0 || T < 0 || H < 0 || max_pages < 0 || window < 0)
     return FA_ERR_INVALID_ARG;
   fa::PagedDecodeArgs a{};
@@ -139,6 +140,7 @@ int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int
   a.window = window >= max_pages * page_size ? 0 : window;
   a.splits = static_cast<fa::PagedDecodeSplit*>(workspace);
   a.by_item = B * K <= plan.ctas;
+  a.by_warps = by_warps;
   a.partials = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.partials);
   a.wait_limit_ns = fa::device_wait_limit_ns();
   a.err = fa::device_error_word();
@@ -156,6 +158,17 @@ int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int
       return status(e4m3 ? fa::launch_paged_decode_h256_e4m3(a, plan.ctas, st)
                          : fa::launch_paged_decode_h256_bf16(a, plan.ctas, st));
   }
+}
+
+int fa_paged_decode(const void* q, const void* k_cache, const void* v_cache, int cache_type,
+                    const float* k_scale, const float* v_scale, int64_t page_stride,
+                    int64_t head_stride, int64_t token_stride, const int32_t* block_table,
+                    const int32_t* lens, int window, void* o, float* lse, void* workspace,
+                    size_t workspace_bytes, int B, int K, int G, int T, int H, int n_pages,
+                    int page_size, int max_pages, void* stream) {
+  return decode(false, q, k_cache, v_cache, cache_type, k_scale, v_scale, page_stride, head_stride, token_stride,
+                block_table, lens, window, o, lse, workspace, workspace_bytes, B, K, G, T, H, n_pages, page_size,
+                max_pages, stream);
 }
 
 size_t fa_paged_decode_shared_workspace_size(int B, int K, int G, int T, int H, int n_groups, int n_members) {
@@ -195,9 +208,9 @@ int fa_paged_decode_shared(const void* q, const void* k_cache, const void* v_cac
   // (as far as the tables reach: the lengths are on the device.  With a group for every member nothing is shared.)
   const double keys = (double)n_members * max_pages * page_size * K * H * (cache_type == FA_CACHE_BF16 ? 4 : 2);
   if (n_groups >= n_members || keys <= kSharedLeast)
-    return fa_paged_decode(q, k_cache, v_cache, cache_type, k_scale, v_scale, page_stride, head_stride,
-                           token_stride, block_table, lens, 0, o, lse, workspace, workspace_bytes, B, K, G, T, H,
-                           n_pages, page_size, max_pages, stream);
+    return decode(true, q, k_cache, v_cache, cache_type, k_scale, v_scale, page_stride, head_stride, token_stride,
+                  block_table, lens, 0, o, lse, workspace, workspace_bytes, B, K, G, T, H, n_pages, page_size,
+                  max_pages, stream);
   char* const ws = static_cast<char*>(workspace);
   a.q = q; a.k_cache = k_cache; a.v_cache = v_cache;
   a.k_scale = k_scale; a.v_scale = v_scale;

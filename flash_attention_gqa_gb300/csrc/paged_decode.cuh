@@ -150,8 +150,8 @@ constexpr float kBelow = F16 ? 11.0f : 0.0f;
 // ------------------------------------------------------------ configuration
 // NT: n-tiles of 8 query rows per warp.  WR: warps of a team, which share a ring
 // and the keys in it, NT * 8 rows each.
-// SOLO (TAIL): the units are dealt to the warps, each of which does what else a CTA does: many short
-// items (paged_tail_solo) lose most of their time where a CTA's warps meet.
+// SOLO: the units are dealt to the warps, each of which does what else a CTA does: many short
+// items (paged_tail_solo, decode_by_warps) lose most of their time where a CTA's warps meet.
 template <int H_, bool E4M3_, int NT_, int WR_, DecodeMode MODE_ = DECODE_ALL, bool SOLO_ = false>
 struct DecodeCfg {
   static constexpr DecodeMode MODE = MODE_;
@@ -177,7 +177,7 @@ struct DecodeCfg {
   // what the queries leave of 212 KB.
   static constexpr int STAGES = TEAM ? (212 * 1024 - QBYTES) / (RINGS * SLOT) : (H == 256 ? 48 : 24) * 1024 / SLOT;
   static constexpr int RING = RINGS * STAGES * SLOT;
-  static_assert(!SOLO || (MODE == DECODE_TAIL && !TEAM && !QSMEM), "");
+  static_assert(!SOLO || (MODE != DECODE_HEAD && !TEAM && !QSMEM), "");
   static constexpr int SMEM = RING + QBYTES;
   static constexpr int MIN_CTAS = !TEAM && H <= 128 ? 2 : 1;
   static_assert(TEAM || (NT < 2 ? NT : 2) * 8 * H * 4 <= SLOT, "16 rows of a warp's O^T fit in a ring slot");

@@ -75,6 +75,28 @@ cudaError_t launch_decode(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
   return launch_decode<C, paged_decode_kernel<C>>(a, grid, st);
 }
 
+// Whether single warps do whole items, where the call leaves it open: one for each of them, and few keys.
+// CTAs and warps, ragged requests of up to 48, 112, 240 and 496 keys, H = 128, 8 rows: 1216 items 12.7 and
+// 10.9 us, 15.9 and 14.6, 20.6 and 22.6, 34.5 and 42.7; 2432 items 22.3 and 15.1, 26.9 and 21.1, 36.9 and 39.0,
+// 56.1 and 67.2; 608 items 7.8 and 8.9, 10.6 and 11.6.  2432 of 32 rows at H = 64: 27.9 and 18.2, 28.8 and
+// 21.5, 33.6 and 29.7, 46.4 and 52.3.
+template <class C>
+bool decode_by_warps(const PagedDecodeArgs& a, int grid) {
+  const int64_t each = (int64_t)a.B * a.K / grid;   // items of a CTA
+  return a.by_warps && each >= 4 && decode_most_tiles<C>(a) * C::TK <= (each >= 8 ? 256 : 128);
+}
+
+// A kernel of NT * 8 rows.
+template <int H, bool E4M3, int NT>
+cudaError_t launch_decode_warps(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
+  if constexpr (H * NT <= 256) {
+    using C = DecodeCfg<H, E4M3, NT, 1, DECODE_ALL, true>;
+    if (decode_by_warps<C>(a, grid)) return launch_decode<C>(a, grid, st);
+  }
+  constexpr int tiles = H == 256 && NT == 4 ? 2 : NT;
+  return launch_decode<DecodeCfg<H, E4M3, tiles, NT / tiles>>(a, grid, st);
+}
+
 // Up to 8, 16 and 32 rows: mma.sync, warps on their own (teams of two for 8-bit
 // caches' 32 rows at H = 256: registers).  More, and over 16 rows of bf16 at H =
 // 256: tcgen05.  Both sides at 16 requests x 4 kv heads x 8192 keys, mma.sync and
@@ -85,11 +107,10 @@ cudaError_t launch_decode(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
 template <int H, bool E4M3>
 cudaError_t launch_decode_rows(const PagedDecodeArgs& a, int grid, cudaStream_t st) {
   const int R = a.G * a.T;
-  if (R <= 8) return launch_decode<DecodeCfg<H, E4M3, 1, 1>>(a, grid, st);
-  if (R <= 16) return launch_decode<DecodeCfg<H, E4M3, 2, 1>>(a, grid, st);
+  if (R <= 8) return launch_decode_warps<H, E4M3, 1>(a, grid, st);
+  if (R <= 16) return launch_decode_warps<H, E4M3, 2>(a, grid, st);
   if constexpr (H <= 128 || E4M3) {
-    constexpr int NT = H == 256 ? 2 : 4;
-    if (R <= 32) return launch_decode<DecodeCfg<H, E4M3, NT, 4 / NT>>(a, grid, st);
+    if (R <= 32) return launch_decode_warps<H, E4M3, 4>(a, grid, st);
   }
   using Tc = DecodeTcCfg<H, E4M3>;
   return launch_decode<Tc, paged_decode_tc_kernel<Tc>>(a, grid, st);

@@ -275,6 +275,31 @@ def test_own_keys_by_warps(lib, name, dtype):
     _ok()
 
 
+# Small calls are decodes, by warps where there are four short items or more for each CTA.
+SMALL = {
+    "h128_rows8": ([(16, _tails(17, 70))] * 20, [0, 1, 33], dict(K=4, G=8, T=1, H=128, page=16)),
+    "h128_rows16": ([(16, _tails(17, 60, 4))] * 20, [0, 1, 3, 40], dict(K=4, G=4, T=4, H=128, page=16)),
+    "h256_rows8": ([(33, _tails(16, 40, 2))] * 10, [0, 1, 50], dict(K=4, G=4, T=2, H=256, page=8)),
+    "h64_rows32": ([(8, _tails(20, 50, 4))] * 17, [0, 2, 70], dict(K=4, G=8, T=4, H=64, page=8)),
+    "h64_rows8": ([(7, _tails(20, 50))] * 31, [0, 70], dict(K=4, G=1, T=1, H=64, page=1)),
+    "longer": ([(64, _tails(31, 150))] * 20, [0, 200], dict(K=4, G=2, T=1, H=64, page=16, layout="token")),
+}
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("name", SMALL)
+def test_small_calls_by_warps(lib, name, dtype):
+    groups, alone, kw = SMALL[name]
+    p = Problem(len(name), groups, alone, dtype=dtype, wide=False, **kw).on_device()
+    each = len(p.lens) * kw["K"] // (152 if kw["H"] == 256 else 304)
+    assert each >= 4 and p.table.shape[1] * kw["page"] <= (256 if each >= 8 else 128)
+    o, lse = p.run()
+    p.check(o, lse)
+    o2, lse2 = p.run()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    _ok()
+
+
 def test_agrees_with_the_decode_on_a_large_case(lib):
     """64 samples of an 8000-token prompt, 8 kv heads: against the decode without sharing, both rounded
     to bf16 once."""
