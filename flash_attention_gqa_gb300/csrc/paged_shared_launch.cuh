@@ -22,16 +22,19 @@ __global__ void __launch_bounds__(THREADS)
 paged_shared_join_kernel(const __grid_constant__ PagedSharedArgs s, int per, int rows_shift) {
   __shared__ float4 sx[THREADS];
   __shared__ float2 sml[THREADS];
-  grid_before();
   const PagedDecodeArgs& a = s.tail;
   const int item = blockIdx.x, b = item / a.K, k = item - b * a.K, R = a.G * a.T, P = paged_partial_rows(R);
   const int shares = blockDim.x / per, share = threadIdx.x / per, at = threadIdx.x % per;
   const int i = blockIdx.y * per + at, tile = i / 32, side = 1 << rows_shift, groups = (R + side - 1) >> rows_shift;
   const int d = tile / groups * (32 >> rows_shift) + (i % 32 >> rows_shift);   // of 4
   const int r = d < H / 4 ? tile % groups * side + (i & (side - 1)) : R;
-  // (written by the grids before, maybe while this one was already there: L2 loads)
-  const int4 tail = __ldcg(reinterpret_cast<const int4*>(a.splits) + item);
+  // (written by the grids before, maybe while this one was already there: L2 loads.  The first kernel's
+  // tables have been there since before HEAD let the next grid start.)
   const int place = r < R ? __ldcg(a.shared.places + b) : -1;
+  int4 c = make_int4(0, 0, 0, 0);
+  if (place >= 0) c = __ldcg(reinterpret_cast<const int4*>(a.shared.chunks + ((place + r) >> 7)) + 1);
+  grid_before();
+  const int4 tail = __ldcg(reinterpret_cast<const int4*>(a.splits) + item);
   // (an entry may hold anything where a wait ran out before it was written)
   const bool tail_split = tail.y >= 0 && tail.z >= tail.y && tail.z < s.tail_parts;
   const int n_tail = tail_split ? tail.z - tail.y + 1 : 1;
@@ -44,7 +47,6 @@ paged_shared_join_kernel(const __grid_constant__ PagedSharedArgs s, int per, int
     const int row = place + r, chunk = row >> 7;
     r_head = row & 127;
     const int4 head = __ldcg(reinterpret_cast<const int4*>(s.head_splits) + (int64_t)chunk * a.K + k);
-    const int4 c = __ldcg(reinterpret_cast<const int4*>(a.shared.chunks + chunk) + 1);
     head_split = head.y >= 0 && head.z >= head.y && head.z < s.head_ctas;
     n_head = head_split ? head.z - head.y + 1 : 1;
     if (!head_split) P_head = (c.x + 7) & ~7;
