@@ -30,6 +30,7 @@ __device__ __forceinline__ int entry_of(const int* list, int n, int x) {
 __global__ void __launch_bounds__(kThreads, 1) paged_shared_setup_kernel(const __grid_constant__ PagedSharedArgs a) {
   extern __shared__ int sm[];
   const int n = a.n_groups, N = a.n_members, B = a.tail.B, T = a.tail.T, R = a.tail.G * T, tid = threadIdx.x;
+  const int threads = blockDim.x;
   int* const starts = sm;              // [n + 1]
   int* const prefix = starts + n + 1;  // [n] the caller's, then what is shared
   int* const least = prefix + n;       // [n] longest prefix that all members' queries see
@@ -46,22 +47,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_shared_setup_kernel(const _
   int member = -1, len = 0;   // of entry tid
   if (tid < N) member = a.members[tid];
   int lo = a.group_starts[0], hi = a.group_starts[n];
-  for (int g = tid; g <= n; g += kThreads) starts[g] = a.group_starts[g];
-  for (int g = tid; g < n; g += kThreads) {
+  for (int g = tid; g <= n; g += threads) starts[g] = a.group_starts[g];
+  for (int g = tid; g < n; g += threads) {
     prefix[g] = a.prefix_lens[g];
     least[g] = lead[g] = INT_MAX;
     live[g] = 0;
   }
-  for (int b = tid; b < B; b += kThreads) claim[b] = INT_MAX;
+  for (int b = tid; b < B; b += threads) claim[b] = INT_MAX;
   if ((unsigned)member < (unsigned)B) len = a.tail.lens[member];
   auto member_of = [&](int i) { return i == tid ? member : a.members[i]; };
   auto length_of = [&](int i, int r) { return min(max(i == tid ? len : a.tail.lens[r], 0), most); };
   __syncthreads();
   bool bad = false;
-  for (int g = tid; g < n; g += kThreads) bad |= starts[g] < 0 || starts[g + 1] < starts[g] || starts[g + 1] > N;
+  for (int g = tid; g < n; g += threads) bad |= starts[g] < 0 || starts[g + 1] < starts[g] || starts[g + 1] > N;
   const bool none = __syncthreads_or(bad) || n == 0;   // no groups to go by
   if (none) lo = hi = 0;
-  for (int i = tid; i < hi; i += kThreads) {
+  for (int i = tid; i < hi; i += threads) {
     if (i < lo) continue;
     const int r = member_of(i);
     if ((unsigned)r < (unsigned)B) atomicMin(&claim[r], i);
@@ -74,7 +75,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_shared_setup_kernel(const _
     const int r = member_of(i);
     return (unsigned)r < (unsigned)B && claim[r] == i ? r : -1;
   };
-  for (int i = tid; i < hi; i += kThreads) {
+  for (int i = tid; i < hi; i += threads) {
     if (i < lo) continue;
     const int r = request_of(i);
     if (r < 0) { bad = true; continue; }
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_shared_setup_kernel(const _
   __syncthreads();
 
   // chunks and padded rows of the groups before each
-  const int per = (n + kThreads - 1) / kThreads, g0 = min(tid * per, n), g1 = min(g0 + per, n);
+  const int per = (n + threads - 1) / threads, g0 = min(tid * per, n), g1 = min(g0 + per, n);
   auto rows_of = [&](int g) { return live[g] > 1 && prefix[g] > 0 ? (starts[g + 1] - starts[g]) * R : 0; };
   int chunks = 0, padded = 0;
   if (!none)
@@ -110,8 +111,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_shared_setup_kernel(const _
   if (lane == 31) { sums[0][warp] = ic; sums[1][warp] = ip; }
   __syncthreads();
   int before = ic - chunks, base_at = ip - padded, all = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
+#pragma unroll 4
+  for (int w = 0; w < threads / 32; ++w) {
     if (w < warp) { before += sums[0][w]; base_at += sums[1][w]; }
     all += sums[0][w];
   }
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_shared_setup_kernel(const _
     *out.n_chunks = all;
   }
   __syncthreads();
-  for (int i = tid; i < N; i += kThreads) {
+  for (int i = tid; i < N; i += threads) {
     const int r = request_of(i);
     out.members[i] = r;
     if (r < 0) continue;
@@ -136,12 +137,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_shared_setup_kernel(const _
     out.begins[r] = shares ? prefix[g] : 0;
     out.places[r] = shares ? first[g] * 128 + (i - starts[g]) * R : -1;
   }
-  for (int b = tid; b < B; b += kThreads)
+  for (int b = tid; b < B; b += threads)
     if (claim[b] == INT_MAX) {
       out.begins[b] = 0;
       out.places[b] = -1;
     }
-  for (int c = tid; c < all; c += kThreads) {
+  for (int c = tid; c < all; c += threads) {
     const int g = entry_of(first, n, c), row = (c - first[g]) * 128;
     int4* const at = reinterpret_cast<int4*>(out.chunks + c);
     at[0] = make_int4(prefix[g], lead[g], starts[g], row);
@@ -163,7 +164,9 @@ cudaError_t launch_paged_shared_setup(const PagedSharedArgs& a, cudaStream_t st)
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(kThreads);
+  // (a thread a member, where that goes: few warps meet sooner)
+  const int most = a.n_members > a.n_groups ? a.n_members : a.n_groups + 1;
+  cfg.blockDim = dim3(most <= 128 ? 128 : most < kThreads ? (most + 31) & ~31 : kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   return cudaLaunchKernelEx(&cfg, paged_shared_setup_kernel, a);
