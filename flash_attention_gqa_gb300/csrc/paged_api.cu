@@ -16,11 +16,16 @@ using namespace fa;
 namespace {
 
 // Bytes of keys and values, each request's counted, up to which a call with shared prefixes does not make use
-// of them: the three grids that it takes more cost 10 to 15 us, and what several requests read comes from
-// L2.  Shared and not, at H = 128: 16 requests x 8 kv heads x 576 keys (38 MB) 21.8 and 10.8 us, x 2112 (138
-// MB) 22.6 and 18.6, x 8256 (541 MB) 25.9 and 51; 64 x 8 x 576 (151 MB) 26 to 30 and 22, x 2112 (554 MB) 32
-// and 53; in e4m3 64 x 8 x 2112 (277 MB) 33 and 38.
-constexpr double kSharedLeast = 200e6;
+// of them: the three grids that it takes more cost some 10 us, what several requests read comes from L2, and a
+// tile of 128 rows takes its time however few of them there are.  Shared and not, in us: bf16 at H = 128,
+// 16 requests of one prefix x 8 kv heads x 2112 keys (138 MB) 21 and 19, x 8256 (541 MB) 24 and 52; 64 x 8 x 576
+// (151 MB) 27 and 22; e4m3 64 x 8 x 2112 (277 MB) 29 and 39, 48 in threes x 4 x 4112 (202 MB) 34 and 29, 48 in fours x 4
+// x 16400 (806 MB) 67 and 104.  In pairs, 48 requests x 4 heads: bf16 at H = 64 x 4112 (202 MB) 36 and 26, at H = 128
+// (404 MB) 49 and 60; e4m3 at H = 64 x 16400 (403 MB) 84 and 79, at H = 256 x 4112 (404 MB) 73 and 60, at H = 128 x
+// 16400 (806 MB) 107 and 124.
+inline double shared_least(bool bf16, int n_groups, int n_members) {
+  return n_members >= 3 * (int64_t)n_groups ? 200e6 : bf16 ? 400e6 : 800e6;
+}
 
 bool decode_shape_ok(int B, int K, int G, int T, int H) {
   return head_dim_ok(H) && (int64_t)G * T <= kMaxPagedRows && B <= kMaxPagedBatch &&
@@ -207,7 +212,7 @@ int fa_paged_decode_shared(const void* q, const void* k_cache, const void* v_cac
     return FA_ERR_INVALID_ARG;
   // (as far as the tables reach: the lengths are on the device.  With a group for every member nothing is shared.)
   const double keys = (double)n_members * max_pages * page_size * K * H * (cache_type == FA_CACHE_BF16 ? 4 : 2);
-  if (n_groups >= n_members || keys <= kSharedLeast)
+  if (n_groups >= n_members || keys <= shared_least(cache_type == FA_CACHE_BF16, n_groups, n_members))
     return decode(true, q, k_cache, v_cache, cache_type, k_scale, v_scale, page_stride, head_stride, token_stride,
                   block_table, lens, 0, o, lse, workspace, workspace_bytes, B, K, G, T, H, n_pages, page_size,
                   max_pages, stream);
