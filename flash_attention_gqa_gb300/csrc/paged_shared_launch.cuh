@@ -17,6 +17,8 @@ namespace fa {
 
 // A thread per 4 dims of a row of item (b, k), a warp up to 8 rows (2^rows_shift) side by side; `per` such
 // a CTA, times shares of the partials, summed in order behind it.  U partials of a thread in flight.
+// Bound by three dependent loads (512 items of 8 rows, H = 128: 5 us of a call), two of them from L2; its
+// first is done while the grid before it runs.
 template <int H, bool TC, int U, int THREADS>
 __global__ void __launch_bounds__(THREADS)
 paged_shared_join_kernel(const __grid_constant__ PagedSharedArgs s, int per, int rows_shift) {
