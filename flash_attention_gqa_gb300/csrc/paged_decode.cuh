@@ -691,7 +691,9 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
       const char* const vs_p = ring + cur * C::SLOT + C::HALF;
       cur = cur + 1 == S ? 0 : cur + 1;
       const int key0 = walk.first + (walk.tile * C::TEAMS + team) * CK;
-      if (key0 >= walk.len) continue;   // this team has no keys in the tile
+      // This team has no keys in the tile: its slot was not written.  (TAIL: a request's prefix may be all
+      // that it has, and end inside the 8 keys that the first tile starts with.)
+      if (key0 >= walk.len || (C::MODE == DECODE_TAIL && walk.low >= walk.len)) continue;
 
       // A slot's keys at once, or with many rows (registers) 16 at a time.
       constexpr int KT2 = NT < 4 ? KT : 1;
