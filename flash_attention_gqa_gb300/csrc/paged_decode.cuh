@@ -1104,6 +1104,61 @@ paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
   if (C::MODE == DECODE_TAIL) grid_before();   // so that this grid's end is the HEAD grid's, too
 }
 
+// Four dims of a row, joined from partials: sums x and l with bases m (log2 units), of which one of
+// -inf has no weight.  It is added all the same: that of a part with no key is all zeros, and one
+// whose scores are all NaN has sums that are NaN, which 0 times them stays.
+struct JoinSum {
+  float M = -INFINITY, L = 0.0f;
+  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+
+  // U partials, as far as `live(u)`; m is -inf for the others.
+  template <int U, class Live>
+  __device__ __forceinline__ void add(const float4 (&y)[U], const float (&m)[U], const float (&l)[U], Live live) {
+    float mn = M;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mn = fmaxf(mn, m[u]);
+    const float low = mn == -INFINITY ? 0.0f : mn, f0 = fast_exp2(M - low);
+    M = mn;
+    L *= f0;
+    x.x *= f0; x.y *= f0; x.z *= f0; x.w *= f0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (live(u)) {
+        const float f = fast_exp2(m[u] - low);
+        L += l[u] * f;
+        x.x += y[u].x * f;
+        x.y += y[u].y * f;
+        x.z += y[u].z * f;
+        x.w += y[u].w * f;
+      }
+    }
+  }
+
+  // The CTA's shares of element `at`, summed in order by share 0.  Every thread calls it.
+  __device__ __forceinline__ void meet(float4* sx, float2* sml, int share, int shares, int at, int per) {
+    sx[threadIdx.x] = x;
+    sml[threadIdx.x] = make_float2(M, L);
+    __syncthreads();
+    if (share == 0) {
+      for (int w = 1; w < shares; ++w) M = fmaxf(M, sml[w * per + at].x);
+      const float low = M == -INFINITY ? 0.0f : M;
+      L = 0.0f;
+      x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+      for (int w = 0; w < shares; ++w) {
+        const float2 ml = sml[w * per + at];
+        const float4 y = sx[w * per + at];
+        const float f = fast_exp2(ml.x - low);
+        L += ml.y * f;
+        x.x += y.x * f;
+        x.y += y.y * f;
+        x.z += y.z * f;
+        x.w += y.w * f;
+      }
+    }
+  }
+};
+
 // Joins the partials of an item that several CTAs of the first kernel share: a
 // thread per four dims of a row and share of the partials, `per` such elements a
 // CTA, whose shares are then summed in order.  U: partials in flight a thread.  TC:
@@ -1131,8 +1186,7 @@ paged_join_kernel(const __grid_constant__ PagedDecodeArgs a, int ctas, int per) 
   const int64_t part = paged_partial_floats(R, H);
   // partial 0 in slot 1 of its CTA, the others in slot 0 of theirs
   const float* const base = a.partials + (int64_t)first * 2 * part;
-  float M = -INFINITY, L = 0.0f;
-  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  JoinSum sum;
   if (r < R) {
     for (int p0 = share; p0 < n; p0 += U * shares) {
       float4 y[U];
@@ -1148,51 +1202,13 @@ paged_join_kernel(const __grid_constant__ PagedDecodeArgs a, int ctas, int per) 
           l[u] = __ldcg(src + P * H + P + r);
         }
       }
-      float mn = M;
-#pragma unroll
-      for (int u = 0; u < U; ++u) mn = fmaxf(mn, m[u]);
-      const float low = mn == -INFINITY ? 0.0f : mn, f0 = fast_exp2(M - low);
-      M = mn;
-      L *= f0;
-      x.x *= f0; x.y *= f0; x.z *= f0; x.w *= f0;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (p0 + u * shares < n) {
-          const float f = fast_exp2(m[u] - low);
-          L += l[u] * f;
-          x.x += y[u].x * f;
-          x.y += y[u].y * f;
-          x.z += y[u].z * f;
-          x.w += y[u].w * f;
-        }
-      }
+      sum.add(y, m, l, [&](int u) { return p0 + u * shares < n; });
     }
   }
-  if (shares > 1) {
-    sx[threadIdx.x] = x;
-    sml[threadIdx.x] = make_float2(M, L);
-    __syncthreads();
-    if (share == 0) {
-      for (int w = 1; w < shares; ++w) M = fmaxf(M, sml[w * per + at].x);
-      const float low = M == -INFINITY ? 0.0f : M;
-      L = 0.0f;
-      x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-      for (int w = 0; w < shares; ++w) {
-        const float2 ml = sml[w * per + at];
-        const float4 y = sx[w * per + at];
-        const float f = fast_exp2(ml.x - low);
-        L += ml.y * f;
-        x.x += y.x * f;
-        x.y += y.y * f;
-        x.z += y.z * f;
-        x.w += y.w * f;
-      }
-    }
-  }
+  if (shares > 1) sum.meet(sx, sml, share, shares, at, per);
   if (share == 0 && r < R)
-    put_result((char*)a.o + (int64_t)item * R * H * 2, a.lse + (int64_t)item * R, H, r, d, x, M, L,
-               a.v_scale ? a.v_scale[item % a.K] : 1.0f);
+    put_result((char*)a.o + (int64_t)item * R * H * 2, a.lse + (int64_t)item * R, H, r, d, sum.x, sum.M,
+               sum.L, a.v_scale ? a.v_scale[item % a.K] : 1.0f);
 }
 
 }  // namespace fa

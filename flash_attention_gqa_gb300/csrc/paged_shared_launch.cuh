@@ -55,8 +55,7 @@ paged_shared_join_kernel(const __grid_constant__ PagedSharedArgs s, int per, int
     head_at = head_split ? s.head_partials + (int64_t)head.y * 2 * part_head
                          : s.head_whole + ((int64_t)c.y * a.K + (int64_t)k * P_head) * (H + 2);
   }
-  float M = -INFINITY, L = 0.0f;
-  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  JoinSum sum;
   if (r < R) {
     const int n = n_head + n_tail;
     for (int p0 = share; p0 < n; p0 += U * shares) {
@@ -79,51 +78,13 @@ paged_shared_join_kernel(const __grid_constant__ PagedSharedArgs s, int per, int
           l[u] = __ldcg(src + (int64_t)rows * (H + 1) + row);
         }
       }
-      float mn = M;
-#pragma unroll
-      for (int u = 0; u < U; ++u) mn = fmaxf(mn, m[u]);
-      const float low = mn == -INFINITY ? 0.0f : mn, f0 = fast_exp2(M - low);
-      M = mn;
-      L *= f0;
-      x.x *= f0; x.y *= f0; x.z *= f0; x.w *= f0;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (p0 + u * shares < n && m[u] != -INFINITY) {   // (one with no key adds nothing)
-          const float f = fast_exp2(m[u] - low);
-          L += l[u] * f;
-          x.x += y[u].x * f;
-          x.y += y[u].y * f;
-          x.z += y[u].z * f;
-          x.w += y[u].w * f;
-        }
-      }
+      sum.add(y, m, l, [&](int u) { return p0 + u * shares < n; });
     }
   }
-  if (shares > 1) {
-    sx[threadIdx.x] = x;
-    sml[threadIdx.x] = make_float2(M, L);
-    __syncthreads();
-    if (share == 0) {
-      for (int w = 1; w < shares; ++w) M = fmaxf(M, sml[w * per + at].x);
-      const float low = M == -INFINITY ? 0.0f : M;
-      L = 0.0f;
-      x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-      for (int w = 0; w < shares; ++w) {
-        const float2 ml = sml[w * per + at];
-        const float4 y = sx[w * per + at];
-        const float f = fast_exp2(ml.x - low);
-        L += ml.y * f;
-        x.x += y.x * f;
-        x.y += y.y * f;
-        x.z += y.z * f;
-        x.w += y.w * f;
-      }
-    }
-  }
+  if (shares > 1) sum.meet(sx, sml, share, shares, at, per);
   if (share == 0 && r < R)
-    put_result((char*)a.o + (int64_t)item * R * H * 2, a.lse + (int64_t)item * R, H, r, d * 4, x, M, L,
-               a.v_scale ? a.v_scale[k] : 1.0f);
+    put_result((char*)a.o + (int64_t)item * R * H * 2, a.lse + (int64_t)item * R, H, r, d * 4, sum.x,
+               sum.M, sum.L, a.v_scale ? a.v_scale[k] : 1.0f);
 }
 
 // A grid that may start while the one before it in the stream still runs.
