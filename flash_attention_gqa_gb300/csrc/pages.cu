@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) pages_compact_kernel(const __grid
     else in_use.put(page);
   }, [&] { cluster.sync(); });   // (the sets are empty)
   if (!wrong) {
-    for (int i = used + g; i < p.n_free; i += grid) {
+    for (int64_t i = (int64_t)used + g; i < p.n_free; i += grid) {   // (lists may end at any int)
       const int page = p.free_pages[i];
       bad |= page < 0 || page >= p.n_pages || unused.put(page);   // (twice in the list)
     }
@@ -461,10 +461,10 @@ __global__ void __launch_bounds__(kThreads, 1) pages_compact_kernel(const __grid
     if (a.shares_out != p.shares)
       for (int i = g; i < p.n_pages; i += grid) a.shares_out[i] = p.shares[i];
     if (a.free_out != p.free_pages)
-      for (int i = max(used, 0) + g; i < p.n_free; i += grid) a.free_out[i] = p.free_pages[i];
+      for (int64_t i = (int64_t)max(used, 0) + g; i < p.n_free; i += grid) a.free_out[i] = p.free_pages[i];
   } else {
-    for (int i = g; i < a.max_moves; i += grid) {
-      const int src = __ldcg(a.moves + (int64_t)i * 3), dst = __ldcg(a.moves + (int64_t)i * 3 + 1);
+    for (int64_t i = g; i < a.max_moves; i += grid) {
+      const int src = __ldcg(a.moves + i * 3), dst = __ldcg(a.moves + i * 3 + 1);
       if (src < 0) continue;
       const int n = p.shares[src];   // (in place: no page is the source of one move and the end of another)
       a.shares_out[dst] = n;
