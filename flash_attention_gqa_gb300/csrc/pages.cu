@@ -89,6 +89,7 @@ __device__ __forceinline__ void over_entries(int rank, int n, Range range, Load 
         const int column = j + k * S * 32 + lane;
         if (column < last) x[k] = load(i, column);
       }
+      __syncwarp();   // (a warp comes to it as one)
       if (!passed) barrier();
       passed = true;
       int y[4];
