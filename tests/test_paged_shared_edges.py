@@ -166,3 +166,41 @@ def test_nan_with_own_keys_by_warps(lib, dtype):
             _put(p.caches[0], p, b, 100, 1, math.nan)
     odd, odd_row = _check(p)
     assert odd_row.sum() == 5 + 5 * 8
+
+
+# ------------------------------------------------------------ pages and tiles, waits
+@TYPES
+@pytest.mark.parametrize("layout", ["head", "token"])
+@pytest.mark.parametrize("page", [128, 256, 1024])
+@pytest.mark.parametrize("H", [64, 128, 256])
+def test_pages_larger_than_a_tile(lib, H, page, layout, dtype):
+    """Tiles of 128 keys (64 at H = 256) that begin anywhere in a page; prefixes that end with a page, at a
+    tile's end within one, and within a tile."""
+    groups = [(2048, [1, 40, 300]), (page + 64, [5, 9]), (1500, [2, 77])]
+    p = Problem(H + page, groups, [30], K=2, G=8, T=1, H=H, page=page, dtype=dtype, layout=layout, pad=64).on_device()
+    p.check(*p.run())
+    _ok()
+
+
+@TYPES
+@pytest.mark.parametrize("H", [64, 128, 256])
+@pytest.mark.parametrize("T", [1, 5])
+def test_short_limits_of_waits(lib, H, T, dtype):
+    """Limits from none to longer than any wait: a call ends with an error, or its results are the same, and
+    the next call's are."""
+    groups = [(5000, [T + 9, T + 40, T + 1])] * 2 + [(640, [T, T + 11])]
+    p = Problem(12, groups, [12], K=2, G=8, T=T, H=H, page=64, dtype=dtype).on_device()
+    want = p.run()
+    p.check(*want)
+    for limit in (1, 300, 1000, 2000, 4000, 8000, 16000, 64000):
+        assert binding.fa_set_wait_limit_ns(limit) == binding.FA_OK
+        try:
+            o, lse = p.run()
+            rc = binding.fa_check_status()
+        finally:
+            assert binding.fa_set_wait_limit_ns(2_000_000_000) == binding.FA_OK
+        assert rc in (binding.FA_OK, binding.FA_ERR_DEVICE_TIMEOUT)
+        assert rc or (torch.equal(o, want[0]) and torch.equal(lse, want[1]))
+        again = p.run()
+        _ok()
+        assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
