@@ -15,14 +15,18 @@ using namespace fa;
 
 namespace {
 
-// Bytes of keys and values, each request's counted, up to which a call with shared prefixes does not make use
-// of them: the three grids that it takes more cost some 10 us, what several requests read comes from L2, and a
-// tile of 128 rows takes its time however few of them there are.  Shared and not, in us: bf16 at H = 128,
-// 16 requests of one prefix x 8 kv heads x 2112 keys (138 MB) 21 and 19, x 8256 (541 MB) 24 and 52; 64 x 8 x 576
-// (151 MB) 27 and 22; e4m3 64 x 8 x 2112 (277 MB) 29 and 39, 48 in threes x 4 x 4112 (202 MB) 34 and 29, 48 in fours x 4
-// x 16400 (806 MB) 67 and 104.  In pairs, 48 requests x 4 heads: bf16 at H = 64 x 4112 (202 MB) 36 and 26, at H = 128
-// (404 MB) 49 and 60; e4m3 at H = 64 x 16400 (403 MB) 84 and 79, at H = 256 x 4112 (404 MB) 73 and 60, at H = 128 x
-// 16400 (806 MB) 107 and 124.
+// Bytes of keys and values, each request's counted as far as its row of the table reaches (lengths are on the
+// device), up to which a call with shared prefixes does not make use of them: the three grids that it takes more
+// cost some 10 us, what several requests read comes from L2, and a tile of 128 rows takes its time however few of
+// them there are.  Shared and not, in us: bf16 at H = 128, 16 requests of one prefix x 8 kv heads x 2112 keys
+// (138 MB) 21 and 19, x 8256 (541 MB) 24 and 52; 64 x 8 x 576 (151 MB) 27 and 22; e4m3 64 x 8 x 2112 (277 MB) 29
+// and 39, 48 in threes x 4 x 4112 (202 MB) 34 and 29, 48 in fours x 4 x 16400 (806 MB) 67 and 104.  In pairs, 48
+// requests x 4 heads: bf16 at H = 64 x 4112 (202 MB) 36 and 26, at H = 128 (404 MB) 49 and 60; e4m3 at H = 64 x 16400
+// (403 MB) 84 and 79, at H = 256 x 4112 (404 MB) 73 and 60, at H = 128 x 16400 (806 MB) 107 and 124.
+// The rule looks at neither the head dim nor how many share beyond three: the threes above are on its wrong side, by
+// 5 us of 29.  And where a table reaches far behind its requests it takes the grids for few keys: with a table for
+// 32768 tokens, 4 requests x 2 heads x 552 keys at H = 256 17.8 us and 8.9, 64 x 8 x 576 27.0 and 22.6, 16 x 8 x 2112
+// 24.3 and 19.6.
 inline double shared_least(bool bf16, int n_groups, int n_members) {
   return n_members >= 3 * (int64_t)n_groups ? 200e6 : bf16 ? 400e6 : 800e6;
 }
@@ -210,7 +214,7 @@ int fa_paged_decode_shared(const void* q, const void* k_cache, const void* v_cac
   const PagedSharedPlan plan = paged_shared_plan(B, K, G * T, H, n_groups, n_members, fa_device_sm_count());
   if (!usable(workspace, 256) || workspace_bytes < std::max(plan.total, paged_decode_plan(G * T, H, fa_device_sm_count()).total))
     return FA_ERR_INVALID_ARG;
-  // (as far as the tables reach: the lengths are on the device.  With a group for every member nothing is shared.)
+  // (With a group for every member nothing is shared.)
   const double keys = (double)n_members * max_pages * page_size * K * H * (cache_type == FA_CACHE_BF16 ? 4 : 2);
   if (n_groups >= n_members || keys <= shared_least(cache_type == FA_CACHE_BF16, n_groups, n_members))
     return decode(true, q, k_cache, v_cache, cache_type, k_scale, v_scale, page_stride, head_stride, token_stride,

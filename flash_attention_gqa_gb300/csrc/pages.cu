@@ -119,8 +119,8 @@ struct KeptRow {
 
 // Decrement the share counts of the pages given back; who meets a count of zero was the last
 // holder, and its page joins the set.  Counts, places by a sum over the set, pages to the list.
-// 256 requests that drop 8 tokens 7.5 us, four barriers with dependent loads between them; 128 rows of 512
-// pages 18 us, by 65536 atomics that return.
+// 256 requests that drop 8 tokens 7.5 us, three barriers of the cluster and six of its CTAs with dependent loads
+// between them; 128 rows of 512 pages 18 us, by 65536 atomics that return.
 __global__ void __launch_bounds__(kThreads, 1) pages_free_kernel(const __grid_constant__ PagesFreeArgs a) {
   extern __shared__ uint32_t bits[];
   __shared__ uint32_t seen[kMaxPagedBatch / 32];   // rows of the call

@@ -206,9 +206,9 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
         *reinterpret_cast<uint4*>(dst + ux * 16) = isv ? c.x : pack(x);
         *reinterpret_cast<uint4*>(dst + uy * 16) = isv ? c.y : pack(y);
       } else {
-        // From fp32, by the scale's reciprocal: 1.5 * 2^-24 off before the rounding to e4m3's 2^-4 (a
-        // division per value takes twice the time of everything else).  `up` keeps the reciprocal a normal
-        // number: 0 / 1e-39 is 0, and 0 times an infinite reciprocal is none.
+        // From fp32, by the scale's reciprocal: off by 2^-23 (its rounding and the product's) before the
+        // rounding to e4m3's 2^-4 (a division per value takes twice the time of everything else).  `up` keeps
+        // the reciprocal a normal number: 0 / 1e-39 is 0, and 0 times an infinite reciprocal is none.
         const float* const scales = isv ? a.v_scale : a.k_scale;
         const float scale = scales ? scales[h] : 1.0f;
         const float up = fabsf(scale) < 0x1p-64f ? 0x1p64f : fabsf(scale) > 0x1p64f ? 0x1p-64f : 1.0f;

@@ -343,7 +343,10 @@ size_t fa_paged_decode_workspace_size(int B, int K, int G, int T, int H);
  * outside [0, B) left out, a request named again left to the first that names it,
  * and where group_starts falls or leaves [0, n_members] nothing is shared.  All
  * of these set FA_ERR_DEVICE_VALUE; results stay right.  (A small call may read every
- * request's keys on their own; it does not look at the groups then.)
+ * request's keys on their own; it does not look at the groups then.  Calls are small by
+ * the keys that their tables reach to, max_pages * page_size for each member, since the
+ * lengths are on the device: the order of sums, and with it the last bit, goes by
+ * that, and a few short requests in a wide table are faster as fa_paged_decode.)
  * `workspace`: as in fa_paged_decode, of fa_paged_decode_shared_workspace_size bytes.
  */
 int fa_paged_decode_shared(const void* q, const void* k_cache, const void* v_cache, int cache_type,
